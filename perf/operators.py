@@ -212,9 +212,9 @@ def _rows(cu, nseq, rows):
 
 
 def _exponent(x):
-    """The smallest e with max |x| <= 448 * 2^e over the last axis."""
+    """The smallest e from -100 on with max |x| <= 448 * 2^e over the last axis."""
     m, e = torch.frexp(x.abs().amax(-1))  # max = m 2^e, 0.5 <= m < 1; 448 = 0.875 * 2^9
-    return (e - 9 + (m > 0.875).to(torch.int32)).clamp(-100, 127)
+    return torch.where(m == 0, -100, e - 9 + (m > 0.875).to(torch.int32)).clamp(-100, 127)
 
 
 def _append(st):
