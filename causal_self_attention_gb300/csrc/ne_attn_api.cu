@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include <cudaTypedefs.h>
@@ -19,7 +20,9 @@
 namespace ne {
 cudaError_t launch_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        const CUtensorMap& tmO, const FwdParams& p, int n_qtiles,
-                       cudaStream_t stream);
+                       cudaStream_t stream, Pair pair);
+int fwd_blocks(Pair pair, int n_qtiles);
+int bwd_group_splits(int n_tot, int max_len, int H, int group);
 cudaError_t launch_rope_rows(const __nv_bfloat16* x0, __nv_bfloat16* xr0,
                              const __nv_bfloat16* x1, __nv_bfloat16* xr1, const Problem& pb,
                              const RopeTable& rope, cudaStream_t stream);
@@ -44,6 +47,17 @@ cudaError_t launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, const 
                           const RopeTable& rope, float scale_log2, float* part,
                           __nv_bfloat16* out, float* lse, int* status, cudaStream_t stream,
                           bool rot);
+cudaError_t launch_kv_append(const __nv_bfloat16* k, const __nv_bfloat16* v, const int* cu,
+                             const int* start_pos, int nseq, int n_tot, const PagedCache& pc,
+                             bool e4m3, const RopeTable& rope, int* status, cudaStream_t stream);
+cudaError_t launch_kv_read(__nv_bfloat16* k, __nv_bfloat16* v, const int* cu,
+                           const int* start_pos, int nseq, int n_tot, const PagedCache& pc,
+                           bool e4m3, int* status, cudaStream_t stream);
+size_t paged_part_bytes(int B, int H, int max_seqlen);
+cudaError_t launch_decode_paged(const __nv_bfloat16* q, const PagedCache& pc, bool e4m3,
+                                const int* seq_lens, int B, int H, const RopeTable& rope,
+                                float scale_log2, float* part, __nv_bfloat16* out, float* lse,
+                                int* status, cudaStream_t stream);
 constexpr unsigned kDecodeBoxRows = 32;  // keys per pipeline stage of the decode kernel
 cudaError_t launch_rmsnorm(const __nv_bfloat16* x, const __nv_bfloat16* g, __nv_bfloat16* xn,
                            float* rstd, int M, int C, float eps, cudaStream_t stream);
@@ -191,7 +205,12 @@ ne_status rope_table(DeviceState& st, float base, int positions, cudaStream_t st
   if (capture != cudaStreamCaptureStatusNone) return NE_ERR_UNSUPPORTED;
   int cap = 4096;
   while (cap < positions) cap *= 2;
-  std::vector<float2> host(static_cast<size_t>(cap) * 64);
+  std::vector<float2> host;
+  try {
+    host.resize(static_cast<size_t>(cap) * 64);
+  } catch (const std::bad_alloc&) {
+    return NE_ERR_OOM;
+  }
   float2* inter = host.data() + static_cast<size_t>(cap) * 32;
   for (int i = 0; i < 32; ++i) {
     const double theta = std::pow(static_cast<double>(base), -(2.0 * i) / 64.0);
@@ -354,6 +373,7 @@ struct Shape {
   const int* cu = nullptr;
   int nseq = 0, n_tot = 0, max_len = 0, H = 0, D = 0;
   bool fixed = true;
+  int group = 1;  // query heads per key/value head
 };
 
 ne_status check_shape(const Shape& s) {
@@ -378,6 +398,7 @@ ne::Problem make_problem(const Shape& s) {
   pb.H = s.H;
   pb.n_tot = s.n_tot;
   pb.lse_fixed = s.fixed ? 1 : 0;
+  pb.group = s.group;
   return pb;
 }
 
@@ -445,9 +466,14 @@ ne_status run_fwd(const Shape& s, const void* q, const void* k, const void* v, f
   const void* keys = mode == Rot::kTrain ? kr_out : k;
   // Temporaries: the rotated keys (long sequences) and, for a packed batch,
   // the compacted item list.
-  const int nblk = (n_qtiles + 1) / 2;
-  const long long n_items = static_cast<long long>(nblk) * s.nseq * s.H;
-  const bool compact = !s.fixed && n_items <= kMaxCompactItems && 2 * nblk + 1 <= kMaxBuckets;
+  const ne::Pair pair = s.group == 1       ? ne::Pair::kRows
+                        : s.group % 2 == 0 ? ne::Pair::kSharedHeads
+                                           : ne::Pair::kSharedRows;
+  const bool head_pairs = pair == ne::Pair::kSharedHeads;
+  const int nblk = ne::fwd_blocks(pair, n_qtiles);
+  const long long n_items = static_cast<long long>(nblk) * s.nseq * (head_pairs ? s.H / 2 : s.H);
+  const int n_buckets = (head_pairs ? nblk : 2 * nblk) + 1;
+  const bool compact = !s.fixed && n_items <= kMaxCompactItems && n_buckets <= kMaxBuckets;
   const size_t kr_bytes =
       (mode == Rot::kRotate && !p.rotate_k) ? static_cast<size_t>(s.n_tot) * s.H * 64 * 2 : 0;
   const size_t tmp_bytes =
@@ -473,8 +499,8 @@ ne_status run_fwd(const Shape& s, const void* q, const void* k, const void* v, f
     if (compact) list = reinterpret_cast<int*>(static_cast<char*>(tmp) + align256(kr_bytes));
   }
   rc = encode_rows(&tq, queries, s.n_tot, s.H);
-  if (rc == NE_OK) rc = encode_rows(&tk, keys, s.n_tot, s.H);
-  if (rc == NE_OK) rc = encode_rows(&tv, v, s.n_tot, s.H);
+  if (rc == NE_OK) rc = encode_rows(&tk, keys, s.n_tot, s.H / s.group);
+  if (rc == NE_OK) rc = encode_rows(&tv, v, s.n_tot, s.H / s.group);
   // O tile stores (bf16 output only; the fp32 output is written per row).
   if (rc == NE_OK) rc = encode_rows(&to, out_f32 ? q : out, s.n_tot, s.H);
   if (rc == NE_OK) {
@@ -490,10 +516,12 @@ ne_status run_fwd(const Shape& s, const void* q, const void* k, const void* v, f
     const bool pass = (mode == Rot::kRotate && !p.rotate_k) || mode == Rot::kTrain;
     if (e == cudaSuccess && g_ev_rot && pass) e = cudaEventRecord(g_ev_rot, cs);
     if (e == cudaSuccess && compact) {
-      e = ne::launch_compact_items(p.pb, 0, nblk, 2 * nblk + 1, list, cs);
+      ne::Problem items = p.pb;
+      if (head_pairs) items.H /= 2;
+      e = ne::launch_compact_items(items, head_pairs ? 2 : 0, nblk, n_buckets, list, cs);
       p.compact = list;
     }
-    if (e == cudaSuccess) e = ne::launch_fwd(tq, tk, tv, to, p, n_qtiles, cs);
+    if (e == cudaSuccess) e = ne::launch_fwd(tq, tk, tv, to, p, n_qtiles, cs, pair);
   }
   if (own) {
     const cudaError_t e2 = cudaFreeAsync(tmp, cs);
@@ -520,7 +548,10 @@ ne_status run_bwd(const Shape& s, const void* q, const void* k, const void* v, c
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(dout) ||
       !aligned4(lse) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
     return NE_ERR_MISALIGNED;
-  const size_t need = ne_attn_bwd_workspace_bytes(s.n_tot, s.H, s.D);
+  const int Hkv = s.H / s.group;
+  const size_t need =
+      s.group == 1 ? ne_attn_bwd_workspace_bytes(s.n_tot, s.H, s.D)
+                   : ne_attn_gqa_bwd_workspace_bytes(s.n_tot, s.max_len, s.H, Hkv, s.D);
   if (workspace && workspace_bytes < need) return NE_ERR_INVALID_ARG;
   if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return NE_ERR_MISALIGNED;
   std::lock_guard<std::mutex> lock(g_mutex);
@@ -549,7 +580,7 @@ ne_status run_bwd(const Shape& s, const void* q, const void* k, const void* v, c
       NE_OK)
     return rc;
   CUtensorMap tq, tk, tv, tdo;
-  if ((rc = encode_rows(&tv, v, s.n_tot, s.H)) != NE_OK) return rc;
+  if ((rc = encode_rows(&tv, v, s.n_tot, Hkv)) != NE_OK) return rc;
   if ((rc = encode_rows(&tdo, dout, s.n_tot, s.H)) != NE_OK) return rc;
   void* ws = workspace;
   bool owned = false;
@@ -567,6 +598,11 @@ ne_status run_bwd(const Shape& s, const void* q, const void* k, const void* v, c
   p.delta = reinterpret_cast<float*>(wsb + acc_bytes);
   p.qr = reinterpret_cast<__nv_bfloat16*>(wsb + acc_bytes + del_bytes);
   p.kr = reinterpret_cast<__nv_bfloat16*>(wsb + acc_bytes + del_bytes + rot_bytes);
+  if (s.group > 1) {  // in place of q', k' (the caller's): the partials of a split group
+    p.splits = ne::bwd_group_splits(s.n_tot, s.max_len, s.H, s.group);
+    p.dk_part = reinterpret_cast<float*>(wsb + acc_bytes + del_bytes);
+    p.dv_part = p.dk_part + static_cast<size_t>(p.splits) * s.n_tot * Hkv * 64;
+  }
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k = static_cast<const __nv_bfloat16*>(k);
   if (!p.rotate_in) {  // the main kernel reads q', k' where the caller keeps them
@@ -575,8 +611,10 @@ ne_status run_bwd(const Shape& s, const void* q, const void* k, const void* v, c
   }
   // Packed batch: the compacted unit list in the library's temporary for this
   // stream (a stream-ordered allocation of the call's own during capture).
-  const long long n_units = static_cast<long long>(n_tiles) * s.nseq * s.H;
-  const bool compact = !s.fixed && n_units <= kMaxCompactItems && n_tiles + 1 <= kMaxBuckets;
+  const int unit_heads = s.group == 1 ? s.H : Hkv * p.splits;
+  const int n_buckets = n_tiles * (s.group == 1 ? 1 : (s.group + p.splits - 1) / p.splits) + 1;
+  const long long n_units = static_cast<long long>(n_tiles) * s.nseq * unit_heads;
+  const bool compact = !s.fixed && n_units <= kMaxCompactItems && n_buckets <= kMaxBuckets;
   int* list = nullptr;
   bool own_list = false;
   if (compact) {
@@ -598,13 +636,15 @@ ne_status run_bwd(const Shape& s, const void* q, const void* k, const void* v, c
   }
   CUtensorMap tdq, tdv, tdk;
   if (rc == NE_OK) rc = encode_rows(&tq, p.qr, s.n_tot, s.H);
-  if (rc == NE_OK) rc = encode_rows(&tk, p.kr, s.n_tot, s.H);
+  if (rc == NE_OK) rc = encode_rows(&tk, p.kr, s.n_tot, Hkv);
   if (rc == NE_OK) rc = encode_rows_f32(&tdq, p.dq_acc, s.n_tot, s.H);
-  if (rc == NE_OK) rc = encode_rows(&tdv, dv, s.n_tot, s.H);
-  if (rc == NE_OK) rc = encode_rows(&tdk, dk, s.n_tot, s.H);
+  if (rc == NE_OK) rc = encode_rows(&tdv, dv, s.n_tot, Hkv);
+  if (rc == NE_OK) rc = encode_rows(&tdk, dk, s.n_tot, Hkv);
   cudaError_t e = cudaSuccess;
   if (rc == NE_OK && compact) {
-    e = ne::launch_compact_items(p.pb, 1, n_tiles, n_tiles + 1, list, cs);
+    ne::Problem units = p.pb;
+    units.H = unit_heads;
+    e = ne::launch_compact_items(units, 1, n_tiles, n_tiles + 1, list, cs);
     p.compact = list;
   }
   if (rc == NE_OK && e == cudaSuccess)
@@ -658,6 +698,7 @@ const char* ne_status_string(ne_status s) {
     case NE_ERR_OOM: return "NE_ERR_OOM";
     case NE_ERR_BAD_SEQLEN: return "NE_ERR_BAD_SEQLEN";
     case NE_ERR_TOO_LARGE: return "NE_ERR_TOO_LARGE";
+    case NE_ERR_BAD_PAGE: return "NE_ERR_BAD_PAGE";
     default: return "NE_ERR_UNKNOWN";
   }
 }
@@ -845,6 +886,208 @@ ne_status ne_attn_varlen_bwd(const ne_bf16* q, const ne_bf16* k, const ne_bf16* 
   s.D = D;
   return run_bwd(s, q, k, v, out, dout, lse, rope_base, scale, dq, dk, dv, workspace,
                  workspace_bytes, stream);
+}
+
+size_t ne_attn_gqa_bwd_workspace_bytes(int n_tot, int max_seqlen, int H, int Hkv, int D) {
+  if (n_tot <= 0 || max_seqlen <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || D != 64) return 0;
+  if (H == Hkv) return ne_attn_bwd_workspace_bytes(n_tot, H, D);
+  const size_t s = ne::bwd_group_splits(n_tot, max_seqlen, H, H / Hkv);
+  return align256(static_cast<size_t>(n_tot) * H * 64 * sizeof(float)) +
+         align256(static_cast<size_t>(n_tot) * H * sizeof(float)) +
+         (s > 1 ? align256(2 * s * n_tot * Hkv * 64 * sizeof(float)) : 0);
+}
+
+namespace {
+// Shape of a packed batch with shared key/value heads; what its own kernels
+// bound beyond check_shape.
+ne_status gqa_shape(const int* cu_seqlens, int nseq, int n_tot, int max_seqlen, int H, int Hkv,
+                    int D, Shape* s) {
+  if (H <= 0 || Hkv <= 0 || H % Hkv != 0) return NE_ERR_INVALID_ARG;
+  if (nseq > 65535) return NE_ERR_INVALID_ARG;  // a grid dimension of the row passes
+  if (nseq > 0 && max_seqlen > 0 &&
+      (static_cast<long long>(max_seqlen) + 127) / 128 * nseq * H > (1LL << 31) - 1)
+    return NE_ERR_INVALID_ARG;  // work items are numbered in 32 bits
+  s->cu = cu_seqlens;
+  s->fixed = false;
+  s->nseq = nseq;
+  s->n_tot = n_tot;
+  s->max_len = max_seqlen;
+  s->H = H;
+  s->D = D;
+  s->group = H / Hkv;
+  return NE_OK;
+}
+}  // namespace
+
+ne_status ne_attn_gqa_varlen_fwd(const ne_bf16* q, const ne_bf16* k, const ne_bf16* v,
+                                 const int* cu_seqlens, int nseq, int n_tot, int max_seqlen,
+                                 int H, int Hkv, int D, float rope_base, float scale,
+                                 ne_bf16* out, float* lse, ne_bf16* qr, ne_bf16* kr,
+                                 void* stream) {
+  Shape s;
+  const ne_status rc = gqa_shape(cu_seqlens, nseq, n_tot, max_seqlen, H, Hkv, D, &s);
+  if (rc != NE_OK) return rc;
+  return run_fwd(s, q, k, v, rope_base, scale, out, 0, lse, stream, Rot::kTrain, qr, kr);
+}
+
+ne_status ne_attn_gqa_varlen_bwd(const ne_bf16* qr, const ne_bf16* kr, const ne_bf16* v,
+                                 const ne_bf16* out, const ne_bf16* dout, const float* lse,
+                                 const int* cu_seqlens, int nseq, int n_tot, int max_seqlen,
+                                 int H, int Hkv, int D, float rope_base, float scale, ne_bf16* dq,
+                                 ne_bf16* dk, ne_bf16* dv, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  Shape s;
+  const ne_status rc = gqa_shape(cu_seqlens, nseq, n_tot, max_seqlen, H, Hkv, D, &s);
+  if (rc != NE_OK) return rc;
+  return run_bwd(s, qr, kr, v, out, dout, lse, rope_base, scale, dq, dk, dv, workspace,
+                 workspace_bytes, stream, Rot::kTrain);
+}
+
+namespace {
+// The checks that every call on a paged cache shares; fills *pc.
+ne_status paged_cache(const void* k_pages, const void* v_pages, const uint8_t* k_scale,
+                      const uint8_t* v_scale, int kv_type, const int* block_table, int max_pages,
+                      int n_pages, int page_size, int Hkv, int D, int max_seqlen,
+                      ne::PagedCache* pc) {
+  if (!k_pages || !v_pages || !block_table) return NE_ERR_INVALID_ARG;
+  if (D != 64) return NE_ERR_UNSUPPORTED;
+  if (kv_type != NE_KV_BF16 && kv_type != NE_KV_E4M3) return NE_ERR_UNSUPPORTED;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 &&
+      page_size != 256)
+    return NE_ERR_UNSUPPORTED;
+  if (max_pages <= 0 || n_pages <= 0 || Hkv <= 0 || max_seqlen <= 0) return NE_ERR_INVALID_ARG;
+  if (max_seqlen > static_cast<long long>(max_pages) * page_size) return NE_ERR_INVALID_ARG;
+  // Rows of a pool are numbered in 32 bits by the tile loads (their
+  // coordinates), with room for a tile that starts inside the last page.
+  if (static_cast<long long>(n_pages) * Hkv > ((1LL << 31) - 1 - 256) / page_size)
+    return NE_ERR_INVALID_ARG;
+  if ((max_seqlen + 127) / 128 > 65535) return NE_ERR_INVALID_ARG;
+  if (kv_type == NE_KV_E4M3 && (!k_scale || !v_scale)) return NE_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(block_table))
+    return NE_ERR_MISALIGNED;
+  if (kv_type == NE_KV_E4M3 && (!aligned16(k_scale) || !aligned16(v_scale)))
+    return NE_ERR_MISALIGNED;
+  pc->k = const_cast<void*>(k_pages);
+  pc->v = const_cast<void*>(v_pages);
+  pc->k_scale = kv_type == NE_KV_E4M3 ? const_cast<uint8_t*>(k_scale) : nullptr;
+  pc->v_scale = kv_type == NE_KV_E4M3 ? const_cast<uint8_t*>(v_scale) : nullptr;
+  pc->block_table = block_table;
+  pc->max_pages = max_pages;
+  pc->n_pages = n_pages;
+  pc->page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6
+                   : page_size == 128 ? 7 : 8;
+  pc->Hkv = Hkv;
+  pc->max_seqlen = max_seqlen;
+  return NE_OK;
+}
+
+// Checks on the packed rows of ne_kv_append and ne_kv_read.
+ne_status packed_rows(const void* k, const void* v, const int* cu_seqlens, const int* start_pos,
+                      int nseq, int n_tot, int Hkv) {
+  if (!k || !v || !cu_seqlens || !start_pos) return NE_ERR_INVALID_ARG;
+  if (nseq <= 0 || n_tot <= 0 || Hkv <= 0) return NE_ERR_INVALID_ARG;
+  if (static_cast<long long>(n_tot) * Hkv > (1LL << 31) - 1) return NE_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(cu_seqlens) || !aligned4(start_pos))
+    return NE_ERR_MISALIGNED;
+  return NE_OK;
+}
+
+bool bad_base_or_none(float rope_base) { return !std::isfinite(rope_base) || rope_base < 0.f; }
+}  // namespace
+
+ne_status ne_kv_append(const ne_bf16* k, const ne_bf16* v, const int* cu_seqlens,
+                       const int* start_pos, int nseq, int n_tot, int Hkv, int D,
+                       float rope_base, int kv_type, void* k_pages, void* v_pages,
+                       uint8_t* k_scale, uint8_t* v_scale, const int* block_table, int max_pages,
+                       int n_pages, int page_size, int max_seqlen, void* stream) {
+  ne::PagedCache pc;
+  ne_status rc = packed_rows(k, v, cu_seqlens, start_pos, nseq, n_tot, Hkv);
+  if (rc != NE_OK) return rc;
+  rc = paged_cache(k_pages, v_pages, k_scale, v_scale, kv_type, block_table, max_pages, n_pages,
+                   page_size, Hkv, D, max_seqlen, &pc);
+  if (rc != NE_OK) return rc;
+  if (bad_base_or_none(rope_base)) return NE_ERR_INVALID_ARG;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != NE_OK) return rc;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  RopeTable rope{nullptr, nullptr, 0};
+  if (rope_base > 0.f && (rc = rope_table(*st, rope_base, max_seqlen, cs, &rope)) != NE_OK)
+    return rc;
+  return cuda_status(ne::launch_kv_append(reinterpret_cast<const __nv_bfloat16*>(k),
+                                          reinterpret_cast<const __nv_bfloat16*>(v), cu_seqlens,
+                                          start_pos, nseq, n_tot, pc, kv_type == NE_KV_E4M3, rope,
+                                          st->status, cs));
+}
+
+ne_status ne_kv_read(int kv_type, const void* k_pages, const void* v_pages,
+                     const uint8_t* k_scale, const uint8_t* v_scale, const int* block_table,
+                     int max_pages, int n_pages, int page_size, int max_seqlen,
+                     const int* cu_seqlens, const int* start_pos, int nseq, int n_tot, int Hkv,
+                     int D, ne_bf16* k, ne_bf16* v, void* stream) {
+  ne::PagedCache pc;
+  ne_status rc = packed_rows(k, v, cu_seqlens, start_pos, nseq, n_tot, Hkv);
+  if (rc != NE_OK) return rc;
+  rc = paged_cache(k_pages, v_pages, k_scale, v_scale, kv_type, block_table, max_pages, n_pages,
+                   page_size, Hkv, D, max_seqlen, &pc);
+  if (rc != NE_OK) return rc;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != NE_OK) return rc;
+  return cuda_status(ne::launch_kv_read(reinterpret_cast<__nv_bfloat16*>(k),
+                                        reinterpret_cast<__nv_bfloat16*>(v), cu_seqlens,
+                                        start_pos, nseq, n_tot, pc, kv_type == NE_KV_E4M3,
+                                        st->status, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ne_attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int max_seqlen) {
+  if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || max_seqlen <= 0) return 0;
+  return ne::paged_part_bytes(B, H, max_seqlen);
+}
+
+ne_status ne_attn_decode_paged(const ne_bf16* q, int kv_type, const void* k_pages,
+                               const void* v_pages, const uint8_t* k_scale,
+                               const uint8_t* v_scale, const int* block_table, int max_pages,
+                               int n_pages, int page_size, int max_seqlen, const int* seq_lens,
+                               int B, int H, int Hkv, int D, float rope_base, float scale,
+                               ne_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  if (!q || !seq_lens || !out || !lse) return NE_ERR_INVALID_ARG;
+  if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0) return NE_ERR_INVALID_ARG;
+  if (B > 65535 || H > 65535) return NE_ERR_INVALID_ARG;
+  ne::PagedCache pc;
+  ne_status rc = paged_cache(k_pages, v_pages, k_scale, v_scale, kv_type, block_table, max_pages,
+                             n_pages, page_size, Hkv, D, max_seqlen, &pc);
+  if (rc != NE_OK) return rc;
+  if (!std::isfinite(scale) || scale <= 0.f || bad_base_or_none(rope_base))
+    return NE_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned4(seq_lens) || !aligned4(lse))
+    return NE_ERR_MISALIGNED;
+  const size_t need = ne_attn_decode_paged_workspace_bytes(B, H, Hkv, max_seqlen);
+  if (workspace && workspace_bytes < need) return NE_ERR_INVALID_ARG;
+  if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 15u)) return NE_ERR_MISALIGNED;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != NE_OK) return rc;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  RopeTable rope{nullptr, nullptr, 0};
+  if (rope_base > 0.f && (rc = rope_table(*st, rope_base, max_seqlen, cs, &rope)) != NE_OK)
+    return rc;
+  void* ws = workspace;
+  const bool owned = !ws;
+  if (owned) {
+    const cudaError_t e = cudaMallocAsync(&ws, need, cs);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  cudaError_t e = ne::launch_decode_paged(
+      reinterpret_cast<const __nv_bfloat16*>(q), pc, kv_type == NE_KV_E4M3, seq_lens, B, H, rope,
+      scale * 1.4426950408889634f, static_cast<float*>(ws), reinterpret_cast<__nv_bfloat16*>(out),
+      lse, st->status, cs);
+  if (owned) {
+    const cudaError_t e2 = cudaFreeAsync(ws, cs);
+    if (e == cudaSuccess) e = e2;
+  }
+  return cuda_status(e);
 }
 
 size_t ne_attn_decode_workspace_bytes(int B, int H, int Tmax) {
@@ -1143,6 +1386,7 @@ ne_status ne_attn_get_device_status(void* stream) {
   g_last_code = code;
   if (code == ne::NE_DEV_OK) return NE_OK;
   if (code == ne::NE_DEV_BAD_SEQLEN) return NE_ERR_BAD_SEQLEN;
+  if (code == ne::NE_DEV_BAD_PAGE) return NE_ERR_BAD_PAGE;
   if (code >= ne::NE_DEV_TIMEOUT_BASE) return NE_ERR_TIMEOUT;
   return NE_ERR_CUDA;
 }

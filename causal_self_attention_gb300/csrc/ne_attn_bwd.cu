@@ -48,6 +48,8 @@
 //               previous unit's last dP^T has completed
 // TMEM columns: S^T 0-127, dP^T 128-255, dV 256-319, dK' 320-383, dQ' 384-447,
 // P^T 448-511 (bf16 pairs).
+#include <algorithm>
+
 #include "ne_rope.cuh"
 #include "ne_sm100.cuh"
 
@@ -344,39 +346,80 @@ __global__ void __launch_bounds__(256, bwd::kPrepCtasPerSm)
 // ---------------------------------------------------------------------------
 namespace bwd {
 
-// One unit: key tile kt of (sequence seq, head h).
+// One unit: key tile kt of (sequence seq, key/value head h), with the query
+// heads h0 .. h0 + n_it / n_qt - 1 that share it (one, h itself, when heads are
+// not shared), one after the other.
 struct Unit {
   int seq, h, kt;
   int start, len;  // the sequence's first row in the packed tensors, its length
-  int n_it;        // query tiles kt .. n_qt - 1
+  int n_qt;        // query tiles kt .. of each of its query heads
+  int n_it;        // steps: n_qt per query head
+  int h0;
+  int split;       // which share of the group's query heads
 };
+
+// Units per sequence and key tile.
+template <bool kShared>
+__device__ __forceinline__ int unit_heads(const BwdParams& p) {
+  return kShared ? p.pb.H / p.pb.group * p.splits : p.pb.H;
+}
 
 // Unit r of the longest-first order; false for an empty unit (the sequence
 // has no such key tile, or a bad cu_seqlens entry).
+template <bool kShared>
 __device__ __forceinline__ bool get_unit(const BwdParams& p, int r, Unit& u) {
-  const int n_sh = p.pb.nseq * p.pb.H;
+  const int n_h = unit_heads<kShared>(p);
+  const int n_sh = p.pb.nseq * n_h;
   const int sh = r % n_sh;
   u.kt = r / n_sh;
-  u.seq = sh / p.pb.H;
-  u.h = sh % p.pb.H;
+  u.seq = sh / n_h;
+  u.h = sh % n_h;
   if (!seq_bounds(p.pb, u.seq, u.start, u.len, nullptr)) return false;
   if (u.kt * kBN >= u.len) return false;
-  u.n_it = (u.len + kBM - 1) / kBM - u.kt;
+  u.n_qt = u.n_it = (u.len + kBM - 1) / kBM - u.kt;
+  u.h0 = u.h;
+  u.split = 0;
+  if constexpr (kShared) {
+    u.split = u.h % p.splits;
+    u.h /= p.splits;
+    // Share `split` of the group, as even as the count allows (none empty:
+    // splits <= group).
+    const int a = p.pb.group * u.split / p.splits, e = p.pb.group * (u.split + 1) / p.splits;
+    u.h0 = u.h * p.pb.group + a;
+    u.n_it = u.n_qt * (e - a);
+  }
   return true;
 }
 
+// Query tile (counted from kt) and query head of step `it` of a unit.
+template <bool kShared>
+__device__ __forceinline__ int step_tile(const Unit& u, int it) {
+  return kShared ? it % u.n_qt : it;
+}
+template <bool kShared>
+__device__ __forceinline__ int step_head(const Unit& u, int it) {
+  return kShared ? u.h0 + it / u.n_qt : u.h;
+}
+
 // The first k' >= k whose unit is not empty (its description in u), or -1.
+template <bool kShared>
 __device__ __forceinline__ int next_unit(const BwdParams& p, int n_units, int c, int G, int k,
                                          Unit& u) {
   for (;; ++k) {
     const int r = dealt_item(p.sched, p.compact, k, c, G, n_units);
     if (r >= n_units) return -1;
-    if (get_unit(p, r, u)) return k;
+    if (get_unit<kShared>(p, r, u)) return k;
   }
 }
 
 }  // namespace bwd
 
+// kShared: key/value heads shared by pb.group query heads.  A unit then walks
+// the query tiles of each of its query heads in turn, so that dV and dK' are
+// summed over the group in TMEM; where that makes the longest unit longer than
+// its fair share of a CTA, the group is split over several units whose fp32
+// sums the postprocess adds in a fixed order.
+template <bool kShared>
 __global__ void __launch_bounds__(512, 1)
     ne_attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
@@ -395,7 +438,7 @@ __global__ void __launch_bounds__(512, 1)
 
   const int G = gridDim.x;
   const int cta = blockIdx.x;
-  const int n_units = n_tiles * p.pb.nseq * p.pb.H;
+  const int n_units = n_tiles * p.pb.nseq * unit_heads<kShared>(p);
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
 
@@ -450,7 +493,7 @@ __global__ void __launch_bounds__(512, 1)
 #define NE_FOR_EACH_UNIT(u)                                                                   \
   for (int k_ = 0, r_ = dealt_item(p.sched, p.compact, 0, cta, G, n_units); r_ < n_units;     \
        ++k_, r_ = dealt_item(p.sched, p.compact, k_, cta, G, n_units))                           \
-    if (Unit u; get_unit(p, r_, u))
+    if (Unit u; get_unit<kShared>(p, r_, u))
 
   if (warp == 13 || warp == 15) {
     // ------------------------------- TMA producers: warp 13 Q'/dO, warp 15 K'/V
@@ -471,10 +514,11 @@ __global__ void __launch_bounds__(512, 1)
             ok = false;
             break;
           }
-          const int qrow = u.start + (u.kt + it) * kBM;
+          const int qrow = u.start + (u.kt + step_tile<kShared>(u, it)) * kBM;
+          const int qh = step_head<kShared>(u, it);
           mbar_arrive_expect_tx(&bars[B_QDO_FULL + s], 2 * kTileBytes);
-          tma_load_3d(sQ + s * kTileBytes, &tmQ, &bars[B_QDO_FULL + s], 0, u.h, qrow);
-          tma_load_3d(sDO + s * kTileBytes, &tmDO, &bars[B_QDO_FULL + s], 0, u.h, qrow);
+          tma_load_3d(sQ + s * kTileBytes, &tmQ, &bars[B_QDO_FULL + s], 0, qh, qrow);
+          tma_load_3d(sDO + s * kTileBytes, &tmDO, &bars[B_QDO_FULL + s], 0, qh, qrow);
           last_issued[s] = g;
         }
       }
@@ -541,7 +585,7 @@ __global__ void __launch_bounds__(512, 1)
       int nu = 0;
       NE_FOR_EACH_UNIT(u) {
         if (!mbar_wait(&bars[B_EPI_FULL], nu & 1, abort_flag, p.status, 50)) break;
-        if ((u.kt + 1) * kBN <= u.len) {
+        if ((u.kt + 1) * kBN <= u.len && (!kShared || p.splits == 1)) {
           const int row0 = u.start + u.kt * kBN;
           tma_store_3d(&tmDV, sDST, 0, u.h, row0);
           tma_store_3d(&tmDK, sDST + kTileBytes, 0, u.h, row0);
@@ -691,17 +735,18 @@ __global__ void __launch_bounds__(512, 1)
     // tiles are staged during the previous unit).  Cursor: unit ua (index
     // ka, -1 past the end), its tile ita, the CTA's tile number ga.
     Unit ua;
-    int ka = next_unit(p, n_units, cta, G, 0, ua);
+    int ka = next_unit<kShared>(p, n_units, cta, G, 0, ua);
     int ita = 0, ga = 0;
     // LSE (log2 units) and D of query row r of the cursor's tile; rows past
     // the sequence get LSE = +inf, hence P = 0.  The loads always address a
     // row of the sequence (read-only loads may run ahead of the condition
     // that guards them).
     auto load_rowstats = [&](float& l2, float& dl) {
-      const int qpos = (ua.kt + ita) * kBM + r;
+      const int qpos = (ua.kt + step_tile<kShared>(ua, ita)) * kBM + r;
       const int qc = qpos < ua.len ? qpos : ua.len - 1;
-      const float l = __ldg(p.lse + lse_index(p.pb, ua.h, ua.seq, ua.start, qc));
-      const float d = __ldg(p.delta + static_cast<long long>(ua.h) * p.pb.n_tot + ua.start + qc);
+      const int qh = step_head<kShared>(ua, ita);
+      const float l = __ldg(p.lse + lse_index(p.pb, qh, ua.seq, ua.start, qc));
+      const float d = __ldg(p.delta + static_cast<long long>(qh) * p.pb.n_tot + ua.start + qc);
       l2 = qpos < ua.len ? l * 1.4426950408889634f : INFINITY;
       dl = qpos < ua.len ? d : 0.f;
     };
@@ -721,7 +766,7 @@ __global__ void __launch_bounds__(512, 1)
       ++ga;
       if (++ita == ua.n_it) {
         ita = 0;
-        ka = next_unit(p, n_units, cta, G, ka + 1, ua);
+        ka = next_unit<kShared>(p, n_units, cta, G, ka + 1, ua);
       }
       return true;
     };
@@ -764,9 +809,10 @@ __global__ void __launch_bounds__(512, 1)
         fence_proxy_async_smem();
         named_bar_sync(1, 128);
         if (r == 0) {
-          const int qrow = u.start + (u.kt + it) * kBM;
-          tma_reduce_add_3d(&tmDQ, sDQ, 0, u.h, qrow);
-          tma_reduce_add_3d(&tmDQ, sDQ + kTileBytes, 32, u.h, qrow);
+          const int qrow = u.start + (u.kt + step_tile<kShared>(u, it)) * kBM;
+          const int qh = step_head<kShared>(u, it);
+          tma_reduce_add_3d(&tmDQ, sDQ, 0, qh, qrow);
+          tma_reduce_add_3d(&tmDQ, sDQ + kTileBytes, 32, qh, qrow);
           bulk_commit_group();
         }
         // A failure here is carried into the next tile's vote.
@@ -792,6 +838,7 @@ __global__ void __launch_bounds__(512, 1)
     int nu = 0;  // units
     NE_FOR_EACH_UNIT(u) {
       if (!ok) break;
+      int qt = 0;  // query tile of the step, counted from kt
       for (int it = 0; it < u.n_it; ++it) {
         const int gq = g + it;
         if (!mbar_wait_warp(&bars[B_S_FULL], gq & 1, abort_flag, p.status, 39)) {
@@ -826,7 +873,7 @@ __global__ void __launch_bounds__(512, 1)
             tc_fence_before();
             mbar_arrive(&bars[B_S_FREE]);  // S^T/dP^T may be overwritten now
           }
-          if (it == 0) {
+          if (kShared ? qt == 0 : it == 0) {  // the diagonal tile
 #pragma unroll
             for (int col = 0; col < 32; ++col)
               if (64 * half + 32 * hh + col < r) sv[col] = 0xff800000u;
@@ -877,6 +924,7 @@ __global__ void __launch_bounds__(512, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&bars[B_DS_FULL]);
+        if (kShared && ++qt == u.n_qt) qt = 0;
       }
       if (!ok) break;
       // ---- epilogue of the unit: dV (first half), scale dK' (second half),
@@ -885,7 +933,8 @@ __global__ void __launch_bounds__(512, 1)
       // (Overlapped by the next unit's S^T/dP^T MMAs; its first dV/dK' MMAs
       // need these TMEM columns only after this thread's next DS_FULL arrival.)
       const int kpos = u.kt * kBN + r;
-      const bool full_tile = (u.kt + 1) * kBN <= u.len;
+      const bool split = kShared && p.splits > 1;  // an fp32 partial of dV, scale dK'
+      const bool full_tile = (u.kt + 1) * kBN <= u.len && !split;
       // dV, dK' are final once the last tile's dV/dK' MMAs have completed; a
       // full tile is staged in the dS^T buffer, free once the last dQ' MMA
       // (its last reader) has completed too.
@@ -902,6 +951,24 @@ __global__ void __launch_bounds__(512, 1)
       tmem_ld_wait(gr);
       tmem_ld_wait(gr + 32);
       const float sc = half ? p.scale : 1.f;
+      if constexpr (kShared) {
+        if (split) {
+          if (kpos < u.len) {
+            const int Hkv = p.pb.H / p.pb.group;
+            const long long orow =
+                ((static_cast<long long>(u.split) * p.pb.n_tot + u.start + kpos) * Hkv + u.h) * kHD;
+            float4* dst = reinterpret_cast<float4*>((half ? p.dk_part : p.dv_part) + orow);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              dst[c] = make_float4(__uint_as_float(gr[4 * c]) * sc, __uint_as_float(gr[4 * c + 1]) * sc,
+                                   __uint_as_float(gr[4 * c + 2]) * sc, __uint_as_float(gr[4 * c + 3]) * sc);
+          }
+          mbar_arrive(&bars[B_EPI_FULL]);
+          g += u.n_it;
+          ++nu;
+          continue;
+        }
+      }
       uint4 w[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c)
@@ -925,7 +992,8 @@ __global__ void __launch_bounds__(512, 1)
         // are written, one row per thread.  The dS^T buffer is not used, but
         // the unit still completes both epilogue phases.
         if (kpos < u.len) {
-          const long long orow = (static_cast<long long>(u.start + kpos) * p.pb.H + u.h) * kHD;
+          const int Hkv = kShared ? p.pb.H / p.pb.group : p.pb.H;
+          const long long orow = (static_cast<long long>(u.start + kpos) * Hkv + u.h) * kHD;
           uint4* dst = reinterpret_cast<uint4*>((half ? p.dk : p.dv) + orow);
 #pragma unroll
           for (int c = 0; c < 8; ++c) dst[c] = w[c];
@@ -1043,15 +1111,104 @@ __global__ void __launch_bounds__(kPostThreads)
   pdl_launch_dependents();
 }
 
+// ---------------------------------------------------------------------------
+// 3'. postprocess with shared key/value heads: as above, with dq over H heads
+//     (grid layer z = 0) and dk over H / group (z = 1); where the units split
+//     the groups, dk and dv (z = 2) are first summed over the splits' fp32
+//     partials, in their order, so that they are rounded once and do not
+//     depend on which unit ran first.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kPostThreads)
+    ne_attn_gqa_postprocess_kernel(const float* __restrict__ dq_acc,
+                                   const float* __restrict__ dk_part,
+                                   const float* __restrict__ dv_part, int splits,
+                                   __nv_bfloat16* __restrict__ dq, __nv_bfloat16* __restrict__ dk,
+                                   __nv_bfloat16* __restrict__ dv, const Problem pb, RopeTable rope,
+                                   float scale) {
+  pdl_wait();  // the main kernel's dQ' reduce-adds and dK, dV stores have completed
+  const int seq = blockIdx.y;
+  int start, len;
+  if (!seq_bounds(pb, seq, start, len, nullptr)) return;
+  const int z = blockIdx.z;
+  const int H = z == 0 ? pb.H : pb.H / pb.group;
+  const long long w = static_cast<long long>(blockIdx.x) * kPostThreads + threadIdx.x;
+  if (w >= static_cast<long long>(len) * H * kPostParts) return;
+  const int part = static_cast<int>(w % kPostParts);
+  const int rh = static_cast<int>(w / kPostParts);
+  const int pos = rh / H, h = rh - pos * H;
+  const long long row_off = (static_cast<long long>(start + pos) * H + h) * kHD;
+  float a[4], b[4];
+  __nv_bfloat16* d;
+  if (z == 0 || splits > 1) {
+    const float* src = z == 0 ? dq_acc : (z == 1 ? dk_part : dv_part);
+    const long long stride = static_cast<long long>(pb.n_tot) * H * kHD;
+    const int n = z == 0 ? 1 : splits;
+    const float sc = z == 0 ? scale : 1.f;
+    float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+    for (int i = 0; i < n; ++i) {
+      const float4 l = *reinterpret_cast<const float4*>(src + i * stride + row_off + part * 4);
+      const float4 u = *reinterpret_cast<const float4*>(src + i * stride + row_off + 32 + part * 4);
+      lo.x += l.x; lo.y += l.y; lo.z += l.z; lo.w += l.w;
+      hi.x += u.x; hi.y += u.y; hi.z += u.z; hi.w += u.w;
+    }
+    a[0] = lo.x * sc; a[1] = lo.y * sc; a[2] = lo.z * sc; a[3] = lo.w * sc;
+    b[0] = hi.x * sc; b[1] = hi.y * sc; b[2] = hi.z * sc; b[3] = hi.w * sc;
+    d = (z == 0 ? dq : (z == 1 ? dk : dv)) + row_off;
+  } else {  // scale dK', bf16, as the main kernel wrote it
+    d = dk + row_off;
+    const uint2 lo = *reinterpret_cast<const uint2*>(d + part * 4);
+    const uint2 hi = *reinterpret_cast<const uint2*>(d + 32 + part * 4);
+    a[0] = bf16lo_to_f32(lo.x); a[1] = bf16hi_to_f32(lo.x);
+    a[2] = bf16lo_to_f32(lo.y); a[3] = bf16hi_to_f32(lo.y);
+    b[0] = bf16lo_to_f32(hi.x); b[1] = bf16hi_to_f32(hi.x);
+    b[2] = bf16lo_to_f32(hi.y); b[3] = bf16hi_to_f32(hi.y);
+  }
+  if (z < 2) {
+    const float4* cs4 =
+        reinterpret_cast<const float4*>(rope.cs + static_cast<long long>(pos) * 32 + part * 4);
+    const float4 t0 = __ldg(cs4), t1 = __ldg(cs4 + 1);  // (cos, sin) of dims 4c .. 4c + 3
+    const float cz[4] = {t0.x, t0.z, t1.x, t1.z};
+    const float sz[4] = {t0.y, t0.w, t1.y, t1.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = a[i], y = b[i];
+      a[i] = x * cz[i] + y * sz[i];
+      b[i] = y * cz[i] - x * sz[i];
+    }
+  }
+  *reinterpret_cast<uint2*>(d + part * 4) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+  *reinterpret_cast<uint2*>(d + 32 + part * 4) =
+      make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
+  pdl_launch_dependents();
+}
+
+// Units per (key tile, key/value head): the fewest for which the longest unit
+// (the first key tile of a sequence of max_len rows) stays within a tenth of
+// the mean work of a CTA, on the reckoning that the rows make up as many
+// sequences of max_len as they can; at most one query head each.  152: the
+// SMs of the part (the reckoning is the same on the host that sizes the
+// workspace).
+int bwd_group_splits(int n_tot, int max_len, int H, int group) {
+  const long long nt = (static_cast<long long>(max_len) + kBM - 1) / kBM;
+  const long long n_full = std::max(1, n_tot / max_len);
+  const double mean = 0.5 * H * n_full * nt * (nt + 1) / 152.0;
+  int s = 1;
+  while (s < group && static_cast<double>((group + s - 1) / s) * nt > 1.1 * mean) ++s;
+  return s;
+}
+
 cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        const CUtensorMap& tmDO, const CUtensorMap& tmDQ, const CUtensorMap& tmDV,
                        const CUtensorMap& tmDK, const BwdParams& p, int n_tiles,
                        cudaStream_t stream, cudaEvent_t ev_pre, cudaEvent_t ev_main) {
   static bool attr_set = false;
   if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(ne_attn_bwd_kernel,
+    cudaError_t e = cudaFuncSetAttribute(ne_attn_bwd_kernel<false>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          bwd::SMEM_BYTES);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(ne_attn_bwd_kernel<true>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, bwd::SMEM_BYTES);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(ne_attn_bwd_prep_stream_kernel,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1068,7 +1225,9 @@ cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
   if (!sm_count[dev] &&
       (e = cudaDeviceGetAttribute(&sm_count[dev], cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return e;
-  const long long n_units = static_cast<long long>(n_tiles) * p.pb.nseq * p.pb.H;
+  const bool shared = p.pb.group > 1;
+  const long long n_units = static_cast<long long>(n_tiles) * p.pb.nseq * (p.pb.H / p.pb.group) *
+                            p.splits;
   const int G = static_cast<int>(n_units < sm_count[dev] ? n_units : sm_count[dev]);
   BwdParams pm = p;
   if (pm.sched && pm.sched_ctas != G) pm.sched = nullptr;  // made for another grid: snake order
@@ -1087,11 +1246,19 @@ cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
   }
   if (e != cudaSuccess) return e;
   if (ev_pre && (e = cudaEventRecord(ev_pre, stream)) != cudaSuccess) return e;
-  e = launch_pdl(ne_attn_bwd_kernel, dim3(G), dim3(bwd::kThreads), bwd::SMEM_BYTES, stream, tmQ,
+  e = launch_pdl(shared ? ne_attn_bwd_kernel<true> : ne_attn_bwd_kernel<false>, dim3(G), dim3(bwd::kThreads), bwd::SMEM_BYTES, stream, tmQ,
                  tmK, tmV, tmDO, tmDQ, tmDV, tmDK, pm, n_tiles);
   if (e != cudaSuccess) return e;
   if (ev_main && (e = cudaEventRecord(ev_main, stream)) != cudaSuccess) return e;
   const long long post_items = static_cast<long long>(n_tiles) * kBM * p.pb.H * kPostParts;
+  if (shared) {
+    dim3 grid(static_cast<unsigned>((post_items + kPostThreads - 1) / kPostThreads), p.pb.nseq,
+              p.splits > 1 ? 3 : 2);
+    return launch_pdl(ne_attn_gqa_postprocess_kernel, grid, dim3(kPostThreads), 0, stream,
+                      static_cast<const float*>(p.dq_acc), static_cast<const float*>(p.dk_part),
+                      static_cast<const float*>(p.dv_part), p.splits, p.dq, p.dk, p.dv, p.pb,
+                      p.rope, p.scale);
+  }
   // Layer z = 0: dQ from the accumulator; z = 1: dK rotated in place (not
   // when the gradient w.r.t. k' is asked for: the main kernel wrote it).
   dim3 pgrid(static_cast<unsigned>((post_items + kPostThreads - 1) / kPostThreads), p.pb.nseq,

@@ -42,6 +42,14 @@
 // and l keep a common reference).
 // Key tiles entirely above the diagonal are never loaded or computed.
 //
+// Shared key/value heads (kPair != Pair::kRows, keys and queries rotated
+// beforehand): query head h reads key/value head h / group.  With an even
+// group an item is one 128-row tile of two neighbouring heads of the group,
+// which share every K'/V tile and end on the same diagonal tile: a sequence of
+// up to 128 rows then still fills both tiles, where two consecutive row tiles
+// of one head leave tile B empty (32 packed prompts and times below).  An odd
+// group keeps the consecutive row tiles.
+//
 // Barrier phases: the K and V rings count K tiles over all items of the CTA;
 // S_FULL / S_FREE / P_FULL / PV_DONE of tile X count the steps of tile X over
 // all items; Q_* (per Q buffer), O_FINAL and O_FREE count items.
@@ -96,7 +104,7 @@ constexpr uint32_t kIdescO = make_idesc_bf16(128, 64, false, true);    // P V (V
 
 // One work item: block `blk` of 256 query rows of (sequence seq, head h).
 struct Item {
-  int seq, h, blk;
+  int seq, h, blk;  // tile X: head h + X * head_step, rows from rowA + X * row_step
   int start, len;  // the sequence's first row in the packed tensors, its length
   int rowA;        // first row of tile A in the sequence
   bool hasB;       // tile B has rows inside the sequence
@@ -107,15 +115,25 @@ struct Item {
 // first (they have the most key tiles), then the next lower, ...  Returns
 // false for an empty item (the sequence has no such block, or a bad
 // cu_seqlens entry, which is reported once).
+template <Pair kPair>
 __device__ __forceinline__ bool get_item(const FwdParams& p, int nblk, int r, Item& it,
                                          bool report) {
-  const int n_sh = p.pb.nseq * p.pb.H;
+  const int n_h = kPair == Pair::kSharedHeads ? p.pb.H / 2 : p.pb.H;
+  const int n_sh = p.pb.nseq * n_h;
   const int sh = r % n_sh;
   it.blk = nblk - 1 - r / n_sh;
-  it.seq = sh / p.pb.H;
-  it.h = sh % p.pb.H;
+  it.seq = sh / n_h;
+  it.h = sh % n_h;
   if (!seq_bounds(p.pb, it.seq, it.start, it.len, (report && it.blk == 0) ? p.status : nullptr))
     return false;
+  if constexpr (kPair == Pair::kSharedHeads) {
+    it.h *= 2;
+    it.rowA = it.blk * kBM;
+    if (it.rowA >= it.len) return false;
+    it.hasB = true;
+    it.nkvA = it.nkvB = it.nkv = it.blk + 1;
+    return true;
+  }
   it.rowA = 2 * it.blk * kBM;
   if (it.rowA >= it.len) return false;
   it.hasB = it.rowA + kBM < it.len;
@@ -123,6 +141,20 @@ __device__ __forceinline__ bool get_item(const FwdParams& p, int nblk, int r, It
   it.nkvB = it.hasB ? 2 * it.blk + 2 : 0;
   it.nkv = it.hasB ? it.nkvB : it.nkvA;
   return true;
+}
+
+// First row in its sequence, and head, of tile x of an item; its key/value head.
+template <Pair kPair>
+__device__ __forceinline__ int tile_row(const Item& it, int x) {
+  return kPair == Pair::kSharedHeads ? it.rowA : it.rowA + x * kBM;
+}
+template <Pair kPair>
+__device__ __forceinline__ int tile_head(const Item& it, int x) {
+  return kPair == Pair::kSharedHeads ? it.h + x : it.h;
+}
+template <Pair kPair>
+__device__ __forceinline__ int kv_head(const FwdParams& p, const Item& it) {
+  return kPair == Pair::kRows ? it.h : it.h / p.pb.group;
 }
 
 }  // namespace fwd
@@ -135,7 +167,7 @@ __device__ __forceinline__ bool get_item(const FwdParams& p, int nblk, int r, It
 // e.g. by the QKV projection's epilogue).  Separate instantiations, so that
 // each compiles only its own epilogue (registers are tight in the softmax
 // warps).
-template <bool kRotateK, bool kRotateQ>
+template <bool kRotateK, bool kRotateQ, Pair kPair = Pair::kRows>
 __global__ void __launch_bounds__(fwd::kThreads, 1)
     ne_attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
@@ -151,7 +183,10 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
 
   const int G = gridDim.x;
   const int cta = blockIdx.x;
-  const int n_items = nblk * p.pb.nseq * p.pb.H;
+  static_assert(kPair == Pair::kRows || (!kRotateK && !kRotateQ),
+                "shared heads: operands rotated beforehand");
+  const int n_items =
+      nblk * p.pb.nseq * (kPair == Pair::kSharedHeads ? p.pb.H / 2 : p.pb.H);
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
 
@@ -202,7 +237,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
 #define NE_FOR_EACH_ITEM(it)                                                        \
   for (int k_ = 0, r_ = dealt_item(nullptr, p.compact, 0, cta, G, n_items); r_ < n_items;       \
        ++k_, r_ = dealt_item(nullptr, p.compact, k_, cta, G, n_items))                             \
-    if (Item it; get_item(p, nblk, r_, it, threadIdx.x == 0))
+    if (Item it; get_item<kPair>(p, nblk, r_, it, threadIdx.x == 0))
 
   if (warp == 13 || warp == 14) {
     // ------------------------------------ TMA producers: warp 13 K, warp 14 V
@@ -230,10 +265,11 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
           mbar_arrive_expect_tx(&bars[B_Q_FULL + b], 2 * kTileBytes);
           tma_load_3d(sQ + 2 * b * kTileBytes, &tmQ, &bars[B_Q_FULL + b], 0, it.h,
                       it.start + it.rowA);
-          tma_load_3d(sQ + (2 * b + 1) * kTileBytes, &tmQ, &bars[B_Q_FULL + b], 0, it.h,
-                      it.start + it.rowA + kBM);
+          tma_load_3d(sQ + (2 * b + 1) * kTileBytes, &tmQ, &bars[B_Q_FULL + b], 0,
+                      tile_head<kPair>(it, 1), it.start + tile_row<kPair>(it, 1));
           ++nq;
         }
+        const int hk = kv_head<kPair>(p, it);
         for (int j = 0; j < it.nkv; ++j, ++g) {
           const int s = g % kStages;
           if (g >= kStages &&
@@ -243,7 +279,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(&full[s], kTileBytes);
-          tma_load_3d(ring + s * kTileBytes, tm, &full[s], 0, it.h, it.start + j * kBN);
+          tma_load_3d(ring + s * kTileBytes, tm, &full[s], 0, hk, it.start + j * kBN);
         }
       }
       if (!ok || *abort_flag) {
@@ -284,9 +320,10 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
           if (x == 1 && !it.hasB) continue;
           if (!(ok = mbar_wait(&bars[B_OST_FULL + x], nst[x] & 1, abort_flag, p.status, 16))) break;
           ++nst[x];
-          const int row0 = it.rowA + x * kBM;
+          const int row0 = tile_row<kPair>(it, x);
           if (!p.out_f32 && row0 + kBM <= it.len)
-            tma_store_3d(&tmO, sQ + (2 * b + x) * kTileBytes, 0, it.h, it.start + row0);
+            tma_store_3d(&tmO, sQ + (2 * b + x) * kTileBytes, 0, tile_head<kPair>(it, x),
+                         it.start + row0);
         }
         if (!ok) break;
         bulk_commit_group();
@@ -460,7 +497,8 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
       const int nkv_x = x ? it.nkvB : it.nkvA;
       if constexpr (!kRotateK) ++nq;
       if (nkv_x == 0) continue;  // tile B outside the sequence
-      const int diag = x ? 2 * it.blk + 1 : 2 * it.blk;
+      const int diag =
+          kPair == Pair::kSharedHeads ? it.blk : (x ? 2 * it.blk + 1 : 2 * it.blk);
       float m_ref = 0.f;  // reference max (log2 units) the P values are taken against
       float l_sum = 0.f;
       for (int j = 0; j < nkv_x; ++j) {
@@ -556,8 +594,9 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
       // index, so that none of it stays live (in registers or spilled) through
       // the loop above.
       Item e;
-      get_item(p, nblk, opaque_int(r_), e, false);
-      const int erow = e.rowA + x * kBM + r;
+      get_item<kPair>(p, nblk, opaque_int(r_), e, false);
+      const int erow = tile_row<kPair>(e, x) + r;
+      const int eh = tile_head<kPair>(e, x);
       tc_fence_after();
       uint32_t o[64];
       tmem_ld_x32(tO, o);
@@ -570,7 +609,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
         // Every row written by its own thread.
         if (erow < e.len) {
           const float inv_l = 1.f / l_sum;
-          const long long orow = (static_cast<long long>(e.start + erow) * p.pb.H + e.h) * kHD;
+          const long long orow = (static_cast<long long>(e.start + erow) * p.pb.H + eh) * kHD;
           if (p.out_f32) {
             float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow);
 #pragma unroll
@@ -592,12 +631,12 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
             }
           }
           // LSE in natural-log units: (m_ref + log2 l) * ln 2.
-          p.lse[lse_index(p.pb, e.h, e.seq, e.start, erow)] =
+          p.lse[lse_index(p.pb, eh, e.seq, e.start, erow)] =
               (m_ref + __log2f(l_sum)) * 0.69314718055994531f;
         }
       } else {
         const float inv_l = 1.f / l_sum;
-        const long long orow = (static_cast<long long>(e.start + erow) * p.pb.H + e.h) * kHD;
+        const long long orow = (static_cast<long long>(e.start + erow) * p.pb.H + eh) * kHD;
         if (p.out_f32) {
           if (erow < e.len) {
             float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow);
@@ -613,7 +652,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
           // tile (item nq - 1's buffer), and warp 14, lane 1 stores it with
           // TMA; the sequence's last, partial tile is written one row per
           // thread.
-          const bool whole = e.rowA + x * kBM + kBM <= e.len;
+          const bool whole = tile_row<kPair>(e, x) + kBM <= e.len;
           uint8_t* slot = sQ + (2 * (opaque_int(nq - 1) & 1) + x) * kTileBytes;
           uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow);
 #pragma unroll
@@ -633,7 +672,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
         mbar_arrive(&bars[B_OST_FULL + x]);
         // LSE in natural-log units: (m_ref + log2 l) * ln 2.
         if (erow < e.len)
-          p.lse[lse_index(p.pb, e.h, e.seq, e.start, erow)] =
+          p.lse[lse_index(p.pb, eh, e.seq, e.start, erow)] =
               (m_ref + __log2f(l_sum)) * 0.69314718055994531f;
       }
     }
@@ -673,7 +712,7 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int seq = blockIdx.y;
   int start, len;
   if (!seq_bounds(pb, seq, start, len, nullptr)) return;
-  const int H = pb.H;
+  const int H = blockIdx.z ? pb.H / pb.group : pb.H;
   const long long w = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
   if (w < static_cast<long long>(len) * H * kRopeParts) {
     const int c = static_cast<int>(w % kRopeParts);
@@ -704,7 +743,8 @@ __global__ void __launch_bounds__(kRopeThreads)
   pdl_launch_dependents();
 }
 
-// x1, xr1: a second tensor rotated by the same launch, or null.
+// x1, xr1: a second tensor (of pb.H / pb.group heads) rotated by the same
+// launch, or null.
 cudaError_t launch_rope_rows(const __nv_bfloat16* x0, __nv_bfloat16* xr0,
                              const __nv_bfloat16* x1, __nv_bfloat16* xr1, const Problem& pb,
                              const RopeTable& rope, cudaStream_t stream) {
@@ -715,9 +755,15 @@ cudaError_t launch_rope_rows(const __nv_bfloat16* x0, __nv_bfloat16* xr0,
                     xr1, pb, rope);
 }
 
+// Blocks of the longest sequence that a launch enumerates, and heads (or head
+// pairs) per sequence.
+int fwd_blocks(Pair pair, int n_qtiles) {
+  return pair == Pair::kSharedHeads ? n_qtiles : (n_qtiles + 1) / 2;
+}
+
 cudaError_t launch_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        const CUtensorMap& tmO, const FwdParams& p, int n_qtiles,
-                       cudaStream_t stream) {
+                       cudaStream_t stream, Pair pair) {
   static bool attr_set = false;
   if (!attr_set) {
     cudaError_t e = cudaFuncSetAttribute(ne_attn_fwd_kernel<true, true>,
@@ -728,6 +774,12 @@ cudaError_t launch_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
                                cudaFuncAttributeMaxDynamicSharedMemorySize, fwd::SMEM_BYTES);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(ne_attn_fwd_kernel<false, false>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, fwd::SMEM_BYTES);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(ne_attn_fwd_kernel<false, false, Pair::kSharedRows>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, fwd::SMEM_BYTES);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(ne_attn_fwd_kernel<false, false, Pair::kSharedHeads>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, fwd::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     attr_set = true;
@@ -742,9 +794,16 @@ cudaError_t launch_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
     e = cudaDeviceGetAttribute(&sm_count[dev], cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
   }
-  const int nblk = (n_qtiles + 1) / 2;
-  const long long n_items = static_cast<long long>(nblk) * p.pb.nseq * p.pb.H;
+  const int nblk = fwd_blocks(pair, n_qtiles);
+  const long long n_items = static_cast<long long>(nblk) * p.pb.nseq *
+                            (pair == Pair::kSharedHeads ? p.pb.H / 2 : p.pb.H);
   const int G = static_cast<int>(n_items < sm_count[dev] ? n_items : sm_count[dev]);
+  if (pair == Pair::kSharedRows)
+    return launch_pdl(ne_attn_fwd_kernel<false, false, Pair::kSharedRows>, dim3(G),
+                      dim3(fwd::kThreads), fwd::SMEM_BYTES, stream, tmQ, tmK, tmV, tmO, p, nblk);
+  if (pair == Pair::kSharedHeads)
+    return launch_pdl(ne_attn_fwd_kernel<false, false, Pair::kSharedHeads>, dim3(G),
+                      dim3(fwd::kThreads), fwd::SMEM_BYTES, stream, tmQ, tmK, tmV, tmO, p, nblk);
   if (p.rotate_k)
     return launch_pdl(ne_attn_fwd_kernel<true, true>, dim3(G), dim3(fwd::kThreads),
                       fwd::SMEM_BYTES, stream, tmQ, tmK, tmV, tmO, p, nblk);

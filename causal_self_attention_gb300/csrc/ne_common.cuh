@@ -20,6 +20,7 @@ constexpr int kTileBytes = kBM * kHD * 2;  // 16 KiB: one 128 x 64 bf16 tile
 constexpr int NE_DEV_OK = 0;
 constexpr int NE_DEV_BAD_SEQLEN = 1;        // a sequence longer than max_seqlen, or
                                             // cu_seqlens outside [0, n_tot]
+constexpr int NE_DEV_BAD_PAGE = 2;          // a block table entry outside [0, n_pages)
 constexpr int NE_DEV_TIMEOUT_BASE = 0x100;  // + wait site id
 
 // RoPE table: for position p and frequency i < 32, rope[p * 32 + i] = (cos, sin)
@@ -43,6 +44,34 @@ struct Problem {
   int H;
   int n_tot;              // total rows
   int lse_fixed;          // 1: LSE is [B, H, T]; 0: LSE is [H, N_tot]
+  int group = 1;          // query heads per key/value head (k, v, dk, dv: [N_tot, H / group, 64])
+};
+
+// A paged key/value cache: n_pages pages of 2^page_shift positions, each
+// [Hkv, page, 64] in both pools (a head's positions of a page are contiguous,
+// so that one copy fetches them), bf16 or e4m3.  Position n of sequence s
+// lies in slot n % page of page block_table[s * max_pages + n / page].  e4m3
+// rows have a scale byte each (scale [n_pages, Hkv, page]): the row's values
+// are e4m3 * 2^(byte - 127); byte 255 marks a row that held an infinity or NaN.
+struct PagedCache {
+  void* k;
+  void* v;
+  uint8_t* k_scale;  // nullptr for bf16
+  uint8_t* v_scale;
+  const int* block_table;
+  int max_pages;   // entries per sequence of the block table
+  int n_pages;
+  int page_shift;
+  int Hkv;
+  int max_seqlen;  // every position is below this (<= max_pages pages)
+};
+
+// How the two query tiles of a forward work item relate (template parameter of
+// the forward kernel).
+enum class Pair {
+  kRows,        // consecutive 128-row tiles of one head, one key/value head per query head
+  kSharedRows,  // the same, key/value heads shared by pb.group query heads
+  kSharedHeads  // one 128-row tile of two neighbouring query heads of a group
 };
 
 struct FwdParams {
@@ -84,6 +113,10 @@ struct BwdParams {
   const int* sched = nullptr;  // work schedule of the persistent main kernel, or
   int sched_ctas = 0;          // nullptr for the snake order; the grid it was made for
   const int* compact = nullptr;  // packed batch: the non-empty units (dealt_item), or nullptr
+  int splits = 1;                // shared heads: units per (key tile, key/value head), each
+                                 // with a share of the group's query heads
+  float* dk_part = nullptr;      // splits > 1: fp32 [splits, N_tot, H / group, 64] partials of
+  float* dv_part = nullptr;      // scale dK' and dV
 };
 
 // Sequence bounds of sequence s.  Returns false (and raises the device status)

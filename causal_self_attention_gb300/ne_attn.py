@@ -21,7 +21,8 @@ _lib = None
 NE_OK = 0
 STATUS_NAMES = {0: "NE_OK", 1: "NE_ERR_INVALID_ARG", 2: "NE_ERR_UNSUPPORTED",
                 3: "NE_ERR_MISALIGNED", 4: "NE_ERR_CUDA", 5: "NE_ERR_TIMEOUT", 6: "NE_ERR_OOM",
-                7: "NE_ERR_BAD_SEQLEN", 8: "NE_ERR_TOO_LARGE"}
+                7: "NE_ERR_BAD_SEQLEN", 8: "NE_ERR_TOO_LARGE", 9: "NE_ERR_BAD_PAGE"}
+KV_BF16, KV_E4M3 = 0, 1  # types of a paged cache's pools
 
 EXPORTED = ("ne_attn_fwd", "ne_attn_fwd_f32out", "ne_attn_bwd", "ne_attn_bwd_workspace_bytes",
             "ne_attn_bwd_noalloc", "ne_attn_decode", "ne_attn_decode_rotated",
@@ -34,7 +35,9 @@ EXPORTED = ("ne_attn_fwd", "ne_attn_fwd_f32out", "ne_attn_bwd", "ne_attn_bwd_wor
             "ne_attn_fwd_rotated", "ne_attn_bwd_rotated", "ne_attn_fwd_train",
             "ne_attn_bwd_train", "ne_attn_varlen_fwd_train", "ne_attn_varlen_bwd_train",
             "ne_attn_set_fwd_phase_event", "ne_mtp_head", "ne_mtp_head_workspace_bytes",
-            "ne_debug_schedule")
+            "ne_debug_schedule", "ne_attn_gqa_varlen_fwd", "ne_attn_gqa_varlen_bwd",
+            "ne_attn_gqa_bwd_workspace_bytes", "ne_kv_append", "ne_kv_read",
+            "ne_attn_decode_paged", "ne_attn_decode_paged_workspace_bytes", "ne_debug_kv_place")
 
 
 class NeAttnError(RuntimeError):
@@ -88,6 +91,12 @@ def lib():
         "ne_attn_set_fwd_phase_event": [P],
         "ne_mtp_head": [P, P, P, I, I, I, I, P, P, P, P, P, Z, P],
         "ne_debug_schedule": [I, I, I, I, P, I],
+        "ne_attn_gqa_varlen_fwd": [P, P, P, P, I, I, I, I, I, I, F, F, P, P, P, P, P],
+        "ne_attn_gqa_varlen_bwd": [P, P, P, P, P, P, P, I, I, I, I, I, I, F, F, P, P, P, P, Z, P],
+        "ne_kv_append": [P, P, P, P, I, I, I, I, F, I, P, P, P, P, P, I, I, I, I, P],
+        "ne_kv_read": [I, P, P, P, P, P, I, I, I, I, P, P, I, I, I, I, P, P, P],
+        "ne_attn_decode_paged": [P, I, P, P, P, P, P, I, I, I, I, P, I, I, I, I, F, F, P, P, P, Z,
+                                 P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -99,6 +108,10 @@ def lib():
     L.ne_mtp_head_workspace_bytes.restype = Z
     L.ne_attn_decode_workspace_bytes.argtypes = [I, I, I]
     L.ne_attn_decode_workspace_bytes.restype = Z
+    L.ne_attn_gqa_bwd_workspace_bytes.argtypes = [I, I, I, I, I]
+    L.ne_attn_gqa_bwd_workspace_bytes.restype = Z
+    L.ne_attn_decode_paged_workspace_bytes.argtypes = [I, I, I, I]
+    L.ne_attn_decode_paged_workspace_bytes.restype = Z
     L.ne_status_string.argtypes = [I]
     L.ne_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -470,6 +483,240 @@ def ne_attn_varlen_bwd_train(qr, kr, v, out, dout, lse, cu_seqlens, max_seqlen,
     return dq, dk, dv
 
 
+# ------------------------------------------- grouped heads and the paged cache
+
+class _Launch:
+    """Where a call runs: the tensors' device (all on one, made the current
+    device while the call launches) and the stream, under which the tensors
+    that the call creates are allocated too.  ``stream``: a torch stream, a
+    raw ``cudaStream_t``, or None for the device's current stream."""
+
+    def __init__(self, stream, *tensors):
+        devices = {t.device for t in tensors if t is not None}
+        if len(devices) != 1:
+            raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
+        self.device = devices.pop()
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        if stream.device != self.device:
+            raise ValueError(f"stream on {stream.device}, tensors on {self.device}")
+        self.stream = ctypes.c_void_p(stream.cuda_stream)
+        self._ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+
+def _out(t, shape, dtype, device, name):
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    return t
+
+
+def _ws_bytes(workspace):
+    if workspace is None:
+        return 0
+    if not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace.numel() * workspace.element_size()
+
+
+def _gqa_shapes(q, k, v, cu_seqlens, names=("q", "k", "v")):
+    for t, n in zip((q, k, v), names):
+        _need(t, torch.bfloat16, n)
+    _need(cu_seqlens, torch.int32, "cu_seqlens")
+    N, H, D = q.shape
+    Hkv = k.shape[1]
+    if tuple(k.shape) != (N, Hkv, D) or k.shape != v.shape or Hkv == 0 or H % Hkv:
+        raise ValueError(f"shapes: {names[0]} [N, H, D], {names[1]}, {names[2]} [N, Hkv, D] with "
+                         "H a multiple of Hkv")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be [nseq + 1]")
+    return N, H, Hkv, D, cu_seqlens.numel() - 1
+
+
+def ne_attn_gqa_varlen_fwd(q, k, v, cu_seqlens, max_seqlen, rope_base=10000.0, scale=None,
+                           out=None, lse=None, qr=None, kr=None, stream=None):
+    """Causal attention over packed prompts with shared key/value heads: ``q``
+    ``[N_tot, H, 64]``, ``k``, ``v`` ``[N_tot, Hkv, 64]`` bf16 with H a multiple
+    of Hkv (query head h reads key/value head ``h // (H // Hkv)``),
+    ``cu_seqlens`` int32 CUDA ``[nseq + 1]``.  Returns ``(out, lse, qr, kr)``:
+    ``lse`` ``[H, N_tot]`` fp32, and the rotated operands for the backward (or,
+    ``kr``, for a cache: :func:`ne_kv_append` with ``rope_base=0``)."""
+    N, H, Hkv, D, nseq = _gqa_shapes(q, k, v, cu_seqlens)
+    scale = D ** -0.5 if scale is None else scale
+    with _Launch(stream, q, k, v, cu_seqlens, out, lse, qr, kr) as on:
+        out = _out(out, q.shape, torch.bfloat16, on.device, "out")
+        lse = _out(lse, (H, N), torch.float32, on.device, "lse")
+        qr = _out(qr, q.shape, torch.bfloat16, on.device, "qr")
+        kr = _out(kr, k.shape, torch.bfloat16, on.device, "kr")
+        _check("ne_attn_gqa_varlen_fwd", lib().ne_attn_gqa_varlen_fwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), nseq, N, int(max_seqlen), H, Hkv, D,
+            float(rope_base), float(scale), _ptr(out), _ptr(lse), _ptr(qr), _ptr(kr), on.stream))
+    return out, lse, qr, kr
+
+
+def ne_attn_gqa_bwd_workspace_bytes(n_tot: int, max_seqlen: int, H: int, Hkv: int,
+                                    D: int = 64) -> int:
+    return int(lib().ne_attn_gqa_bwd_workspace_bytes(int(n_tot), int(max_seqlen), int(H),
+                                                     int(Hkv), int(D)))
+
+
+def ne_attn_gqa_varlen_bwd(qr, kr, v, out, dout, lse, cu_seqlens, max_seqlen, rope_base=10000.0,
+                           scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Backward of :func:`ne_attn_gqa_varlen_fwd` from its ``qr``, ``kr``, ``out``
+    and ``lse``.  Returns ``(dq, dk, dv)``: gradients w.r.t. the un-rotated q, k
+    and v, ``dk`` and ``dv`` summed over the query heads that share them."""
+    N, H, Hkv, D, nseq = _gqa_shapes(qr, kr, v, cu_seqlens, ("qr", "kr", "v"))
+    for t, n in ((out, "out"), (dout, "dout")):
+        _need(t, torch.bfloat16, n)
+        if t.shape != qr.shape:
+            raise ValueError(f"{n} must have the shape {tuple(qr.shape)}")
+    _out(lse, (H, N), torch.float32, None, "lse")
+    scale = D ** -0.5 if scale is None else scale
+    ws_bytes = _ws_bytes(workspace)
+    with _Launch(stream, qr, kr, v, out, dout, lse, cu_seqlens, dq, dk, dv, workspace) as on:
+        dq = _out(dq, qr.shape, torch.bfloat16, on.device, "dq")
+        dk = _out(dk, kr.shape, torch.bfloat16, on.device, "dk")
+        dv = _out(dv, v.shape, torch.bfloat16, on.device, "dv")
+        _check("ne_attn_gqa_varlen_bwd", lib().ne_attn_gqa_varlen_bwd(
+            _ptr(qr), _ptr(kr), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), _ptr(cu_seqlens), nseq,
+            N, int(max_seqlen), H, Hkv, D, float(rope_base), float(scale), _ptr(dq), _ptr(dk),
+            _ptr(dv), _ptr(workspace), ws_bytes, on.stream))
+    return dq, dk, dv
+
+
+def _paged(k_pages, v_pages, k_scale, v_scale, block_table, nseq):
+    """Checks a paged cache; returns (kv_type, n_pages, Hkv, page_size, max_pages)."""
+    if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError("k_pages must be bfloat16 or float8_e4m3fn")
+    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _need(t, k_pages.dtype, n)
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != 64:
+        raise ValueError("k_pages, v_pages must be [n_pages, Hkv, page_size, 64]")
+    _need(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != nseq:
+        raise ValueError(f"block_table must be [{nseq}, max_pages]")
+    n_pages, Hkv, page_size, _ = k_pages.shape
+    kv_type = KV_BF16 if k_pages.dtype == torch.bfloat16 else KV_E4M3
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if kv_type == KV_BF16:
+            if t is not None:
+                raise ValueError(f"{n}: a bfloat16 cache has no scales")
+            continue
+        if t is None:
+            raise ValueError(f"{n}: a float8_e4m3fn cache needs its scales")
+        _need(t, torch.uint8, n)
+        if tuple(t.shape) != (n_pages, Hkv, page_size):
+            raise ValueError(f"{n} must be [n_pages, Hkv, page_size]")
+    return kv_type, n_pages, Hkv, page_size, block_table.shape[1]
+
+
+def _row_places(cu_seqlens, start_pos):
+    for t, n in ((cu_seqlens, "cu_seqlens"), (start_pos, "start_pos")):
+        _need(t, torch.int32, n)
+    nseq = start_pos.numel()
+    if cu_seqlens.numel() != nseq + 1:
+        raise ValueError("cu_seqlens must be [nseq + 1] for start_pos [nseq]")
+    return nseq
+
+
+def ne_kv_append(k, v, cu_seqlens, start_pos, k_pages, v_pages, block_table, max_seqlen,
+                 k_scale=None, v_scale=None, rope_base=10000.0, stream=None):
+    """Write new rows into a paged cache: row i of sequence s of ``k``, ``v``
+    (``[n_tot, Hkv, 64]`` bf16, packed by ``cu_seqlens``) goes to position
+    ``start_pos[s] + i``.  ``k_pages``, ``v_pages``: ``[n_pages, Hkv, page_size,
+    64]``, bfloat16, or float8_e4m3fn with ``k_scale``, ``v_scale`` uint8
+    ``[n_pages, Hkv, page_size]``; ``block_table`` int32 ``[nseq, max_pages]``.
+    ``rope_base=0``: ``k`` is rotated already.  Returns ``(k_pages, v_pages)``,
+    written in place."""
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, torch.bfloat16, n)
+    nseq = _row_places(cu_seqlens, start_pos)
+    kv_type, n_pages, Hkv, page_size, max_pages = _paged(k_pages, v_pages, k_scale, v_scale,
+                                                         block_table, nseq)
+    n_tot, _, D = k.shape
+    if tuple(k.shape) != (n_tot, Hkv, D) or k.shape != v.shape:
+        raise ValueError("k, v must be [n_tot, Hkv, 64] with the pages' Hkv")
+    with _Launch(stream, k, v, cu_seqlens, start_pos, k_pages, v_pages, k_scale, v_scale,
+                 block_table) as on:
+        _check("ne_kv_append", lib().ne_kv_append(
+            _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(start_pos), nseq, n_tot, Hkv, D,
+            float(rope_base), kv_type, _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+            _ptr(v_scale), _ptr(block_table), max_pages, n_pages, page_size, int(max_seqlen),
+            on.stream))
+    return k_pages, v_pages
+
+
+def ne_kv_read(k_pages, v_pages, block_table, cu_seqlens, start_pos, n_tot, k_scale=None,
+               v_scale=None, max_seqlen=None, k=None, v=None, stream=None):
+    """Read rows of a paged cache back as bf16: row i of sequence s of the
+    result (``[n_tot, Hkv, 64]``, packed by ``cu_seqlens``) from position
+    ``start_pos[s] + i``.  The keys come rotated, as the cache holds them.
+    ``max_seqlen``: the block table's reach unless given.  Returns ``(k, v)``;
+    rows of the caller's ``k``, ``v`` that no sequence covers stay as they are."""
+    nseq = _row_places(cu_seqlens, start_pos)
+    kv_type, n_pages, Hkv, page_size, max_pages = _paged(k_pages, v_pages, k_scale, v_scale,
+                                                         block_table, nseq)
+    if max_seqlen is None:
+        max_seqlen = min(max_pages * page_size, 65535 * 128)
+    with _Launch(stream, k_pages, v_pages, k_scale, v_scale, block_table, cu_seqlens, start_pos,
+                 k, v) as on:
+        k = _out(k, (int(n_tot), Hkv, 64), torch.bfloat16, on.device, "k")
+        v = _out(v, (int(n_tot), Hkv, 64), torch.bfloat16, on.device, "v")
+        _check("ne_kv_read", lib().ne_kv_read(
+            kv_type, _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_table), max_pages, n_pages, page_size, int(max_seqlen), _ptr(cu_seqlens),
+            _ptr(start_pos), nseq, int(n_tot), Hkv, 64, _ptr(k), _ptr(v), on.stream))
+    return k, v
+
+
+def ne_attn_decode_paged_workspace_bytes(B: int, H: int, Hkv: int, max_seqlen: int) -> int:
+    return int(lib().ne_attn_decode_paged_workspace_bytes(int(B), int(H), int(Hkv),
+                                                          int(max_seqlen)))
+
+
+def ne_attn_decode_paged(q, k_pages, v_pages, block_table, seq_lens, max_seqlen, k_scale=None,
+                         v_scale=None, rope_base=10000.0, scale=None, out=None, lse=None,
+                         workspace=None, stream=None):
+    """Decode attention over a paged cache: ``q`` ``[B, H, 64]`` bf16 (the new
+    tokens, un-rotated; ``rope_base=0``: rotated already), the cache as in
+    :func:`ne_kv_append` with the new tokens' rows in it, ``seq_lens`` int32
+    ``[B]`` on the device (positions 0 .. seq_lens[b] - 1 are attended; 0 gives
+    zeros and -inf).  Returns ``(out [B, H, 64] bf16, lse [B, H] fp32)``."""
+    _need(q, torch.bfloat16, "q")
+    _need(seq_lens, torch.int32, "seq_lens")
+    B, H, D = q.shape
+    if seq_lens.numel() != B:
+        raise ValueError("seq_lens must be [B]")
+    kv_type, n_pages, Hkv, page_size, max_pages = _paged(k_pages, v_pages, k_scale, v_scale,
+                                                         block_table, B)
+    if Hkv == 0 or H % Hkv:
+        raise ValueError("q must be [B, H, 64] with H a multiple of the pages' Hkv")
+    scale = D ** -0.5 if scale is None else scale
+    ws_bytes = _ws_bytes(workspace)
+    with _Launch(stream, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, out, lse,
+                 workspace) as on:
+        out = _out(out, q.shape, torch.bfloat16, on.device, "out")
+        lse = _out(lse, (B, H), torch.float32, on.device, "lse")
+        _check("ne_attn_decode_paged", lib().ne_attn_decode_paged(
+            _ptr(q), kv_type, _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_table), max_pages, n_pages, page_size, int(max_seqlen), _ptr(seq_lens), B,
+            H, Hkv, D, float(rope_base), float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+            ws_bytes, on.stream))
+    return out, lse
+
+
 def ne_attn_set_fwd_phase_event(ev_after_rotation=None) -> None:
     """Record the given torch.cuda.Event between the rotation pass and the
     attention kernel of every following forward that runs such a pass (None: off)."""
@@ -543,6 +790,22 @@ def ne_debug_schedule(nseq, H, T, G):
     if m == 0:
         return None
     return list(buf[:G + 1]), list(buf[G + 1:m])
+
+
+def ne_debug_kv_place(cu_seqlens, start_pos, block_table, Hkv, n_pages, page_size, max_seqlen,
+                      pair):
+    """Where a (row, head) pair of a packed batch lies in a paged cache (host
+    only; CPU int32 tensors): ``(code, src, slot, pos)``, see
+    include/ne_attn_debug.h."""
+    P, I = ctypes.c_void_p, ctypes.c_int
+    fn = lib().ne_debug_kv_place
+    fn.argtypes = [P, P, P, I, I, I, I, I, I, I, P, P, P]
+    src, slot, pos = ctypes.c_longlong(-1), ctypes.c_longlong(-1), ctypes.c_int(-1)
+    code = fn(_ptr(cu_seqlens), _ptr(start_pos), _ptr(block_table), start_pos.numel(), int(Hkv),
+              block_table.shape[1], int(n_pages), int(page_size).bit_length() - 1,
+              int(max_seqlen), int(pair), ctypes.byref(src), ctypes.byref(slot),
+              ctypes.byref(pos))
+    return code, src.value, slot.value, pos.value
 
 
 def ne_debug_pipeline(src, n_items, drop_item=-1, wait_limit_cycles=2_000_000_000, stream=None):

@@ -75,8 +75,10 @@ typedef int ne_status;
 #define NE_ERR_CUDA 4        /* a CUDA runtime / driver call failed */
 #define NE_ERR_TIMEOUT 5     /* a device pipeline wait expired (reported by get_device_status) */
 #define NE_ERR_OOM 6         /* allocation of a table or temporary failed */
-#define NE_ERR_BAD_SEQLEN 7  /* a varlen sequence was longer than max_seqlen (device-detected) */
+#define NE_ERR_BAD_SEQLEN 7  /* a varlen sequence or a cached position beyond max_seqlen
+                                (device-detected) */
 #define NE_ERR_TOO_LARGE 8   /* problem exceeds the fixed scratch of ne_attn_bwd_noalloc */
+#define NE_ERR_BAD_PAGE 9    /* a block table entry outside the page pool (device-detected) */
 
 typedef uint16_t ne_bf16; /* raw bfloat16 bits */
 
@@ -284,6 +286,104 @@ ne_status ne_attn_decode_rotated(const ne_bf16* qr, const ne_bf16* kr_cache,
                                  int D, float scale, ne_bf16* out, float* lse, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* Attention over whole prompts with shared key/value heads (grouped heads),
+ * causal, packed sequences of different lengths, and its backward.  q, out,
+ * dout, qr, dq: [n_tot, H, 64] bf16; k, v, kr, dk, dv: [n_tot, Hkv, 64] bf16;
+ * lse: [H, n_tot] fp32.  H is a multiple of Hkv, and query head h reads
+ * key/value head h / (H / Hkv) (Hkv = H: a head of its own each; Hkv = 1: one
+ * for all).  Otherwise as ne_attn_varlen_fwd_train / ne_attn_varlen_bwd_train:
+ * the forward writes q' = R(m) q and k' = R(n) k (for the backward, and k' for
+ * a cache: ne_kv_append with rope_base 0) and attends with them; the backward
+ * takes them and returns the gradients w.r.t. the un-rotated q, k and v, dk
+ * and dv summed over the query heads that share them (in fp32, in a fixed
+ * order: deterministic; dq as in ne_attn_bwd).  Sequences of length zero are
+ * allowed; rows behind the last sequence are left as they are (in the
+ * backward too).  nseq <= 65535, and ceil(max_seqlen / 128) * nseq * H < 2^31.
+ * workspace: ne_attn_gqa_bwd_workspace_bytes(n_tot, max_seqlen, H, Hkv, D)
+ * bytes, 256-byte aligned, or NULL for a stream-ordered temporary. */
+ne_status ne_attn_gqa_varlen_fwd(const ne_bf16* q, const ne_bf16* k, const ne_bf16* v,
+                                 const int* cu_seqlens, int nseq, int n_tot, int max_seqlen,
+                                 int H, int Hkv, int D, float rope_base, float scale,
+                                 ne_bf16* out, float* lse, ne_bf16* qr, ne_bf16* kr,
+                                 void* stream);
+size_t ne_attn_gqa_bwd_workspace_bytes(int n_tot, int max_seqlen, int H, int Hkv, int D);
+ne_status ne_attn_gqa_varlen_bwd(const ne_bf16* qr, const ne_bf16* kr, const ne_bf16* v,
+                                 const ne_bf16* out, const ne_bf16* dout, const float* lse,
+                                 const int* cu_seqlens, int nseq, int n_tot, int max_seqlen,
+                                 int H, int Hkv, int D, float rope_base, float scale, ne_bf16* dq,
+                                 ne_bf16* dk, ne_bf16* dv, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* A paged key/value cache for generation.  Two pools of n_pages pages, each
+ * page [Hkv, page_size, 64] (a head's positions of a page are contiguous),
+ * page_size 16, 32, 64, 128 or 256 (NE_ERR_UNSUPPORTED otherwise), of type
+ *   NE_KV_BF16  bf16;
+ *   NE_KV_E4M3  8-bit e4m3, each row of 64 values with a scale byte of its
+ *               own (k_scale, v_scale: uint8 [n_pages, Hkv, page_size]):
+ *               value = e4m3 * 2^(byte - 127); byte 255 marks a row that held
+ *               an infinity or NaN and reads back as NaN.
+ * Position n of sequence s lies in slot n % page_size of page
+ * block_table[s * max_pages + n / page_size] (DEVICE int32 [nseq, max_pages];
+ * entries past a sequence's positions are not read).  The keys of the cache
+ * are rotated keys k' = R(n) k.
+ *   max_seqlen: every position touched is below it; at most max_pages *
+ *     page_size and 65535 * 128 (it bounds the RoPE table and the launch).
+ *   n_pages * Hkv * page_size < 2^31 - 256.
+ *   Pools and scales 16-byte aligned; scales may be NULL for NE_KV_BF16.
+ * A position outside [0, max_seqlen) is reported as NE_ERR_BAD_SEQLEN, and a
+ * block table entry outside [0, n_pages) as NE_ERR_BAD_PAGE, by
+ * ne_attn_get_device_status; such a row is neither read nor written.
+ *
+ * ne_kv_append writes new rows: row i of sequence s of k, v [n_tot, Hkv, 64]
+ * bf16 (rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1; DEVICE int32 [nseq + 1],
+ * nondecreasing; a sequence may have none) goes to position start_pos[s] + i
+ * (DEVICE int32 [nseq]): a whole prompt, part of one, or a token per sequence.
+ * rope_base > 0: k is rotated at its position (the fp32 rule of
+ * ne_attn_fwd); rope_base = 0: k is k' already.  e4m3: with a row's largest
+ * magnitude a, the scale is 2^e with the smallest e >= -100 that has
+ * a <= 448 * 2^e, and the values are rounded to nearest even.  Two rows of one
+ * call must not go to the same slot.
+ *
+ * ne_kv_read reads rows back, as bf16 (exact): row i of sequence s of k, v
+ * from position start_pos[s] + i; the keys come as the cache holds them (k').
+ * Rows of k, v that belong to no sequence, or whose position or page is bad,
+ * are left as they are. */
+#define NE_KV_BF16 0
+#define NE_KV_E4M3 1
+ne_status ne_kv_append(const ne_bf16* k, const ne_bf16* v, const int* cu_seqlens,
+                       const int* start_pos, int nseq, int n_tot, int Hkv, int D,
+                       float rope_base, int kv_type, void* k_pages, void* v_pages,
+                       uint8_t* k_scale, uint8_t* v_scale, const int* block_table, int max_pages,
+                       int n_pages, int page_size, int max_seqlen, void* stream);
+ne_status ne_kv_read(int kv_type, const void* k_pages, const void* v_pages,
+                     const uint8_t* k_scale, const uint8_t* v_scale, const int* block_table,
+                     int max_pages, int n_pages, int page_size, int max_seqlen,
+                     const int* cu_seqlens, const int* start_pos, int nseq, int n_tot, int Hkv,
+                     int D, ne_bf16* k, ne_bf16* v, void* stream);
+
+/* Decode attention over a paged cache: one new token per sequence attends to
+ * every cached position, its own included (already appended).
+ *   q:        [B, H, 64] bf16; rope_base > 0: un-rotated, rotated here at
+ *             position seq_lens[b] - 1 and rounded to bf16; rope_base = 0: q'.
+ *   seq_lens: DEVICE int32 [B], cached positions 0 .. seq_lens[b] - 1 are
+ *             attended, 0 <= seq_lens[b] <= max_seqlen.  0: the sequence has
+ *             nothing to attend to; its outputs are zero and -inf.
+ *   out:      [B, H, 64] bf16;  lse: [B, H] fp32, natural log (both written).
+ * H is a multiple of Hkv; query head h reads cached head h / (H / Hkv).
+ * B, H <= 65535.  A sequence whose seq_lens entry or a page is bad is reported
+ * as above and its outputs are zero and -inf.  What the cache holds beyond a
+ * sequence's length never reaches its outputs.  workspace:
+ * ne_attn_decode_paged_workspace_bytes(B, H, Hkv, max_seqlen) bytes, 16-byte
+ * aligned, or NULL for a stream-ordered temporary. */
+size_t ne_attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int max_seqlen);
+ne_status ne_attn_decode_paged(const ne_bf16* q, int kv_type, const void* k_pages,
+                               const void* v_pages, const uint8_t* k_scale,
+                               const uint8_t* v_scale, const int* block_table, int max_pages,
+                               int n_pages, int page_size, int max_seqlen, const int* seq_lens,
+                               int B, int H, int Hkv, int D, float rope_base, float scale,
+                               ne_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
 /* The step before the attention in a transformer layer: RMSNorm, then the
  * QKV projection, with RoPE applied to q and k in the projection's epilogue
  * (NanoEuler Show HN page, paragraph 2: the CUDA engine has RMSNorm and RoPE
@@ -344,8 +444,8 @@ ne_status ne_mtp_head(const ne_bf16* h, const ne_bf16* w, const int* targets, in
                       void* workspace, size_t workspace_bytes, void* stream);
 
 /* Synchronize `stream`, then return and clear the device status word of the
- * current device: NE_OK, NE_ERR_TIMEOUT or NE_ERR_BAD_SEQLEN (or NE_ERR_CUDA
- * if the synchronization itself failed). */
+ * current device: NE_OK, NE_ERR_TIMEOUT, NE_ERR_BAD_SEQLEN or NE_ERR_BAD_PAGE
+ * (or NE_ERR_CUDA if the synchronization itself failed). */
 ne_status ne_attn_get_device_status(void* stream);
 
 /* Detail of the last device status read by ne_attn_get_device_status: the raw

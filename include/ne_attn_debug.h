@@ -61,6 +61,15 @@ ne_status ne_debug_umma(int form, const ne_bf16* a, const ne_bf16* b, float* d, 
 ne_status ne_debug_pipeline(const ne_bf16* src, int n_rows, int H, int n_items, int drop_item,
                             long long wait_limit_cycles, float* d, void* stream);
 
+/* Host only: where ne_kv_append and ne_kv_read place (row, head) pair `pair`
+ * = row * Hkv + head of a packed batch, from HOST arrays.  Returns 0 (*src: the
+ * row's element offset in the packed tensors, *slot: its row in the pools,
+ * *pos: its position), -1 for a row of no sequence, 1 for a bad position, 2
+ * for a page outside [0, n_pages). */
+int ne_debug_kv_place(const int* cu_seqlens, const int* start_pos, const int* block_table,
+                      int nseq, int Hkv, int max_pages, int n_pages, int page_shift,
+                      int max_seqlen, int pair, long long* src, long long* slot, int* pos);
+
 /* The work schedule the fixed-length backward calls give their persistent
  * main kernel (host only, no device needed): its units (one key tile of one
  * sequence and head, longest first) for a batch of nseq sequences of length
