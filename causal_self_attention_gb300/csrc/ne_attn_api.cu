@@ -53,11 +53,14 @@ cudaError_t launch_kv_append(const __nv_bfloat16* k, const __nv_bfloat16* v, con
 cudaError_t launch_kv_read(__nv_bfloat16* k, __nv_bfloat16* v, const int* cu,
                            const int* start_pos, int nseq, int n_tot, const PagedCache& pc,
                            bool e4m3, int* status, cudaStream_t stream);
-size_t paged_part_bytes(int B, int H, int max_seqlen);
-cudaError_t launch_decode_paged(const __nv_bfloat16* q, const PagedCache& pc, bool e4m3,
+size_t paged_part_bytes(int B, int H, int Hkv, int max_seqlen);
+size_t paged_counter_bytes();
+unsigned paged_box_rows(int page_size);
+cudaError_t launch_decode_paged(const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                const __nv_bfloat16* q, const PagedCache& pc, bool e4m3,
                                 const int* seq_lens, int B, int H, const RopeTable& rope,
-                                float scale_log2, float* part, __nv_bfloat16* out, float* lse,
-                                int* status, cudaStream_t stream);
+                                float scale_log2, float* part, int* arrived, __nv_bfloat16* out,
+                                float* lse, int sms, int* status, cudaStream_t stream);
 constexpr unsigned kDecodeBoxRows = 32;  // keys per pipeline stage of the decode kernel
 cudaError_t launch_rmsnorm(const __nv_bfloat16* x, const __nv_bfloat16* g, __nv_bfloat16* xn,
                            float* rstd, int M, int C, float eps, cudaStream_t stream);
@@ -105,6 +108,7 @@ struct DeviceState {
   std::vector<RopeEntry> tables;
   std::vector<float2*> retired;  // replaced tables, freed by ne_attn_release
   std::vector<StreamScratch> scratch;
+  std::vector<StreamScratch> counters;  // per stream, zero between launches
   std::vector<SchedEntry> scheds;
 };
 
@@ -131,6 +135,29 @@ ne_status stream_scratch(DeviceState& st, cudaStream_t stream, size_t bytes, voi
   e.bytes = bytes;
   st.scratch.push_back(e);
   *out = e.ptr;
+  return NE_OK;
+}
+
+// Arrival counters for the launches of one stream: zeroed once, and left zero
+// by every launch that uses them (caller holds g_mutex; not during a capture).
+ne_status stream_counters(DeviceState& st, cudaStream_t stream, size_t bytes, int** out) {
+  for (auto& e : st.counters)
+    if (e.stream == stream) {
+      *out = static_cast<int*>(e.ptr);
+      return NE_OK;
+    }
+  StreamScratch e;
+  e.stream = stream;
+  e.bytes = bytes;
+  cudaError_t r = cudaMallocAsync(&e.ptr, bytes, stream);
+  if (r != cudaSuccess) return r == cudaErrorMemoryAllocation ? NE_ERR_OOM : NE_ERR_CUDA;
+  r = cudaMemsetAsync(e.ptr, 0, bytes, stream);
+  if (r != cudaSuccess) {
+    cudaFreeAsync(e.ptr, stream);
+    return NE_ERR_CUDA;
+  }
+  st.counters.push_back(e);
+  *out = static_cast<int*>(e.ptr);
   return NE_OK;
 }
 
@@ -1042,7 +1069,8 @@ ne_status ne_kv_read(int kv_type, const void* k_pages, const void* v_pages,
 
 size_t ne_attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int max_seqlen) {
   if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || max_seqlen <= 0) return 0;
-  return ne::paged_part_bytes(B, H, max_seqlen);
+  // The arrival counters of a captured call, then the parts.
+  return align256(ne::paged_counter_bytes()) + ne::paged_part_bytes(B, H, Hkv, max_seqlen);
 }
 
 ne_status ne_attn_decode_paged(const ne_bf16* q, int kv_type, const void* k_pages,
@@ -1073,16 +1101,36 @@ ne_status ne_attn_decode_paged(const ne_bf16* q, int kv_type, const void* k_page
   RopeTable rope{nullptr, nullptr, 0};
   if (rope_base > 0.f && (rc = rope_table(*st, rope_base, max_seqlen, cs, &rope)) != NE_OK)
     return rc;
+  CUtensorMap tk{}, tv{};  // the bf16 pools, one page or one tile a box
+  if (kv_type == NE_KV_BF16) {
+    if ((rc = get_encoder()) != NE_OK) return rc;
+    const long long rows = static_cast<long long>(n_pages) * Hkv * page_size;
+    const unsigned box = ne::paged_box_rows(page_size);
+    if ((rc = encode_mat(&tk, k_pages, rows, 64, box)) != NE_OK) return rc;
+    if ((rc = encode_mat(&tv, v_pages, rows, 64, box)) != NE_OK) return rc;
+  }
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(cs, &capture) != cudaSuccess) return NE_ERR_CUDA;
+  const bool captured = capture != cudaStreamCaptureStatusNone;
+  int* arrived = nullptr;
+  if (!captured && (rc = stream_counters(*st, cs, ne::paged_counter_bytes(), &arrived)) != NE_OK)
+    return rc;
   void* ws = workspace;
   const bool owned = !ws;
-  if (owned) {
-    const cudaError_t e = cudaMallocAsync(&ws, need, cs);
-    if (e != cudaSuccess) return cuda_status(e);
+  cudaError_t e = cudaSuccess;
+  if (owned && (e = cudaMallocAsync(&ws, need, cs)) != cudaSuccess) return cuda_status(e);
+  if (captured) {
+    // A graph may be replayed while other calls of this stream run elsewhere:
+    // it has counters of its own, in its workspace, cleared on every replay.
+    arrived = static_cast<int*>(ws);
+    e = cudaMemsetAsync(arrived, 0, ne::paged_counter_bytes(), cs);
   }
-  cudaError_t e = ne::launch_decode_paged(
-      reinterpret_cast<const __nv_bfloat16*>(q), pc, kv_type == NE_KV_E4M3, seq_lens, B, H, rope,
-      scale * 1.4426950408889634f, static_cast<float*>(ws), reinterpret_cast<__nv_bfloat16*>(out),
-      lse, st->status, cs);
+  if (e == cudaSuccess)
+    e = ne::launch_decode_paged(
+        tk, tv, reinterpret_cast<const __nv_bfloat16*>(q), pc, kv_type == NE_KV_E4M3, seq_lens, B,
+        H, rope, scale * 1.4426950408889634f,
+        reinterpret_cast<float*>(static_cast<char*>(ws) + align256(ne::paged_counter_bytes())),
+        arrived, reinterpret_cast<__nv_bfloat16*>(out), lse, st->sm_count, st->status, cs);
   if (owned) {
     const cudaError_t e2 = cudaFreeAsync(ws, cs);
     if (e == cudaSuccess) e = e2;
@@ -1402,7 +1450,8 @@ void ne_attn_release(void) {
   cudaGetDevice(&cur);
   for (int d = 0; d < kMaxDevices; ++d) {
     DeviceState& st = g_dev[d];
-    if (st.tables.empty() && st.retired.empty() && st.scratch.empty() && st.scheds.empty())
+    if (st.tables.empty() && st.retired.empty() && st.scratch.empty() && st.scheds.empty() &&
+        st.counters.empty())
       continue;
     cudaSetDevice(d);
     for (auto& t : st.tables) cudaFree(t.dev);
@@ -1411,7 +1460,9 @@ void ne_attn_release(void) {
     st.scheds.clear();
     for (auto* p : st.retired) cudaFree(p);
     for (auto& e : st.scratch) cudaFreeAsync(e.ptr, e.stream);
-    if (!st.scratch.empty()) cudaDeviceSynchronize();
+    for (auto& e : st.counters) cudaFreeAsync(e.ptr, e.stream);
+    if (!st.scratch.empty() || !st.counters.empty()) cudaDeviceSynchronize();
+    st.counters.clear();
     st.tables.clear();
     st.retired.clear();
     st.scratch.clear();

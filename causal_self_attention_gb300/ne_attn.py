@@ -485,32 +485,36 @@ def ne_attn_varlen_bwd_train(qr, kr, v, out, dout, lse, cu_seqlens, max_seqlen,
 
 # ------------------------------------------- grouped heads and the paged cache
 
-class _Launch:
-    """Where a call runs: the tensors' device (all on one, made the current
-    device while the call launches) and the stream, under which the tensors
-    that the call creates are allocated too.  ``stream``: a torch stream, a
-    raw ``cudaStream_t``, or None for the device's current stream."""
+def _on(stream, first, *rest):
+    """Where a call on these tensors (None: one left out) runs: the raw stream,
+    and the context that makes their device and the stream current -- also for
+    the tensors that the call creates -- or None where they are current already.
+    ``stream``: a torch stream, a raw ``cudaStream_t``, or None for the device's
+    current stream.  The context is entered; the caller leaves it."""
+    dev = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    if stream is None:
+        if dev == torch.cuda.current_device():
+            return torch._C._cuda_getCurrentRawStream(dev), None
+        stream = torch.cuda.current_stream(dev)
+    elif not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on {first.device}")
+    ctx = torch.cuda.stream(stream)
+    ctx.__enter__()
+    return stream.cuda_stream, ctx
 
-    def __init__(self, stream, *tensors):
-        devices = {t.device for t in tensors if t is not None}
-        if len(devices) != 1:
-            raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
-        self.device = devices.pop()
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        elif not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        if stream.device != self.device:
-            raise ValueError(f"stream on {stream.device}, tensors on {self.device}")
-        self.stream = ctypes.c_void_p(stream.cuda_stream)
-        self._ctx = torch.cuda.stream(stream)
 
-    def __enter__(self):
-        self._ctx.__enter__()
-        return self
+def _leave(ctx):
+    if ctx is not None:
+        ctx.__exit__(None, None, None)
 
-    def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc)
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _out(t, shape, dtype, device, name):
@@ -555,14 +559,18 @@ def ne_attn_gqa_varlen_fwd(q, k, v, cu_seqlens, max_seqlen, rope_base=10000.0, s
     ``kr``, for a cache: :func:`ne_kv_append` with ``rope_base=0``)."""
     N, H, Hkv, D, nseq = _gqa_shapes(q, k, v, cu_seqlens)
     scale = D ** -0.5 if scale is None else scale
-    with _Launch(stream, q, k, v, cu_seqlens, out, lse, qr, kr) as on:
-        out = _out(out, q.shape, torch.bfloat16, on.device, "out")
-        lse = _out(lse, (H, N), torch.float32, on.device, "lse")
-        qr = _out(qr, q.shape, torch.bfloat16, on.device, "qr")
-        kr = _out(kr, k.shape, torch.bfloat16, on.device, "kr")
+    raw, ctx = _on(stream, q, k, v, cu_seqlens, out, lse, qr, kr)
+    try:
+        dev = q.device
+        out = _out(out, q.shape, torch.bfloat16, dev, "out")
+        lse = _out(lse, (H, N), torch.float32, dev, "lse")
+        qr = _out(qr, q.shape, torch.bfloat16, dev, "qr")
+        kr = _out(kr, k.shape, torch.bfloat16, dev, "kr")
         _check("ne_attn_gqa_varlen_fwd", lib().ne_attn_gqa_varlen_fwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), nseq, N, int(max_seqlen), H, Hkv, D,
-            float(rope_base), float(scale), _ptr(out), _ptr(lse), _ptr(qr), _ptr(kr), on.stream))
+            _addr(q), _addr(k), _addr(v), _addr(cu_seqlens), nseq, N, int(max_seqlen), H, Hkv, D,
+            float(rope_base), float(scale), _addr(out), _addr(lse), _addr(qr), _addr(kr), raw))
+    finally:
+        _leave(ctx)
     return out, lse, qr, kr
 
 
@@ -585,14 +593,18 @@ def ne_attn_gqa_varlen_bwd(qr, kr, v, out, dout, lse, cu_seqlens, max_seqlen, ro
     _out(lse, (H, N), torch.float32, None, "lse")
     scale = D ** -0.5 if scale is None else scale
     ws_bytes = _ws_bytes(workspace)
-    with _Launch(stream, qr, kr, v, out, dout, lse, cu_seqlens, dq, dk, dv, workspace) as on:
-        dq = _out(dq, qr.shape, torch.bfloat16, on.device, "dq")
-        dk = _out(dk, kr.shape, torch.bfloat16, on.device, "dk")
-        dv = _out(dv, v.shape, torch.bfloat16, on.device, "dv")
+    raw, ctx = _on(stream, qr, kr, v, out, dout, lse, cu_seqlens, dq, dk, dv, workspace)
+    try:
+        dev = qr.device
+        dq = _out(dq, qr.shape, torch.bfloat16, dev, "dq")
+        dk = _out(dk, kr.shape, torch.bfloat16, dev, "dk")
+        dv = _out(dv, v.shape, torch.bfloat16, dev, "dv")
         _check("ne_attn_gqa_varlen_bwd", lib().ne_attn_gqa_varlen_bwd(
-            _ptr(qr), _ptr(kr), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), _ptr(cu_seqlens), nseq,
-            N, int(max_seqlen), H, Hkv, D, float(rope_base), float(scale), _ptr(dq), _ptr(dk),
-            _ptr(dv), _ptr(workspace), ws_bytes, on.stream))
+            _addr(qr), _addr(kr), _addr(v), _addr(out), _addr(dout), _addr(lse),
+            _addr(cu_seqlens), nseq, N, int(max_seqlen), H, Hkv, D, float(rope_base), float(scale), _addr(dq), _addr(dk),
+            _addr(dv), _addr(workspace), ws_bytes, raw))
+    finally:
+        _leave(ctx)
     return dq, dk, dv
 
 
@@ -648,13 +660,16 @@ def ne_kv_append(k, v, cu_seqlens, start_pos, k_pages, v_pages, block_table, max
     n_tot, _, D = k.shape
     if tuple(k.shape) != (n_tot, Hkv, D) or k.shape != v.shape:
         raise ValueError("k, v must be [n_tot, Hkv, 64] with the pages' Hkv")
-    with _Launch(stream, k, v, cu_seqlens, start_pos, k_pages, v_pages, k_scale, v_scale,
-                 block_table) as on:
+    raw, ctx = _on(stream, k, v, cu_seqlens, start_pos, k_pages, v_pages, k_scale, v_scale,
+                   block_table)
+    try:
         _check("ne_kv_append", lib().ne_kv_append(
-            _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(start_pos), nseq, n_tot, Hkv, D,
-            float(rope_base), kv_type, _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
-            _ptr(v_scale), _ptr(block_table), max_pages, n_pages, page_size, int(max_seqlen),
-            on.stream))
+            _addr(k), _addr(v), _addr(cu_seqlens), _addr(start_pos), nseq, n_tot, Hkv, D,
+            float(rope_base), kv_type, _addr(k_pages), _addr(v_pages), _addr(k_scale),
+            _addr(v_scale), _addr(block_table), max_pages, n_pages, page_size, int(max_seqlen),
+            raw))
+    finally:
+        _leave(ctx)
     return k_pages, v_pages
 
 
@@ -670,14 +685,18 @@ def ne_kv_read(k_pages, v_pages, block_table, cu_seqlens, start_pos, n_tot, k_sc
                                                          block_table, nseq)
     if max_seqlen is None:
         max_seqlen = min(max_pages * page_size, 65535 * 128)
-    with _Launch(stream, k_pages, v_pages, k_scale, v_scale, block_table, cu_seqlens, start_pos,
-                 k, v) as on:
-        k = _out(k, (int(n_tot), Hkv, 64), torch.bfloat16, on.device, "k")
-        v = _out(v, (int(n_tot), Hkv, 64), torch.bfloat16, on.device, "v")
+    raw, ctx = _on(stream, k_pages, v_pages, k_scale, v_scale, block_table, cu_seqlens,
+                   start_pos, k, v)
+    try:
+        dev = k_pages.device
+        k = _out(k, (int(n_tot), Hkv, 64), torch.bfloat16, dev, "k")
+        v = _out(v, (int(n_tot), Hkv, 64), torch.bfloat16, dev, "v")
         _check("ne_kv_read", lib().ne_kv_read(
-            kv_type, _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
-            _ptr(block_table), max_pages, n_pages, page_size, int(max_seqlen), _ptr(cu_seqlens),
-            _ptr(start_pos), nseq, int(n_tot), Hkv, 64, _ptr(k), _ptr(v), on.stream))
+            kv_type, _addr(k_pages), _addr(v_pages), _addr(k_scale), _addr(v_scale),
+            _addr(block_table), max_pages, n_pages, page_size, int(max_seqlen), _addr(cu_seqlens),
+            _addr(start_pos), nseq, int(n_tot), Hkv, 64, _addr(k), _addr(v), raw))
+    finally:
+        _leave(ctx)
     return k, v
 
 
@@ -705,15 +724,19 @@ def ne_attn_decode_paged(q, k_pages, v_pages, block_table, seq_lens, max_seqlen,
         raise ValueError("q must be [B, H, 64] with H a multiple of the pages' Hkv")
     scale = D ** -0.5 if scale is None else scale
     ws_bytes = _ws_bytes(workspace)
-    with _Launch(stream, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, out, lse,
-                 workspace) as on:
-        out = _out(out, q.shape, torch.bfloat16, on.device, "out")
-        lse = _out(lse, (B, H), torch.float32, on.device, "lse")
+    raw, ctx = _on(stream, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, out,
+                   lse, workspace)
+    try:
+        dev = q.device
+        out = _out(out, q.shape, torch.bfloat16, dev, "out")
+        lse = _out(lse, (B, H), torch.float32, dev, "lse")
         _check("ne_attn_decode_paged", lib().ne_attn_decode_paged(
-            _ptr(q), kv_type, _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
-            _ptr(block_table), max_pages, n_pages, page_size, int(max_seqlen), _ptr(seq_lens), B,
-            H, Hkv, D, float(rope_base), float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
-            ws_bytes, on.stream))
+            _addr(q), kv_type, _addr(k_pages), _addr(v_pages), _addr(k_scale), _addr(v_scale),
+            _addr(block_table), max_pages, n_pages, page_size, int(max_seqlen), _addr(seq_lens), B,
+            H, Hkv, D, float(rope_base), float(scale), _addr(out), _addr(lse), _addr(workspace),
+            ws_bytes, raw))
+    finally:
+        _leave(ctx)
     return out, lse
 
 
