@@ -108,7 +108,9 @@ struct DeviceState {
   std::vector<RopeEntry> tables;
   std::vector<float2*> retired;  // replaced tables, freed by ne_attn_release
   std::vector<StreamScratch> scratch;
-  std::vector<StreamScratch> counters;  // per stream, zero between launches
+  std::vector<StreamScratch> counters;  // each stream's counter set
+  std::vector<void*> counter_blocks;
+  int counter_sets_left = 0;  // in the last block
   std::vector<SchedEntry> scheds;
 };
 
@@ -138,29 +140,6 @@ ne_status stream_scratch(DeviceState& st, cudaStream_t stream, size_t bytes, voi
   return NE_OK;
 }
 
-// Arrival counters for the launches of one stream: zeroed once, and left zero
-// by every launch that uses them (caller holds g_mutex; not during a capture).
-ne_status stream_counters(DeviceState& st, cudaStream_t stream, size_t bytes, int** out) {
-  for (auto& e : st.counters)
-    if (e.stream == stream) {
-      *out = static_cast<int*>(e.ptr);
-      return NE_OK;
-    }
-  StreamScratch e;
-  e.stream = stream;
-  e.bytes = bytes;
-  cudaError_t r = cudaMallocAsync(&e.ptr, bytes, stream);
-  if (r != cudaSuccess) return r == cudaErrorMemoryAllocation ? NE_ERR_OOM : NE_ERR_CUDA;
-  r = cudaMemsetAsync(e.ptr, 0, bytes, stream);
-  if (r != cudaSuccess) {
-    cudaFreeAsync(e.ptr, stream);
-    return NE_ERR_CUDA;
-  }
-  st.counters.push_back(e);
-  *out = static_cast<int*>(e.ptr);
-  return NE_OK;
-}
-
 std::mutex g_mutex;
 DeviceState g_dev[kMaxDevices];
 int g_last_code = 0;
@@ -171,6 +150,47 @@ ne_status cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return NE_OK;
   if (e == cudaErrorMemoryAllocation) return NE_ERR_OOM;
   return NE_ERR_CUDA;
+}
+
+// Arrival counters, in sets of `bytes` that are zero between launches (every
+// launch leaves them so).  A set belongs to one stream, whose launches run one
+// after the other, or to one captured call, whose replays do.  Sets come in
+// blocks, cleared before first use; *out = nullptr when none is left during a
+// capture, which allows no new block (caller holds g_mutex).
+constexpr int kCounterSets = 128;
+ne_status counter_set(DeviceState& st, cudaStream_t stream, bool captured, size_t bytes,
+                      int** out) {
+  *out = nullptr;
+  if (!captured)
+    for (auto& e : st.counters)
+      if (e.stream == stream) {
+        *out = static_cast<int*>(e.ptr);
+        return NE_OK;
+      }
+  if (st.counter_sets_left == 0) {
+    if (captured) return NE_OK;
+    void* block = nullptr;
+    cudaError_t r = cudaMalloc(&block, kCounterSets * bytes);
+    if (r != cudaSuccess) return cuda_status(r);
+    r = cudaMemsetAsync(block, 0, kCounterSets * bytes, stream);
+    if (r == cudaSuccess) r = cudaStreamSynchronize(stream);  // other streams use the block too
+    if (r != cudaSuccess) {
+      cudaFree(block);
+      return cuda_status(r);
+    }
+    st.counter_blocks.push_back(block);
+    st.counter_sets_left = kCounterSets;
+  }
+  --st.counter_sets_left;
+  void* set = static_cast<char*>(st.counter_blocks.back()) + st.counter_sets_left * bytes;
+  if (!captured) {
+    StreamScratch e;
+    e.stream = stream;
+    e.ptr = set;
+    st.counters.push_back(e);
+  }
+  *out = static_cast<int*>(set);
+  return NE_OK;
 }
 
 // Per-device set-up (caller holds g_mutex).
@@ -1113,15 +1133,13 @@ ne_status ne_attn_decode_paged(const ne_bf16* q, int kv_type, const void* k_page
   if (cudaStreamIsCapturing(cs, &capture) != cudaSuccess) return NE_ERR_CUDA;
   const bool captured = capture != cudaStreamCaptureStatusNone;
   int* arrived = nullptr;
-  if (!captured && (rc = stream_counters(*st, cs, ne::paged_counter_bytes(), &arrived)) != NE_OK)
+  if ((rc = counter_set(*st, cs, captured, ne::paged_counter_bytes(), &arrived)) != NE_OK)
     return rc;
   void* ws = workspace;
   const bool owned = !ws;
   cudaError_t e = cudaSuccess;
   if (owned && (e = cudaMallocAsync(&ws, need, cs)) != cudaSuccess) return cuda_status(e);
-  if (captured) {
-    // A graph may be replayed while other calls of this stream run elsewhere:
-    // it has counters of its own, in its workspace, cleared on every replay.
+  if (!arrived) {  // counters in the workspace, cleared by a node of the graph
     arrived = static_cast<int*>(ws);
     e = cudaMemsetAsync(arrived, 0, ne::paged_counter_bytes(), cs);
   }
@@ -1451,7 +1469,7 @@ void ne_attn_release(void) {
   for (int d = 0; d < kMaxDevices; ++d) {
     DeviceState& st = g_dev[d];
     if (st.tables.empty() && st.retired.empty() && st.scratch.empty() && st.scheds.empty() &&
-        st.counters.empty())
+        st.counter_blocks.empty())
       continue;
     cudaSetDevice(d);
     for (auto& t : st.tables) cudaFree(t.dev);
@@ -1460,9 +1478,11 @@ void ne_attn_release(void) {
     st.scheds.clear();
     for (auto* p : st.retired) cudaFree(p);
     for (auto& e : st.scratch) cudaFreeAsync(e.ptr, e.stream);
-    for (auto& e : st.counters) cudaFreeAsync(e.ptr, e.stream);
-    if (!st.scratch.empty() || !st.counters.empty()) cudaDeviceSynchronize();
+    for (auto* b : st.counter_blocks) cudaFree(b);
+    if (!st.scratch.empty()) cudaDeviceSynchronize();
     st.counters.clear();
+    st.counter_blocks.clear();
+    st.counter_sets_left = 0;
     st.tables.clear();
     st.retired.clear();
     st.scratch.clear();

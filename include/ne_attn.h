@@ -39,7 +39,8 @@
  *    the first call on that stream outside graph capture and grown when
  *    needed; inside a capture each call allocates and frees its own), the
  *    backward's work-schedule tables (one per fixed-length shape, a few KB,
- *    made on first use outside graph capture) -- all released by
+ *    made on first use outside graph capture), the paged decode's arrival
+ *    counters (in blocks; 2 KB for each stream and each captured call) -- all released by
  *    ne_attn_release -- and, when a backward is given no workspace, a
  *    stream-ordered temporary it frees itself.
  *  - `stream` is a cudaStream_t (NULL = legacy default stream).  Work is
@@ -372,7 +373,9 @@ ne_status ne_kv_read(int kv_type, const void* k_pages, const void* v_pages,
  * H is a multiple of Hkv; query head h reads cached head h / (H / Hkv).
  * B, H <= 65535.  A sequence whose seq_lens entry or a page is bad is reported
  * as above and its outputs are zero and -inf.  What the cache holds beyond a
- * sequence's length never reaches its outputs.  workspace:
+ * sequence's length never reaches its outputs.  How the work is split depends
+ * on the whole batch's lengths, and with it the last bits of a result; the
+ * same call gives the same bits.  workspace:
  * ne_attn_decode_paged_workspace_bytes(B, H, Hkv, max_seqlen) bytes, 16-byte
  * aligned, or NULL for a stream-ordered temporary. */
 size_t ne_attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int max_seqlen);

@@ -255,9 +255,10 @@ def test_decode_long(na, e4m3, B, n):
     _check_decode(na, c, 8, lens, BASE, 49)
 
 
-@pytest.mark.parametrize("e4m3", [False, True])
-def test_decode_many_sequences(na, e4m3):
-    lens = [(37 * i) % 200 for i in range(300)]
+@pytest.mark.parametrize("e4m3,B", [(False, 300), (True, 300), (False, 1100)])
+def test_decode_many_sequences(na, e4m3, B):
+    """More than a launch takes (512) among them."""
+    lens = [(37 * i) % 200 for i in range(B)]
     c = Cache(lens, 1, 16, e4m3, seed=50).fill_random(51)
     _check_decode(na, c, 4, lens, BASE, 52)
 
@@ -332,7 +333,12 @@ def test_decode_bad_lengths_and_pages_give_zero_and_minus_infinity(na, e4m3):
         assert na.ne_attn_get_device_status() == 7
         assert bool((out[1] == 0).all()) and bool((lse[1] == -float("inf")).all())
         for s in (0, 2, 3):
-            assert torch.equal(out[s], want_out[s]) and torch.equal(lse[s], want_lse[s])
+            # Another batch may be split at other positions: the difference of two
+            # results that are each within the bound of the exact one.
+            q1 = rotate(_randn(66, 4, 4, 64)[s:s + 1], torch.tensor([lens[s] - 1], device="cuda"))
+            _, _, oe, le = attention(q1.bfloat16(), *c.rows(s, lens[s]), 0.125)
+            within(out[s], want_out[s], 2 * oe[0], "out")
+            within(lse[s], want_lse[s], 2 * le[:, 0], "lse")
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
