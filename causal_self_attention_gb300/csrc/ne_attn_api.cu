@@ -16,6 +16,7 @@
 #include "ne_attn.h"
 #include "ne_attn_debug.h"
 #include "ne_common.cuh"
+#include "ne_items.cuh"
 
 namespace ne {
 cudaError_t launch_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
@@ -29,7 +30,11 @@ cudaError_t launch_rope_rows(const __nv_bfloat16* x0, __nv_bfloat16* xr0,
 cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        const CUtensorMap& tmDO, const CUtensorMap& tmDQ, const CUtensorMap& tmDV,
                        const CUtensorMap& tmDK, const BwdParams& p, int n_tiles,
-                       cudaStream_t stream, cudaEvent_t ev_pre, cudaEvent_t ev_main);
+                       cudaStream_t stream, cudaEvent_t ev_pre, cudaEvent_t ev_main,
+                       const ItemList& list);
+cudaError_t launch_gqa_rotate(const __nv_bfloat16* q, __nv_bfloat16* qr, const __nv_bfloat16* k,
+                              __nv_bfloat16* kr, const Problem& pb, const RopeTable& rope,
+                              const ItemList& list, cudaStream_t stream);
 cudaError_t launch_debug_tile(const CUtensorMap& tm, int h, int row0, int rotate, int pos0,
                               RopeTable rope, void* dst_raw, __nv_bfloat16* dst_rows,
                               int* status, cudaStream_t stream);
@@ -550,7 +555,22 @@ ne_status run_fwd(const Shape& s, const void* q, const void* k, const void* v, f
   if (rc == NE_OK) rc = encode_rows(&tv, v, s.n_tot, s.H / s.group);
   // O tile stores (bf16 output only; the fp32 output is written per row).
   if (rc == NE_OK) rc = encode_rows(&to, out_f32 ? q : out, s.n_tot, s.H);
-  if (rc == NE_OK) {
+  if (rc == NE_OK && s.group > 1) {
+    // Shared heads: the rotation pass builds the work list too.
+    ne::ItemList items;
+    items.kind = head_pairs ? ne::Items::kHeadPairs : ne::Items::kRowPairs;
+    items.n_blocks = nblk;
+    items.n_heads = head_pairs ? s.H / 2 : s.H;
+    items.n_buckets = n_buckets;
+    items.out = list;
+    p.compact = list;
+    e = ne::launch_gqa_rotate(static_cast<const __nv_bfloat16*>(q),
+                              static_cast<__nv_bfloat16*>(qr_out),
+                              static_cast<const __nv_bfloat16*>(k),
+                              static_cast<__nv_bfloat16*>(kr_out), p.pb, p.rope, items, cs);
+    if (e == cudaSuccess && g_ev_rot) e = cudaEventRecord(g_ev_rot, cs);
+    if (e == cudaSuccess) e = ne::launch_fwd(tq, tk, tv, to, p, n_qtiles, cs, pair);
+  } else if (rc == NE_OK) {
     if (mode == Rot::kRotate && !p.rotate_k)
       e = ne::launch_rope_rows(static_cast<const __nv_bfloat16*>(k),
                                static_cast<__nv_bfloat16*>(kr), nullptr, nullptr, p.pb, p.rope,
@@ -563,9 +583,7 @@ ne_status run_fwd(const Shape& s, const void* q, const void* k, const void* v, f
     const bool pass = (mode == Rot::kRotate && !p.rotate_k) || mode == Rot::kTrain;
     if (e == cudaSuccess && g_ev_rot && pass) e = cudaEventRecord(g_ev_rot, cs);
     if (e == cudaSuccess && compact) {
-      ne::Problem items = p.pb;
-      if (head_pairs) items.H /= 2;
-      e = ne::launch_compact_items(items, head_pairs ? 2 : 0, nblk, n_buckets, list, cs);
+      e = ne::launch_compact_items(p.pb, 0, nblk, n_buckets, list, cs);
       p.compact = list;
     }
     if (e == cudaSuccess) e = ne::launch_fwd(tq, tk, tv, to, p, n_qtiles, cs, pair);
@@ -659,7 +677,8 @@ ne_status run_bwd(const Shape& s, const void* q, const void* k, const void* v, c
   // Packed batch: the compacted unit list in the library's temporary for this
   // stream (a stream-ordered allocation of the call's own during capture).
   const int unit_heads = s.group == 1 ? s.H : Hkv * p.splits;
-  const int n_buckets = n_tiles * (s.group == 1 ? 1 : (s.group + p.splits - 1) / p.splits) + 1;
+  const int n_buckets = n_tiles + 1;  // (a unit's steps are these times its query heads)
+  ne::ItemList items;
   const long long n_units = static_cast<long long>(n_tiles) * s.nseq * unit_heads;
   const bool compact = !s.fixed && n_units <= kMaxCompactItems && n_buckets <= kMaxBuckets;
   int* list = nullptr;
@@ -689,13 +708,19 @@ ne_status run_bwd(const Shape& s, const void* q, const void* k, const void* v, c
   if (rc == NE_OK) rc = encode_rows(&tdk, dk, s.n_tot, Hkv);
   cudaError_t e = cudaSuccess;
   if (rc == NE_OK && compact) {
-    ne::Problem units = p.pb;
-    units.H = unit_heads;
-    e = ne::launch_compact_items(units, 1, n_tiles, n_tiles + 1, list, cs);
     p.compact = list;
+    if (s.group > 1) {  // the preprocess builds it
+      items.kind = ne::Items::kKeyTiles;
+      items.n_blocks = n_tiles;
+      items.n_heads = unit_heads;
+      items.n_buckets = n_tiles + 1;
+      items.out = list;
+    } else {
+      e = ne::launch_compact_items(p.pb, 1, n_tiles, n_buckets, list, cs);
+    }
   }
   if (rc == NE_OK && e == cudaSuccess)
-    e = ne::launch_bwd(tq, tk, tv, tdo, tdq, tdv, tdk, p, n_tiles, cs, g_ev_pre, g_ev_main);
+    e = ne::launch_bwd(tq, tk, tv, tdo, tdq, tdv, tdk, p, n_tiles, cs, g_ev_pre, g_ev_main, items);
   else if (rc != NE_OK)
     e = cudaErrorInvalidValue;
   if (own_list) {

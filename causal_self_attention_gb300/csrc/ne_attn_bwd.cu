@@ -50,6 +50,7 @@
 // P^T 448-511 (bf16 pairs).
 #include <algorithm>
 
+#include "ne_items.cuh"
 #include "ne_rope.cuh"
 #include "ne_sm100.cuh"
 
@@ -210,6 +211,8 @@ __global__ void __launch_bounds__(256)
 //     shuffle tree of the kernel above, so that D is bitwise the same.  Rows
 //     outside every sequence (a packed batch with gaps, or a sequence with
 //     bad bounds) get D and zeroed dQ' rows too; nothing reads them.
+//     kList (shared key/value heads, packed batch): one more CTA, the first,
+//     builds the main kernel's work list.
 // ---------------------------------------------------------------------------
 namespace bwd {
 constexpr int kPrepPairs = 128;  // pairs per chunk
@@ -220,13 +223,22 @@ constexpr int kPrepStageBytes = 2 * kPrepPairs * kPrepRowBytes;  // O rows, then
 constexpr int PREP_SMEM_BYTES = kPrepStages * kPrepStageBytes + kPrepStages * 8 + 16;
 }  // namespace bwd
 
+template <bool kList>
 __global__ void __launch_bounds__(256, bwd::kPrepCtasPerSm)
     ne_attn_bwd_prep_stream_kernel(const __nv_bfloat16* __restrict__ out,
                                    const __nv_bfloat16* __restrict__ dout,
                                    float* __restrict__ delta, float* __restrict__ dq_acc,
-                                   const Problem pb, int* status) {
+                                   const Problem pb, int* status, const ItemList list) {
   using namespace bwd;
   extern __shared__ __align__(1024) uint8_t smem[];
+  if (kList && blockIdx.x == 0) {
+    pdl_wait();  // cu_seqlens may come from the kernel before
+    build_items(pb, list, reinterpret_cast<int*>(smem));
+    pdl_launch_dependents();
+    return;
+  }
+  const int grid = static_cast<int>(gridDim.x) - (kList ? 1 : 0);
+  const int cta = static_cast<int>(blockIdx.x) - (kList ? 1 : 0);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPrepStages * kPrepStageBytes);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(full + kPrepStages);
   const int tid = threadIdx.x;
@@ -240,7 +252,7 @@ __global__ void __launch_bounds__(256, bwd::kPrepCtasPerSm)
   // of the call, which the forward does not write; a prefetch is only a hint).
   if (tid == 0) {
     const long long all = static_cast<long long>(pb.n_tot) * pb.H;
-    const long long a = all * blockIdx.x / gridDim.x, e = all * (blockIdx.x + 1) / gridDim.x;
+    const long long a = all * cta / grid, e = all * (cta + 1) / grid;
     if (e > a)
       asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
                        reinterpret_cast<uint64_t>(dout + a * kHD)),
@@ -250,7 +262,7 @@ __global__ void __launch_bounds__(256, bwd::kPrepCtasPerSm)
   pdl_wait();  // the forward that wrote O (and anything before it) has completed
   // Bad cu_seqlens entries are reported here; the main kernel and the
   // postprocess skip those sequences.
-  if (pb.cu_seqlens && blockIdx.x == 0) {
+  if (pb.cu_seqlens && cta == 0) {
     for (int s = tid; s < pb.nseq; s += 256) {
       int a, l;
       seq_bounds(pb, s, a, l, status);
@@ -258,8 +270,8 @@ __global__ void __launch_bounds__(256, bwd::kPrepCtasPerSm)
   }
   const int H = pb.H;
   const long long n_pairs = static_cast<long long>(pb.n_tot) * H;
-  const long long p0 = n_pairs * blockIdx.x / gridDim.x;
-  const int mine = static_cast<int>(n_pairs * (blockIdx.x + 1) / gridDim.x - p0);
+  const long long p0 = n_pairs * cta / grid;
+  const int mine = static_cast<int>(n_pairs * (cta + 1) / grid - p0);
   const int n_ch = (mine + kPrepPairs - 1) / kPrepPairs;
   // Chunk j: pairs p0 + first(j) .. p0 + first(j + 1) - 1 (at most kPrepPairs),
   // split as evenly as the count allows (32-bit arithmetic from here on: the
@@ -479,7 +491,7 @@ __global__ void __launch_bounds__(512, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // the preprocess (q', k', D, zeroed dQ') has completed
-  pdl_launch_dependents();
+  if constexpr (!kShared) pdl_launch_dependents();
 
   uint8_t* sK = smem + OFF_K;
   uint8_t* sV = smem + OFF_V;
@@ -968,6 +980,30 @@ __global__ void __launch_bounds__(512, 1)
           ++nu;
           continue;
         }
+        // dK = R(n)^T (scale dK') here, in fp32, so that it is rounded once (the
+        // unit of a group is long enough for the table row's latency; with a
+        // head to a unit it held the next one up, and the postprocess rotates).
+        if (half) {
+          const int pos = kpos < u.len ? kpos : u.len - 1;
+          const float4* cs =
+              reinterpret_cast<const float4*>(p.rope.cs + static_cast<long long>(pos) * 32);
+#pragma unroll
+          for (int i0 = 0; i0 < 16; i0 += 8) {
+            float4 t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = __ldg(cs + i0 + i);  // (cos, sin) of two dims
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int d = 2 * (i0 + i) + e;
+                const float co = e ? t[i].z : t[i].x, si = e ? t[i].w : t[i].y;
+                const float a = __uint_as_float(gr[d]), b = __uint_as_float(gr[d + 32]);
+                gr[d] = __float_as_uint(a * co + b * si);
+                gr[d + 32] = __float_as_uint(b * co - a * si);
+              }
+          }
+        }
       }
       uint4 w[8];
 #pragma unroll
@@ -1112,74 +1148,109 @@ __global__ void __launch_bounds__(kPostThreads)
 }
 
 // ---------------------------------------------------------------------------
-// 3'. postprocess with shared key/value heads: as above, with dq over H heads
-//     (grid layer z = 0) and dk over H / group (z = 1); where the units split
-//     the groups, dk and dv (z = 2) are first summed over the splits' fp32
-//     partials, in their order, so that they are rounded once and do not
-//     depend on which unit ran first.
+// 3'. postprocess with shared key/value heads: dq over H heads as above, and,
+//     where the units split the groups, dk and dv over H / group: sums of the
+//     splits' fp32 partials in their order, so that they are rounded once and
+//     do not depend on which unit ran first.  (Unsplit, the main kernel writes
+//     them itself.)
+//     The CTAs take the packed rows in equal blocks, as the rotation pass of
+//     the forward does (ne_attn_gqa_rotate_kernel): eight lanes per (row,
+//     head), the heads of dq, dk and dv one after the other.  Rows of
+//     no sequence, or of one with bad bounds, are left alone.
 // ---------------------------------------------------------------------------
+constexpr int kGqaPostItems = 1;   // pairs of an octet in flight
+constexpr int kGqaPostRounds = 4;  // rounds of a CTA, about
+
 __global__ void __launch_bounds__(kPostThreads)
     ne_attn_gqa_postprocess_kernel(const float* __restrict__ dq_acc,
                                    const float* __restrict__ dk_part,
                                    const float* __restrict__ dv_part, int splits,
                                    __nv_bfloat16* __restrict__ dq, __nv_bfloat16* __restrict__ dk,
                                    __nv_bfloat16* __restrict__ dv, const Problem pb, RopeTable rope,
-                                   float scale) {
+                                   float scale, int rows_per_cta) {
+  extern __shared__ int row_pos[];
   pdl_wait();  // the main kernel's dQ' reduce-adds and dK, dV stores have completed
-  const int seq = blockIdx.y;
-  int start, len;
-  if (!seq_bounds(pb, seq, start, len, nullptr)) return;
-  const int z = blockIdx.z;
-  const int H = z == 0 ? pb.H : pb.H / pb.group;
-  const long long w = static_cast<long long>(blockIdx.x) * kPostThreads + threadIdx.x;
-  if (w >= static_cast<long long>(len) * H * kPostParts) return;
-  const int part = static_cast<int>(w % kPostParts);
-  const int rh = static_cast<int>(w / kPostParts);
-  const int pos = rh / H, h = rh - pos * H;
-  const long long row_off = (static_cast<long long>(start + pos) * H + h) * kHD;
-  float a[4], b[4];
-  __nv_bfloat16* d;
-  if (z == 0 || splits > 1) {
-    const float* src = z == 0 ? dq_acc : (z == 1 ? dk_part : dv_part);
-    const long long stride = static_cast<long long>(pb.n_tot) * H * kHD;
-    const int n = z == 0 ? 1 : splits;
-    const float sc = z == 0 ? scale : 1.f;
-    float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-    for (int i = 0; i < n; ++i) {
-      const float4 l = *reinterpret_cast<const float4*>(src + i * stride + row_off + part * 4);
-      const float4 u = *reinterpret_cast<const float4*>(src + i * stride + row_off + 32 + part * 4);
-      lo.x += l.x; lo.y += l.y; lo.z += l.z; lo.w += l.w;
-      hi.x += u.x; hi.y += u.y; hi.z += u.z; hi.w += u.w;
-    }
-    a[0] = lo.x * sc; a[1] = lo.y * sc; a[2] = lo.z * sc; a[3] = lo.w * sc;
-    b[0] = hi.x * sc; b[1] = hi.y * sc; b[2] = hi.z * sc; b[3] = hi.w * sc;
-    d = (z == 0 ? dq : (z == 1 ? dk : dv)) + row_off;
-  } else {  // scale dK', bf16, as the main kernel wrote it
-    d = dk + row_off;
-    const uint2 lo = *reinterpret_cast<const uint2*>(d + part * 4);
-    const uint2 hi = *reinterpret_cast<const uint2*>(d + 32 + part * 4);
-    a[0] = bf16lo_to_f32(lo.x); a[1] = bf16hi_to_f32(lo.x);
-    a[2] = bf16lo_to_f32(lo.y); a[3] = bf16hi_to_f32(lo.y);
-    b[0] = bf16lo_to_f32(hi.x); b[1] = bf16hi_to_f32(hi.x);
-    b[2] = bf16lo_to_f32(hi.y); b[3] = bf16hi_to_f32(hi.y);
-  }
-  if (z < 2) {
-    const float4* cs4 =
-        reinterpret_cast<const float4*>(rope.cs + static_cast<long long>(pos) * 32 + part * 4);
-    const float4 t0 = __ldg(cs4), t1 = __ldg(cs4 + 1);  // (cos, sin) of dims 4c .. 4c + 3
-    const float cz[4] = {t0.x, t0.z, t1.x, t1.z};
-    const float sz[4] = {t0.y, t0.w, t1.y, t1.w};
+  constexpr int kOctets = kPostThreads / kPostParts;
+  const int row0 = static_cast<int>(blockIdx.x) * rows_per_cta;
+  const int rows = min(rows_per_cta, pb.n_tot - row0);
+  const int H = pb.H, Hkv = pb.H / pb.group;
+  const int heads = H + (splits > 1 ? 2 * Hkv : 0);
+  const int part = threadIdx.x % kPostParts;
+  const int row_step = kOctets / heads, head_step = kOctets - row_step * heads;
+  int row = (threadIdx.x / kPostParts) / heads;
+  int head = threadIdx.x / kPostParts - row * heads;
+  const long long split_stride = static_cast<long long>(pb.n_tot) * Hkv * kHD;
+  bool first = true;
+  while (true) {
+    float4 lo[kGqaPostItems], hi[kGqaPostItems];
+    int rr[kGqaPostItems], hh[kGqaPostItems];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = a[i], y = b[i];
-      a[i] = x * cz[i] + y * sz[i];
-      b[i] = y * cz[i] - x * sz[i];
+    for (int u = 0; u < kGqaPostItems; ++u) {
+      rr[u] = row;
+      hh[u] = head;
+      const long long r = row0 + min(row, rows - 1);  // past the last row: that one, discarded
+      const bool is_v = head >= H + Hkv;
+      const float* src = head < H ? dq_acc + (r * H + head) * kHD
+                                  : (is_v ? dv_part : dk_part) +
+                                        (r * Hkv + (head - H - (is_v ? Hkv : 0))) * kHD;
+      lo[u] = *reinterpret_cast<const float4*>(src + part * 4);
+      hi[u] = *reinterpret_cast<const float4*>(src + 32 + part * 4);
+      const int n = head < H ? 1 : splits;
+      for (int i = 1; i < n; ++i) {
+        src += split_stride;
+        const float4 l = *reinterpret_cast<const float4*>(src + part * 4);
+        const float4 h = *reinterpret_cast<const float4*>(src + 32 + part * 4);
+        lo[u].x += l.x; lo[u].y += l.y; lo[u].z += l.z; lo[u].w += l.w;
+        hi[u].x += h.x; hi[u].y += h.y; hi[u].z += h.z; hi[u].w += h.w;
+      }
+      row += row_step;
+      head += head_step;
+      if (head >= heads) {
+        head -= heads;
+        ++row;
+      }
+    }
+    if (first) {
+      first = false;
+      for (int r = threadIdx.x; r < rows; r += kPostThreads) {
+        const int s = find_sequence(pb.cu_seqlens, pb.nseq, row0 + r);
+        int start = 0, len = 0;
+        row_pos[r] = s >= 0 && seq_bounds(pb, s, start, len, nullptr) ? row0 + r - start : -1;
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < kGqaPostItems; ++u) {
+      if (rr[u] >= rows) return;
+      const int pos = row_pos[rr[u]];
+      if (pos < 0) continue;
+      const long long r = row0 + rr[u];
+      const bool is_q = hh[u] < H, is_v = hh[u] >= H + Hkv;
+      const float sc = is_q ? scale : 1.f;
+      float a[4] = {lo[u].x * sc, lo[u].y * sc, lo[u].z * sc, lo[u].w * sc};
+      float b[4] = {hi[u].x * sc, hi[u].y * sc, hi[u].z * sc, hi[u].w * sc};
+      if (!is_v) {
+        const float4* cs4 =
+            reinterpret_cast<const float4*>(rope.cs + static_cast<long long>(pos) * 32 + part * 4);
+        const float4 t0 = __ldg(cs4), t1 = __ldg(cs4 + 1);  // (cos, sin) of dims 4c .. 4c + 3
+        const float cz[4] = {t0.x, t0.z, t1.x, t1.z};
+        const float sz[4] = {t0.y, t0.w, t1.y, t1.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = a[i], y = b[i];
+          a[i] = x * cz[i] + y * sz[i];
+          b[i] = y * cz[i] - x * sz[i];
+        }
+      }
+      __nv_bfloat16* d = is_q ? dq + (r * H + hh[u]) * kHD
+                              : (is_v ? dv + (r * Hkv + (hh[u] - H - Hkv)) * kHD
+                                      : dk + (r * Hkv + (hh[u] - H)) * kHD);
+      *reinterpret_cast<uint2*>(d + part * 4) =
+          make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+      *reinterpret_cast<uint2*>(d + 32 + part * 4) =
+          make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
     }
   }
-  *reinterpret_cast<uint2*>(d + part * 4) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-  *reinterpret_cast<uint2*>(d + 32 + part * 4) =
-      make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
-  pdl_launch_dependents();
 }
 
 // Units per (key tile, key/value head): the fewest for which the longest unit
@@ -1200,7 +1271,8 @@ int bwd_group_splits(int n_tot, int max_len, int H, int group) {
 cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        const CUtensorMap& tmDO, const CUtensorMap& tmDQ, const CUtensorMap& tmDV,
                        const CUtensorMap& tmDK, const BwdParams& p, int n_tiles,
-                       cudaStream_t stream, cudaEvent_t ev_pre, cudaEvent_t ev_main) {
+                       cudaStream_t stream, cudaEvent_t ev_pre, cudaEvent_t ev_main,
+                       const ItemList& list) {
   static bool attr_set = false;
   if (!attr_set) {
     cudaError_t e = cudaFuncSetAttribute(ne_attn_bwd_kernel<false>,
@@ -1210,7 +1282,11 @@ cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
       e = cudaFuncSetAttribute(ne_attn_bwd_kernel<true>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, bwd::SMEM_BYTES);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(ne_attn_bwd_prep_stream_kernel,
+      e = cudaFuncSetAttribute(ne_attn_bwd_prep_stream_kernel<false>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               bwd::PREP_SMEM_BYTES);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(ne_attn_bwd_prep_stream_kernel<true>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                bwd::PREP_SMEM_BYTES);
     if (e != cudaSuccess) return e;
@@ -1241,8 +1317,10 @@ cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
                              bwd::kPrepPairs;
     const long long slots = static_cast<long long>(bwd::kPrepCtasPerSm) * sm_count[dev];
     const int pg = static_cast<int>(chunks < slots ? (chunks > 0 ? chunks : 1) : slots);
-    e = launch_pdl(ne_attn_bwd_prep_stream_kernel, dim3(pg), dim3(256), bwd::PREP_SMEM_BYTES,
-                   stream, p.out, p.dout, p.delta, p.dq_acc, p.pb, p.status);
+    e = launch_pdl(list.out ? ne_attn_bwd_prep_stream_kernel<true>
+                            : ne_attn_bwd_prep_stream_kernel<false>,
+                   dim3(pg + (list.out ? 1 : 0)), dim3(256), bwd::PREP_SMEM_BYTES, stream, p.out,
+                   p.dout, p.delta, p.dq_acc, p.pb, p.status, list);
   }
   if (e != cudaSuccess) return e;
   if (ev_pre && (e = cudaEventRecord(ev_pre, stream)) != cudaSuccess) return e;
@@ -1252,12 +1330,14 @@ cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
   if (ev_main && (e = cudaEventRecord(ev_main, stream)) != cudaSuccess) return e;
   const long long post_items = static_cast<long long>(n_tiles) * kBM * p.pb.H * kPostParts;
   if (shared) {
-    dim3 grid(static_cast<unsigned>((post_items + kPostThreads - 1) / kPostThreads), p.pb.nseq,
-              p.splits > 1 ? 3 : 2);
-    return launch_pdl(ne_attn_gqa_postprocess_kernel, grid, dim3(kPostThreads), 0, stream,
+    const int heads = p.pb.H + (p.splits > 1 ? 2 * (p.pb.H / p.pb.group) : 0);
+    const int rows = std::max(
+        1, kGqaPostRounds * kGqaPostItems * kPostThreads / kPostParts / heads);
+    return launch_pdl(ne_attn_gqa_postprocess_kernel, dim3((p.pb.n_tot + rows - 1) / rows),
+                      dim3(kPostThreads), sizeof(int) * rows, stream,
                       static_cast<const float*>(p.dq_acc), static_cast<const float*>(p.dk_part),
                       static_cast<const float*>(p.dv_part), p.splits, p.dq, p.dk, p.dv, p.pb,
-                      p.rope, p.scale);
+                      p.rope, p.scale, rows);
   }
   // Layer z = 0: dQ from the accumulator; z = 1: dK rotated in place (not
   // when the gradient w.r.t. k' is asked for: the main kernel wrote it).

@@ -9,12 +9,14 @@
 
 #include "ne_attn.h"
 #include "ne_common.cuh"
+#include "ne_items.cuh"
 
 namespace ne {
 cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        const CUtensorMap& tmDO, const CUtensorMap& tmDQ, const CUtensorMap& tmDV,
                        const CUtensorMap& tmDK, const BwdParams& p, int n_tiles,
-                       cudaStream_t stream, cudaEvent_t ev_pre, cudaEvent_t ev_main);
+                       cudaStream_t stream, cudaEvent_t ev_pre, cudaEvent_t ev_main,
+                       const ItemList& list);
 ne_status internal_prepare(int** status_word);
 ne_status internal_encode_rows(CUtensorMap* map, const void* base, int n_rows, int H);
 ne_status internal_encode_rows_f32(CUtensorMap* map, void* base, int n_rows, int H);
@@ -165,7 +167,8 @@ extern "C" ne_status ne_attn_bwd_noalloc(const ne_bf16* q, const ne_bf16* k, con
   if ((rc = ne::internal_encode_rows(&tdv, dv, n_tot, H)) != NE_OK) return rc;
   if ((rc = ne::internal_encode_rows(&tdk, dk, n_tot, H)) != NE_OK) return rc;
   const cudaError_t e = ne::launch_bwd(tq, tk, tv, tdo, tdq, tdv, tdk, p, n_tiles,
-                                       static_cast<cudaStream_t>(stream), nullptr, nullptr);
+                                       static_cast<cudaStream_t>(stream), nullptr, nullptr,
+                                       ne::ItemList{});
   if (e == cudaSuccess) return NE_OK;
   return e == cudaErrorMemoryAllocation ? NE_ERR_OOM : NE_ERR_CUDA;
 }

@@ -223,7 +223,6 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
     mbar_fence_init();
   }
   pdl_wait();  // whatever wrote q, the lengths and the cache has completed
-  pdl_launch_dependents();
 
   // The cost of every sequence's units, then their prefix sums.
   const int B = p.B, J = p.pc.Hkv * p.row_tiles;

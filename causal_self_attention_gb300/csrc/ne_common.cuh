@@ -139,6 +139,27 @@ __device__ __forceinline__ bool seq_bounds(const Problem& pb, int s, int& start,
   return true;
 }
 
+__host__ __device__ __forceinline__ int load_int(const int* p) {
+#ifdef __CUDA_ARCH__
+  return __ldg(p);
+#else
+  return *p;
+#endif
+}
+
+// The sequence of packed row r: the last s with cu[s] <= r (sequences of
+// length zero are passed over), or -1 for a row outside every sequence.  Reads
+// cu[0 .. nseq] only, whatever it holds.
+__host__ __device__ __forceinline__ int find_sequence(const int* cu, int nseq, int r) {
+  int lo = 0, hi = nseq;
+  if (load_int(cu) > r || load_int(cu + nseq) <= r) return -1;
+  while (hi - lo > 1) {  // cu[lo] <= r < cu[hi]
+    const int mid = lo + ((hi - lo) >> 1);
+    if (load_int(cu + mid) <= r) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
 // Work dealing of the persistent kernels: the index r (in the longest-first
 // order of work items) of the k-th item of CTA c among G, or n when CTA c has
 // fewer than k + 1 items.  With a schedule -- offsets sched[0..G], then the

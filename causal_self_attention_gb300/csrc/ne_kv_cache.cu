@@ -93,7 +93,6 @@ __global__ void __launch_bounds__(kv::kThreads)
                         int n_tot, const PagedCache pc, RopeTable rope, int* status) {
   using namespace kv;
   pdl_wait();  // the kernel that wrote k, v (and anything before it) has completed
-  pdl_launch_dependents();
   const long long w = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   const int c = static_cast<int>(w % kParts);
   const long long rh = w / kParts;
@@ -149,7 +148,6 @@ __global__ void __launch_bounds__(kv::kThreads)
                       int n_tot, const PagedCache pc, int* status) {
   using namespace kv;
   pdl_wait();  // the kernel that filled the cache has completed
-  pdl_launch_dependents();
   const long long w = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   const int c = static_cast<int>(w % kParts);
   const long long rh = w / kParts;

@@ -13,27 +13,6 @@ struct Place {
   int pos;
 };
 
-__host__ __device__ __forceinline__ int load_int(const int* p) {
-#ifdef __CUDA_ARCH__
-  return __ldg(p);
-#else
-  return *p;
-#endif
-}
-
-// The sequence of packed row r: the last s with cu[s] <= r (sequences of
-// length zero are passed over), or -1 for a row outside every sequence.  Reads
-// cu[0 .. nseq] only, whatever it holds.
-__host__ __device__ __forceinline__ int find_sequence(const int* cu, int nseq, int r) {
-  int lo = 0, hi = nseq;
-  if (load_int(cu) > r || load_int(cu + nseq) <= r) return -1;
-  while (hi - lo > 1) {  // cu[lo] <= r < cu[hi]
-    const int mid = lo + ((hi - lo) >> 1);
-    if (load_int(cu + mid) <= r) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 // Row index in the pools of (page, head, position), or -1 for a page outside
 // the pool.
 __host__ __device__ __forceinline__ long long pool_row(const PagedCache& pc, int page, int h,

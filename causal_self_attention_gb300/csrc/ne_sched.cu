@@ -57,9 +57,7 @@ namespace ne {
 //   kind 0: forward items, r -> block n_blocks - 1 - r / (nseq H) (pairs of
 //           128-row query tiles), steps = key tiles of its last query tile;
 //   kind 1: backward units, r -> key tile r / (nseq H), steps = query tiles
-//           from it to the end of its sequence;
-//   kind 2: forward items of head pairs, r -> 128-row tile n_blocks - 1 -
-//           r / (nseq H), steps = its key tiles.
+//           from it to the end of its sequence.
 // Bucket b of the sort holds the items of b steps; bucket 0 the kept items of
 // invalid sequences; -1 marks an empty item.
 // ---------------------------------------------------------------------------
@@ -73,10 +71,6 @@ __device__ __forceinline__ int item_bucket(const Problem& pb, int kind, int n_bl
     const int b = n_blocks - 1 - blk;  // the item's block of two query tiles
     if (2 * b * kBM >= len) return -1;
     return (2 * b + 1) * kBM < len ? 2 * b + 2 : 2 * b + 1;
-  }
-  if (kind == 2) {
-    const int b = n_blocks - 1 - blk;
-    return b * kBM >= len ? -1 : b + 1;
   }
   if (blk * kBM >= len) return -1;
   return (len + kBM - 1) / kBM - blk;

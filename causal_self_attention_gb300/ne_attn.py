@@ -485,16 +485,31 @@ def ne_attn_varlen_bwd_train(qr, kr, v, out, dout, lse, cu_seqlens, max_seqlen,
 
 # ------------------------------------------- grouped heads and the paged cache
 
-def _on(stream, first, *rest):
-    """Where a call on these tensors (None: one left out) runs: the raw stream,
-    and the context that makes their device and the stream current -- also for
-    the tensors that the call creates -- or None where they are current already.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_E4M3 = torch.float8_e4m3fn
+
+
+def _need_on(t, dtype, dev, name):
+    """As _need, and on device `dev` (the index of the first argument's)."""
+    if not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+        if t.is_cuda and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the first argument on cuda:{dev}")
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
+
+
+def _device(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return dev
+
+
+def _on(stream, dev):
+    """Where a call on the tensors of device `dev` runs: the raw stream, and the
+    context that makes the device and the stream current -- also for the
+    tensors that the call creates -- or None where they are current already.
     ``stream``: a torch stream, a raw ``cudaStream_t``, or None for the device's
     current stream.  The context is entered; the caller leaves it."""
-    dev = first.get_device()
-    for t in rest:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
     if stream is None:
         if dev == torch.cuda.current_device():
             return torch._C._cuda_getCurrentRawStream(dev), None
@@ -502,7 +517,7 @@ def _on(stream, first, *rest):
     elif not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     if stream.device.index != dev:
-        raise ValueError(f"stream on {stream.device}, tensors on {first.device}")
+        raise ValueError(f"stream on {stream.device}, tensors on cuda:{dev}")
     ctx = torch.cuda.stream(stream)
     ctx.__enter__()
     return stream.cuda_stream, ctx
@@ -517,36 +532,35 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _out(t, shape, dtype, device, name):
-    """The caller's output tensor, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+def _given(t, shape, dtype, dev, name):
+    """Checks an output (or input) of a known shape."""
+    _need_on(t, dtype, dev, name)
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
-    return t
 
 
-def _ws_bytes(workspace):
+def _ws_bytes(workspace, dev):
     if workspace is None:
         return 0
-    if not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     return workspace.numel() * workspace.element_size()
 
 
 def _gqa_shapes(q, k, v, cu_seqlens, names=("q", "k", "v")):
-    for t, n in zip((q, k, v), names):
-        _need(t, torch.bfloat16, n)
-    _need(cu_seqlens, torch.int32, "cu_seqlens")
+    dev = _device(q, names[0])
+    _need_on(q, _BF16, dev, names[0])
+    _need_on(k, _BF16, dev, names[1])
+    _need_on(v, _BF16, dev, names[2])
+    _need_on(cu_seqlens, _I32, dev, "cu_seqlens")
     N, H, D = q.shape
-    Hkv = k.shape[1]
-    if tuple(k.shape) != (N, Hkv, D) or k.shape != v.shape or Hkv == 0 or H % Hkv:
+    n, Hkv, d = k.shape
+    if n != N or d != D or k.shape != v.shape or Hkv == 0 or H % Hkv:
         raise ValueError(f"shapes: {names[0]} [N, H, D], {names[1]}, {names[2]} [N, Hkv, D] with "
                          "H a multiple of Hkv")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be [nseq + 1]")
-    return N, H, Hkv, D, cu_seqlens.numel() - 1
+    return dev, N, H, Hkv, D, cu_seqlens.numel() - 1
 
 
 def ne_attn_gqa_varlen_fwd(q, k, v, cu_seqlens, max_seqlen, rope_base=10000.0, scale=None,
@@ -557,20 +571,25 @@ def ne_attn_gqa_varlen_fwd(q, k, v, cu_seqlens, max_seqlen, rope_base=10000.0, s
     ``cu_seqlens`` int32 CUDA ``[nseq + 1]``.  Returns ``(out, lse, qr, kr)``:
     ``lse`` ``[H, N_tot]`` fp32, and the rotated operands for the backward (or,
     ``kr``, for a cache: :func:`ne_kv_append` with ``rope_base=0``)."""
-    N, H, Hkv, D, nseq = _gqa_shapes(q, k, v, cu_seqlens)
-    scale = D ** -0.5 if scale is None else scale
-    raw, ctx = _on(stream, q, k, v, cu_seqlens, out, lse, qr, kr)
+    dev, N, H, Hkv, D, nseq = _gqa_shapes(q, k, v, cu_seqlens)
+    for t, like, name in ((out, q, "out"), (qr, q, "qr"), (kr, k, "kr")):
+        if t is not None:
+            _given(t, like.shape, _BF16, dev, name)
+    if lse is not None:
+        _given(lse, (H, N), _F32, dev, "lse")
+    raw, ctx = _on(stream, dev)
     try:
-        dev = q.device
-        out = _out(out, q.shape, torch.bfloat16, dev, "out")
-        lse = _out(lse, (H, N), torch.float32, dev, "lse")
-        qr = _out(qr, q.shape, torch.bfloat16, dev, "qr")
-        kr = _out(kr, k.shape, torch.bfloat16, dev, "kr")
-        _check("ne_attn_gqa_varlen_fwd", lib().ne_attn_gqa_varlen_fwd(
-            _addr(q), _addr(k), _addr(v), _addr(cu_seqlens), nseq, N, int(max_seqlen), H, Hkv, D,
-            float(rope_base), float(scale), _addr(out), _addr(lse), _addr(qr), _addr(kr), raw))
+        out = torch.empty_like(q) if out is None else out
+        lse = torch.empty((H, N), dtype=_F32, device=q.device) if lse is None else lse
+        qr = torch.empty_like(q) if qr is None else qr
+        kr = torch.empty_like(k) if kr is None else kr
+        rc = lib().ne_attn_gqa_varlen_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), nseq, N,
+            int(max_seqlen),            H, Hkv, D, rope_base, D ** -0.5 if scale is None else scale, out.data_ptr(),
+            lse.data_ptr(), qr.data_ptr(), kr.data_ptr(), raw)
     finally:
         _leave(ctx)
+    _check("ne_attn_gqa_varlen_fwd", rc)
     return out, lse, qr, kr
 
 
@@ -585,58 +604,58 @@ def ne_attn_gqa_varlen_bwd(qr, kr, v, out, dout, lse, cu_seqlens, max_seqlen, ro
     """Backward of :func:`ne_attn_gqa_varlen_fwd` from its ``qr``, ``kr``, ``out``
     and ``lse``.  Returns ``(dq, dk, dv)``: gradients w.r.t. the un-rotated q, k
     and v, ``dk`` and ``dv`` summed over the query heads that share them."""
-    N, H, Hkv, D, nseq = _gqa_shapes(qr, kr, v, cu_seqlens, ("qr", "kr", "v"))
-    for t, n in ((out, "out"), (dout, "dout")):
-        _need(t, torch.bfloat16, n)
-        if t.shape != qr.shape:
-            raise ValueError(f"{n} must have the shape {tuple(qr.shape)}")
-    _out(lse, (H, N), torch.float32, None, "lse")
-    scale = D ** -0.5 if scale is None else scale
-    ws_bytes = _ws_bytes(workspace)
-    raw, ctx = _on(stream, qr, kr, v, out, dout, lse, cu_seqlens, dq, dk, dv, workspace)
+    dev, N, H, Hkv, D, nseq = _gqa_shapes(qr, kr, v, cu_seqlens, ("qr", "kr", "v"))
+    _given(out, qr.shape, _BF16, dev, "out")
+    _given(dout, qr.shape, _BF16, dev, "dout")
+    _given(lse, (H, N), _F32, dev, "lse")
+    for t, like, name in ((dq, qr, "dq"), (dk, kr, "dk"), (dv, v, "dv")):
+        if t is not None:
+            _given(t, like.shape, _BF16, dev, name)
+    ws_bytes = _ws_bytes(workspace, dev)
+    raw, ctx = _on(stream, dev)
     try:
-        dev = qr.device
-        dq = _out(dq, qr.shape, torch.bfloat16, dev, "dq")
-        dk = _out(dk, kr.shape, torch.bfloat16, dev, "dk")
-        dv = _out(dv, v.shape, torch.bfloat16, dev, "dv")
-        _check("ne_attn_gqa_varlen_bwd", lib().ne_attn_gqa_varlen_bwd(
-            _addr(qr), _addr(kr), _addr(v), _addr(out), _addr(dout), _addr(lse),
-            _addr(cu_seqlens), nseq, N, int(max_seqlen), H, Hkv, D, float(rope_base), float(scale), _addr(dq), _addr(dk),
-            _addr(dv), _addr(workspace), ws_bytes, raw))
+        dq = torch.empty_like(qr) if dq is None else dq
+        dk = torch.empty_like(kr) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        rc = lib().ne_attn_gqa_varlen_bwd(
+            qr.data_ptr(), kr.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
+            lse.data_ptr(), cu_seqlens.data_ptr(), nseq, N, int(max_seqlen), H, Hkv, D, rope_base,
+            D ** -0.5 if scale is None else scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+            _addr(workspace), ws_bytes, raw)
     finally:
         _leave(ctx)
+    _check("ne_attn_gqa_varlen_bwd", rc)
     return dq, dk, dv
 
 
-def _paged(k_pages, v_pages, k_scale, v_scale, block_table, nseq):
+def _paged(k_pages, v_pages, k_scale, v_scale, block_table, nseq, dev):
     """Checks a paged cache; returns (kv_type, n_pages, Hkv, page_size, max_pages)."""
-    if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+    dtype = k_pages.dtype
+    if dtype is not _BF16 and dtype is not _E4M3:
         raise ValueError("k_pages must be bfloat16 or float8_e4m3fn")
-    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        _need(t, k_pages.dtype, n)
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != 64:
+    _need_on(k_pages, dtype, dev, "k_pages")
+    _need_on(v_pages, dtype, dev, "v_pages")
+    _need_on(block_table, _I32, dev, "block_table")
+    shape = k_pages.shape
+    if len(shape) != 4 or shape != v_pages.shape or shape[3] != 64:
         raise ValueError("k_pages, v_pages must be [n_pages, Hkv, page_size, 64]")
-    _need(block_table, torch.int32, "block_table")
-    if block_table.dim() != 2 or block_table.shape[0] != nseq:
+    table = block_table.shape
+    if len(table) != 2 or table[0] != nseq:
         raise ValueError(f"block_table must be [{nseq}, max_pages]")
-    n_pages, Hkv, page_size, _ = k_pages.shape
-    kv_type = KV_BF16 if k_pages.dtype == torch.bfloat16 else KV_E4M3
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if kv_type == KV_BF16:
-            if t is not None:
-                raise ValueError(f"{n}: a bfloat16 cache has no scales")
-            continue
-        if t is None:
-            raise ValueError(f"{n}: a float8_e4m3fn cache needs its scales")
-        _need(t, torch.uint8, n)
-        if tuple(t.shape) != (n_pages, Hkv, page_size):
-            raise ValueError(f"{n} must be [n_pages, Hkv, page_size]")
-    return kv_type, n_pages, Hkv, page_size, block_table.shape[1]
+    if dtype is _BF16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale, v_scale: a bfloat16 cache has no scales")
+    elif k_scale is None or v_scale is None:
+        raise ValueError("k_scale, v_scale: a float8_e4m3fn cache needs its scales")
+    else:
+        _given(k_scale, shape[:3], _U8, dev, "k_scale")
+        _given(v_scale, shape[:3], _U8, dev, "v_scale")
+    return (KV_BF16 if dtype is _BF16 else KV_E4M3,) + shape[:3] + table[1:]
 
 
-def _row_places(cu_seqlens, start_pos):
-    for t, n in ((cu_seqlens, "cu_seqlens"), (start_pos, "start_pos")):
-        _need(t, torch.int32, n)
+def _row_places(cu_seqlens, start_pos, dev):
+    _need_on(cu_seqlens, _I32, dev, "cu_seqlens")
+    _need_on(start_pos, _I32, dev, "start_pos")
     nseq = start_pos.numel()
     if cu_seqlens.numel() != nseq + 1:
         raise ValueError("cu_seqlens must be [nseq + 1] for start_pos [nseq]")
@@ -652,24 +671,25 @@ def ne_kv_append(k, v, cu_seqlens, start_pos, k_pages, v_pages, block_table, max
     ``[n_pages, Hkv, page_size]``; ``block_table`` int32 ``[nseq, max_pages]``.
     ``rope_base=0``: ``k`` is rotated already.  Returns ``(k_pages, v_pages)``,
     written in place."""
-    for t, n in ((k, "k"), (v, "v")):
-        _need(t, torch.bfloat16, n)
-    nseq = _row_places(cu_seqlens, start_pos)
+    dev = _device(k, "k")
+    _need_on(k, _BF16, dev, "k")
+    _need_on(v, _BF16, dev, "v")
+    nseq = _row_places(cu_seqlens, start_pos, dev)
     kv_type, n_pages, Hkv, page_size, max_pages = _paged(k_pages, v_pages, k_scale, v_scale,
-                                                         block_table, nseq)
-    n_tot, _, D = k.shape
-    if tuple(k.shape) != (n_tot, Hkv, D) or k.shape != v.shape:
+                                                         block_table, nseq, dev)
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != Hkv or shape[2] != 64 or shape != v.shape:
         raise ValueError("k, v must be [n_tot, Hkv, 64] with the pages' Hkv")
-    raw, ctx = _on(stream, k, v, cu_seqlens, start_pos, k_pages, v_pages, k_scale, v_scale,
-                   block_table)
+    raw, ctx = _on(stream, dev)
     try:
-        _check("ne_kv_append", lib().ne_kv_append(
-            _addr(k), _addr(v), _addr(cu_seqlens), _addr(start_pos), nseq, n_tot, Hkv, D,
-            float(rope_base), kv_type, _addr(k_pages), _addr(v_pages), _addr(k_scale),
-            _addr(v_scale), _addr(block_table), max_pages, n_pages, page_size, int(max_seqlen),
-            raw))
+        rc = lib().ne_kv_append(
+            k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), start_pos.data_ptr(), nseq,
+            shape[0], Hkv, 64, rope_base, kv_type, k_pages.data_ptr(), v_pages.data_ptr(),
+            _addr(k_scale), _addr(v_scale), block_table.data_ptr(), max_pages, n_pages, page_size,
+            int(max_seqlen), raw)
     finally:
         _leave(ctx)
+    _check("ne_kv_append", rc)
     return k_pages, v_pages
 
 
@@ -680,23 +700,30 @@ def ne_kv_read(k_pages, v_pages, block_table, cu_seqlens, start_pos, n_tot, k_sc
     ``start_pos[s] + i``.  The keys come rotated, as the cache holds them.
     ``max_seqlen``: the block table's reach unless given.  Returns ``(k, v)``;
     rows of the caller's ``k``, ``v`` that no sequence covers stay as they are."""
-    nseq = _row_places(cu_seqlens, start_pos)
+    dev = _device(k_pages, "k_pages")
+    nseq = _row_places(cu_seqlens, start_pos, dev)
     kv_type, n_pages, Hkv, page_size, max_pages = _paged(k_pages, v_pages, k_scale, v_scale,
-                                                         block_table, nseq)
+                                                         block_table, nseq, dev)
     if max_seqlen is None:
         max_seqlen = min(max_pages * page_size, 65535 * 128)
-    raw, ctx = _on(stream, k_pages, v_pages, k_scale, v_scale, block_table, cu_seqlens,
-                   start_pos, k, v)
+    n_tot = int(n_tot)
+    shape = (n_tot, Hkv, 64)
+    if k is not None:
+        _given(k, shape, _BF16, dev, "k")
+    if v is not None:
+        _given(v, shape, _BF16, dev, "v")
+    raw, ctx = _on(stream, dev)
     try:
-        dev = k_pages.device
-        k = _out(k, (int(n_tot), Hkv, 64), torch.bfloat16, dev, "k")
-        v = _out(v, (int(n_tot), Hkv, 64), torch.bfloat16, dev, "v")
-        _check("ne_kv_read", lib().ne_kv_read(
-            kv_type, _addr(k_pages), _addr(v_pages), _addr(k_scale), _addr(v_scale),
-            _addr(block_table), max_pages, n_pages, page_size, int(max_seqlen), _addr(cu_seqlens),
-            _addr(start_pos), nseq, int(n_tot), Hkv, 64, _addr(k), _addr(v), raw))
+        k = torch.empty(shape, dtype=_BF16, device=k_pages.device) if k is None else k
+        v = torch.empty_like(k) if v is None else v
+        rc = lib().ne_kv_read(
+            kv_type, k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scale), _addr(v_scale),
+            block_table.data_ptr(), max_pages, n_pages, page_size,
+            int(max_seqlen), cu_seqlens.data_ptr(), start_pos.data_ptr(), nseq, n_tot, Hkv, 64, k.data_ptr(),
+            v.data_ptr(), raw)
     finally:
         _leave(ctx)
+    _check("ne_kv_read", rc)
     return k, v
 
 
@@ -713,30 +740,34 @@ def ne_attn_decode_paged(q, k_pages, v_pages, block_table, seq_lens, max_seqlen,
     :func:`ne_kv_append` with the new tokens' rows in it, ``seq_lens`` int32
     ``[B]`` on the device (positions 0 .. seq_lens[b] - 1 are attended; 0 gives
     zeros and -inf).  Returns ``(out [B, H, 64] bf16, lse [B, H] fp32)``."""
-    _need(q, torch.bfloat16, "q")
-    _need(seq_lens, torch.int32, "seq_lens")
+    dev = _device(q, "q")
+    _need_on(q, _BF16, dev, "q")
+    _need_on(seq_lens, _I32, dev, "seq_lens")
     B, H, D = q.shape
     if seq_lens.numel() != B:
         raise ValueError("seq_lens must be [B]")
     kv_type, n_pages, Hkv, page_size, max_pages = _paged(k_pages, v_pages, k_scale, v_scale,
-                                                         block_table, B)
+                                                         block_table, B, dev)
     if Hkv == 0 or H % Hkv:
         raise ValueError("q must be [B, H, 64] with H a multiple of the pages' Hkv")
-    scale = D ** -0.5 if scale is None else scale
-    ws_bytes = _ws_bytes(workspace)
-    raw, ctx = _on(stream, q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, out,
-                   lse, workspace)
+    if out is not None:
+        _given(out, q.shape, _BF16, dev, "out")
+    if lse is not None:
+        _given(lse, (B, H), _F32, dev, "lse")
+    ws_bytes = _ws_bytes(workspace, dev)
+    raw, ctx = _on(stream, dev)
     try:
-        dev = q.device
-        out = _out(out, q.shape, torch.bfloat16, dev, "out")
-        lse = _out(lse, (B, H), torch.float32, dev, "lse")
-        _check("ne_attn_decode_paged", lib().ne_attn_decode_paged(
-            _addr(q), kv_type, _addr(k_pages), _addr(v_pages), _addr(k_scale), _addr(v_scale),
-            _addr(block_table), max_pages, n_pages, page_size, int(max_seqlen), _addr(seq_lens), B,
-            H, Hkv, D, float(rope_base), float(scale), _addr(out), _addr(lse), _addr(workspace),
-            ws_bytes, raw))
+        out = torch.empty_like(q) if out is None else out
+        lse = torch.empty((B, H), dtype=_F32, device=q.device) if lse is None else lse
+        rc = lib().ne_attn_decode_paged(
+            q.data_ptr(), kv_type, k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scale),
+            _addr(v_scale), block_table.data_ptr(), max_pages, n_pages, page_size,
+            int(max_seqlen), seq_lens.data_ptr(), B, H, Hkv, D, rope_base,
+            D ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(),
+            _addr(workspace), ws_bytes, raw)
     finally:
         _leave(ctx)
+    _check("ne_attn_decode_paged", rc)
     return out, lse
 
 

@@ -67,7 +67,7 @@ def _check(na, lens, H, Hkv, seed=0, qscale=1.0, max_seqlen=None, behind=0, grad
                                                          lse[:, r], 0.125)
             p = torch.arange(m, device="cuda")
             res += [("dq", dq[r], rotate(gq, p, BASE, back=True), unrotate_bound(gq, eq, 1)),
-                    ("dk", dk[r], rotate(gk, p, BASE, back=True), unrotate_bound(gk, ek, 2)),
+                    ("dk", dk[r], rotate(gk, p, BASE, back=True), unrotate_bound(gk, ek, 1)),
                     ("dv", dv[r], gv, ev)]
         for name, a, b, e in res:
             worst[name] = max(worst.get(name, 0.0), within(a, b, e, f"{name} of sequence {s}"))

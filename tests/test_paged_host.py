@@ -234,8 +234,9 @@ def test_binding_refuses_before_the_library(monkeypatch):
     with pytest.raises(ValueError):
         na.ne_attn_decode_paged(bf(1, 4, 64), bf(2, 2, 16, 64), bf(2, 2, 16, 64), i(1, 2), i(1), 16)
     # The device checks aside (a stand-in for CUDA tensors), shapes and types.
-    monkeypatch.setattr(na, "_need", lambda t, dtype, name: t.dtype == dtype or
+    monkeypatch.setattr(na, "_need_on", lambda t, dtype, dev, name: t.dtype == dtype or
                         (_ for _ in ()).throw(ValueError(name)))
+    monkeypatch.setattr(na, "_device", lambda t, name: -1)
     e4 = lambda *s: torch.zeros(s).to(torch.float8_e4m3fn)  # noqa: E731
     u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
     bad = [
@@ -243,16 +244,16 @@ def test_binding_refuses_before_the_library(monkeypatch):
         lambda: na.ne_attn_gqa_varlen_fwd(bf(4, 4, 64), bf(5, 2, 64), bf(5, 2, 64), i(2), 4),
         lambda: na.ne_attn_gqa_varlen_fwd(bf(4, 4, 64), bf(4, 2, 64), bf(4, 1, 64), i(2), 4),
         lambda: na.ne_attn_gqa_varlen_fwd(bf(4, 4, 64), bf(4, 2, 64), bf(4, 2, 64), i(1), 4),
-        lambda: na._paged(e4(2, 2, 16, 64), e4(2, 2, 16, 64), None, u8(2, 2, 16), i(1, 2), 1),
-        lambda: na._paged(e4(2, 2, 16, 64), e4(2, 2, 16, 64), u8(2, 2, 8), u8(2, 2, 16), i(1, 2), 1),
-        lambda: na._paged(bf(2, 2, 16, 64), bf(2, 2, 16, 64), u8(2, 2, 16), None, i(1, 2), 1),
-        lambda: na._paged(bf(2, 2, 16, 64), e4(2, 2, 16, 64), None, None, i(1, 2), 1),
-        lambda: na._paged(bf(2, 2, 16, 64), bf(3, 2, 16, 64), None, None, i(1, 2), 1),
-        lambda: na._paged(bf(2, 2, 16, 32), bf(2, 2, 16, 32), None, None, i(1, 2), 1),
-        lambda: na._paged(bf(2, 2, 16, 64), bf(2, 2, 16, 64), None, None, i(2, 2), 1),
-        lambda: na._paged(bf(2, 2, 16, 64).half(), bf(2, 2, 16, 64).half(), None, None, i(1, 2), 1),
-        lambda: na._row_places(i(3), i(1)),
-        lambda: na._out(bf(2, 3), (2, 4), torch.bfloat16, None, "out"),
+        lambda: na._paged(e4(2, 2, 16, 64), e4(2, 2, 16, 64), None, u8(2, 2, 16), i(1, 2), 1, -1),
+        lambda: na._paged(e4(2, 2, 16, 64), e4(2, 2, 16, 64), u8(2, 2, 8), u8(2, 2, 16), i(1, 2), 1, -1),
+        lambda: na._paged(bf(2, 2, 16, 64), bf(2, 2, 16, 64), u8(2, 2, 16), None, i(1, 2), 1, -1),
+        lambda: na._paged(bf(2, 2, 16, 64), e4(2, 2, 16, 64), None, None, i(1, 2), 1, -1),
+        lambda: na._paged(bf(2, 2, 16, 64), bf(3, 2, 16, 64), None, None, i(1, 2), 1, -1),
+        lambda: na._paged(bf(2, 2, 16, 32), bf(2, 2, 16, 32), None, None, i(1, 2), 1, -1),
+        lambda: na._paged(bf(2, 2, 16, 64), bf(2, 2, 16, 64), None, None, i(2, 2), 1, -1),
+        lambda: na._paged(bf(2, 2, 16, 64).half(), bf(2, 2, 16, 64).half(), None, None, i(1, 2), 1, -1),
+        lambda: na._row_places(i(3), i(1), -1),
+        lambda: na._given(bf(2, 3), (2, 4), torch.bfloat16, -1, "out"),
     ]
     for n, call in enumerate(bad):
         with pytest.raises(ValueError):
