@@ -969,11 +969,16 @@ __global__ void __launch_bounds__(512, 1)
             const int Hkv = p.pb.H / p.pb.group;
             const long long orow =
                 ((static_cast<long long>(u.split) * p.pb.n_tot + u.start + kpos) * Hkv + u.h) * kHD;
-            float4* dst = reinterpret_cast<float4*>((half ? p.dk_part : p.dv_part) + orow);
+            float* dst = (half ? p.dk_part : p.dv_part) + orow;
+            // Whole 32-byte sectors (16-byte pieces of 128 rows cost more than
+            // the rest of the unit's end).
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-              dst[c] = make_float4(__uint_as_float(gr[4 * c]) * sc, __uint_as_float(gr[4 * c + 1]) * sc,
-                                   __uint_as_float(gr[4 * c + 2]) * sc, __uint_as_float(gr[4 * c + 3]) * sc);
+            for (int c = 0; c < 64; c += 8) {
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(gr[c + e]) * sc;
+              store_f32x8(dst + c, v);
+            }
           }
           mbar_arrive(&bars[B_EPI_FULL]);
           g += u.n_it;
@@ -1253,19 +1258,35 @@ __global__ void __launch_bounds__(kPostThreads)
   }
 }
 
-// Units per (key tile, key/value head): the fewest for which the longest unit
-// (the first key tile of a sequence of max_len rows) stays within a tenth of
-// the mean work of a CTA, on the reckoning that the rows make up as many
-// sequences of max_len as they can; at most one query head each.  152: the
-// SMs of the part (the reckoning is the same on the host that sizes the
-// workspace).
+// Units per (key tile, key/value head): the divisor of the group for which the
+// backward is reckoned shortest, in microseconds, as if the rows made up as
+// many sequences of max_len as they can.  The busiest CTA has the longest unit
+// (the first key tile of a sequence) or the mean plus an eighth of it, at 1.75
+// a query tile; a unit's ends cost 2.6; and the partials of split groups are
+// written and read at 5 TB/s.  (Measured: 8 x 1024, 12 query heads on 4: one
+// unit 72, three 98; on 1: four 74, three 83, twelve 101; 1 x 16384, 12 on 2:
+// one 1342, two 1240, three 1213; 2 x 4096, 12 on 4: one 190, three 198.
+// Uneven shares lose: two of three heads 218.)  152: the SMs of the part -- the
+// reckoning is the host's that sizes the workspace, too.
 int bwd_group_splits(int n_tot, int max_len, int H, int group) {
-  const long long nt = (static_cast<long long>(max_len) + kBM - 1) / kBM;
-  const long long n_full = std::max(1, n_tot / max_len);
-  const double mean = 0.5 * H * n_full * nt * (nt + 1) / 152.0;
-  int s = 1;
-  while (s < group && static_cast<double>((group + s - 1) / s) * nt > 1.1 * mean) ++s;
-  return s;
+  const double nt = static_cast<double>((static_cast<long long>(max_len) + kBM - 1) / kBM);
+  const double n_seq = std::max(1, n_tot / max_len), Hkv = H / group;
+  const double mean = 0.5 * H * n_seq * nt * (nt + 1) / 152.0;
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= group && s <= 64; ++s) {
+    if (group % s) continue;
+    const double longest = group / s * nt;
+    const double busiest = std::max(longest, mean + 0.125 * longest);
+    const double bytes = s > 1 ? 2.0 * s * n_tot * Hkv * kHD * 8.0 : 0.0;
+    const double t = 1.75 * busiest + 2.6 * std::max(1.0, nt * n_seq * Hkv * s / 152.0) +
+                     bytes / 5e6;
+    if (s == 1 || t < least) {
+      best = s;
+      least = t;
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,

@@ -475,6 +475,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// One 32-byte store (32-byte aligned).
+__device__ __forceinline__ void store_f32x8(float* dst, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
 // The value v, hidden from the optimiser: it can neither reuse earlier
 // results computed from v nor hoist work on v out of the enclosing loop (used
 // to keep such results out of scarce registers).
