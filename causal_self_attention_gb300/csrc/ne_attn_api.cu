@@ -21,8 +21,12 @@
 namespace ne {
 cudaError_t launch_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        const CUtensorMap& tmO, const FwdParams& p, int n_qtiles,
-                       cudaStream_t stream, Pair pair);
-int fwd_blocks(Pair pair, int n_qtiles);
+                       cudaStream_t stream);
+ItemList gqa_fwd_items(const Problem& pb, int n_qtiles, long long* n_items);
+cudaError_t launch_gqa_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                           const CUtensorMap& tmO, const Problem& pb, __nv_bfloat16* out,
+                           float* lse, float scale_log2, const ItemList& items, int n_items,
+                           int sms, int* status, cudaStream_t stream);
 int bwd_group_splits(int n_tot, int max_len, int H, int group);
 cudaError_t launch_rope_rows(const __nv_bfloat16* x0, __nv_bfloat16* xr0,
                              const __nv_bfloat16* x1, __nv_bfloat16* xr1, const Problem& pb,
@@ -61,6 +65,7 @@ cudaError_t launch_kv_read(__nv_bfloat16* k, __nv_bfloat16* v, const int* cu,
 size_t paged_part_bytes(int B, int H, int Hkv, int max_seqlen);
 size_t paged_counter_bytes();
 unsigned paged_box_rows(int page_size);
+int paged_batch(int H, int Hkv, int max_seqlen);
 cudaError_t launch_decode_paged(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                 const __nv_bfloat16* q, const PagedCache& pc, bool e4m3,
                                 const int* seq_lens, int B, int H, const RopeTable& rope,
@@ -518,13 +523,14 @@ ne_status run_fwd(const Shape& s, const void* q, const void* k, const void* v, f
   const void* keys = mode == Rot::kTrain ? kr_out : k;
   // Temporaries: the rotated keys (long sequences) and, for a packed batch,
   // the compacted item list.
-  const ne::Pair pair = s.group == 1       ? ne::Pair::kRows
-                        : s.group % 2 == 0 ? ne::Pair::kSharedHeads
-                                           : ne::Pair::kSharedRows;
-  const bool head_pairs = pair == ne::Pair::kSharedHeads;
-  const int nblk = ne::fwd_blocks(pair, n_qtiles);
-  const long long n_items = static_cast<long long>(nblk) * s.nseq * (head_pairs ? s.H / 2 : s.H);
-  const int n_buckets = (head_pairs ? nblk : 2 * nblk) + 1;
+  const int nblk = (n_qtiles + 1) / 2;
+  long long n_items = static_cast<long long>(nblk) * s.nseq * s.H;
+  int n_buckets = 2 * nblk + 1;
+  ne::ItemList items;
+  if (s.group > 1) {
+    items = ne::gqa_fwd_items(p.pb, n_qtiles, &n_items);
+    n_buckets = items.n_buckets;
+  }
   const bool compact = !s.fixed && n_items <= kMaxCompactItems && n_buckets <= kMaxBuckets;
   const size_t kr_bytes =
       (mode == Rot::kRotate && !p.rotate_k) ? static_cast<size_t>(s.n_tot) * s.H * 64 * 2 : 0;
@@ -557,19 +563,16 @@ ne_status run_fwd(const Shape& s, const void* q, const void* k, const void* v, f
   if (rc == NE_OK) rc = encode_rows(&to, out_f32 ? q : out, s.n_tot, s.H);
   if (rc == NE_OK && s.group > 1) {
     // Shared heads: the rotation pass builds the work list too.
-    ne::ItemList items;
-    items.kind = head_pairs ? ne::Items::kHeadPairs : ne::Items::kRowPairs;
-    items.n_blocks = nblk;
-    items.n_heads = head_pairs ? s.H / 2 : s.H;
-    items.n_buckets = n_buckets;
     items.out = list;
-    p.compact = list;
     e = ne::launch_gqa_rotate(static_cast<const __nv_bfloat16*>(q),
                               static_cast<__nv_bfloat16*>(qr_out),
                               static_cast<const __nv_bfloat16*>(k),
                               static_cast<__nv_bfloat16*>(kr_out), p.pb, p.rope, items, cs);
     if (e == cudaSuccess && g_ev_rot) e = cudaEventRecord(g_ev_rot, cs);
-    if (e == cudaSuccess) e = ne::launch_fwd(tq, tk, tv, to, p, n_qtiles, cs, pair);
+    if (e == cudaSuccess)
+      e = ne::launch_gqa_fwd(tq, tk, tv, to, p.pb, static_cast<__nv_bfloat16*>(out), lse,
+                             p.scale_log2, items, static_cast<int>(n_items), st->sm_count,
+                             st->status, cs);
   } else if (rc == NE_OK) {
     if (mode == Rot::kRotate && !p.rotate_k)
       e = ne::launch_rope_rows(static_cast<const __nv_bfloat16*>(k),
@@ -586,7 +589,7 @@ ne_status run_fwd(const Shape& s, const void* q, const void* k, const void* v, f
       e = ne::launch_compact_items(p.pb, 0, nblk, n_buckets, list, cs);
       p.compact = list;
     }
-    if (e == cudaSuccess) e = ne::launch_fwd(tq, tk, tv, to, p, n_qtiles, cs, pair);
+    if (e == cudaSuccess) e = ne::launch_fwd(tq, tk, tv, to, p, n_qtiles, cs);
   }
   if (own) {
     const cudaError_t e2 = cudaFreeAsync(tmp, cs);
@@ -1136,6 +1139,7 @@ ne_status ne_attn_decode_paged(const ne_bf16* q, int kv_type, const void* k_page
     return NE_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned4(seq_lens) || !aligned4(lse))
     return NE_ERR_MISALIGNED;
+  if (ne::paged_batch(H, Hkv, max_seqlen) < 1) return NE_ERR_INVALID_ARG;
   const size_t need = ne_attn_decode_paged_workspace_bytes(B, H, Hkv, max_seqlen);
   if (workspace && workspace_bytes < need) return NE_ERR_INVALID_ARG;
   if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 15u)) return NE_ERR_MISALIGNED;

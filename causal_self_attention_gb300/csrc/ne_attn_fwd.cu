@@ -42,26 +42,9 @@
 // and l keep a common reference).
 // Key tiles entirely above the diagonal are never loaded or computed.
 //
-// Shared key/value heads (kPair != Pair::kRows, keys and queries rotated
-// beforehand): query head h reads key/value head h / group.  With an even
-// group an item is one 128-row tile of two neighbouring heads of the group,
-// which share every K'/V tile and end on the same diagonal tile: a sequence of
-// up to 128 rows then still fills both tiles, where two consecutive row tiles
-// of one head leave tile B empty.  An odd group keeps the consecutive row
-// tiles.  Warps 8-11, which have nothing to rotate, are the epilogue: they wait
-// for an item's last P V, divide by the softmax sums (through shared memory)
-// and store, while the softmax warps take the next item's scores.  On short
-// prompts that is most of an item: of the ~6,500 cycles that the softmax of a
-// single tile took from item to item, it waited ~900 for the last P V and spent
-// ~2,000 on the epilogue and ~1,000 on looking the next item up (whose index
-// is now fetched one item ahead).
-//
 // Barrier phases: the K and V rings count K tiles over all items of the CTA;
 // S_FULL / S_FREE / P_FULL / PV_DONE of tile X count the steps of tile X over
 // all items; Q_* (per Q buffer), O_FINAL and O_FREE count items.
-#include <algorithm>
-
-#include "ne_items.cuh"
 #include "ne_rope.cuh"
 #include "ne_sm100.cuh"
 
@@ -79,8 +62,7 @@ constexpr int OFF_K = OFF_Q + 4 * kTileBytes;         // kStages
 constexpr int OFF_V = OFF_K + kStages * kTileBytes;   // kStages
 constexpr int OFF_BAR = OFF_V + kStages * kTileBytes;
 constexpr int kBarBytes = 512;  // mbarriers, TMEM address, abort flag
-constexpr int OFF_SUM = OFF_BAR + kBarBytes;  // shared heads: the softmax sums, 2 x 128 fp32
-constexpr int SMEM_BYTES = OFF_SUM + 2 * 128 * 4 + 1024;  // + slack for 1024-byte alignment
+constexpr int SMEM_BYTES = OFF_BAR + kBarBytes + 1024;  // + slack for 1024-byte alignment
 static_assert(SMEM_BYTES <= 232448, "more shared memory than an sm_103 CTA may have");
 
 enum Bar {
@@ -100,8 +82,7 @@ enum Bar {
   B_O_FREE = B_O_FINAL + 2,           // per tile: the epilogue has read O_X
   B_OST_FULL = B_O_FREE + 2,          // per tile: O_X (bf16) staged in its Q slot
   B_MMA_DONE = B_OST_FULL + 2,        // per issuing warp (S, P V)
-  B_SUM_FULL = B_MMA_DONE + 2,        // per tile, shared heads: the rows' sums are in OFF_SUM
-  B_COUNT = B_SUM_FULL + 2
+  B_COUNT = B_MMA_DONE + 2
 };
 static_assert(8 * B_COUNT + 8 <= kBarBytes, "barrier region overflow");
 
@@ -115,7 +96,7 @@ constexpr uint32_t kIdescO = make_idesc_bf16(128, 64, false, true);    // P V (V
 
 // One work item: block `blk` of 256 query rows of (sequence seq, head h).
 struct Item {
-  int seq, h, blk;  // tile X: head h + X * head_step, rows from rowA + X * row_step
+  int seq, h, blk;
   int start, len;  // the sequence's first row in the packed tensors, its length
   int rowA;        // first row of tile A in the sequence
   bool hasB;       // tile B has rows inside the sequence
@@ -126,25 +107,15 @@ struct Item {
 // first (they have the most key tiles), then the next lower, ...  Returns
 // false for an empty item (the sequence has no such block, or a bad
 // cu_seqlens entry, which is reported once).
-template <Pair kPair>
 __device__ __forceinline__ bool get_item(const FwdParams& p, int nblk, int r, Item& it,
                                          bool report) {
-  const int n_h = kPair == Pair::kSharedHeads ? p.pb.H / 2 : p.pb.H;
-  const int n_sh = p.pb.nseq * n_h;
+  const int n_sh = p.pb.nseq * p.pb.H;
   const int sh = r % n_sh;
   it.blk = nblk - 1 - r / n_sh;
-  it.seq = sh / n_h;
-  it.h = sh % n_h;
+  it.seq = sh / p.pb.H;
+  it.h = sh % p.pb.H;
   if (!seq_bounds(p.pb, it.seq, it.start, it.len, (report && it.blk == 0) ? p.status : nullptr))
     return false;
-  if constexpr (kPair == Pair::kSharedHeads) {
-    it.h *= 2;
-    it.rowA = it.blk * kBM;
-    if (it.rowA >= it.len) return false;
-    it.hasB = true;
-    it.nkvA = it.nkvB = it.nkv = it.blk + 1;
-    return true;
-  }
   it.rowA = 2 * it.blk * kBM;
   if (it.rowA >= it.len) return false;
   it.hasB = it.rowA + kBM < it.len;
@@ -152,20 +123,6 @@ __device__ __forceinline__ bool get_item(const FwdParams& p, int nblk, int r, It
   it.nkvB = it.hasB ? 2 * it.blk + 2 : 0;
   it.nkv = it.hasB ? it.nkvB : it.nkvA;
   return true;
-}
-
-// First row in its sequence, and head, of tile x of an item; its key/value head.
-template <Pair kPair>
-__device__ __forceinline__ int tile_row(const Item& it, int x) {
-  return kPair == Pair::kSharedHeads ? it.rowA : it.rowA + x * kBM;
-}
-template <Pair kPair>
-__device__ __forceinline__ int tile_head(const Item& it, int x) {
-  return kPair == Pair::kSharedHeads ? it.h + x : it.h;
-}
-template <Pair kPair>
-__device__ __forceinline__ int kv_head(const FwdParams& p, const Item& it) {
-  return kPair == Pair::kRows ? it.h : it.h / p.pb.group;
 }
 
 }  // namespace fwd
@@ -178,7 +135,7 @@ __device__ __forceinline__ int kv_head(const FwdParams& p, const Item& it) {
 // e.g. by the QKV projection's epilogue).  Separate instantiations, so that
 // each compiles only its own epilogue (registers are tight in the softmax
 // warps).
-template <bool kRotateK, bool kRotateQ, Pair kPair = Pair::kRows>
+template <bool kRotateK, bool kRotateQ>
 __global__ void __launch_bounds__(fwd::kThreads, 1)
     ne_attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
@@ -194,11 +151,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
 
   const int G = gridDim.x;
   const int cta = blockIdx.x;
-  static_assert(kPair == Pair::kRows || (!kRotateK && !kRotateQ),
-                "shared heads: operands rotated beforehand");
-  constexpr bool kEpilogueWarps = kPair != Pair::kRows;
-  const int n_items =
-      nblk * p.pb.nseq * (kPair == Pair::kSharedHeads ? p.pb.H / 2 : p.pb.H);
+  const int n_items = nblk * p.pb.nseq * p.pb.H;
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
 
@@ -228,8 +181,6 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
     }
     mbar_init(&bars[B_MMA_DONE], 1);
     mbar_init(&bars[B_MMA_DONE + 1], 1);
-    if constexpr (kEpilogueWarps)
-      for (int x = 0; x < 2; ++x) mbar_init(&bars[B_SUM_FULL + x], 128);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -242,21 +193,16 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // whatever the stream ran before (e.g. the kernel that wrote q, k, v) has completed
-  // (Not with shared heads: the next rotation pass, launched early, would take
-  // the place of this grid's last CTAs -- and this grid's CTAs, an SM each, that
-  // of the pass's: neither triggers early there, 32 packed prompts 90 -> 70 us.)
-  if constexpr (!kEpilogueWarps) pdl_launch_dependents();
+  pdl_launch_dependents();
 
   uint8_t* sQ = smem + OFF_Q;  // buffer b: Q_A at 2b tiles, Q_B at 2b + 1
   uint8_t* sK = smem + OFF_K;
   uint8_t* sV = smem + OFF_V;
   // The items of this CTA, in order (the same sequence in every role).
-  // (With epilogue warps the next item's index is fetched an item ahead.)
-  auto deal = [&](int k) { return dealt_item(nullptr, p.compact, k, cta, G, n_items); };
 #define NE_FOR_EACH_ITEM(it)                                                        \
-  for (int k_ = 0, r_ = deal(0), rn_ = kEpilogueWarps ? deal(1) : 0; r_ < n_items;              \
-       ++k_, r_ = kEpilogueWarps ? rn_ : deal(k_), rn_ = kEpilogueWarps ? deal(k_ + 1) : 0)        \
-    if (Item it; get_item<kPair>(p, nblk, r_, it, threadIdx.x == 0))
+  for (int k_ = 0, r_ = dealt_item(nullptr, p.compact, 0, cta, G, n_items); r_ < n_items;       \
+       ++k_, r_ = dealt_item(nullptr, p.compact, k_, cta, G, n_items))                             \
+    if (Item it; get_item(p, nblk, r_, it, threadIdx.x == 0))
 
   if (warp == 13 || warp == 14) {
     // ------------------------------------ TMA producers: warp 13 K, warp 14 V
@@ -284,11 +230,10 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
           mbar_arrive_expect_tx(&bars[B_Q_FULL + b], 2 * kTileBytes);
           tma_load_3d(sQ + 2 * b * kTileBytes, &tmQ, &bars[B_Q_FULL + b], 0, it.h,
                       it.start + it.rowA);
-          tma_load_3d(sQ + (2 * b + 1) * kTileBytes, &tmQ, &bars[B_Q_FULL + b], 0,
-                      tile_head<kPair>(it, 1), it.start + tile_row<kPair>(it, 1));
+          tma_load_3d(sQ + (2 * b + 1) * kTileBytes, &tmQ, &bars[B_Q_FULL + b], 0, it.h,
+                      it.start + it.rowA + kBM);
           ++nq;
         }
-        const int hk = kv_head<kPair>(p, it);
         for (int j = 0; j < it.nkv; ++j, ++g) {
           const int s = g % kStages;
           if (g >= kStages &&
@@ -298,7 +243,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(&full[s], kTileBytes);
-          tma_load_3d(ring + s * kTileBytes, tm, &full[s], 0, hk, it.start + j * kBN);
+          tma_load_3d(ring + s * kTileBytes, tm, &full[s], 0, it.h, it.start + j * kBN);
         }
       }
       if (!ok || *abort_flag) {
@@ -339,10 +284,9 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
           if (x == 1 && !it.hasB) continue;
           if (!(ok = mbar_wait(&bars[B_OST_FULL + x], nst[x] & 1, abort_flag, p.status, 16))) break;
           ++nst[x];
-          const int row0 = tile_row<kPair>(it, x);
+          const int row0 = it.rowA + x * kBM;
           if (!p.out_f32 && row0 + kBM <= it.len)
-            tma_store_3d(&tmO, sQ + (2 * b + x) * kTileBytes, 0, tile_head<kPair>(it, x),
-                         it.start + row0);
+            tma_store_3d(&tmO, sQ + (2 * b + x) * kTileBytes, 0, it.h, it.start + row0);
         }
         if (!ok) break;
         bulk_commit_group();
@@ -377,8 +321,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
       const int b = nq & 1;
       const int g0 = g;
       if (isS) {
-        ok = mbar_wait_warp(&bars[(kEpilogueWarps ? B_Q_FULL : B_Q_ROT) + b], (nq >> 1) & 1,
-                            abort_flag, p.status, 2);
+        ok = mbar_wait_warp(&bars[B_Q_ROT + b], (nq >> 1) & 1, abort_flag, p.status, 2);
         for (int j = 0; ok && j < it.nkv; ++j) {
           const int gj = g0 + j, s = gj % kStages;
           if (!mbar_wait_warp(&bars[(kRotateK ? B_K_ROT : B_K_FULL) + s], (gj / kStages) & 1,
@@ -465,60 +408,6 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
     while (!mbar_try_wait(done, 0) && clock64() - t0 < NE_WAIT_LIMIT_CYCLES) {
     }
     __syncwarp();
-  } else if (kEpilogueWarps && warp >= 8) {
-    // -------------------------------------------------------- epilogue warps
-    regs_decrease<kRegsRotate>();
-    const int wq = warp & 3;
-    const int r = wq * 32 + lane;  // row in tile
-    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-    const float* sums = reinterpret_cast<const float*>(smem + OFF_SUM);
-    bool ok = true;
-    int nq = 0, nit[2] = {0, 0};
-    NE_FOR_EACH_ITEM(it) {
-      if (!ok) break;
-#pragma unroll 1
-      for (int x = 0; x < 2 && ok; ++x) {
-        if (x == 1 && !it.hasB) continue;
-        const int ph = nit[x] & 1;
-        if (!(ok = mbar_wait_warp(&bars[B_SUM_FULL + x], ph, abort_flag, p.status, 17) &&
-                   mbar_wait_warp(&bars[B_O_FINAL + x], ph, abort_flag, p.status, 11)))
-          break;
-        ++nit[x];
-        tc_fence_after();
-        const float inv_l = 1.f / sums[x * 128 + r];
-        uint32_t o[64];
-        const uint32_t tO = tmem + lane_base + kColO + 64 * x;
-        tmem_ld_x32(tO, o);
-        tmem_ld_x32(tO + 32, o + 32);
-        tmem_ld_wait(o);
-        tmem_ld_wait(o + 32);
-        tc_fence_before();
-        mbar_arrive(&bars[B_O_FREE + x]);  // O_X and the sums may be overwritten
-        const int row = tile_row<kPair>(it, x) + r;
-        // A whole tile goes into the swizzled Q slot of this tile, and warp 14,
-        // lane 1 stores it with TMA; a partial one is written a row per thread.
-        const bool whole = tile_row<kPair>(it, x) + kBM <= it.len;
-        uint8_t* slot = sQ + (2 * (nq & 1) + x) * kTileBytes;
-        uint4* dst = reinterpret_cast<uint4*>(
-            static_cast<__nv_bfloat16*>(p.out) +
-            (static_cast<long long>(it.start + row) * p.pb.H + tile_head<kPair>(it, x)) * kHD);
-#pragma unroll
-        for (int cc = 0; cc < 8; ++cc) {
-          uint4 w;
-          w.x = pack_bf16x2(__uint_as_float(o[8 * cc + 0]) * inv_l, __uint_as_float(o[8 * cc + 1]) * inv_l);
-          w.y = pack_bf16x2(__uint_as_float(o[8 * cc + 2]) * inv_l, __uint_as_float(o[8 * cc + 3]) * inv_l);
-          w.z = pack_bf16x2(__uint_as_float(o[8 * cc + 4]) * inv_l, __uint_as_float(o[8 * cc + 5]) * inv_l);
-          w.w = pack_bf16x2(__uint_as_float(o[8 * cc + 6]) * inv_l, __uint_as_float(o[8 * cc + 7]) * inv_l);
-          if (whole)
-            *reinterpret_cast<uint4*>(slot + sw128_offset(r, cc)) = w;
-          else if (row < it.len)
-            dst[cc] = w;
-        }
-        if (whole) fence_proxy_async_smem();
-        mbar_arrive(&bars[B_OST_FULL + x]);
-      }
-      ++nq;
-    }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ RoPE warps
     regs_decrease<kRegsRotate>();
@@ -571,13 +460,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
       const int nkv_x = x ? it.nkvB : it.nkvA;
       if constexpr (!kRotateK) ++nq;
       if (nkv_x == 0) continue;  // tile B outside the sequence
-      const int diag =
-          kPair == Pair::kSharedHeads ? it.blk : (x ? 2 * it.blk + 1 : 2 * it.blk);
-      // Index of this row's LSE, or -1 past the sequence's end.
-      int lse_at = -1;
-      if constexpr (kEpilogueWarps)
-        if (tile_row<kPair>(it, x) + r < it.len)
-          lse_at = tile_head<kPair>(it, x) * p.pb.n_tot + it.start + tile_row<kPair>(it, x) + r;
+      const int diag = x ? 2 * it.blk + 1 : 2 * it.blk;
       float m_ref = 0.f;  // reference max (log2 units) the P values are taken against
       float l_sum = 0.f;
       for (int j = 0; j < nkv_x; ++j) {
@@ -639,12 +522,12 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
         // P_X and O_X are in use by the P V of the previous tile until it
         // completes (waited every tile, so PV_DONE is never two phases behind;
         // at an item's first tile the previous item's epilogue has already
-        // seen its last P V complete, unless it runs in warps of its own).
-        if (j > 0 || (kEpilogueWarps && c > 0)) {
+        // seen its last P V complete).
+        if (j > 0) {
           if (!(ok = mbar_wait_warp(&bars[B_PV_DONE + x], (c - 1) & 1, abort_flag, p.status, 9)))
             break;
           tc_fence_after();
-          if ((!kEpilogueWarps || j > 0) && __any_sync(0xffffffffu, grow)) {
+          if (__any_sync(0xffffffffu, grow)) {
             uint32_t o[32];
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
@@ -666,18 +549,6 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
       }
       if (!ok) break;
       cnt += nkv_x;
-      if constexpr (kEpilogueWarps) {
-        if (lse_at >= 0) p.lse[lse_at] = (m_ref + __log2f(l_sum)) * 0.69314718055994531f;
-        // The sums' place is free once the previous item's epilogue is done
-        // with O_X (waited every item, so O_FREE is never two phases behind).
-        if (nit >= 1 && !(ok = mbar_wait_warp(&bars[B_O_FREE + x], (nit - 1) & 1, abort_flag,
-                                              p.status, 18)))
-          break;
-        reinterpret_cast<float*>(smem + OFF_SUM)[x * 128 + r] = l_sum;
-        mbar_arrive(&bars[B_SUM_FULL + x]);
-        ++nit;
-        continue;
-      }
       // ---- epilogue: O / l and LSE for rows inside the sequence -----------
       if (!(ok = mbar_wait_warp(&bars[B_O_FINAL + x], nit & 1, abort_flag, p.status, 11))) break;
       ++nit;
@@ -685,9 +556,8 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
       // index, so that none of it stays live (in registers or spilled) through
       // the loop above.
       Item e;
-      get_item<kPair>(p, nblk, opaque_int(r_), e, false);
-      const int erow = tile_row<kPair>(e, x) + r;
-      const int eh = tile_head<kPair>(e, x);
+      get_item(p, nblk, opaque_int(r_), e, false);
+      const int erow = e.rowA + x * kBM + r;
       tc_fence_after();
       uint32_t o[64];
       tmem_ld_x32(tO, o);
@@ -700,7 +570,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
         // Every row written by its own thread.
         if (erow < e.len) {
           const float inv_l = 1.f / l_sum;
-          const long long orow = (static_cast<long long>(e.start + erow) * p.pb.H + eh) * kHD;
+          const long long orow = (static_cast<long long>(e.start + erow) * p.pb.H + e.h) * kHD;
           if (p.out_f32) {
             float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow);
 #pragma unroll
@@ -722,12 +592,12 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
             }
           }
           // LSE in natural-log units: (m_ref + log2 l) * ln 2.
-          p.lse[lse_index(p.pb, eh, e.seq, e.start, erow)] =
+          p.lse[lse_index(p.pb, e.h, e.seq, e.start, erow)] =
               (m_ref + __log2f(l_sum)) * 0.69314718055994531f;
         }
       } else {
         const float inv_l = 1.f / l_sum;
-        const long long orow = (static_cast<long long>(e.start + erow) * p.pb.H + eh) * kHD;
+        const long long orow = (static_cast<long long>(e.start + erow) * p.pb.H + e.h) * kHD;
         if (p.out_f32) {
           if (erow < e.len) {
             float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow);
@@ -743,7 +613,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
           // tile (item nq - 1's buffer), and warp 14, lane 1 stores it with
           // TMA; the sequence's last, partial tile is written one row per
           // thread.
-          const bool whole = tile_row<kPair>(e, x) + kBM <= e.len;
+          const bool whole = e.rowA + x * kBM + kBM <= e.len;
           uint8_t* slot = sQ + (2 * (opaque_int(nq - 1) & 1) + x) * kTileBytes;
           uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow);
 #pragma unroll
@@ -763,7 +633,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
         mbar_arrive(&bars[B_OST_FULL + x]);
         // LSE in natural-log units: (m_ref + log2 l) * ln 2.
         if (erow < e.len)
-          p.lse[lse_index(p.pb, eh, e.seq, e.start, erow)] =
+          p.lse[lse_index(p.pb, e.h, e.seq, e.start, erow)] =
               (m_ref + __log2f(l_sum)) * 0.69314718055994531f;
       }
     }
@@ -845,125 +715,9 @@ cudaError_t launch_rope_rows(const __nv_bfloat16* x0, __nv_bfloat16* xr0,
                     xr1, pb, rope);
 }
 
-// ---------------------------------------------------------------------------
-// Rotation pass with shared key/value heads: q' = R(m) q over H heads and k' =
-// R(n) k over H / group, with the rule above, and, by the last CTA, the
-// attention kernel's work list.  The CTAs take the packed rows in equal blocks
-// (not sequence by sequence, whose lengths differ: a grid of the longest
-// sequence times nseq had half its CTAs empty on a batch of 64 to 2048 rows),
-// so the sequence of a row is searched, once per row and CTA, while the first
-// loads are in flight.  Rows of no sequence, or of one with bad bounds (the
-// attention kernel reports it), are left alone.
-//
-// Four lanes take a (row, head), as above; a CTA's (row, head) pairs -- the
-// keys' heads behind the queries' -- go round its 64 quads, each quad moving
-// on by 64 pairs with an addition (a division per pair was a third of the
-// instructions).
-// ---------------------------------------------------------------------------
-constexpr int kGqaItems = 2;   // pairs of a quad in flight
-constexpr int kGqaRounds = 1;  // rounds of a CTA, about
-
-__global__ void __launch_bounds__(kRopeThreads)
-    ne_attn_gqa_rotate_kernel(const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ qr,
-                              const __nv_bfloat16* __restrict__ k, __nv_bfloat16* __restrict__ kr,
-                              const Problem pb, RopeTable rope, int rows_per_cta,
-                              const ItemList list) {
-  extern __shared__ int dyn[];  // the list's buckets, or the rows' positions
-  pdl_wait();                   // the kernel that wrote q, k (and anything before it) has completed
-  if (blockIdx.x == 0 && list.out) {
-    build_items(pb, list, dyn);
-    return;
-  }
-  constexpr int kQuads = kRopeThreads / kRopeParts;
-  const int row0 = (static_cast<int>(blockIdx.x) - (list.out ? 1 : 0)) * rows_per_cta;
-  const int rows = min(rows_per_cta, pb.n_tot - row0);
-  const int H = pb.H, Hkv = pb.H / pb.group, heads = H + Hkv;
-  q += static_cast<long long>(row0) * H * kHD;
-  qr += static_cast<long long>(row0) * H * kHD;
-  k += static_cast<long long>(row0) * Hkv * kHD;
-  kr += static_cast<long long>(row0) * Hkv * kHD;
-  const int c = threadIdx.x % kRopeParts;
-  const int row_step = kQuads / heads, head_step = kQuads - row_step * heads;
-  int row = (threadIdx.x / kRopeParts) / heads;
-  int head = threadIdx.x / kRopeParts - row * heads;
-  bool first = true;
-  while (true) {
-    uint4 lo[kGqaItems], hi[kGqaItems];
-    int rr[kGqaItems], off[kGqaItems];  // the pairs' rows, and offsets in 16-byte units
-    bool is_k[kGqaItems];
-#pragma unroll
-    for (int u = 0; u < kGqaItems; ++u) {
-      rr[u] = row;
-      is_k[u] = head >= H;
-      const int r = min(row, rows - 1);  // a quad past the last row reads that one, discarded
-      off[u] = (is_k[u] ? r * Hkv + (head - H) : r * H + head) * (kHD / 8) + c;
-      const uint4* src = reinterpret_cast<const uint4*>(is_k[u] ? k : q) + off[u];
-      lo[u] = __ldg(src);
-      hi[u] = __ldg(src + 4);
-      row += row_step;
-      head += head_step;
-      if (head >= heads) {
-        head -= heads;
-        ++row;
-      }
-    }
-    if (first) {
-      first = false;
-      for (int r = threadIdx.x; r < rows; r += kRopeThreads) {
-        const int s = find_sequence(pb.cu_seqlens, pb.nseq, row0 + r);
-        int start = 0, len = 0;
-        dyn[r] = s >= 0 && seq_bounds(pb, s, start, len, nullptr) ? row0 + r - start : -1;
-      }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int u = 0; u < kGqaItems; ++u) {
-      if (rr[u] >= rows) return;
-      const int pos = dyn[rr[u]];
-      if (pos < 0) continue;
-      const float4* cs =
-          reinterpret_cast<const float4*>(rope.cs + static_cast<long long>(pos) * 32 + 8 * c);
-      uint32_t wl[4] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w};
-      uint32_t wh[4] = {hi[u].x, hi[u].y, hi[u].z, hi[u].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 t = __ldg(cs + j);  // (cos, sin) of dims 8c + 2j and 8c + 2j + 1
-        const float a0 = bf16lo_to_f32(wl[j]), a1 = bf16hi_to_f32(wl[j]);
-        const float b0 = bf16lo_to_f32(wh[j]), b1 = bf16hi_to_f32(wh[j]);
-        const float lo0 = __fmaf_rn(a0, t.x, -__fmul_rn(b0, t.y));
-        const float hi0 = __fmaf_rn(b0, t.x, __fmul_rn(a0, t.y));
-        const float lo1 = __fmaf_rn(a1, t.z, -__fmul_rn(b1, t.w));
-        const float hi1 = __fmaf_rn(b1, t.z, __fmul_rn(a1, t.w));
-        wl[j] = pack_bf16x2(lo0, lo1);
-        wh[j] = pack_bf16x2(hi0, hi1);
-      }
-      uint4* dst = reinterpret_cast<uint4*>(is_k[u] ? kr : qr) + off[u];
-      dst[0] = make_uint4(wl[0], wl[1], wl[2], wl[3]);
-      dst[4] = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-    }
-  }
-}
-
-cudaError_t launch_gqa_rotate(const __nv_bfloat16* q, __nv_bfloat16* qr, const __nv_bfloat16* k,
-                              __nv_bfloat16* kr, const Problem& pb, const RopeTable& rope,
-                              const ItemList& list, cudaStream_t stream) {
-  const int heads = pb.H + pb.H / pb.group;
-  const int rows = std::max(1, kGqaRounds * kGqaItems * kRopeThreads / kRopeParts / heads);
-  const int ctas = (pb.n_tot + rows - 1) / rows + (list.out ? 1 : 0);
-  const size_t smem = sizeof(int) * std::max(rows, list.out ? list.n_buckets : 0);
-  return launch_pdl(ne_attn_gqa_rotate_kernel, dim3(ctas), dim3(kRopeThreads), smem, stream, q, qr,
-                    k, kr, pb, rope, rows, list);
-}
-
-// Blocks of the longest sequence that a launch enumerates, and heads (or head
-// pairs) per sequence.
-int fwd_blocks(Pair pair, int n_qtiles) {
-  return pair == Pair::kSharedHeads ? n_qtiles : (n_qtiles + 1) / 2;
-}
-
 cudaError_t launch_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        const CUtensorMap& tmO, const FwdParams& p, int n_qtiles,
-                       cudaStream_t stream, Pair pair) {
+                       cudaStream_t stream) {
   static bool attr_set = false;
   if (!attr_set) {
     cudaError_t e = cudaFuncSetAttribute(ne_attn_fwd_kernel<true, true>,
@@ -974,12 +728,6 @@ cudaError_t launch_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
                                cudaFuncAttributeMaxDynamicSharedMemorySize, fwd::SMEM_BYTES);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(ne_attn_fwd_kernel<false, false>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, fwd::SMEM_BYTES);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(ne_attn_fwd_kernel<false, false, Pair::kSharedRows>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, fwd::SMEM_BYTES);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(ne_attn_fwd_kernel<false, false, Pair::kSharedHeads>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, fwd::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     attr_set = true;
@@ -994,16 +742,9 @@ cudaError_t launch_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
     e = cudaDeviceGetAttribute(&sm_count[dev], cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
   }
-  const int nblk = fwd_blocks(pair, n_qtiles);
-  const long long n_items = static_cast<long long>(nblk) * p.pb.nseq *
-                            (pair == Pair::kSharedHeads ? p.pb.H / 2 : p.pb.H);
+  const int nblk = (n_qtiles + 1) / 2;
+  const long long n_items = static_cast<long long>(nblk) * p.pb.nseq * p.pb.H;
   const int G = static_cast<int>(n_items < sm_count[dev] ? n_items : sm_count[dev]);
-  if (pair == Pair::kSharedRows)
-    return launch_pdl(ne_attn_fwd_kernel<false, false, Pair::kSharedRows>, dim3(G),
-                      dim3(fwd::kThreads), fwd::SMEM_BYTES, stream, tmQ, tmK, tmV, tmO, p, nblk);
-  if (pair == Pair::kSharedHeads)
-    return launch_pdl(ne_attn_fwd_kernel<false, false, Pair::kSharedHeads>, dim3(G),
-                      dim3(fwd::kThreads), fwd::SMEM_BYTES, stream, tmQ, tmK, tmV, tmO, p, nblk);
   if (p.rotate_k)
     return launch_pdl(ne_attn_fwd_kernel<true, true>, dim3(G), dim3(fwd::kThreads),
                       fwd::SMEM_BYTES, stream, tmQ, tmK, tmV, tmO, p, nblk);

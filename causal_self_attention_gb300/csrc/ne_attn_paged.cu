@@ -48,6 +48,8 @@
 // Keys of a tile past the sequence's end (what the page holds there, or an
 // older tile's bytes) get the score -inf, and their value rows are cleared in
 // shared memory, as 0 * NaN would show.
+#include <algorithm>
+
 #include "ne_paged.cuh"
 #include "ne_sm100.cuh"
 
@@ -82,7 +84,8 @@ struct Cfg {
   static constexpr int OFF_Q = OFF_RED + kWarps * kRows * kRedRow * 4;
   static constexpr int kQBytes = kRows * kQRow + 256;    // q rows, one row of the RoPE table
   static constexpr int OFF_PREFIX = OFF_Q + kQSlots * kQBytes;
-  static constexpr int OFF_BAR = OFF_PREFIX + (kMaxBatch + 2) * 4;
+  static constexpr int OFF_LEN = OFF_PREFIX + (kMaxBatch + 2) * 4;
+  static constexpr int OFF_BAR = OFF_LEN + kMaxBatch * 4;
   static constexpr int BYTES = OFF_BAR + 2 * (kStages + kQSlots) * 8 + kStages * 4 + 16 + 1024;
 };
 
@@ -104,18 +107,24 @@ struct Params {
 
 // The part of one unit -- (sequence, cached head, row tile) -- in a range.
 struct Segment {
-  int b, j;       // sequence; unit of the sequence (cached head * row_tiles + row tile)
-  int t0, t1;     // its tiles (t0 >= t1: none, only overhead falls into the range)
-  int n_tiles;    // of the whole unit
-  long long at;   // the flat position of the unit's first tile
-  long long next; // the flat position behind the segment
+  int b, j;     // sequence; unit of the sequence (cached head * row_tiles + row tile)
+  int t0, t1;   // its tiles (t0 >= t1: none, only overhead falls into the range)
+  int n_tiles;  // of the whole unit
+  int at;       // the flat position of the unit's first tile
+  int next;     // the flat position behind the segment
 };
 
 // The flat order: sequence b's units start at prefix[b] * J, unit j's at + j *
-// cost(b), cost(b) = kOverhead + its tiles, the overhead first.
-__device__ __forceinline__ Segment segment_at(const int* prefix, int B, int J, long long x,
-                                              long long end) {
-  const int y = static_cast<int>(x / J);
+// cost(b), cost(b) = kOverhead + its tiles, the overhead first.  (Positions are
+// below 2^31: the launch sees to it.)
+__device__ __forceinline__ void clip_segment(Segment& s, int unit, int x, int end) {
+  s.at = unit + kOverhead;
+  s.next = min(s.at + s.n_tiles, end);
+  s.t0 = max(x - s.at, 0);
+  s.t1 = max(s.next - s.at, 0);
+}
+__device__ __forceinline__ Segment first_segment(const int* prefix, int B, int J, int x, int end) {
+  const int y = x / J;
   int lo = 0, hi = B;  // prefix[lo] <= y < prefix[hi]: the last such lo has tiles
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -123,16 +132,20 @@ __device__ __forceinline__ Segment segment_at(const int* prefix, int B, int J, l
   }
   Segment s;
   s.b = lo;
-  const int cost = prefix[lo + 1] - prefix[lo];
-  const long long first = static_cast<long long>(prefix[lo]) * J;
-  s.j = static_cast<int>((x - first) / cost);
-  const long long unit = first + static_cast<long long>(s.j) * cost;
+  const int cost = prefix[lo + 1] - prefix[lo], first = prefix[lo] * J;
+  s.j = (x - first) / cost;
   s.n_tiles = cost - kOverhead;
-  s.at = unit + kOverhead;
-  s.next = unit + cost < end ? unit + cost : end;
-  s.t0 = x > s.at ? static_cast<int>(x - s.at) : 0;
-  s.t1 = s.next > s.at ? static_cast<int>(s.next - s.at) : 0;
+  clip_segment(s, first + s.j * cost, x, end);
   return s;
+}
+// The segment that starts where s ends (s.next < end).
+__device__ __forceinline__ void next_segment(Segment& s, const int* prefix, int J, int end) {
+  if (++s.j == J) {
+    s.j = 0;
+    do ++s.b; while (prefix[s.b + 1] == prefix[s.b]);
+    s.n_tiles = prefix[s.b + 1] - prefix[s.b] - kOverhead;
+  }
+  clip_segment(s, s.next, s.next, end);
 }
 
 // D += A * B, m16n8k16, fp32 accumulators; A row-major, B column-major.
@@ -200,6 +213,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   int* prefix = reinterpret_cast<int*>(smem + L::OFF_PREFIX);
+  int* lens = reinterpret_cast<int*>(smem + L::OFF_LEN);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* empty = full + kStages;
   uint64_t* qfull = empty + kStages;
@@ -230,6 +244,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
     const int n = __ldg(p.seq_lens + b);
     const bool ok = n >= 0 && n <= p.pc.max_seqlen;
     if (!ok && blockIdx.x == 0) atomicCAS(p.status, 0, NE_DEV_BAD_SEQLEN);
+    lens[b] = n;
     prefix[b + 1] = ok && n > 0 ? (n + T::kTile - 1) / T::kTile + kOverhead : 0;
   }
   __syncthreads();
@@ -259,15 +274,15 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
       for (int i = tid; i < p.H * (kHD / 2); i += kThreads) o[i] = 0u;
       for (int i = tid; i < p.H; i += kThreads) p.lse[static_cast<long long>(b) * p.H + i] = -INFINITY;
     }
-  const long long total = static_cast<long long>(prefix[B]) * J;
-  const long long most = static_cast<long long>(prefix[kMaxBatch + 1]) * J * kMaxParts;
-  long long W = gridDim.x;
-  W = W < total ? W : total;
-  W = W < most ? W : most;
-  W = W < (total + 1) / 2 ? W : (total + 1) / 2;  // two tiles of work at the least
-  const long long w = blockIdx.x;
-  if (w >= W) return;
-  const long long x0 = total * w / W, x1 = total * (w + 1) / W;
+  // Equal ranges, of two tiles of work at the least, and at most about kMaxParts
+  // to a unit.
+  const int total = prefix[B] * J;
+  int W = static_cast<int>(gridDim.x);
+  if (total / kMaxParts < W) W = min(W, max(1, prefix[kMaxBatch + 1] * J) * kMaxParts);
+  const int range = max((total + W - 1) / W, 2);
+  const int w = blockIdx.x;
+  const int x0 = w * range, x1 = min(x0 + range, total);
+  if (x0 >= total) return;
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ the loads
@@ -281,13 +296,14 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
     const int box = page_size < T::kTile ? page_size : T::kTile;  // keys per copy
     bool ok = true;
     int g = 0, nq = 0;  // tiles, segments loaded
-    for (long long x = x0; ok && x < x1;) {
-      const Segment s = segment_at(prefix, B, J, x, x1);
-      x = s.next;
-      if (s.t0 >= s.t1) continue;
+    for (Segment s = first_segment(prefix, B, J, x0, x1);; next_segment(s, prefix, J, x1)) {
+      if (s.t0 >= s.t1) {
+        if (s.next >= x1) break;
+        continue;
+      }
       const int hk = s.j / p.row_tiles, h0 = hk * p.group + (s.j - hk * p.row_tiles) * kRows;
       const int rows = min(kRows, (hk + 1) * p.group - h0);
-      const int n = __ldg(p.seq_lens + s.b);
+      const int n = lens[s.b];
       const int pages = (n + page_size - 1) >> p.pc.page_shift;
       const int* table = p.pc.block_table + static_cast<long long>(s.b) * p.pc.max_pages;
       int have = (s.t0 * T::kTile) >> p.pc.page_shift;  // lane i holds the entry of page have + i
@@ -355,6 +371,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
         }
         __syncwarp();
       }
+      if (!ok || s.next >= x1) break;
     }
     // After an abort, the copies in flight land before the CTA exits (on the
     // normal path the consumers have waited for them).
@@ -379,11 +396,14 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
   const int r = lane >> 2, c = lane & 3;
   bool ok = true;
   int g = 0, nq = 0;
-  for (long long x = x0; x < x1;) {
-    const Segment s = segment_at(prefix, B, J, x, x1);
-    x = s.next;
+  Segment s = first_segment(prefix, B, J, x0, x1);
+  for (bool begun = false;; begun = true) {
+    if (begun) {
+      if (s.next >= x1) break;
+      next_segment(s, prefix, J, x1);
+    }
     if (s.t0 >= s.t1) continue;
-    const int n = __ldg(p.seq_lens + s.b);
+    const int n = lens[s.b];
     const int hk = s.j / p.row_tiles, h0 = hk * p.group + (s.j - hk * p.row_tiles) * kRows;
     const int rows = min(kRows, (hk + 1) * p.group - h0);  // query heads of this unit
 
@@ -703,9 +723,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
       }
     if (!named_bar_and(1, kWarps * 32, ok)) break;
     const bool whole = s.t0 == 0 && s.t1 == s.n_tiles;
-    // Workers of this unit: the first takes its slot 1, the others slot 0.
-    const int w_first = static_cast<int>(((s.at + 1) * W - 1) / total);  // holds its first tile
-    const int w_last = static_cast<int>(((s.at + s.n_tiles) * W - 1) / total);
+    // Of the workers of a unit the first takes its slot 1, the others slot 0.
     float* part = p.part + (static_cast<long long>(w) * 2 + (s.t0 == 0 ? 1 : 0)) * kRows * kPartRow;
     // Eight threads a row, 8 dims each.
     for (int row = tid >> 3; row < rows; row += kWarps * 4) {
@@ -752,14 +770,15 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
       named_bar_sync(1, kWarps * 32);  // red is free again
       continue;
     }
-    __threadfence();
+    const int w_first = s.at / range, w_last = (s.at + s.n_tiles - 1) / range;
+    const int n_parts = w_last - w_first + 1;
     named_bar_sync(1, kWarps * 32);
     if (tid == 0) {
-      const int n_parts = w_last - w_first + 1;
+      __threadfence();  // the CTA's part (ordered before this by the barrier), then the arrival
       const bool last = atomicAdd(p.arrived + w_first, 1) == n_parts - 1;
       if (last) p.arrived[w_first] = 0;  // as the next launch wants it
       *last_flag = last;
-      __threadfence();
+      __threadfence();  // and the other parts after it
     }
     named_bar_sync(1, kWarps * 32);
     if (!*last_flag) continue;
@@ -768,7 +787,6 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
     // groups, and group i takes the parts 8 i .. 8 i + 7, then those 8 groups on
     // (one row's parts in flight at once: a part's latency, not its bytes, is
     // what joining costs).  The order of every sum is fixed by the split.
-    const int n_parts = w_last - w_first + 1;
     const int row_slots = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
     const int groups = kWarps * 4 / row_slots;
     const int group = (tid >> 3) / row_slots, row = (tid >> 3) % row_slots;
@@ -883,6 +901,15 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p
 }
 }  // namespace
 
+// Sequences that a launch takes: what its shared memory holds, and so many that
+// their tiles and overheads are numbered in 31 bits (0: not one).
+int paged_batch(int H, int Hkv, int max_seqlen) {
+  const int rows = paged_rows(H, Hkv), tile = Tile<false>::kTile;  // the smaller tile
+  const long long J = static_cast<long long>(Hkv) * ((H / Hkv + rows - 1) / rows);
+  const long long one = J * ((max_seqlen + tile - 1) / tile + kOverhead);
+  return static_cast<int>(std::min<long long>(kMaxBatch, ((1LL << 31) - (1 << 25)) / one));
+}
+
 constexpr int kPagedSms = 160;  // an upper bound on the part's SMs (152), for the workspace's size
 
 size_t paged_part_bytes(int B, int H, int Hkv, int max_seqlen) {
@@ -916,8 +943,9 @@ cudaError_t launch_decode_paged(const CUtensorMap& tmK, const CUtensorMap& tmV,
   p.part = part;
   p.arrived = arrived;
   p.status = status;
-  for (int b0 = 0; b0 < B; b0 += kMaxBatch) {
-    p.B = B - b0 < kMaxBatch ? B - b0 : kMaxBatch;
+  const int batch = paged_batch(H, pc.Hkv, pc.max_seqlen);
+  for (int b0 = 0; b0 < B; b0 += batch) {
+    p.B = B - b0 < batch ? B - b0 : batch;
     p.q = q + static_cast<long long>(b0) * H * kHD;
     p.seq_lens = seq_lens + b0;
     p.pc.block_table = pc.block_table + static_cast<long long>(b0) * pc.max_pages;

@@ -66,14 +66,6 @@ struct PagedCache {
   int max_seqlen;  // every position is below this (<= max_pages pages)
 };
 
-// How the two query tiles of a forward work item relate (template parameter of
-// the forward kernel).
-enum class Pair {
-  kRows,        // consecutive 128-row tiles of one head, one key/value head per query head
-  kSharedRows,  // the same, key/value heads shared by pb.group query heads
-  kSharedHeads  // one 128-row tile of two neighbouring query heads of a group
-};
-
 struct FwdParams {
   Problem pb;
   void* out;         // bf16 or fp32 [N_tot, H, 64]

@@ -14,41 +14,51 @@
 namespace ne {
 
 enum class Items {
-  kRowPairs,   // forward: block n_blocks - 1 - i of 256 rows, steps = key tiles of its last tile
-  kHeadPairs,  // forward: block n_blocks - 1 - i of 128 rows, steps = its key tiles
+  kHeadPairs,  // forward: 128-row block n_blocks - 1 - i of two heads, steps = its key tiles
   kKeyTiles    // backward: key tile i, steps = query tiles from it to its sequence's end
 };
 
+// Items are numbered block * nseq * n_heads + sequence * n_heads + head; a
+// forward's second kind (odd heads: 256-row block n_blocks2 - 1 - i of one head,
+// steps = key tiles of its last row tile) follows from `second` on.
 struct ItemList {
-  Items kind = Items::kRowPairs;
+  Items kind = Items::kKeyTiles;
   int n_blocks = 0;   // blocks (key tiles) of the longest sequence
-  int n_heads = 0;    // heads, head pairs, or units per sequence and key tile
+  int n_heads = 0;    // head pairs, or units per sequence and key tile
+  int n_blocks2 = 0;
+  int n_heads2 = 0;   // odd heads (0: none)
+  int second = 0;
   int n_buckets = 0;  // the most steps an item can have, plus one
-  int* out = nullptr; // [1 + n_blocks * nseq * n_heads]: count, items; nullptr: none wanted
+  int* out = nullptr; // [1 + number of items]: count, items; nullptr: none wanted
 };
 
-// Bucket (steps) of pair i = block * nseq + sequence; 0: bad bounds, -1: empty.
-__device__ __forceinline__ int pair_bucket(const Problem& pb, const ItemList& l, int i) {
+// Bucket (steps) of pair i = block * nseq + sequence, the second kind's behind
+// the first's n1; 0: bad bounds, -1: empty.
+__device__ __forceinline__ int pair_bucket(const Problem& pb, const ItemList& l, int i, int n1) {
+  const bool two = i >= n1;
+  if (two) i -= n1;
   const int blk = i / pb.nseq, seq = i - blk * pb.nseq;
   int start, len;
   if (!seq_bounds(pb, seq, start, len, nullptr)) return 0;
-  const int b = l.kind == Items::kKeyTiles ? blk : l.n_blocks - 1 - blk;
-  if (l.kind == Items::kRowPairs) {
+  if (two) {
+    const int b = l.n_blocks2 - 1 - blk;
     if (2 * b * kBM >= len) return -1;
     return (2 * b + 1) * kBM < len ? 2 * b + 2 : 2 * b + 1;
   }
+  const int b = l.kind == Items::kKeyTiles ? blk : l.n_blocks - 1 - blk;
   if (b * kBM >= len) return -1;
   return l.kind == Items::kHeadPairs ? b + 1 : (len + kBM - 1) / kBM - b;
 }
 
 // Every thread of the CTA calls this; bucket: n_buckets ints of shared memory.
 __device__ __forceinline__ void build_items(const Problem& pb, const ItemList& l, int* bucket) {
-  const int n = l.n_blocks * pb.nseq;
+  const int n1 = l.n_heads ? l.n_blocks * pb.nseq : 0;
+  const int n = n1 + (l.n_heads2 ? l.n_blocks2 * pb.nseq : 0);
   for (int b = threadIdx.x; b < l.n_buckets; b += blockDim.x) bucket[b] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int b = pair_bucket(pb, l, i);
-    if (b >= 0) atomicAdd(bucket + b, 1);
+    const int b = pair_bucket(pb, l, i, n1);
+    if (b >= 0) atomicAdd(bucket + b, i < n1 ? l.n_heads : l.n_heads2);
   }
   __syncthreads();
   if (threadIdx.x < 32) {  // first slots: the most steps first, bucket 0 last
@@ -66,17 +76,18 @@ __device__ __forceinline__ void build_items(const Problem& pb, const ItemList& l
       if (b >= 0) bucket[b] = at + v - c;
       at += __shfl_sync(0xffffffffu, v, 31);
     }
-    if (lane == 0) l.out[0] = at * l.n_heads;
+    if (lane == 0) l.out[0] = at;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int b = pair_bucket(pb, l, i);
+    const int b = pair_bucket(pb, l, i, n1);
     if (b < 0) continue;
-    const int slot = atomicAdd(bucket + b, 1);
-    int* dst = l.out + 1 + static_cast<long long>(slot) * l.n_heads;
+    const int heads = i < n1 ? l.n_heads : l.n_heads2;
+    const int first = i < n1 ? i * heads : l.second + (i - n1) * heads;
     // (items of equal length in no fixed order: each is computed the same way
     // by whichever CTA gets it)
-    for (int h = 0; h < l.n_heads; ++h) dst[h] = i * l.n_heads + h;
+    int* dst = l.out + 1 + atomicAdd(bucket + b, heads);
+    for (int h = 0; h < heads; ++h) dst[h] = first + h;
   }
 }
 
