@@ -1294,29 +1294,18 @@ cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
                        const CUtensorMap& tmDK, const BwdParams& p, int n_tiles,
                        cudaStream_t stream, cudaEvent_t ev_pre, cudaEvent_t ev_main,
                        const ItemList& list) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(ne_attn_bwd_kernel<false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         bwd::SMEM_BYTES);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(ne_attn_bwd_kernel<true>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, bwd::SMEM_BYTES);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(ne_attn_bwd_prep_stream_kernel<false>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               bwd::PREP_SMEM_BYTES);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(ne_attn_bwd_prep_stream_kernel<true>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               bwd::PREP_SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static bool done[4][64] = {};
+  cudaError_t e = allow_smem(ne_attn_bwd_kernel<false>, bwd::SMEM_BYTES, done[0]);
+  if (e == cudaSuccess) e = allow_smem(ne_attn_bwd_kernel<true>, bwd::SMEM_BYTES, done[1]);
+  if (e == cudaSuccess)
+    e = allow_smem(ne_attn_bwd_prep_stream_kernel<false>, bwd::PREP_SMEM_BYTES, done[2]);
+  if (e == cudaSuccess)
+    e = allow_smem(ne_attn_bwd_prep_stream_kernel<true>, bwd::PREP_SMEM_BYTES, done[3]);
+  if (e != cudaSuccess) return e;
   // One persistent CTA per SM (at most one per unit).
   static int sm_count[64] = {0};
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!sm_count[dev] &&

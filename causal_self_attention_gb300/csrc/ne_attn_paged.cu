@@ -59,7 +59,7 @@ namespace paged {
 constexpr int kWarps = 4;                      // consumers
 constexpr int kThreads = (kWarps + 1) * 32;    // and the loading warp
 constexpr int kMaxBatch = 512;                 // sequences per launch (prefix sums in shared memory)
-constexpr int kMaxParts = 128;                 // parts of one (sequence, head), about
+constexpr int kMaxParts = 96;                  // parts of one (sequence, head), about
 constexpr int kOverhead = 4;                   // tiles that a segment's start and end cost
 constexpr int kPartRow = 68;                   // floats: lse (log2 units), 3 pad, o[64]
 constexpr float kBad = INFINITY;               // lse of a part that met a page outside the pool
@@ -886,16 +886,12 @@ int paged_ctas(long long B, int H, int Hkv, int max_seqlen, bool e4m3, int sms) 
 template <bool kE4m3, int kRows>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int ctas,
                    cudaStream_t stream) {
-  static bool attr_set = false;
   constexpr int bytes = Cfg<kE4m3, kRows>::BYTES;
   static_assert(Cfg<kE4m3, kRows>::kCtas * (bytes + 1024) <= 233472,
                 "CTAs of an SM share its 228 KiB");
-  if (!attr_set) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        ne_attn_paged_kernel<kE4m3, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static bool done[64] = {};
+  const cudaError_t e = allow_smem(ne_attn_paged_kernel<kE4m3, kRows>, bytes, done);
+  if (e != cudaSuccess) return e;
   return launch_pdl(ne_attn_paged_kernel<kE4m3, kRows>, dim3(ctas), dim3(kThreads), bytes, stream,
                     tk, tv, p);
 }

@@ -148,6 +148,20 @@ __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Dynamic shared memory of up to `bytes` for `kernel` on the current device;
+// done[device] remembers that it is set (an attribute belongs to a device).
+template <typename... KArgs>
+inline cudaError_t allow_smem(void (*kernel)(KArgs...), int bytes, bool (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  done[dev] = e == cudaSuccess;
+  return e;
+}
+
 // Launch `kernel` on `stream` with programmatic stream serialization allowed,
 // so that its CTAs may start while the previous kernel on the stream drains.
 template <typename... KArgs, typename... Args>

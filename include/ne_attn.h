@@ -56,7 +56,9 @@
  *    sequence longer than max_seqlen, a pipeline wait that timed out) are
  *    recorded in a device status word read by ne_attn_get_device_status.
  *  - Nothing here calls exit, abort or traps the GPU.
- *  - Calls are thread-safe; the RoPE table cache is per device.
+ *  - Calls are thread-safe; the RoPE table cache is per device.  A workspace
+ *    belongs to one call at a time: calls (or graphs) that may run at once
+ *    need one each.
  */
 #ifndef NE_ATTN_H
 #define NE_ATTN_H
@@ -201,15 +203,15 @@ ne_status ne_attn_varlen_bwd_train(const ne_bf16* qr, const ne_bf16* kr, const n
 /* Timing hook for profilers and benchmarks.  When set (non-NULL cudaEvent_t
  * handles created by the caller on the current device), every following
  * backward call (ne_attn_bwd, ne_attn_varlen_bwd and their _rotated / _train
- * forms) records ev_after_preprocess right after its preprocess kernel and
+ * forms, ne_attn_gqa_varlen_bwd) records ev_after_preprocess right after its preprocess kernel and
  * ev_after_main right after its main kernel, on the call's stream, so the
  * three backward kernels can be timed apart.  Pass NULL, NULL to turn it off.
  * Process-wide; not for concurrent callers. */
 ne_status ne_attn_set_bwd_phase_events(void* ev_after_preprocess, void* ev_after_main);
 
 /* The same for the forward: every following forward call that runs a
- * rotation pass before its attention kernel (the _train forms; ne_attn_fwd
- * from 2048 positions on) records ev_after_rotation between the two.  NULL
+ * rotation pass before its attention kernel (the _train and gqa forms;
+ * ne_attn_fwd from 2048 positions on) records ev_after_rotation between the two.  NULL
  * turns it off. */
 ne_status ne_attn_set_fwd_phase_event(void* ev_after_rotation);
 
@@ -459,8 +461,9 @@ int ne_attn_last_device_code(void);
 const char* ne_status_string(ne_status s);
 
 /* Free the RoPE tables, the work-schedule tables and the per-stream
- * temporaries kept for every device.  Call only when no launch that may read them is still pending, and
- * before destroying a stream the library was given. */
+ * temporaries and counters kept for every device.  Call only when no launch
+ * that may use them is still pending (no graph with such a launch is replayed
+ * afterwards), and before destroying a stream the library was given. */
 void ne_attn_release(void);
 
 #ifdef __cplusplus
