@@ -535,7 +535,8 @@ ne_status run_fwd(const Shape& s, const void* q, const void* k, const void* v, f
   const size_t kr_bytes =
       (mode == Rot::kRotate && !p.rotate_k) ? static_cast<size_t>(s.n_tot) * s.H * 64 * 2 : 0;
   const size_t tmp_bytes =
-      align256(kr_bytes) + (compact ? static_cast<size_t>(n_items + 1) * sizeof(int) : 0);
+      align256(kr_bytes) + (compact ? static_cast<size_t>(n_items + 1) * sizeof(int) : 0) +
+      (s.group > 1 ? sizeof(int) : 0);
   bool own = false;
   void* tmp = nullptr;
   void* kr = nullptr;
@@ -564,6 +565,7 @@ ne_status run_fwd(const Shape& s, const void* q, const void* k, const void* v, f
   if (rc == NE_OK && s.group > 1) {
     // Shared heads: the rotation pass builds the work list too.
     items.out = list;
+    items.counter = static_cast<int*>(tmp) + (compact ? n_items + 1 : 0);
     e = ne::launch_gqa_rotate(static_cast<const __nv_bfloat16*>(q),
                               static_cast<__nv_bfloat16*>(qr_out),
                               static_cast<const __nv_bfloat16*>(k),

@@ -17,34 +17,47 @@
 //
 // * Warps 8-11, which have nothing to rotate here, are the epilogue: they wait
 //   for an item's last P V, divide by the softmax sums (through shared memory)
-//   and store O, while the softmax warps take the next item's scores.  On short
-//   prompts that is most of an item: of the ~6,500 cycles that the softmax of a
-//   single tile took from item to item, it waited ~900 for the last P V and
-//   spent ~2,000 on the epilogue and ~1,000 on looking the next item up (whose
-//   index is now fetched an item ahead).
+//   and store O, while the softmax warps take the next item's scores.
 //
-// What bounds it (clock stamps of every warp, 16384 tokens): the serial stream
-// of one softmax warp, ~2,300 cycles a tile -- scores 170, maximum 370,
-// exponentials 800-1,000 (512 at the exponential unit's rate for the warp, and
-// two warps share a sub-partition's), ~600 in waits that are long satisfied,
-// stores 110 -- with the tensor pipe 39% busy.  Sixteen softmax warps of half a
-// row each, with a vote of both halves per step, were slower (507 against 410
-// us), and so were waits and arrivals by one lane of a warp (456, 462).
+// * The items are taken from a counter, longest first, by the thread that loads
+//   K', once the loads of the item before are issued (a ring of tiles ahead of
+//   the softmax), and handed to the other roles through shared memory.  When
+//   every role looked its items up itself -- the list, the sequence's bounds,
+//   four divisions -- a softmax warp spent 2,600 cycles an item on it, and items
+//   dealt in fixed rounds left the slowest CTA 18% behind the mean (now 8%).
+//   (32 packed prompts of 64 to 2048 tokens 67.4 -> 63; which CTA computes an
+//   item does not change its results.)
+//
+// What bounds it (clock stamps, 16384 tokens): the two softmax warps of an SM
+// sub-partition, 1,970 cycles for a step of both, of which the exponential unit
+// is busy 1,024 and, with the maxima, the packed products, sums and roundings
+// issued beside them, a loop of that arithmetic alone takes 1,500 (a
+// probe with two warps a sub-partition).  The loop body is longer than the
+// innermost instruction cache, so that each branch in it costs: a wait that polls once
+// for the whole warp with a 32-bit clock as its limit, phase parity instead of a
+// test for the first step, selects for the moving reference, and registers
+// enough (192) to spill nothing took a step from 2,300 to 1,970 cycles.  Slower
+// were: one arrival a warp (a branch and a reconvergence: 421 against 361 us),
+// the maximum of a half row while the other half loads (380), the two tiles'
+// exponentials in turns (457 against 413), sixteen softmax warps of half a row
+// (507 against 410), the softmax first in the code (424 against 413).
+// 351 us for 16384 tokens, 12 heads on 2 (1,170 TFLOP/s with the pass), 56 us
+// for the packed prompts.
 //
 // Warp roles (512 threads, registers re-split per warpgroup with setmaxnreg):
-//   warps 0-3   softmax A: thread t owns row t of tile A (TMEM lane t), 176 regs
+//   warps 0-3   softmax A: thread t owns row t of tile A (TMEM lane t), 192 regs
 //   warps 4-7   softmax B: same for tile B
-//   warps 8-11  epilogue, 104 regs
+//   warps 8-11  epilogue, 80 regs
 //   warp 12     MMA: allocates TMEM; one elected lane issues S_X = Q_X K^T
-//   warp 13     TMA: lane 0 loads each item's Q_A, Q_B and the K' ring
+//   warp 13     TMA: lane 0 takes the items, loads Q_A, Q_B and the K' ring
 //   warp 14     TMA: lane 0 loads the V ring; lane 1 stores whole O tiles
-//   warp 15     MMA: one elected lane issues O_X += P_X V; warps 12-15 at 56 regs
+//   warp 15     MMA: one elected lane issues O_X += P_X V; warps 12-15 at 48 regs
 // TMEM columns: S_A 0-127, S_B 128-255, O_A 256-319, O_B 320-383,
 // P_A 384-447, P_B 448-511 (bf16 pairs: P is the TMEM A operand of P V).
 //
 // Barrier phases: the K and V rings count key tiles over all items of the CTA;
 // S_* / P_FULL / PV_DONE of tile X count the steps of tile X over all items;
-// Q_* (per Q buffer), SUM_FULL, O_* count items.
+// Q_* (per Q buffer), IT_* (per slot), SUM_FULL, O_* count items.
 #include <algorithm>
 
 #include "ne_items.cuh"
@@ -56,16 +69,19 @@ namespace gqa {
 
 constexpr int kThreads = 512;
 // Registers per thread of each warpgroup after setmaxnreg (launch: 128).
-constexpr uint32_t kRegsSoftmax = 176, kRegsEpilogue = 104, kRegsOther = 56;
+constexpr uint32_t kRegsSoftmax = 192, kRegsEpilogue = 80, kRegsOther = 48;
 static_assert(valid_reg_split(kRegsSoftmax, kRegsEpilogue, kRegsOther), "register split");
 constexpr int kStages = 5;                            // K ring and V ring
+constexpr int kSlots = 4;     // items between the thread that takes them and the roles
+constexpr int kReaders = 16;  // of an item: 12 + 2 warps, two lanes of warp 14
 constexpr int OFF_Q = 0;                              // 2 buffers x (Q_A, Q_B)
 constexpr int OFF_K = OFF_Q + 4 * kTileBytes;         // kStages
 constexpr int OFF_V = OFF_K + kStages * kTileBytes;   // kStages
 constexpr int OFF_BAR = OFF_V + kStages * kTileBytes;
 constexpr int kBarBytes = 512;                // mbarriers, TMEM address, abort flag
 constexpr int OFF_SUM = OFF_BAR + kBarBytes;  // the rows' softmax sums, 2 x 128 fp32
-constexpr int SMEM_BYTES = OFF_SUM + 2 * 128 * 4 + 1024;  // + slack for 1024-byte alignment
+constexpr int OFF_ITEM = OFF_SUM + 2 * 128 * 4;  // kSlots items of 8 ints
+constexpr int SMEM_BYTES = OFF_ITEM + kSlots * 32 + 1024;  // + slack for 1024-byte alignment
 static_assert(SMEM_BYTES <= 232448, "more shared memory than an sm_103 CTA may have");
 
 enum Bar {
@@ -84,7 +100,9 @@ enum Bar {
   B_SUM_FULL = B_O_FREE + 2,       // per tile: the rows' sums are in shared memory
   B_OST_FULL = B_SUM_FULL + 2,     // per tile: O_X (bf16) staged in its Q slot
   B_MMA_DONE = B_OST_FULL + 2,     // per issuing warp (S, P V)
-  B_COUNT = B_MMA_DONE + 2
+  B_IT_FULL = B_MMA_DONE + 2,      // kSlots: an item is in its slot
+  B_IT_EMPTY = B_IT_FULL + kSlots, // kSlots: every role has read it
+  B_COUNT = B_IT_EMPTY + kSlots
 };
 static_assert(8 * B_COUNT + 8 <= kBarBytes, "barrier region overflow");
 
@@ -95,6 +113,23 @@ constexpr uint32_t kColP = 384;  // P_X at 384 + 64 * X
 
 constexpr uint32_t kIdescS = make_idesc_bf16(128, 128, false, false);  // Q K^T
 constexpr uint32_t kIdescO = make_idesc_bf16(128, 64, false, true);    // P V (V MN-major)
+
+// mbar_wait_warp with one decision of the whole warp per poll and a 32-bit clock:
+// fewer registers and branches.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          int* status, int site) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    if (__any_sync(0xffffffffu, *abort_flag != 0 || static_cast<uint32_t>(clock()) - t0 >
+                                                        static_cast<uint32_t>(NE_WAIT_LIMIT_CYCLES))) {
+      *abort_flag = 1;
+      atomicCAS(status, 0, NE_DEV_TIMEOUT_BASE + site);
+      return false;
+    }
+  }
+  return true;
+}
 
 struct Params {
   Problem pb;
@@ -197,6 +232,10 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
       mbar_init(&bars[B_OST_FULL + x], 128);
       mbar_init(&bars[B_MMA_DONE + x], 1);
     }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&bars[B_IT_FULL + s], 1);
+      mbar_init(&bars[B_IT_EMPTY + s], kReaders);
+    }
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -215,17 +254,43 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
   uint8_t* sQ = smem + OFF_Q;  // buffer b: Q_A at 2b tiles, Q_B at 2b + 1
   uint8_t* sK = smem + OFF_K;
   uint8_t* sV = smem + OFF_V;
-  // The items of this CTA, in order (the same sequence in every role); the next
-  // one's index is fetched an item ahead.
-  auto deal = [&](int k) { return dealt_item(nullptr, p.list, k, cta, G, n_items); };
-#define NE_FOR_EACH_ITEM(it)                                             \
-  for (int k_ = 0, r_ = deal(0), rn_ = deal(1); r_ < n_items;             \
-       ++k_, r_ = rn_, rn_ = deal(k_ + 1))                                \
-    if (Item it; get_item(p, r_, it, threadIdx.x == 0))
+  // The items of this CTA: warp 13, lane 0 finds them and puts them into the
+  // slots, the other roles read them there (nkv = 0: no more).
+  int4* slots = reinterpret_cast<int4*>(smem + OFF_ITEM);
+  auto read_slot = [&](int k, Item& it) {
+    const int4 a = slots[2 * (k % kSlots)], b = slots[2 * (k % kSlots) + 1];
+    it.start = a.x;
+    it.len = a.y;
+    it.rowA = a.z;
+    it.h = a.w;
+    it.hk = b.x;
+    it.row_step = b.y;
+    it.head_step = b.y ? 0 : 1;
+    it.nkvA = b.z;
+    it.nkvB = b.w;
+    it.hasB = b.w > 0;
+    it.nkv = max(b.z, b.w);
+    return b.z > 0;
+  };
+  auto next_warp = [&](int k, Item& it) {  // for a whole warp
+    if (!wait_warp(&bars[B_IT_FULL + k % kSlots], (k / kSlots) & 1, abort_flag, p.status, 19))
+      return false;
+    const bool more = read_slot(k, it);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[B_IT_EMPTY + k % kSlots]);
+    return more;
+  };
+  auto next_lane = [&](int k, Item& it) {  // for a single lane
+    if (!mbar_wait(&bars[B_IT_FULL + k % kSlots], (k / kSlots) & 1, abort_flag, p.status, 19))
+      return false;
+    const bool more = read_slot(k, it);
+    mbar_arrive(&bars[B_IT_EMPTY + k % kSlots]);
+    return more;
+  };
+#define NE_FOR_EACH_ITEM(it, next) \
+  Item it;                         \
+  for (int k_ = 0; next(k_, it); ++k_)
 
-  // (The order of the branches is that of the code in memory, which the
-  // instruction caches feel: 413 us for 16384 tokens as it is, 424 with the
-  // softmax first.)
   if (warp == 13 || warp == 14) {
     // ------------------------------------ TMA producers: warp 13 K, warp 14 V
     regs_decrease<kRegsOther>();
@@ -240,9 +305,34 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
       bool ok = true;
       int g = 0;   // K (or V) tiles loaded so far by this CTA
       int nq = 0;  // items whose Q has been loaded
-      NE_FOR_EACH_ITEM(it) {
-        if (!ok) break;
+      // The CTA's first item is that of its number; the next is taken once the
+      // loads of the last are issued, a ring of tiles ahead of the softmax.
+      const int n = p.list ? __ldg(p.list) : n_items;
+      const int head = p.list ? __ldg(p.list + 1 + cta) : cta;
+      bool first = true;
+      auto take = [&](Item& it) {
+        while (true) {
+          const int m = first ? cta : G + atomicAdd(p.items.counter, 1);
+          if (m >= n) return false;
+          const int r = first ? head : p.list ? __ldg(p.list + 1 + m) : m;
+          first = false;
+          if (get_item(p, r, it, true)) return true;
+        }
+      };
+      for (int k = 0;; ++k) {
+        Item it;
         if (isK) {
+          const bool more = take(it);
+          const int s = k % kSlots;
+          if (k >= kSlots && !mbar_wait(&bars[B_IT_EMPTY + s], ((k - kSlots) / kSlots) & 1,
+                                        abort_flag, p.status, 20)) {
+            ok = false;
+            break;
+          }
+          slots[2 * s] = make_int4(it.start, it.len, it.rowA, it.h);
+          slots[2 * s + 1] = make_int4(it.hk, it.row_step, more ? it.nkvA : 0, more ? it.nkvB : 0);
+          mbar_arrive(&bars[B_IT_FULL + s]);
+          if (!more) break;
           const int b = nq & 1;
           if (nq >= 2 && !mbar_wait(&bars[B_Q_EMPTY + b], ((nq - 2) >> 1) & 1, abort_flag,
                                     p.status, 14)) {
@@ -256,8 +346,10 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
           tma_load_3d(sQ + (2 * b + 1) * kTileBytes, &tmQ, &bars[B_Q_FULL + b], 0,
                       it.h + it.head_step, it.start + it.rowA + it.row_step);
           ++nq;
+        } else if (!next_lane(k, it)) {
+          break;
         }
-        for (int j = 0; j < it.nkv; ++j, ++g) {
+        for (int j = 0; ok && j < it.nkv; ++j, ++g) {
           const int s = g % kStages;
           if (g >= kStages &&
               !mbar_wait(&empty[s], ((g - kStages) / kStages) & 1, abort_flag, p.status,
@@ -268,6 +360,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
           mbar_arrive_expect_tx(&full[s], kTileBytes);
           tma_load_3d(ring + s * kTileBytes, tm, &full[s], 0, it.hk, it.start + j * kBN);
         }
+        if (!ok) break;
       }
       if (!ok || *abort_flag) {
         // Let the copies still in flight land before the CTA exits: every
@@ -295,7 +388,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
       // back to the loader.
       tma_prefetch_desc(&tmO);
       int nq = 0, nst[2] = {0, 0};
-      NE_FOR_EACH_ITEM(it) {
+      NE_FOR_EACH_ITEM(it, next_lane) {
         const int b = nq & 1;
         bool ok = true;
         for (int x = 0; x < 2 && ok; ++x) {
@@ -334,14 +427,14 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
     int nq = 0;           // items started (Q buffer and phase)
     int cnt[2] = {0, 0};  // steps of tile X over all items
     int nit[2] = {0, 0};  // items in which tile X took part
-    NE_FOR_EACH_ITEM(it) {
+    NE_FOR_EACH_ITEM(it, next_warp) {
       if (!ok) break;
       const int b = nq & 1;
       if (isS) {
-        ok = mbar_wait_warp(&bars[B_Q_FULL + b], (nq >> 1) & 1, abort_flag, p.status, 2);
+        ok = wait_warp(&bars[B_Q_FULL + b], (nq >> 1) & 1, abort_flag, p.status, 2);
         for (int j = 0; ok && j < it.nkv; ++j) {
           const int gj = g + j, s = gj % kStages;
-          if (!mbar_wait_warp(&bars[B_K_FULL + s], (gj / kStages) & 1, abort_flag, p.status, 3)) {
+          if (!wait_warp(&bars[B_K_FULL + s], (gj / kStages) & 1, abort_flag, p.status, 3)) {
             ok = false;
             break;
           }
@@ -350,7 +443,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
           for (int x = 0; x < 2; ++x) {
             if (!ok || j >= (x ? it.nkvB : it.nkvA)) continue;
             const int c = cnt[x] + j;
-            if (c >= 1 && !mbar_wait_warp(&bars[B_S_FREE + x], (c - 1) & 1, abort_flag, p.status, 4)) {
+            if (c >= 1 && !wait_warp(&bars[B_S_FREE + x], (c - 1) & 1, abort_flag, p.status, 4)) {
               ok = false;
               continue;
             }
@@ -373,7 +466,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
       } else {
         for (int jj = 0; ok && jj < it.nkv; ++jj) {
           const int gj = g + jj, s = gj % kStages;
-          if (!mbar_wait_warp(&bars[B_V_FULL + s], (gj / kStages) & 1, abort_flag, p.status, 13)) {
+          if (!wait_warp(&bars[B_V_FULL + s], (gj / kStages) & 1, abort_flag, p.status, 13)) {
             ok = false;
             break;
           }
@@ -382,14 +475,14 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
           for (int x = 0; x < 2; ++x) {
             if (!ok || jj >= (x ? it.nkvB : it.nkvA)) continue;
             const int c = cnt[x] + jj;
-            if (!mbar_wait_warp(&bars[B_P_FULL + x], c & 1, abort_flag, p.status, 5)) {
+            if (!wait_warp(&bars[B_P_FULL + x], c & 1, abort_flag, p.status, 5)) {
               ok = false;
               continue;
             }
             // The first P V of an item overwrites O_X: the previous item's
             // epilogue must have read it.
             if (jj == 0 && nit[x] >= 1 &&
-                !mbar_wait_warp(&bars[B_O_FREE + x], (nit[x] - 1) & 1, abort_flag, p.status, 15)) {
+                !wait_warp(&bars[B_O_FREE + x], (nit[x] - 1) & 1, abort_flag, p.status, 15)) {
               ok = false;
               continue;
             }
@@ -433,26 +526,19 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
     const float* sums = reinterpret_cast<const float*>(smem + OFF_SUM);
     bool ok = true;
     int nq = 0, nit[2] = {0, 0};
-    NE_FOR_EACH_ITEM(it) {
+    NE_FOR_EACH_ITEM(it, next_warp) {
       if (!ok) break;
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
         if (x == 1 && !it.hasB) continue;
         const int ph = nit[x] & 1;
-        ok = mbar_wait_warp(&bars[B_SUM_FULL + x], ph, abort_flag, p.status, 17) &&
-             mbar_wait_warp(&bars[B_O_FINAL + x], ph, abort_flag, p.status, 11);
+        ok = wait_warp(&bars[B_SUM_FULL + x], ph, abort_flag, p.status, 17) &&
+             wait_warp(&bars[B_O_FINAL + x], ph, abort_flag, p.status, 11);
         if (!ok) break;
         ++nit[x];
         tc_fence_after();
         const float inv_l = 1.f / sums[x * 128 + r];
-        uint32_t o[64];
         const uint32_t tO = tmem + lane_base + kColO + 64 * x;
-        tmem_ld_x32(tO, o);
-        tmem_ld_x32(tO + 32, o + 32);
-        tmem_ld_wait(o);
-        tmem_ld_wait(o + 32);
-        tc_fence_before();
-        mbar_arrive(&bars[B_O_FREE + x]);  // O_X and the sums may be overwritten
         const int row0 = it.rowA + x * it.row_step, row = row0 + r;
         // A whole tile goes into the swizzled Q slot of this tile (no S MMA reads
         // it any more), and warp 14, lane 1 stores it with TMA; the sequence's
@@ -461,17 +547,27 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
         uint8_t* slot = sQ + (2 * (nq & 1) + x) * kTileBytes;
         uint4* dst = reinterpret_cast<uint4*>(
             p.out + (static_cast<long long>(it.start + row) * p.pb.H + it.h + x * it.head_step) * kHD);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {  // (half a row at a time: registers)
+          uint32_t o[32];
+          tmem_ld_x32(tO + 32 * half, o);
+          tmem_ld_wait(o);
+          if (half) {
+            tc_fence_before();
+            mbar_arrive(&bars[B_O_FREE + x]);  // O_X and the sums may be overwritten
+          }
 #pragma unroll
-        for (int cc = 0; cc < 8; ++cc) {
-          uint4 w;
-          w.x = pack_bf16x2(__uint_as_float(o[8 * cc + 0]) * inv_l, __uint_as_float(o[8 * cc + 1]) * inv_l);
-          w.y = pack_bf16x2(__uint_as_float(o[8 * cc + 2]) * inv_l, __uint_as_float(o[8 * cc + 3]) * inv_l);
-          w.z = pack_bf16x2(__uint_as_float(o[8 * cc + 4]) * inv_l, __uint_as_float(o[8 * cc + 5]) * inv_l);
-          w.w = pack_bf16x2(__uint_as_float(o[8 * cc + 6]) * inv_l, __uint_as_float(o[8 * cc + 7]) * inv_l);
-          if (whole)
-            *reinterpret_cast<uint4*>(slot + sw128_offset(r, cc)) = w;
-          else if (row < it.len)
-            dst[cc] = w;
+          for (int cc = 0; cc < 4; ++cc) {
+            uint4 w;
+            w.x = pack_bf16x2(__uint_as_float(o[8 * cc + 0]) * inv_l, __uint_as_float(o[8 * cc + 1]) * inv_l);
+            w.y = pack_bf16x2(__uint_as_float(o[8 * cc + 2]) * inv_l, __uint_as_float(o[8 * cc + 3]) * inv_l);
+            w.z = pack_bf16x2(__uint_as_float(o[8 * cc + 4]) * inv_l, __uint_as_float(o[8 * cc + 5]) * inv_l);
+            w.w = pack_bf16x2(__uint_as_float(o[8 * cc + 6]) * inv_l, __uint_as_float(o[8 * cc + 7]) * inv_l);
+            if (whole)
+              *reinterpret_cast<uint4*>(slot + sw128_offset(r, 4 * half + cc)) = w;
+            else if (row < it.len)
+              dst[4 * half + cc] = w;
+          }
         }
         if (whole) fence_proxy_async_smem();
         mbar_arrive(&bars[B_OST_FULL + x]);
@@ -492,21 +588,20 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
     bool ok = true;
     int cnt = 0;  // steps of this tile over all items
     int nit = 0;  // items in which this tile took part
-    NE_FOR_EACH_ITEM(it) {
+    NE_FOR_EACH_ITEM(it, next_warp) {
       if (!ok) break;
       const int nkv_x = x ? it.nkvB : it.nkvA;
       if (nkv_x == 0) continue;  // tile B outside the sequence
       const int row0 = it.rowA + x * it.row_step;
-      const int diag = row0 / kBM;
       // Index of this row's LSE, or -1 past the sequence's end.
       const int lse_at = row0 + r < it.len ? (it.h + x * it.head_step) * p.pb.n_tot + it.start +
                                                  row0 + r
                                            : -1;
-      float m_ref = 0.f;  // reference max (log2 units) the P values are taken against
-      float l_sum = 0.f;
-      for (int j = 0; j < nkv_x; ++j) {
-        const int c = cnt + j;
-        if (!(ok = mbar_wait_warp(&bars[B_S_FULL + x], c & 1, abort_flag, p.status, 8))) break;
+      float m_ref = -INFINITY;  // reference max (log2 units) the P values are taken against
+      float l_sum = 0.f;        // 0: no step yet (a step adds at least 1, or NaN)
+#pragma unroll 1
+      for (int left = nkv_x; left > 0; --left, ++cnt) {
+        if (!(ok = wait_warp(&bars[B_S_FULL + x], cnt & 1, abort_flag, p.status, 8))) break;
         tc_fence_after();
         // The whole S row in one TMEM round trip; S_X is then free for Q_X K_{j+1}^T.
         uint32_t sr[128];
@@ -520,7 +615,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
         tmem_ld_wait(sr + 96);
         tc_fence_before();
         mbar_arrive(&bars[B_S_FREE + x]);
-        if (j == diag) {  // diagonal tile: keys after the query get no weight
+        if (left == 1) {  // diagonal tile: keys after the query get no weight
 #pragma unroll
           for (int cc = 0; cc < 128; ++cc)
             if (cc > r) sr[cc] = 0xff800000u;  // -inf
@@ -536,63 +631,64 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
         // Move the reference max only when the row max outgrows it by more
         // than 2^8 (exact: O and l keep a common reference).
-        const bool grow = (j == 0) || (mx > m_ref + 8.0f);
-        float alpha = 1.f;
-        if (grow) {
-          alpha = (j == 0) ? 0.f : ex2_approx(m_ref - mx);
-          m_ref = mx;
-        }
-        // P = 2^(x - m_ref) in bf16 pairs, computed before P_X / O_X are touched.
+        const bool first = l_sum == 0.f;
+        const bool grow = first || (mx > m_ref + 8.0f);
+        const float m_new = grow ? mx : m_ref;
+        const float alpha = first ? 0.f : ex2_approx(m_ref - m_new);
+        m_ref = m_new;
+        // P = 2^(x - m_ref) in bf16 pairs, half a row at a time: the second half's
+        // exponentials overlap the store of the first.
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
         const uint64_t negm2 = f2_pack(-m_ref, -m_ref);
-        uint64_t acc[4] = {0, 0, 0, 0};  // packed partial row sums (0 = +0.f, +0.f)
+        uint64_t acc[2] = {0, 0};  // packed partial row sums (0 = +0.f, +0.f)
         uint32_t pw[64];
+        auto exponentials = [&](int half) {
 #pragma unroll
-        for (int cc = 0; cc < 128; cc += 2) {
-          const uint64_t t = f2_fma(f2_pack(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])),
-                                    sl2x2, negm2);
-          float t0, t1;
-          f2_unpack(t, t0, t1);
-          const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
-          acc[(cc >> 1) & 3] = f2_add(acc[(cc >> 1) & 3], f2_pack(p0, p1));
-          pw[cc >> 1] = pack_bf16x2(p0, p1);
-        }
-        float rs0, rs1;
-        f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), rs0, rs1);
-        const float rs = rs0 + rs1;
+          for (int cc = 64 * half; cc < 64 * half + 64; cc += 2) {
+            const uint64_t t = f2_fma(f2_pack(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])),
+                                      sl2x2, negm2);
+            float t0, t1;
+            f2_unpack(t, t0, t1);
+            const float p0 = ex2_approx(t0), p1 = ex2_approx(t1);
+            acc[(cc >> 1) & 1] = f2_add(acc[(cc >> 1) & 1], f2_pack(p0, p1));
+            pw[cc >> 1] = pack_bf16x2(p0, p1);
+          }
+        };
+        exponentials(0);
         // P_X and O_X are in use by the P V of the tile's previous step until it
-        // completes (waited every step, so PV_DONE is never two phases behind).
-        if (c > 0) {
-          if (!(ok = mbar_wait_warp(&bars[B_PV_DONE + x], (c - 1) & 1, abort_flag, p.status, 9)))
-            break;
-          tc_fence_after();
-          if (j > 0 && __any_sync(0xffffffffu, grow)) {
-            uint32_t o[32];
+        // completes (waited every step, so PV_DONE is never two phases behind;
+        // before the first step of all the parity is that of the phase before).
+        if (!(ok = wait_warp(&bars[B_PV_DONE + x], (cnt - 1) & 1, abort_flag, p.status, 9))) break;
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, grow && !first)) {
+          uint32_t o[32];
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              tmem_ld_x32(tO + half * 32, o);
-              tmem_ld_wait(o);
+          for (int half = 0; half < 2; ++half) {
+            tmem_ld_x32(tO + half * 32, o);
+            tmem_ld_wait(o);
 #pragma unroll
-              for (int cc = 0; cc < 32; ++cc) o[cc] = __float_as_uint(__uint_as_float(o[cc]) * alpha);
-              tmem_st_x32(tO + half * 32, o);
-              tmem_st_wait();  // the store has consumed `o` before it is reloaded
-            }
+            for (int cc = 0; cc < 32; ++cc) o[cc] = __float_as_uint(__uint_as_float(o[cc]) * alpha);
+            tmem_st_x32(tO + half * 32, o);
+            tmem_st_wait();  // the store has consumed `o` before it is reloaded
           }
         }
         tmem_st_x32(tP, pw);
+        exponentials(1);
         tmem_st_x32(tP + 32, pw + 32);
+        float rs0, rs1;
+        f2_unpack(f2_add(acc[0], acc[1]), rs0, rs1);
+        const float rs = rs0 + rs1;
         tmem_st_wait();
         l_sum = l_sum * alpha + rs;
         tc_fence_before();
         mbar_arrive(&bars[B_P_FULL + x]);
       }
       if (!ok) break;
-      cnt += nkv_x;
       // LSE in natural-log units: (m_ref + log2 l) * ln 2.
       if (lse_at >= 0) p.lse[lse_at] = (m_ref + __log2f(l_sum)) * 0.69314718055994531f;
       // The sums' place is free once the previous item's epilogue is done with
       // O_X (waited every item, so O_FREE is never two phases behind).
-      if (nit >= 1 && !(ok = mbar_wait_warp(&bars[B_O_FREE + x], (nit - 1) & 1, abort_flag,
+      if (nit >= 1 && !(ok = wait_warp(&bars[B_O_FREE + x], (nit - 1) & 1, abort_flag,
                                             p.status, 18)))
         break;
       reinterpret_cast<float*>(smem + OFF_SUM)[x * 128 + r] = l_sum;
@@ -678,6 +774,7 @@ __global__ void __launch_bounds__(kRopeThreads)
                               const ItemList list) {
   extern __shared__ int dyn[];  // the list's buckets, or the rows' positions
   pdl_wait();                   // the kernel that wrote q, k (and anything before it) has completed
+  if (blockIdx.x == 0 && threadIdx.x == 0) *list.counter = 0;
   if (blockIdx.x == 0 && list.out) {
     build_items(pb, list, dyn);
     return;

@@ -30,6 +30,7 @@ struct ItemList {
   int second = 0;
   int n_buckets = 0;  // the most steps an item can have, plus one
   int* out = nullptr; // [1 + number of items]: count, items; nullptr: none wanted
+  int* counter = nullptr;  // forward: how many items past the first of each CTA are taken
 };
 
 // Bucket (steps) of pair i = block * nseq + sequence, the second kind's behind
