@@ -60,7 +60,7 @@ namespace bwd {
 
 constexpr int kThreads = 512;
 // Registers per thread of each warpgroup after setmaxnreg (launch: 128).
-constexpr uint32_t kRegsSoftmax = 168, kRegsDrain = 104, kRegsMma = 72;
+constexpr uint32_t kRegsSoftmax = 176, kRegsDrain = 96, kRegsMma = 64;
 static_assert(valid_reg_split(kRegsSoftmax, kRegsDrain, kRegsMma), "register split");
 constexpr int kQStages = 3;                          // Q_i / dO_i ring depth
 constexpr int OFF_K = 0;                               // 2 buffers (units alternate)
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(512, 1)
     }
     for (int s = 0; s < kRowSlots; ++s) {
       mbar_init(&bars[B_ROW_FULL + s], 128);
-      mbar_init(&bars[B_ROW_EMPTY + s], 8);  // one arrival per softmax warp
+      mbar_init(&bars[B_ROW_EMPTY + s], 256);
     }
     mbar_init(&bars[B_S_FULL], 1);
     mbar_init(&bars[B_S_FREE], 256);
@@ -631,15 +631,15 @@ __global__ void __launch_bounds__(512, 1)
       NE_FOR_EACH_UNIT(u) {
         if (!ok) break;
         const int b = nu & 1;
-        if (!mbar_wait_warp(&bars[B_K_FULL + b], (nu >> 1) & 1, abort_flag, p.status, 32) ||
-            !mbar_wait_warp(&bars[B_V_FULL], nu & 1, abort_flag, p.status, 38)) {
+        if (!mbar_poll_warp(&bars[B_K_FULL + b], (nu >> 1) & 1, abort_flag, p.status, 32) ||
+            !mbar_poll_warp(&bars[B_V_FULL], nu & 1, abort_flag, p.status, 38)) {
           ok = false;
           break;
         }
         for (int it = 0; it < u.n_it; ++it, ++g) {
           const int sn = g % kQStages;
-          if (!mbar_wait_warp(&bars[B_QDO_FULL + sn], (g / kQStages) & 1, abort_flag, p.status, 33) ||
-              (g >= 1 && !mbar_wait_warp(&bars[B_S_FREE], (g - 1) & 1, abort_flag, p.status, 34))) {
+          if (!mbar_poll_warp(&bars[B_QDO_FULL + sn], (g / kQStages) & 1, abort_flag, p.status, 33) ||
+              (g >= 1 && !mbar_poll_warp(&bars[B_S_FREE], (g - 1) & 1, abort_flag, p.status, 34))) {
             ok = false;
             break;
           }
@@ -674,13 +674,13 @@ __global__ void __launch_bounds__(512, 1)
         if (!ok) break;
         const int b = nu & 1;
         // K' of this unit (B operand of dQ') has landed.
-        if (!mbar_wait_warp(&bars[B_K_FULL + b], (nu >> 1) & 1, abort_flag, p.status, 37)) {
+        if (!mbar_poll_warp(&bars[B_K_FULL + b], (nu >> 1) & 1, abort_flag, p.status, 37)) {
           ok = false;
           break;
         }
         for (int it = 0; it < u.n_it; ++it, ++g) {
           const int s = g % kQStages;
-          if (!mbar_wait_warp(&bars[B_DS_FULL], g & 1, abort_flag, p.status, 35)) {
+          if (!mbar_poll_warp(&bars[B_DS_FULL], g & 1, abort_flag, p.status, 35)) {
             ok = false;
             break;
           }
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(512, 1)
           }
           __syncwarp();
           // dQ'_i = dS K'  (A: dS^T read MN-major, i.e. as dS; B: K' MN-major)
-          if (g >= 1 && !mbar_wait_warp(&bars[B_DQ_FREE], (g - 1) & 1, abort_flag, p.status, 36)) {
+          if (g >= 1 && !mbar_poll_warp(&bars[B_DQ_FREE], (g - 1) & 1, abort_flag, p.status, 36)) {
             ok = false;
             break;
           }
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(512, 1)
     auto stage_rowstats = [&](float l2, float dl) -> bool {
       const int sl = ga % kRowSlots;
       if (ga >= kRowSlots &&
-          !mbar_wait_warp(&bars[B_ROW_EMPTY + sl], ((ga - kRowSlots) / kRowSlots) & 1, abort_flag,
+          !mbar_poll_warp(&bars[B_ROW_EMPTY + sl], ((ga - kRowSlots) / kRowSlots) & 1, abort_flag,
                           p.status, 44))
         return false;
       sLSE[sl * 128 + r] = -l2;
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(512, 1)
         // meet at named barriers; a warp whose bounded wait gave up carries
         // that into the first barrier's vote, and all four leave together.
         uint32_t v0[32], v1[32];
-        bool wok = mbar_wait_warp(&bars[B_DQ_FULL], gq & 1, abort_flag, p.status, 43);
+        bool wok = mbar_poll_warp(&bars[B_DQ_FULL], gq & 1, abort_flag, p.status, 43);
         if (wok) {
           tc_fence_after();
           tmem_ld_x32(tmem + lane_base + kColDQ, v0);
@@ -853,13 +853,10 @@ __global__ void __launch_bounds__(512, 1)
       int qt = 0;  // query tile of the step, counted from kt
       for (int it = 0; it < u.n_it; ++it) {
         const int gq = g + it;
-        if (!mbar_wait_warp(&bars[B_S_FULL], gq & 1, abort_flag, p.status, 39)) {
-          ok = false;
-          break;
-        }
         // LSE/D of this query tile are staged in slot gq % kRowSlots.
         const int sl = gq % kRowSlots;
-        if (!mbar_wait_warp(&bars[B_ROW_FULL + sl], (gq / kRowSlots) & 1, abort_flag, p.status, 40)) {
+        if (!mbar_poll_warp(&bars[B_S_FULL], gq & 1, &bars[B_ROW_FULL + sl], (gq / kRowSlots) & 1,
+                            abort_flag, p.status, 39)) {
           ok = false;
           break;
         }
@@ -910,18 +907,14 @@ __global__ void __launch_bounds__(512, 1)
             }
           }
         }
-        // This warp is done with the slot's row terms.
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[B_ROW_EMPTY + sl]);
+        // This thread is done with the slot's row terms.
+        mbar_arrive(&bars[B_ROW_EMPTY + sl]);
         // P^T (TMEM) / dS^T (smem): free once the MMAs of the previous tile are
         // done, and at a unit's first tile once the previous unit's dV/dK tile
-        // stores have read the dS^T buffer.
-        if (gq >= 1 && !mbar_wait_warp(&bars[B_PDS_FREE], (gq - 1) & 1, abort_flag, p.status, 41)) {
-          ok = false;
-          break;
-        }
-        if (it == 0 && nu >= 1 &&
-            !mbar_wait_warp(&bars[B_EPI_READ], (nu - 1) & 1, abort_flag, p.status, 49)) {
+        // stores have read the dS^T buffer (polled at every tile: no branch; before
+        // the first, the parity is that of the phase before).
+        if (!mbar_poll_warp(&bars[B_PDS_FREE], (gq - 1) & 1, &bars[B_EPI_READ], (nu - 1) & 1,
+                            abort_flag, p.status, 41)) {
           ok = false;
           break;
         }
@@ -951,8 +944,8 @@ __global__ void __launch_bounds__(512, 1)
       // full tile is staged in the dS^T buffer, free once the last dQ' MMA
       // (its last reader) has completed too.
       const int last = g + u.n_it - 1;
-      if (!(ok = full_tile ? mbar_wait_warp(&bars[B_PDS_FREE], last & 1, abort_flag, p.status, 42)
-                           : mbar_wait_warp(&bars[B_QDO_EMPTY + last % kQStages],
+      if (!(ok = full_tile ? mbar_poll_warp(&bars[B_PDS_FREE], last & 1, abort_flag, p.status, 42)
+                           : mbar_poll_warp(&bars[B_QDO_EMPTY + last % kQStages],
                                             (last / kQStages) & 1, abort_flag, p.status, 42)))
         break;
       tc_fence_after();

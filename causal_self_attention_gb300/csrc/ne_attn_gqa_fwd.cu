@@ -114,23 +114,6 @@ constexpr uint32_t kColP = 384;  // P_X at 384 + 64 * X
 constexpr uint32_t kIdescS = make_idesc_bf16(128, 128, false, false);  // Q K^T
 constexpr uint32_t kIdescO = make_idesc_bf16(128, 64, false, true);    // P V (V MN-major)
 
-// mbar_wait_warp with one decision of the whole warp per poll and a 32-bit clock:
-// fewer registers and branches.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          int* status, int site) {
-  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
-  const uint32_t t0 = static_cast<uint32_t>(clock());
-  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
-    if (__any_sync(0xffffffffu, *abort_flag != 0 || static_cast<uint32_t>(clock()) - t0 >
-                                                        static_cast<uint32_t>(NE_WAIT_LIMIT_CYCLES))) {
-      *abort_flag = 1;
-      atomicCAS(status, 0, NE_DEV_TIMEOUT_BASE + site);
-      return false;
-    }
-  }
-  return true;
-}
-
 struct Params {
   Problem pb;
   __nv_bfloat16* out;
@@ -273,7 +256,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
     return b.z > 0;
   };
   auto next_warp = [&](int k, Item& it) {  // for a whole warp
-    if (!wait_warp(&bars[B_IT_FULL + k % kSlots], (k / kSlots) & 1, abort_flag, p.status, 19))
+    if (!mbar_poll_warp(&bars[B_IT_FULL + k % kSlots], (k / kSlots) & 1, abort_flag, p.status, 19))
       return false;
     const bool more = read_slot(k, it);
     __syncwarp();
@@ -431,10 +414,10 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
       if (!ok) break;
       const int b = nq & 1;
       if (isS) {
-        ok = wait_warp(&bars[B_Q_FULL + b], (nq >> 1) & 1, abort_flag, p.status, 2);
+        ok = mbar_poll_warp(&bars[B_Q_FULL + b], (nq >> 1) & 1, abort_flag, p.status, 2);
         for (int j = 0; ok && j < it.nkv; ++j) {
           const int gj = g + j, s = gj % kStages;
-          if (!wait_warp(&bars[B_K_FULL + s], (gj / kStages) & 1, abort_flag, p.status, 3)) {
+          if (!mbar_poll_warp(&bars[B_K_FULL + s], (gj / kStages) & 1, abort_flag, p.status, 3)) {
             ok = false;
             break;
           }
@@ -443,7 +426,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
           for (int x = 0; x < 2; ++x) {
             if (!ok || j >= (x ? it.nkvB : it.nkvA)) continue;
             const int c = cnt[x] + j;
-            if (c >= 1 && !wait_warp(&bars[B_S_FREE + x], (c - 1) & 1, abort_flag, p.status, 4)) {
+            if (c >= 1 && !mbar_poll_warp(&bars[B_S_FREE + x], (c - 1) & 1, abort_flag, p.status, 4)) {
               ok = false;
               continue;
             }
@@ -466,7 +449,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
       } else {
         for (int jj = 0; ok && jj < it.nkv; ++jj) {
           const int gj = g + jj, s = gj % kStages;
-          if (!wait_warp(&bars[B_V_FULL + s], (gj / kStages) & 1, abort_flag, p.status, 13)) {
+          if (!mbar_poll_warp(&bars[B_V_FULL + s], (gj / kStages) & 1, abort_flag, p.status, 13)) {
             ok = false;
             break;
           }
@@ -475,14 +458,14 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
           for (int x = 0; x < 2; ++x) {
             if (!ok || jj >= (x ? it.nkvB : it.nkvA)) continue;
             const int c = cnt[x] + jj;
-            if (!wait_warp(&bars[B_P_FULL + x], c & 1, abort_flag, p.status, 5)) {
+            if (!mbar_poll_warp(&bars[B_P_FULL + x], c & 1, abort_flag, p.status, 5)) {
               ok = false;
               continue;
             }
             // The first P V of an item overwrites O_X: the previous item's
             // epilogue must have read it.
             if (jj == 0 && nit[x] >= 1 &&
-                !wait_warp(&bars[B_O_FREE + x], (nit[x] - 1) & 1, abort_flag, p.status, 15)) {
+                !mbar_poll_warp(&bars[B_O_FREE + x], (nit[x] - 1) & 1, abort_flag, p.status, 15)) {
               ok = false;
               continue;
             }
@@ -532,8 +515,8 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
       for (int x = 0; x < 2; ++x) {
         if (x == 1 && !it.hasB) continue;
         const int ph = nit[x] & 1;
-        ok = wait_warp(&bars[B_SUM_FULL + x], ph, abort_flag, p.status, 17) &&
-             wait_warp(&bars[B_O_FINAL + x], ph, abort_flag, p.status, 11);
+        ok = mbar_poll_warp(&bars[B_SUM_FULL + x], ph, abort_flag, p.status, 17) &&
+             mbar_poll_warp(&bars[B_O_FINAL + x], ph, abort_flag, p.status, 11);
         if (!ok) break;
         ++nit[x];
         tc_fence_after();
@@ -601,7 +584,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
       float l_sum = 0.f;        // 0: no step yet (a step adds at least 1, or NaN)
 #pragma unroll 1
       for (int left = nkv_x; left > 0; --left, ++cnt) {
-        if (!(ok = wait_warp(&bars[B_S_FULL + x], cnt & 1, abort_flag, p.status, 8))) break;
+        if (!(ok = mbar_poll_warp(&bars[B_S_FULL + x], cnt & 1, abort_flag, p.status, 8))) break;
         tc_fence_after();
         // The whole S row in one TMEM round trip; S_X is then free for Q_X K_{j+1}^T.
         uint32_t sr[128];
@@ -658,7 +641,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
         // P_X and O_X are in use by the P V of the tile's previous step until it
         // completes (waited every step, so PV_DONE is never two phases behind;
         // before the first step of all the parity is that of the phase before).
-        if (!(ok = wait_warp(&bars[B_PV_DONE + x], (cnt - 1) & 1, abort_flag, p.status, 9))) break;
+        if (!(ok = mbar_poll_warp(&bars[B_PV_DONE + x], (cnt - 1) & 1, abort_flag, p.status, 9))) break;
         tc_fence_after();
         if (__any_sync(0xffffffffu, grow && !first)) {
           uint32_t o[32];
@@ -688,7 +671,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
       if (lse_at >= 0) p.lse[lse_at] = (m_ref + __log2f(l_sum)) * 0.69314718055994531f;
       // The sums' place is free once the previous item's epilogue is done with
       // O_X (waited every item, so O_FREE is never two phases behind).
-      if (nit >= 1 && !(ok = wait_warp(&bars[B_O_FREE + x], (nit - 1) & 1, abort_flag,
+      if (nit >= 1 && !(ok = mbar_poll_warp(&bars[B_O_FREE + x], (nit - 1) & 1, abort_flag,
                                             p.status, 18)))
         break;
       reinterpret_cast<float*>(smem + OFF_SUM)[x * 128 + r] = l_sum;

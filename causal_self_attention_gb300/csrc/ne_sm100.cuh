@@ -102,6 +102,33 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
   return __all_sync(0xffffffffu, ok);
 }
 
+// The same with one decision of the whole warp per poll and a 32-bit clock: fewer
+// branches and registers, for loops that are longer than the innermost
+// instruction cache.  The second form waits for two barriers' phases.
+__device__ __forceinline__ bool mbar_poll_warp(uint64_t* bar, uint32_t parity, uint64_t* bar2,
+                                               uint32_t parity2, volatile int* abort_flag,
+                                               int* status, int site) {
+  if (__all_sync(0xffffffffu,
+                 mbar_test_wait(bar, parity) && (!bar2 || mbar_test_wait(bar2, parity2))))
+    return true;
+  const uint32_t t0 = static_cast<uint32_t>(clock());
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity) &&
+                                      (!bar2 || mbar_try_wait(bar2, parity2)))) {
+    if (__any_sync(0xffffffffu, *abort_flag != 0 ||
+                                    static_cast<uint32_t>(clock()) - t0 >
+                                        static_cast<uint32_t>(NE_WAIT_LIMIT_CYCLES))) {
+      *abort_flag = 1;
+      atomicCAS(status, 0, NE_DEV_TIMEOUT_BASE + site);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool mbar_poll_warp(uint64_t* bar, uint32_t parity,
+                                               volatile int* abort_flag, int* status, int site) {
+  return mbar_poll_warp(bar, parity, nullptr, 0, abort_flag, status, site);
+}
+
 // One lane of a fully converged warp gets true (elect.sync).  The MMA issuers
 // run their loops with the whole warp and issue each group of tcgen05.mma from
 // the elected lane: a loop that runs in a single-lane divergent branch pays
