@@ -403,14 +403,23 @@ __device__ __forceinline__ bool get_unit(const BwdParams& p, int r, Unit& u) {
   return true;
 }
 
-// Query tile (counted from kt) and query head of step `it` of a unit.
-template <bool kShared>
-__device__ __forceinline__ int step_tile(const Unit& u, int it) {
-  return kShared ? it % u.n_qt : it;
+// The tiles of a unit in order: rows and query head of the current one.
+struct Walk {
+  int left, qt, n_qt;  // tiles left; tile of the head (counted from kt), tiles per head
+  int row, h;          // the tile's first row in the packed tensors; its query head
+};
+__device__ __forceinline__ Walk walk(const Unit& u) {
+  return Walk{u.n_it, 0, u.n_qt, u.start + u.kt * kBM, u.h0};
 }
 template <bool kShared>
-__device__ __forceinline__ int step_head(const Unit& u, int it) {
-  return kShared ? u.h0 + it / u.n_qt : u.h;
+__device__ __forceinline__ void step(Walk& w) {
+  --w.left;
+  w.row += kBM;
+  if (kShared && ++w.qt == w.n_qt) {
+    w.row -= w.n_qt * kBM;
+    w.qt = 0;
+    ++w.h;
+  }
 }
 
 // The first k' >= k whose unit is not empty (its description in u), or -1.
@@ -518,7 +527,7 @@ __global__ void __launch_bounds__(512, 1)
       int last_issued[kQStages] = {-1, -1, -1};
       NE_FOR_EACH_UNIT(u) {
         if (!ok) break;
-        for (int it = 0; it < u.n_it; ++it, ++g) {
+        for (Walk w = walk(u); w.left > 0; step<kShared>(w), ++g) {
           const int s = g % kQStages;
           if (g >= kQStages &&
               !mbar_wait(&bars[B_QDO_EMPTY + s], ((g - kQStages) / kQStages) & 1, abort_flag,
@@ -526,11 +535,9 @@ __global__ void __launch_bounds__(512, 1)
             ok = false;
             break;
           }
-          const int qrow = u.start + (u.kt + step_tile<kShared>(u, it)) * kBM;
-          const int qh = step_head<kShared>(u, it);
           mbar_arrive_expect_tx(&bars[B_QDO_FULL + s], 2 * kTileBytes);
-          tma_load_3d(sQ + s * kTileBytes, &tmQ, &bars[B_QDO_FULL + s], 0, qh, qrow);
-          tma_load_3d(sDO + s * kTileBytes, &tmDO, &bars[B_QDO_FULL + s], 0, qh, qrow);
+          tma_load_3d(sQ + s * kTileBytes, &tmQ, &bars[B_QDO_FULL + s], 0, w.h, w.row);
+          tma_load_3d(sDO + s * kTileBytes, &tmDO, &bars[B_QDO_FULL + s], 0, w.h, w.row);
           last_issued[s] = g;
         }
       }
@@ -744,23 +751,31 @@ __global__ void __launch_bounds__(512, 1)
     bool ok = true;
     // Row terms: a stream over all of the CTA's query tiles, across unit
     // boundaries, kRowSlots - 1 tiles ahead of the drain (so a unit's first
-    // tiles are staged during the previous unit).  Cursor: unit ua (index
-    // ka, -1 past the end), its tile ita, the CTA's tile number ga.
-    Unit ua;
-    int ka = next_unit<kShared>(p, n_units, cta, G, 0, ua);
-    int ita = 0, ga = 0;
+    // tiles are staged during the previous unit).  Cursor: tile wa of unit ka
+    // (-1 past the end), the CTA's tile number ga.
+    Walk wa{};
+    int ka = -1, ga = 0, end = 0;  // end: the end of the cursor's sequence
+    long long lse0 = 0;            // a head each: LSE of packed row m at lse0 + m
+    auto next = [&](int k) {
+      Unit u;
+      ka = next_unit<kShared>(p, n_units, cta, G, k, u);
+      if (ka < 0) return;
+      wa = walk(u);
+      end = u.start + u.len;
+      if (!kShared) lse0 = lse_index(p.pb, u.h, u.seq, u.start, 0) - u.start;
+    };
+    next(0);
     // LSE (log2 units) and D of query row r of the cursor's tile; rows past
     // the sequence get LSE = +inf, hence P = 0.  The loads always address a
     // row of the sequence (read-only loads may run ahead of the condition
     // that guards them).
     auto load_rowstats = [&](float& l2, float& dl) {
-      const int qpos = (ua.kt + step_tile<kShared>(ua, ita)) * kBM + r;
-      const int qc = qpos < ua.len ? qpos : ua.len - 1;
-      const int qh = step_head<kShared>(ua, ita);
-      const float l = __ldg(p.lse + lse_index(p.pb, qh, ua.seq, ua.start, qc));
-      const float d = __ldg(p.delta + static_cast<long long>(qh) * p.pb.n_tot + ua.start + qc);
-      l2 = qpos < ua.len ? l * 1.4426950408889634f : INFINITY;
-      dl = qpos < ua.len ? d : 0.f;
+      const int row = wa.row + r, rc = min(row, end - 1);
+      const long long at = static_cast<long long>(wa.h) * p.pb.n_tot + rc;
+      const float l = __ldg(p.lse + (kShared ? at : lse0 + rc));
+      const float d = __ldg(p.delta + at);
+      l2 = row < end ? l * 1.4426950408889634f : INFINITY;
+      dl = row < end ? d : 0.f;
     };
     // Stored negated: P = 2^(fma(s, scale log2 e, -LSE)), dS = P (dP - D).
     // The slot last held tile ga - kRowSlots, whose readers have all
@@ -776,10 +791,8 @@ __global__ void __launch_bounds__(512, 1)
       sDEL[sl * 128 + r] = -dl;
       mbar_arrive(&bars[B_ROW_FULL + sl]);
       ++ga;
-      if (++ita == ua.n_it) {
-        ita = 0;
-        ka = next_unit<kShared>(p, n_units, cta, G, ka + 1, ua);
-      }
+      step<kShared>(wa);
+      if (wa.left == 0) next(ka + 1);
       return true;
     };
     float l2, dl;
@@ -787,10 +800,9 @@ __global__ void __launch_bounds__(512, 1)
       load_rowstats(l2, dl);
       stage_rowstats(l2, dl);
     }
-    int g = 0;  // query tiles over all units
+    int gq = 0;  // query tiles over all units
     NE_FOR_EACH_UNIT(u) {
-      for (int it = 0; it < u.n_it; ++it) {
-        const int gq = g + it;
+      for (Walk w = walk(u); w.left > 0; step<kShared>(w), ++gq) {
         const bool ahead = ka >= 0;  // tile gq + kRowSlots - 1 exists: its row terms are next
         if (ahead) load_rowstats(l2, dl);  // loads in flight during the drain
         // dQ'_it: TMEM -> swizzled fp32 staging (columns 0-31 and 32-63) ->
@@ -821,10 +833,8 @@ __global__ void __launch_bounds__(512, 1)
         fence_proxy_async_smem();
         named_bar_sync(1, 128);
         if (r == 0) {
-          const int qrow = u.start + (u.kt + step_tile<kShared>(u, it)) * kBM;
-          const int qh = step_head<kShared>(u, it);
-          tma_reduce_add_3d(&tmDQ, sDQ, 0, qh, qrow);
-          tma_reduce_add_3d(&tmDQ, sDQ + kTileBytes, 32, qh, qrow);
+          tma_reduce_add_3d(&tmDQ, sDQ, 0, w.h, w.row);
+          tma_reduce_add_3d(&tmDQ, sDQ + kTileBytes, 32, w.h, w.row);
           bulk_commit_group();
         }
         // A failure here is carried into the next tile's vote.
@@ -832,7 +842,6 @@ __global__ void __launch_bounds__(512, 1)
       }
       // (No exit here: a failure reaches the next tile's vote, or the loops
       // simply end after the CTA's last tile.)
-      g += u.n_it;
     }
     // Every reduce-add has completed (not only read its source) before the
     // kernel ends.
@@ -846,13 +855,13 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const float sl2 = p.scale_log2;
     bool ok = true;
-    int g = 0;   // query tiles over all units
+    int gq = 0;  // query tiles over all units
     int nu = 0;  // units
     NE_FOR_EACH_UNIT(u) {
       if (!ok) break;
       int qt = 0;  // query tile of the step, counted from kt
-      for (int it = 0; it < u.n_it; ++it) {
-        const int gq = g + it;
+#pragma unroll 1
+      for (int left = u.n_it; left > 0; --left, ++gq) {
         // LSE/D of this query tile are staged in slot gq % kRowSlots.
         const int sl = gq % kRowSlots;
         if (!mbar_poll_warp(&bars[B_S_FULL], gq & 1, &bars[B_ROW_FULL + sl], (gq / kRowSlots) & 1,
@@ -882,7 +891,7 @@ __global__ void __launch_bounds__(512, 1)
             tc_fence_before();
             mbar_arrive(&bars[B_S_FREE]);  // S^T/dP^T may be overwritten now
           }
-          if (kShared ? qt == 0 : it == 0) {  // the diagonal tile
+          if (qt == 0) {  // the diagonal tile
 #pragma unroll
             for (int col = 0; col < 32; ++col)
               if (64 * half + 32 * hh + col < r) sv[col] = 0xff800000u;
@@ -929,7 +938,8 @@ __global__ void __launch_bounds__(512, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&bars[B_DS_FULL]);
-        if (kShared && ++qt == u.n_qt) qt = 0;
+        ++qt;
+        if (kShared && qt == u.n_qt) qt = 0;
       }
       if (!ok) break;
       // ---- epilogue of the unit: dV (first half), scale dK' (second half),
@@ -943,7 +953,7 @@ __global__ void __launch_bounds__(512, 1)
       // dV, dK' are final once the last tile's dV/dK' MMAs have completed; a
       // full tile is staged in the dS^T buffer, free once the last dQ' MMA
       // (its last reader) has completed too.
-      const int last = g + u.n_it - 1;
+      const int last = gq - 1;
       if (!(ok = full_tile ? mbar_poll_warp(&bars[B_PDS_FREE], last & 1, abort_flag, p.status, 42)
                            : mbar_poll_warp(&bars[B_QDO_EMPTY + last % kQStages],
                                             (last / kQStages) & 1, abort_flag, p.status, 42)))
@@ -974,7 +984,6 @@ __global__ void __launch_bounds__(512, 1)
             }
           }
           mbar_arrive(&bars[B_EPI_FULL]);
-          g += u.n_it;
           ++nu;
           continue;
         }
@@ -1034,7 +1043,6 @@ __global__ void __launch_bounds__(512, 1)
         }
         mbar_arrive(&bars[B_EPI_FULL]);
       }
-      g += u.n_it;
       ++nu;
     }
   }
