@@ -99,6 +99,7 @@ struct RopeEntry {
 // comes, reused by every later call on the stream, whose kernels it orders.
 struct StreamScratch {
   cudaStream_t stream = nullptr;
+  unsigned long long thread_id = 0;  // of the stream that cudaStreamPerThread names here
   void* ptr = nullptr;
   size_t bytes = 0;
 };
@@ -124,10 +125,21 @@ struct DeviceState {
   std::vector<SchedEntry> scheds;
 };
 
+// cudaStreamPerThread is one handle for a stream per thread: what is kept for a
+// stream is kept for the thread's own (0: any other handle, a stream of its own).
+ne_status per_thread_id(cudaStream_t stream, unsigned long long* id) {
+  *id = 0;
+  if (stream != cudaStreamPerThread) return NE_OK;
+  return cudaStreamGetId(stream, id) == cudaSuccess ? NE_OK : NE_ERR_CUDA;
+}
+
 // The forward's per-stream temporary of at least `bytes` (caller holds g_mutex).
 ne_status stream_scratch(DeviceState& st, cudaStream_t stream, size_t bytes, void** out) {
+  unsigned long long id = 0;
+  const ne_status rc = per_thread_id(stream, &id);
+  if (rc != NE_OK) return rc;
   for (auto& e : st.scratch)
-    if (e.stream == stream) {
+    if (e.stream == stream && e.thread_id == id) {
       if (e.bytes < bytes) {
         // Enqueued after every earlier use of the old buffer on this stream.
         if (cudaFreeAsync(e.ptr, stream) != cudaSuccess) return NE_ERR_CUDA;
@@ -142,6 +154,7 @@ ne_status stream_scratch(DeviceState& st, cudaStream_t stream, size_t bytes, voi
     }
   StreamScratch e;
   e.stream = stream;
+  e.thread_id = id;
   cudaError_t r = cudaMallocAsync(&e.ptr, bytes, stream);
   if (r != cudaSuccess) return r == cudaErrorMemoryAllocation ? NE_ERR_OOM : NE_ERR_CUDA;
   e.bytes = bytes;
@@ -171,9 +184,12 @@ constexpr int kCounterSets = 128;
 ne_status counter_set(DeviceState& st, cudaStream_t stream, bool captured, size_t bytes,
                       int** out) {
   *out = nullptr;
+  unsigned long long id = 0;
+  const ne_status rc = captured ? NE_OK : per_thread_id(stream, &id);
+  if (rc != NE_OK) return rc;
   if (!captured)
     for (auto& e : st.counters)
-      if (e.stream == stream) {
+      if (e.stream == stream && e.thread_id == id) {
         *out = static_cast<int*>(e.ptr);
         return NE_OK;
       }
@@ -196,6 +212,7 @@ ne_status counter_set(DeviceState& st, cudaStream_t stream, bool captured, size_
   if (!captured) {
     StreamScratch e;
     e.stream = stream;
+    e.thread_id = id;
     e.ptr = set;
     st.counters.push_back(e);
   }
@@ -208,6 +225,13 @@ ne_status device_state(DeviceState** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return NE_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return NE_ERR_UNSUPPORTED;
+  // A host thread that has made no CUDA call has no context yet, and the tensor
+  // maps come from a driver call, which makes none.
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    if (cudaSetDevice(dev) != cudaSuccess) return NE_ERR_CUDA;
+    bound = dev;
+  }
   DeviceState& st = g_dev[dev];
   if (!st.ready) {
     int major = 0, minor = 0;

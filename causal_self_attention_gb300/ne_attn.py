@@ -585,7 +585,7 @@ def ne_attn_gqa_varlen_fwd(q, k, v, cu_seqlens, max_seqlen, rope_base=10000.0, s
         kr = torch.empty_like(k) if kr is None else kr
         rc = lib().ne_attn_gqa_varlen_fwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), nseq, N,
-            int(max_seqlen),            H, Hkv, D, rope_base, D ** -0.5 if scale is None else scale, out.data_ptr(),
+            int(max_seqlen), H, Hkv, D, rope_base, D ** -0.5 if scale is None else scale, out.data_ptr(),
             lse.data_ptr(), qr.data_ptr(), kr.data_ptr(), raw)
     finally:
         _leave(ctx)

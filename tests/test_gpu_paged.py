@@ -1,6 +1,8 @@
 """The paged cache -- writing rows, reading them back, decode attention over it --
 against the plain 64-bit implementations of grouped.py, with bounds that count
 the roundings (derived there)."""
+from concurrent.futures import ThreadPoolExecutor
+
 import pytest
 import torch
 
@@ -426,6 +428,48 @@ def test_two_calls_at_once(na):
     torch.cuda.synchronize()
     for g, w in zip(got, want):
         assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+def test_first_call_of_a_thread(na):
+    """A host thread that has made no CUDA call before."""
+    c = Cache([100], 2, 64, False, seed=88).fill_random(89)
+    q, n = _randn(95, 1, 8, 64), _i32([100])
+    want = [t.clone() for t in _decode(na, c, q, n, 100)]
+    qkv = [_randn(96 + i, 1, 64, 2, 64) for i in range(3)]
+    fwd = na.ne_attn_fwd(*qkv)
+    outs = [torch.empty_like(t) for t in (*want, *fwd)]
+    torch.cuda.synchronize()
+    calls = (lambda: _decode(na, c, q, n, 100, out=outs[0], lse=outs[1]),
+             lambda: na.ne_attn_fwd(*qkv, out=outs[2], lse=outs[3]))
+    for call in calls:
+        with ThreadPoolExecutor(1) as pool:
+            pool.submit(call).result()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, (*want, *fwd)))
+
+
+def test_threads_on_their_own_default_streams(na):
+    """cudaStreamPerThread (the handle 2) names another stream in each thread."""
+    lens = [3000, 100]
+    c = Cache(lens, 2, 64, False, seed=86).fill_random(87)
+    n = _i32(lens)
+    qs = [_randn(90 + i, 2, 8, 64) for i in range(4)]
+    want = [[t.clone() for t in _decode(na, c, q, n, 3000)] for q in qs]
+    need = na.ne_attn_decode_paged_workspace_bytes(2, 8, 2, 3000)
+    bufs = [(torch.empty_like(q), torch.empty((2, 8), device="cuda"),
+             torch.empty(need, dtype=torch.uint8, device="cuda")) for q in qs]
+    torch.cuda.synchronize()
+
+    def run(i):
+        out, lse, ws = bufs[i]
+        for _ in range(50):
+            _decode(na, c, qs[i], n, 3000, out=out, lse=lse, workspace=ws, stream=2)
+
+    with ThreadPoolExecutor(len(qs)) as pool:
+        list(pool.map(run, range(len(qs))))
+    torch.cuda.synchronize()
+    for (out, lse, _), w in zip(bufs, want):
+        assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
 
 
 def test_append_replayed_from_a_graph(na):
