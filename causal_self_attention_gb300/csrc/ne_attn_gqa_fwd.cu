@@ -174,6 +174,10 @@ __device__ __forceinline__ bool get_item(const Params& p, int r, Item& it, bool 
 
 }  // namespace gqa
 
+// kList: the items come from a list, which has no empty ones but those of
+// sequences with bad bounds; without one (more items than it holds, for a bound
+// far above the lengths) nearly all may be empty.
+template <bool kList>
 __global__ void __launch_bounds__(gqa::kThreads, 1)
     ne_attn_gqa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmK,
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
   uint8_t* sK = smem + OFF_K;
   uint8_t* sV = smem + OFF_V;
   // The items of this CTA: warp 13, lane 0 finds them and puts them into the
-  // slots, the other roles read them there (nkv = 0: no more).
+  // slots, the other roles read them there (nkvA = 0: empty; -1: no more).
   int4* slots = reinterpret_cast<int4*>(smem + OFF_ITEM);
   auto read_slot = [&](int k, Item& it) {
     const int4 a = slots[2 * (k % kSlots)], b = slots[2 * (k % kSlots) + 1];
@@ -253,22 +257,27 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
     it.nkvB = b.w;
     it.hasB = b.w > 0;
     it.nkv = max(b.z, b.w);
-    return b.z > 0;
+    return b.z;
   };
-  auto next_warp = [&](int k, Item& it) {  // for a whole warp
-    if (!mbar_poll_warp(&bars[B_IT_FULL + k % kSlots], (k / kSlots) & 1, abort_flag, p.status, 19))
-      return false;
-    const bool more = read_slot(k, it);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars[B_IT_EMPTY + k % kSlots]);
-    return more;
+  auto next_warp = [&](int& k, Item& it) {  // for a whole warp
+    while (mbar_poll_warp(&bars[B_IT_FULL + k % kSlots], (k / kSlots) & 1, abort_flag, p.status,
+                          19)) {
+      const int steps = read_slot(k, it);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_IT_EMPTY + k % kSlots]);
+      if (kList || steps) return steps > 0;
+      ++k;
+    }
+    return false;
   };
-  auto next_lane = [&](int k, Item& it) {  // for a single lane
-    if (!mbar_wait(&bars[B_IT_FULL + k % kSlots], (k / kSlots) & 1, abort_flag, p.status, 19))
-      return false;
-    const bool more = read_slot(k, it);
-    mbar_arrive(&bars[B_IT_EMPTY + k % kSlots]);
-    return more;
+  auto next_lane = [&](int& k, Item& it) {  // for a single lane
+    while (mbar_wait(&bars[B_IT_FULL + k % kSlots], (k / kSlots) & 1, abort_flag, p.status, 19)) {
+      const int steps = read_slot(k, it);
+      mbar_arrive(&bars[B_IT_EMPTY + k % kSlots]);
+      if (kList || steps) return steps > 0;
+      ++k;
+    }
+    return false;
   };
 #define NE_FOR_EACH_ITEM(it, next) \
   Item it;                         \
@@ -290,20 +299,26 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
       int nq = 0;  // items whose Q has been loaded
       // The CTA's first item is that of its number; the next is taken once the
       // loads of the last are issued, a ring of tiles ahead of the softmax.
-      const int n = p.list ? __ldg(p.list) : n_items;
-      const int head = p.list ? __ldg(p.list + 1 + cta) : cta;
+      const int n = kList ? __ldg(p.list) : n_items;
+      const int head = kList ? __ldg(p.list + 1 + cta) : cta;
       bool first = true;
+      // False: none left.  Without a list an empty one (nkv = 0) goes through the
+      // slots as well, so that no role waits for long while a CTA passes many.
       auto take = [&](Item& it) {
         while (true) {
-          const int m = first ? cta : G + atomicAdd(p.items.counter, 1);
-          if (m >= n) return false;
-          const int r = first ? head : p.list ? __ldg(p.list + 1 + m) : m;
+          const unsigned m = first ? cta : G + atomicAdd(p.items.counter, 1);
+          if (m >= static_cast<unsigned>(n)) return false;
+          const int r = first ? head : kList ? __ldg(p.list + 1 + m) : static_cast<int>(m);
           first = false;
           if (get_item(p, r, it, true)) return true;
+          if (!kList) {
+            it.nkvA = it.nkvB = it.nkv = 0;
+            return true;
+          }
         }
       };
       for (int k = 0;; ++k) {
-        Item it;
+        Item it{};
         if (isK) {
           const bool more = take(it);
           const int s = k % kSlots;
@@ -313,9 +328,10 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
             break;
           }
           slots[2 * s] = make_int4(it.start, it.len, it.rowA, it.h);
-          slots[2 * s + 1] = make_int4(it.hk, it.row_step, more ? it.nkvA : 0, more ? it.nkvB : 0);
+          slots[2 * s + 1] = make_int4(it.hk, it.row_step, more ? it.nkvA : -1, it.nkvB);
           mbar_arrive(&bars[B_IT_FULL + s]);
           if (!more) break;
+          if (!kList && it.nkv == 0) continue;
           const int b = nq & 1;
           if (nq >= 2 && !mbar_wait(&bars[B_Q_EMPTY + b], ((nq - 2) >> 1) & 1, abort_flag,
                                     p.status, 14)) {
@@ -711,8 +727,9 @@ cudaError_t launch_gqa_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
                            const CUtensorMap& tmO, const Problem& pb, __nv_bfloat16* out,
                            float* lse, float scale_log2, const ItemList& items, int n_items,
                            int sms, int* status, cudaStream_t stream) {
-  static bool done[64] = {};
-  const cudaError_t e = allow_smem(ne_attn_gqa_fwd_kernel, gqa::SMEM_BYTES, done);
+  static bool done[2][64] = {};
+  cudaError_t e = allow_smem(ne_attn_gqa_fwd_kernel<false>, gqa::SMEM_BYTES, done[0]);
+  if (e == cudaSuccess) e = allow_smem(ne_attn_gqa_fwd_kernel<true>, gqa::SMEM_BYTES, done[1]);
   if (e != cudaSuccess) return e;
   gqa::Params p;
   p.pb = pb;
@@ -723,8 +740,8 @@ cudaError_t launch_gqa_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
   p.list = items.out;
   p.items = items;
   // One persistent CTA per SM (at most one per item).
-  return launch_pdl(ne_attn_gqa_fwd_kernel, dim3(n_items < sms ? n_items : sms),
-                    dim3(gqa::kThreads), gqa::SMEM_BYTES, stream, tmQ, tmK, tmV, tmO, p, n_items);
+  return launch_pdl(items.out ? ne_attn_gqa_fwd_kernel<true> : ne_attn_gqa_fwd_kernel<false>,
+                    dim3(n_items < sms ? n_items : sms), dim3(gqa::kThreads), gqa::SMEM_BYTES, stream, tmQ, tmK, tmV, tmO, p, n_items);
 }
 
 // ---------------------------------------------------------------------------

@@ -118,6 +118,11 @@ def _shares(na, lens, H, Hkv):
     return max(1, round(extra / (2 * n * Hkv * 256)))
 
 
+def test_more_items_than_a_list_holds(na):
+    """A bound so far above the lengths that nearly all of the items are empty."""
+    _check(na, [(i * 7) % 23 for i in range(300)] + [700], 6, 2, seed=165, max_seqlen=40000)
+
+
 @pytest.mark.parametrize("shares", [1, 2, 3, 5])
 def test_every_share_of_a_group(na, shares):
     """A group as one unit, in shares of several heads, even and uneven, and with a
