@@ -1219,7 +1219,9 @@ __global__ void __launch_bounds__(kPostThreads)
     if (first) {
       first = false;
       for (int r = threadIdx.x; r < rows; r += kPostThreads) {
-        const int s = find_sequence(pb.cu_seqlens, pb.nseq, row0 + r);
+        // (One probe at a time: seven take eight registers more, and two of the
+        // eight CTAs that 32 of them leave room for on an SM.)
+        const int s = find_sequence<1>(pb.cu_seqlens, pb.nseq, row0 + r);
         int start = 0, len = 0;
         row_pos[r] = s >= 0 && seq_bounds(pb, s, start, len, nullptr) ? row0 + r - start : -1;
       }

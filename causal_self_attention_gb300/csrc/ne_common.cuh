@@ -141,15 +141,41 @@ __host__ __device__ __forceinline__ int load_int(const int* p) {
 
 // The sequence of packed row r: the last s with cu[s] <= r (sequences of
 // length zero are passed over), or -1 for a row outside every sequence.  Reads
-// cu[0 .. nseq] only, whatever it holds.
+// cu[0 .. nseq] only, whatever it holds.  kProbes at a time, loaded together:
+// what a search costs is the latency of its rounds (two for 64 sequences; one
+// probe a round takes six).
+template <int kProbes = 7>
 __host__ __device__ __forceinline__ int find_sequence(const int* cu, int nseq, int r) {
+  const int first = load_int(cu), last = load_int(cu + nseq);
   int lo = 0, hi = nseq;
-  if (load_int(cu) > r || load_int(cu + nseq) <= r) return -1;
-  while (hi - lo > 1) {  // cu[lo] <= r < cu[hi]
-    const int mid = lo + ((hi - lo) >> 1);
-    if (load_int(cu + mid) <= r) lo = mid; else hi = mid;
+  while (hi - lo > 1) {  // cu[lo] <= r < cu[hi], if first <= r < last
+    const int step = (hi - lo + kProbes) / (kProbes + 1);
+    int v[kProbes];
+#ifdef __CUDA_ARCH__
+#pragma unroll
+#endif
+    for (int i = 0; i < kProbes; ++i) {
+      const int at = lo + (i + 1) * step;
+      v[i] = load_int(cu + (at < hi ? at : hi - 1));
+    }
+    int below = lo, above = hi;
+#ifdef __CUDA_ARCH__
+#pragma unroll
+#endif
+    for (int i = kProbes - 1; i >= 0; --i) {  // the first probe past r ends the new range
+      int at = lo + (i + 1) * step;
+      at = at < hi ? at : hi - 1;
+      if (v[i] > r) {
+        above = at;
+        below = lo;
+      } else if (below == lo) {
+        below = at;
+      }
+    }
+    lo = below;
+    hi = above;
   }
-  return lo;
+  return first <= r && last > r ? lo : -1;
 }
 
 // Work dealing of the persistent kernels: the index r (in the longest-first
