@@ -440,6 +440,15 @@ __device__ __forceinline__ int next_unit(const BwdParams& p, int n_units, int c,
 // summed over the group in TMEM; where that makes the longest unit longer than
 // its fair share of a CTA, the group is split over several units whose fp32
 // sums the postprocess adds in a fixed order.
+//
+// Measured with shared heads (12 on 4, 8 x 1024 / 12 on 2, 16384 tokens): 57 /
+// 1105 us of 69 / 1149 with the passes.  A tile takes about 3,450 cycles: the
+// softmax warps' arithmetic 2,400 and their stores 525, the rest waits (clock
+// stamps); the five products take 1,280 of them, and what a tile moves through
+// shared memory -- operands, dS^T, dQ' in and out of its staging, loads: 300 KB
+// -- is another 2,400 cycles at 128 bytes a cycle beside them.  Not faster: all
+// of a tile's scores loaded ahead (registers), by quarters ahead, halves in a
+// rolled loop with their stores inside, units taken from a counter.
 template <bool kShared>
 __global__ void __launch_bounds__(512, 1)
     ne_attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ,

@@ -25,24 +25,25 @@
 //   every role looked its items up itself -- the list, the sequence's bounds,
 //   four divisions -- a softmax warp spent 2,600 cycles an item on it, and items
 //   dealt in fixed rounds left the slowest CTA 18% behind the mean (now 8%).
-//   (32 packed prompts of 64 to 2048 tokens 67.4 -> 63; which CTA computes an
+//   (Packed prompts of 64 to 2048 tokens 67.4 -> 63 us; which CTA computes an
 //   item does not change its results.)
 //
 // What bounds it (clock stamps, 16384 tokens): the two softmax warps of an SM
 // sub-partition, 1,970 cycles for a step of both, of which the exponential unit
 // is busy 1,024 and, with the maxima, the packed products, sums and roundings
 // issued beside them, a loop of that arithmetic alone takes 1,500 (a
-// probe with two warps a sub-partition).  The loop body is longer than the
-// innermost instruction cache, so that each branch in it costs: a wait that polls once
-// for the whole warp with a 32-bit clock as its limit, phase parity instead of a
-// test for the first step, selects for the moving reference, and registers
+// probe with two warps a sub-partition).  Each branch in the loop costs more than
+// its instructions (the unrolled body is some 10 KB of code): a wait that polls
+// once for the whole warp with a 32-bit clock as its limit, phase parity instead
+// of a test for the first step, selects for the moving reference, and registers
 // enough (192) to spill nothing took a step from 2,300 to 1,970 cycles.  Slower
 // were: one arrival a warp (a branch and a reconvergence: 421 against 361 us),
 // the maximum of a half row while the other half loads (380), the two tiles'
 // exponentials in turns (457 against 413), sixteen softmax warps of half a row
 // (507 against 410), the softmax first in the code (424 against 413).
-// 351 us for 16384 tokens, 12 heads on 2 (1,170 TFLOP/s with the pass), 56 us
-// for the packed prompts.
+// 351 us for 16384 tokens, 12 heads on 2 (1,170 TFLOP/s with the pass); 55 us for
+// the packed prompts, 12 heads on 4, of which the pass is 16, the way to the
+// first scores 3, and a CTA's six items of four steps each the rest.
 //
 // Warp roles (512 threads, registers re-split per warpgroup with setmaxnreg):
 //   warps 0-3   softmax A: thread t owns row t of tile A (TMEM lane t), 192 regs
@@ -741,7 +742,8 @@ cudaError_t launch_gqa_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
   p.items = items;
   // One persistent CTA per SM (at most one per item).
   return launch_pdl(items.out ? ne_attn_gqa_fwd_kernel<true> : ne_attn_gqa_fwd_kernel<false>,
-                    dim3(n_items < sms ? n_items : sms), dim3(gqa::kThreads), gqa::SMEM_BYTES, stream, tmQ, tmK, tmV, tmO, p, n_items);
+                    dim3(n_items < sms ? n_items : sms), dim3(gqa::kThreads), gqa::SMEM_BYTES,
+                    stream, tmQ, tmK, tmV, tmO, p, n_items);
 }
 
 // ---------------------------------------------------------------------------

@@ -45,6 +45,14 @@
 //   loses nothing however far the rows' scales are apart; the sum of weights
 //   runs against the scores' own reference m.  Rounding to half: 2^-11.
 //
+// Measured: 16 sequences of 16k, 32 heads on 8, bf16 80.5 us (6.3 TB/s, 94% of the
+// copy rate); 64 ragged sequences of 1 to 16k, e4m3, 28.0 us (3.7 TB/s: the
+// products, weights and conversions of a key take 43% of the issue slots, and
+// the segments' ends, joins and the slowest CTA the rest); one sequence of 777,
+// 7.4 us (launch, prefix sums, a short ring, the join).  Tried: four CTAs an SM
+// with two stages, three q slots, other overheads (2, 3, 6) and part limits
+// (16-256): none faster on all of these.
+//
 // Keys of a tile past the sequence's end (what the page holds there, or an
 // older tile's bytes) get the score -inf, and their value rows are cleared in
 // shared memory, as 0 * NaN would show.
@@ -871,6 +879,11 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
 namespace {
 using namespace paged;
 
+// Query heads (columns of the products) that a unit takes.  16 where a group has
+// more than 8, so that its keys and values are read and converted once: 16 x
+// 16k, 16 heads a group, e4m3 24.6 us against 27.9 by two units of 8 (bf16 31.7
+// and 31.9: L2 serves the second).  Smaller groups would only pad: a ragged
+// e4m3 batch with 4 heads a group 28.1 by 8, 36.9 by 16.
 int paged_rows(int H, int Hkv) { return H / Hkv <= 8 ? 8 : 16; }
 
 // Launched CTAs: no more than the batch can have tiles.

@@ -18,6 +18,12 @@
 // head), lane c the 16-byte chunks c and c + 4 of K and of V, so that each
 // rotation pair (i, i + 32) sits in one lane, a warp moves eight neighbouring
 // 128-byte rows of each tensor, and every thread has four loads in flight.
+// A row's way is a chain of loads -- its sequence (two rounds of probes for 64
+// sequences), the position, the page, the row -- so that small calls are its
+// latency and large ones hide it under the other CTAs' rows.  Measured: a token
+// each for 64 sequences, 4 heads, 2.6 us; 32 prompts, 19,540 rows of 4 heads, to
+// e4m3 8.9 us (3.4 TB/s; the rows of the output stay in L2); 77,305 rows of 8
+// heads read from e4m3 40.9 us (5.8 TB/s, 87% of the copy rate).
 #include "ne_attn_debug.h"
 #include "ne_paged.cuh"
 #include "ne_sm100.cuh"

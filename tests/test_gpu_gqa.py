@@ -118,6 +118,38 @@ def _shares(na, lens, H, Hkv):
     return max(1, round(extra / (2 * n * Hkv * 256)))
 
 
+def test_no_tokens(na):
+    """Every sequence is empty: nothing is written."""
+    _check(na, [0, 0], 3, 1, seed=166, max_seqlen=300, behind=7)
+
+
+def test_two_calls_at_once(na):
+    """Calls in flight on two streams: as one after the other."""
+    lens = [900, 40, 300]
+    cu, sets = _cu(lens), []
+    for i in range(6):
+        q, k, v, do = (_randn(300 + 4 * i + j, sum(lens), h, 64) for j, h in enumerate((6, 2, 2, 6)))
+        sets.append((q, k, v, do))
+
+    def step(q, k, v, do, stream=None):
+        f = na.ne_attn_gqa_varlen_fwd(q, k, v, cu, 900, stream=stream)
+        return f + tuple(na.ne_attn_gqa_varlen_bwd(f[2], f[3], v, f[0], do, f[1], cu, 900,
+                                                   stream=stream))
+
+    want = [step(*x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [step(*x, stream=streams[i % 2]) for i, x in enumerate(sets)]
+    torch.cuda.synchronize()
+    assert na.ne_attn_get_device_status() == 0
+    for g, w in zip(got, want):
+        for i, (a, b) in enumerate(zip(g, w)):
+            if i == 4:  # dq: the order of its fp32 sums
+                assert float((a.double() - b.double()).norm()) <= 1e-3 * float(b.double().norm())
+            else:
+                assert torch.equal(a, b), i
+
+
 def test_more_items_than_a_list_holds(na):
     """A bound so far above the lengths that nearly all of the items are empty."""
     _check(na, [(i * 7) % 23 for i in range(300)] + [700], 6, 2, seed=165, max_seqlen=40000)
