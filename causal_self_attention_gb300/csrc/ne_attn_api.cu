@@ -1190,10 +1190,14 @@ ne_status ne_attn_decode_paged(const ne_bf16* q, int kv_type, const void* k_page
   int* arrived = nullptr;
   if ((rc = counter_set(*st, cs, captured, ne::paged_counter_bytes(), &arrived)) != NE_OK)
     return rc;
+  // No workspace given: the library's temporary for this stream (an allocation and
+  // a release of the call's own take 1 us of host time), or, during capture, nodes
+  // of the graph.
   void* ws = workspace;
-  const bool owned = !ws;
+  const bool owned = !ws && captured;
   cudaError_t e = cudaSuccess;
   if (owned && (e = cudaMallocAsync(&ws, need, cs)) != cudaSuccess) return cuda_status(e);
+  if (!ws && (rc = stream_scratch(*st, cs, need, &ws)) != NE_OK) return rc;
   if (!arrived) {  // counters in the workspace, cleared by a node of the graph
     arrived = static_cast<int*>(ws);
     e = cudaMemsetAsync(arrived, 0, ne::paged_counter_bytes(), cs);
