@@ -441,8 +441,8 @@ __device__ __forceinline__ int next_unit(const BwdParams& p, int n_units, int c,
 // its fair share of a CTA, the group is split over several units whose fp32
 // sums the postprocess adds in a fixed order.
 //
-// Measured with shared heads (12 on 4, 8 x 1024 / 12 on 2, 16384 tokens): 57 /
-// 1105 us of 69 / 1149 with the passes.  A tile takes about 3,450 cycles: the
+// Measured with shared heads (12 on 4, 8 x 1024 / 12 on 2, 16384 tokens): 55 /
+// 1096 us of 67 / 1140 with the passes.  A tile takes about 3,450 cycles: the
 // softmax warps' arithmetic 2,400 and their stores 525, the rest waits (clock
 // stamps); the five products take 1,280 of them, and what a tile moves through
 // shared memory -- operands, dS^T, dQ' in and out of its staging, loads: 300 KB
@@ -996,18 +996,17 @@ __global__ void __launch_bounds__(512, 1)
           ++nu;
           continue;
         }
-        // dK = R(n)^T (scale dK') here, in fp32, so that it is rounded once (the
-        // unit of a group is long enough for the table row's latency; with a
-        // head to a unit it held the next one up, and the postprocess rotates).
+        // dK = R(n)^T (scale dK') here, in fp32, so that it is rounded once, with the
+        // table in the layout whose lines are a warp's 32 positions (the table has
+        // every position of a tile).  The other form's postprocess rotates.  (8 x 1024, a
+        // head each, 78 us as in that form; by rows of the table, a line a lane, 83.)
         if (half) {
-          const int pos = kpos < u.len ? kpos : u.len - 1;
-          const float4* cs =
-              reinterpret_cast<const float4*>(p.rope.cs + static_cast<long long>(pos) * 32);
+          const float4* cs = p.rope.csw + 16LL * 32 * (4 * u.kt + wq) + lane;
 #pragma unroll
           for (int i0 = 0; i0 < 16; i0 += 8) {
             float4 t[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = __ldg(cs + i0 + i);  // (cos, sin) of two dims
+            for (int i = 0; i < 8; ++i) t[i] = __ldg(cs + 32 * (i0 + i));  // two dims
 #pragma unroll
             for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -1323,7 +1322,7 @@ cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
   if (!sm_count[dev] &&
       (e = cudaDeviceGetAttribute(&sm_count[dev], cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return e;
-  const bool shared = p.pb.group > 1;
+  const bool shared = p.grouped != 0;
   const long long n_units = static_cast<long long>(n_tiles) * p.pb.nseq * (p.pb.H / p.pb.group) *
                             p.splits;
   const int G = static_cast<int>(n_units < sm_count[dev] ? n_units : sm_count[dev]);

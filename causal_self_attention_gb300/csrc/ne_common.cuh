@@ -105,6 +105,7 @@ struct BwdParams {
   const int* sched = nullptr;  // work schedule of the persistent main kernel, or
   int sched_ctas = 0;          // nullptr for the snake order; the grid it was made for
   const int* compact = nullptr;  // packed batch: the non-empty units (dealt_item), or nullptr
+  int grouped = 0;               // 1: the kernels for shared heads (whatever the group)
   int splits = 1;                // shared heads: units per (key tile, key/value head), each
                                  // with a share of the group's query heads
   float* dk_part = nullptr;      // splits > 1: fp32 [splits, N_tot, H / group, 64] partials of
