@@ -758,7 +758,9 @@ cudaError_t launch_gqa_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
 // searched, once per row and CTA, while the first loads are in flight; a
 // persistent form with the next block's loads and search ahead was no faster.
 // Rows of no sequence, or of one with bad bounds (the attention kernel reports
-// it), are left alone.
+// it), are left alone.  (The queries rotated by the attention kernel's epilogue
+// warps instead, an item ahead: the first scores wait for it, 59.5 us against 55
+// for the packed prompts, 13.6 against 10.9 for short ones.)
 //
 // Four lanes take a (row, head), lane c the 16-byte chunks c and c + 4; a CTA's
 // (row, head) pairs -- the keys' heads behind the queries' -- go round its 64
