@@ -652,10 +652,37 @@ __global__ void __launch_bounds__(512, 1)
           ok = false;
           break;
         }
+        // Shared heads: where the sequence ends inside a tile, the rows behind it (a
+        // neighbour's, or padding that may hold anything) are cleared before any
+        // product, as the products that sum over rows take them with a weight of
+        // zero, and 0 * NaN would show.  Here, as this warp has time: it waits for
+        // the softmax in most tiles.
+        int to_last = 0;  // tiles to the last one of the query head
+        if constexpr (kShared) {
+          const int keys = u.len - u.kt * kBN;
+          if (keys < kBN) {
+            clear_rows(sK + b * kTileBytes, keys);
+            clear_rows(sV, keys);
+          }
+          to_last = u.n_qt - 1;
+        }
         for (int it = 0; it < u.n_it; ++it, ++g) {
           const int sn = g % kQStages;
-          if (!mbar_poll_warp(&bars[B_QDO_FULL + sn], (g / kQStages) & 1, abort_flag, p.status, 33) ||
-              (g >= 1 && !mbar_poll_warp(&bars[B_S_FREE], (g - 1) & 1, abort_flag, p.status, 34))) {
+          if (!mbar_poll_warp(&bars[B_QDO_FULL + sn], (g / kQStages) & 1, abort_flag, p.status, 33)) {
+            ok = false;
+            break;
+          }
+          if constexpr (kShared) {
+            if (--to_last < 0) {
+              const int rows = u.len - (u.kt + u.n_qt - 1) * kBM;
+              if (rows < kBM) {
+                clear_rows(sQ + sn * kTileBytes, rows);
+                clear_rows(sDO + sn * kTileBytes, rows);
+              }
+              to_last = u.n_qt - 1;
+            }
+          }
+          if (g >= 1 && !mbar_poll_warp(&bars[B_S_FREE], (g - 1) & 1, abort_flag, p.status, 34)) {
             ok = false;
             break;
           }
@@ -775,7 +802,8 @@ __global__ void __launch_bounds__(512, 1)
     };
     next(0);
     // LSE (log2 units) and D of query row r of the cursor's tile; rows past
-    // the sequence get LSE = +inf, hence P = 0.  The loads always address a
+    // the sequence get LSE = +inf, hence P = 0 (with shared heads, where q' and
+    // dO are cleared there, whatever the rows hold).  The loads always address a
     // row of the sequence (read-only loads may run ahead of the condition
     // that guards them).
     auto load_rowstats = [&](float& l2, float& dl) {
@@ -832,6 +860,12 @@ __global__ void __launch_bounds__(512, 1)
         // The staging buffers are free once the previous reductions have read them.
         if (r == 0) bulk_wait_group_read0();
         if (!(ok = named_bar_and(1, 128, ok && wok))) break;
+        // Rows past the sequence's end add nothing to what lies there (their dS is
+        // zero, but a key of the sequence may be NaN).
+        if (kShared && w.row + r >= u.start + u.len) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v0[c] = v1[c] = 0u;
+        }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           *reinterpret_cast<uint4*>(sDQ + sw128_offset(r, c)) =

@@ -234,6 +234,18 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Rows `first` .. 127 of a [128 x 64] bf16 tile that TMA has loaded (rows of 128
+// bytes, swizzled within) become zero, for the MMAs that come after.  A whole warp
+// calls it, once the load has completed and before any MMA reads the tile.
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int first) {
+  const uint32_t base = smem_u32(tile);
+#pragma unroll 1
+  for (int i = first * 2 * kHD + 16 * static_cast<int>(threadIdx.x % 32); i < kTileBytes; i += 512)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + i), "r"(0) : "memory");
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // --------------------------------------------------------------------- TMA --
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
