@@ -470,6 +470,10 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
             ok = false;
             break;
           }
+          // The item's last tile: rows of V behind the sequence (a neighbour's, or
+          // padding that may hold anything) are cleared, as their weight is zero and
+          // 0 * NaN would show.  By this warp, which waits for the softmax next.
+          if (it.len - jj * kBN < kBN) clear_rows(sV + s * kTileBytes, it.len - jj * kBN);
           const uint64_t dV = dV0 + kTileD * s;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {

@@ -301,10 +301,11 @@ ne_status ne_attn_decode_rotated(const ne_bf16* qr, const ne_bf16* kr_cache,
  * and dv summed over the query heads that share them (in fp32, in a fixed
  * order: deterministic; dq as in ne_attn_bwd).  Sequences of length zero are
  * allowed; rows behind the last sequence are left as they are (in the
- * backward too).  What the backward's inputs hold there, or in another sequence,
- * never reaches a sequence's gradients: not an infinity or NaN either.  (Within
- * its sequence a row that is not finite may also show in the rows before and
- * behind it that lie in the same 128, counted from the sequence's first.)
+ * backward too).  What the inputs hold there, or in another sequence, never
+ * reaches a sequence's results: not an infinity or NaN either.  (Within its
+ * sequence a row of v, and in the backward of any input, that is not finite may
+ * also show in the rows before it, and in the backward behind it, that lie in
+ * the same 128, counted from the sequence's first.)
  * nseq <= 65535, and ceil(max_seqlen / 128) * nseq * H < 2^31.
  * workspace: ne_attn_gqa_bwd_workspace_bytes(n_tot, max_seqlen, H, Hkv, D)
  * bytes, 256-byte aligned, or NULL for a stream-ordered temporary. */

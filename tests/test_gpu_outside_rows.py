@@ -6,7 +6,7 @@ times NaN is NaN."""
 import pytest
 import torch
 
-from grouped import attention_grads, rotate, unrotate_bound, within
+from grouped import attention, attention_grads, rotate, unrotate_bound, within
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
@@ -61,6 +61,19 @@ def _backward(na, f, v, do, cu, mx, fill):
 def _holds(t, x):
     """Every element of t is still x."""
     return bool(torch.isnan(t).all()) if x != x else bool((t == torch.tensor(x, dtype=t.dtype)).all())
+
+
+def _check_forward(f, v, lens, which):
+    out, lse, qr, kr = f
+    at = 0
+    for s, m in enumerate(lens):
+        r = slice(at, at + m)
+        at += m
+        if s not in which:
+            continue
+        o, l, oe, le = attention(qr[r], kr[r], v[r], 0.125)
+        within(out[r], o, oe, f"out of sequence {s}")
+        within(lse[:, r], l, le, f"lse of sequence {s}")
 
 
 def _check_backward(f, g, v, do, lens, which):
@@ -141,3 +154,84 @@ def test_backward_beside_a_skipped_sequence(na):
     assert na.ne_attn_get_device_status() == 7
     assert all(_holds(t[100:500], NAN) for t in g)
     _check_backward(f, g, v, do, lens, (0, 2))
+
+
+def test_backward_of_a_padded_step_in_a_graph(na):
+    """The forward and backward of a padded batch, captured once and replayed with
+    other lengths on the device; the padding holds NaN throughout."""
+    room = 1000
+    q, k, v, do = _inputs(31, room, 6, 2)
+    cu = _cu([300, 200, 100])
+    f = _forward(na, q, k, v, cu, 400, 0.0)  # outside the capture first
+    _backward(na, f, v, do, cu, 400, 0.0)
+    clean = [t.clone() for t in (q, k, v, do)]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        f = _forward(na, q, k, v, cu, 400, NAN)
+        g = _backward(na, f, v, do, cu, 400, NAN)
+    for lens in ([300, 200, 100], [1, 0, 129], [400, 399, 77]):
+        for t, c in zip((q, k, v, do), clean):
+            t.copy_(c)
+            t[sum(lens):] = NAN
+        cu.copy_(_cu(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert na.ne_attn_get_device_status() == 0
+        which = [s for s in range(3) if lens[s]]
+        _check_forward(f, v, lens, which)
+        _check_backward(f, g, v, do, lens, which)
+        assert all(_holds(t[sum(lens):], NAN) for t in (f[0], f[1].T, f[2], f[3], *g))
+
+
+# -------------------------------------------------------------------- forward
+
+@pytest.mark.parametrize("last", [1, 60, 127, 128, 300])
+@pytest.mark.parametrize("H,Hkv", HEADS)
+@pytest.mark.parametrize("stale", STALE)
+def test_forward_with_stale_rows_behind(na, stale, H, Hkv, last):
+    lens = [70, last]
+    tot, behind = sum(lens), 150
+    q, k, v, _ = _inputs(41, tot + behind, H, Hkv)
+    for t in (q, k, v):
+        t[tot:] = stale
+    f = _forward(na, q, k, v, _cu(lens), 300, stale)
+    assert na.ne_attn_get_device_status() == 0
+    _check_forward(f, v, lens, range(2))
+    assert all(_holds(t[tot:], stale) for t in (f[0], f[1].T, f[2], f[3]))
+
+
+@pytest.mark.parametrize("stale", [NAN, INF])
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+@pytest.mark.parametrize("H,Hkv", HEADS)
+def test_forward_beside_a_bad_neighbour(na, H, Hkv, name, stale):
+    q, k, v, _ = _inputs(51, sum(LENS), H, Hkv)
+    cu = _cu(LENS)
+    want = _forward(na, q, k, v, cu, 400, 0.0)
+    for bad in range(len(LENS)):
+        r = slice(sum(LENS[:bad]), sum(LENS[:bad + 1]))
+        x = dict(q=q, k=k, v=v)
+        x[name] = x[name].clone()
+        x[name][r] = stale
+        f = _forward(na, x["q"], x["k"], x["v"], cu, 400, 0.0)
+        assert na.ne_attn_get_device_status() == 0
+        others = torch.ones(sum(LENS), dtype=torch.bool, device="cuda")
+        others[r] = False
+        for a, w in zip((f[0], f[1].T, f[2], f[3]), (want[0], want[1].T, want[2], want[3])):
+            assert torch.equal(a[others], w[others])
+
+
+def test_forward_of_a_bound_without_a_work_list_beside_stale_rows(na):
+    """A bound so far above the lengths that no list of the items is made."""
+    lens = [(i * 7) % 23 for i in range(300)] + [700]
+    tot = sum(lens)
+    q, k, v, do = _inputs(61, tot + 50, 6, 2)
+    for t in (q, k, v, do):
+        t[tot:] = NAN
+    cu = _cu(lens)
+    f = _forward(na, q, k, v, cu, 40000, NAN)
+    g = _backward(na, f, v, do, cu, 40000, NAN)
+    assert na.ne_attn_get_device_status() == 0
+    which = [s for s in range(0, 301, 20) if lens[s]]
+    _check_forward(f, v, lens, which)
+    _check_backward(f, g, v, do, lens, which)
