@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
                                                  row0 + r
                                            : -1;
       float m_ref = -INFINITY;  // reference max (log2 units) the P values are taken against
-      float l_sum = 0.f;        // 0: no step yet (a step adds at least 1, or NaN)
+      float l_sum = 0.f;        // 0: no key with a weight yet (the first adds 1, or NaN)
 #pragma unroll 1
       for (int left = nkv_x; left > 0; --left, ++cnt) {
         if (!(ok = mbar_poll_warp(&bars[B_S_FULL + x], cnt & 1, abort_flag, p.status, 8))) break;
@@ -643,7 +643,9 @@ __global__ void __launch_bounds__(gqa::kThreads, 1)
         // P = 2^(x - m_ref) in bf16 pairs, half a row at a time: the second half's
         // exponentials overlap the store of the first.
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
-        const uint64_t negm2 = f2_pack(-m_ref, -m_ref);
+        // (-inf: no finite score yet, nor a weight; not -inf + inf.)
+        const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+        const uint64_t negm2 = f2_pack(neg, neg);
         uint64_t acc[2] = {0, 0};  // packed partial row sums (0 = +0.f, +0.f)
         uint32_t pw[64];
         auto exponentials = [&](int half) {
