@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] += src[4 + d0 + e] * wt;
       }
-      const float inv = 1.f / sum;
+      float inv = 1.f / sum;
       const float lse2 = any_bad ? kBad : ref + __log2f(sum);
       if (whole) {
         const long long oh = static_cast<long long>(s.b) * p.H + h0 + row;
@@ -767,6 +767,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
         if (d0 == 0) p.lse[oh] = any_bad ? -INFINITY : lse2 * 0.69314718055994531f;
       } else {
         float* dst = part + row * kPartRow;
+        if (sum == 0.f) inv = 0.f;  // scores of -inf alone: a part of weight zero, not NaN
         *reinterpret_cast<float4*>(dst + 4 + d0) =
             make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
         *reinterpret_cast<float4*>(dst + 8 + d0) =
@@ -858,7 +859,8 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
       for (int i = 0; i < groups; ++i) {
         const float* src = red + (i * row_slots + row) * L::kRedRow;
         if (8 * i >= n_parts) break;  // a group without parts
-        const float wt = ex2_approx(src[0] == -INFINITY ? -top : src[0] - top);
+        // (-inf: scores of -inf alone, sums of zero, or NaN; any finite factor will do.)
+        const float wt = src[0] == -INFINITY ? 1.f : ex2_approx(src[0] - top);
         sum += src[1] * wt;
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] += src[4 + d0 + e] * wt;

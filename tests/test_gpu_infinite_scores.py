@@ -1,10 +1,10 @@
 """Scores of minus infinity: such a key has weight zero, wherever it stands, also
-where a whole tile of a sequence holds nothing else.  A row with
+where a whole tile or a whole part of a sequence holds nothing else.  A row with
 no other keys has no weights (NaN) and the log-sum-exp -inf."""
 import pytest
 import torch
 
-from grouped import attention, within
+from grouped import Cache, attention, within
 
 pytestmark = pytest.mark.gpu
 HUGE = 3e38  # times 16 overflows fp32
@@ -68,3 +68,49 @@ def test_prompt_with_nothing_but_infinite_scores(na):
     rest[200:300] = False
     within(out[rest], o[rest], oe[rest], "out")
     within(lse[:, rest], l[:, rest], le[:, rest], "lse")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n,bad", [(60, 40), (700, 100), (700, 650), (20000, 5000), (20000, 19990)])
+@pytest.mark.parametrize("low", [False, True])
+def test_decode_whose_first_keys_have_infinite_scores(na, e4m3, n, bad, low):
+    """Parts of a sequence with no other keys among them; low: the others' scores
+    near -600, so that a factor 2^(-score) would overflow."""
+    H, Hkv = 6, 2
+    q, k, v = _qkv(21, 1, n, H, Hkv, bad)
+    q[..., 31] = 16
+    if low:
+        q[..., 0], k[..., 0] = 40, -120
+    c = Cache([n], Hkv, 64, e4m3, seed=24)
+    na.ne_kv_append(k, v, _i32([0, n]), _i32([0]), c.k, c.v, c.table, n, c.ks, c.vs, rope_base=0.0)
+    out, lse = na.ne_attn_decode_paged(q, c.k, c.v, c.table, _i32([n]), n, c.ks, c.vs, rope_base=0.0)
+    assert na.ne_attn_get_device_status() == 0
+    kk, vv = c.rows(0)
+    o, l, oe, le = attention(q, kk[bad:], vv[bad:], 0.125)
+    within(out[0], o[0], oe[0], "out")
+    within(lse[0], l[:, 0], le[:, 0], "lse")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n", [1, 60, 20000])
+def test_decode_with_nothing_but_infinite_scores(na, e4m3, n):
+    q, k, v = _qkv(31, 1, n, 6, 2, n)
+    q[..., 31] = 16
+    c = Cache([n], 2, 64, e4m3, seed=34)
+    na.ne_kv_append(k, v, _i32([0, n]), _i32([0]), c.k, c.v, c.table, n, c.ks, c.vs, rope_base=0.0)
+    out, lse = na.ne_attn_decode_paged(q, c.k, c.v, c.table, _i32([n]), n, c.ks, c.vs, rope_base=0.0)
+    assert na.ne_attn_get_device_status() == 0
+    assert bool(torch.isnan(out).all()) and bool((lse == -float("inf")).all())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("first,last", [(0, 5000), (15000, 20000), (9999, 10000)])
+def test_decode_with_keys_of_nan_shows_them(na, e4m3, first, last):
+    """A NaN score is no minus infinity: it shows, however many keys share it."""
+    n = 20000
+    q, k, v = _qkv(41, 1, n, 6, 2, 0)
+    k[first:last] = float("nan")
+    c = Cache([n], 2, 64, e4m3, seed=44)
+    na.ne_kv_append(k, v, _i32([0, n]), _i32([0]), c.k, c.v, c.table, n, c.ks, c.vs, rope_base=0.0)
+    out, lse = na.ne_attn_decode_paged(q, c.k, c.v, c.table, _i32([n]), n, c.ks, c.vs, rope_base=0.0)
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
