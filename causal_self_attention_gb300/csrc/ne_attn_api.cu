@@ -70,7 +70,8 @@ cudaError_t launch_decode_paged(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                 const __nv_bfloat16* q, const PagedCache& pc, bool e4m3,
                                 const int* seq_lens, int B, int H, const RopeTable& rope,
                                 float scale_log2, float* part, int* arrived, __nv_bfloat16* out,
-                                float* lse, int sms, int* status, cudaStream_t stream);
+                                float* lse, int sms, int* status, cudaStream_t stream,
+                                int drop_cta);
 constexpr unsigned kDecodeBoxRows = 32;  // keys per pipeline stage of the decode kernel
 cudaError_t launch_rmsnorm(const __nv_bfloat16* x, const __nv_bfloat16* g, __nv_bfloat16* xn,
                            float* rstd, int M, int C, float eps, cudaStream_t stream);
@@ -1153,13 +1154,14 @@ size_t ne_attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int max_seqle
   return align256(ne::paged_counter_bytes()) + ne::paged_part_bytes(B, H, Hkv, max_seqlen);
 }
 
-ne_status ne_attn_decode_paged(const ne_bf16* q, int kv_type, const void* k_pages,
-                               const void* v_pages, const uint8_t* k_scale,
-                               const uint8_t* v_scale, const int* block_table, int max_pages,
-                               int n_pages, int page_size, int max_seqlen, const int* seq_lens,
-                               int B, int H, int Hkv, int D, float rope_base, float scale,
-                               ne_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
-                               void* stream) {
+namespace {
+// ne_attn_decode_paged; drop_cta as in launch_decode_paged.
+ne_status decode_paged(const ne_bf16* q, int kv_type, const void* k_pages, const void* v_pages,
+                       const uint8_t* k_scale, const uint8_t* v_scale, const int* block_table,
+                       int max_pages, int n_pages, int page_size, int max_seqlen,
+                       const int* seq_lens, int B, int H, int Hkv, int D, float rope_base,
+                       float scale, ne_bf16* out, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream, int drop_cta) {
   if (!q || !seq_lens || !out || !lse) return NE_ERR_INVALID_ARG;
   if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0) return NE_ERR_INVALID_ARG;
   if (B > 65535 || H > 65535) return NE_ERR_INVALID_ARG;
@@ -1213,12 +1215,36 @@ ne_status ne_attn_decode_paged(const ne_bf16* q, int kv_type, const void* k_page
         tk, tv, reinterpret_cast<const __nv_bfloat16*>(q), pc, kv_type == NE_KV_E4M3, seq_lens, B,
         H, rope, scale * 1.4426950408889634f,
         reinterpret_cast<float*>(static_cast<char*>(ws) + align256(ne::paged_counter_bytes())),
-        arrived, reinterpret_cast<__nv_bfloat16*>(out), lse, st->sm_count, st->status, cs);
+        arrived, reinterpret_cast<__nv_bfloat16*>(out), lse, st->sm_count, st->status, cs,
+        drop_cta);
   if (owned) {
     const cudaError_t e2 = cudaFreeAsync(ws, cs);
     if (e == cudaSuccess) e = e2;
   }
   return cuda_status(e);
+}
+}  // namespace
+
+ne_status ne_attn_decode_paged(const ne_bf16* q, int kv_type, const void* k_pages,
+                               const void* v_pages, const uint8_t* k_scale,
+                               const uint8_t* v_scale, const int* block_table, int max_pages,
+                               int n_pages, int page_size, int max_seqlen, const int* seq_lens,
+                               int B, int H, int Hkv, int D, float rope_base, float scale,
+                               ne_bf16* out, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  return decode_paged(q, kv_type, k_pages, v_pages, k_scale, v_scale, block_table, max_pages,
+                      n_pages, page_size, max_seqlen, seq_lens, B, H, Hkv, D, rope_base, scale,
+                      out, lse, workspace, workspace_bytes, stream, -1);
+}
+
+ne_status ne_debug_decode_drop(const ne_bf16* q, const ne_bf16* k_pages, const ne_bf16* v_pages,
+                               const int* block_table, int max_pages, int n_pages, int page_size,
+                               int max_seqlen, const int* seq_lens, int B, int H, int Hkv,
+                               float scale, ne_bf16* out, float* lse, int drop_cta, void* stream) {
+  if (drop_cta < 0 || (Hkv > 0 && H / Hkv > 8)) return NE_ERR_INVALID_ARG;
+  return decode_paged(q, NE_KV_BF16, k_pages, v_pages, nullptr, nullptr, block_table, max_pages,
+                      n_pages, page_size, max_seqlen, seq_lens, B, H, Hkv, 64, 0.f, scale, out,
+                      lse, nullptr, 0, stream, drop_cta);
 }
 
 size_t ne_attn_decode_workspace_bytes(int B, int H, int Tmax) {

@@ -111,6 +111,7 @@ struct Params {
   __nv_bfloat16* out;
   float* lse;
   int* status;
+  int drop_cta;  // kDrop: whose first tile is never loaded
 };
 
 // The part of one unit -- (sequence, cached head, row tile) -- in a range.
@@ -207,7 +208,8 @@ __device__ __forceinline__ int e4m3_key(int mt, int x) {
 }
 }  // namespace paged
 
-template <bool kE4m3, int kRows>
+// kDrop: a tile of one CTA never arrives, for the tests of a wait that runs out.
+template <bool kE4m3, int kRows, bool kDrop>
 __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCtas)
     ne_attn_paged_kernel(const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const paged::Params p) {
@@ -353,6 +355,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
         const bool page_ok = page >= 0 && page < p.pc.n_pages;
         if (!page_ok) page = 0;  // reported; its rows are not used
         const bool bad = __any_sync(0xffffffffu, mine && !page_ok);
+        if (kDrop && g == 0 && w == p.drop_cta) continue;
         uint8_t* sk = smem + st * T::kStageBytes;
         uint8_t* sv = sk + T::kPool;
         if (lane == 0) {
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&qempty[slot]);
+    if (ok && lane == 0) mbar_arrive(&qempty[slot]);
 
     // References (the same in every lane of a column), sums (this lane's keys).
     float m[kNT][2], m2[kNT][2], l[kNT][2];
@@ -729,7 +732,10 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
           for (int hf = 0; hf < 2; ++hf)
             dst[4 + (kE4m3 ? 8 * r + 2 * i + hf : 16 * i + r + 8 * hf)] = o[nt][i][2 * hf + e];
       }
-    if (!named_bar_and(1, kWarps * 32, ok)) break;
+    // A wait that gave up (reported): this segment and the CTA's later ones have no
+    // result.  They still count as arrived, as bad parts, so that the counters are
+    // zero again after the launch; no further wait is made.
+    ok = named_bar_and(1, kWarps * 32, ok);
     const bool whole = s.t0 == 0 && s.t1 == s.n_tiles;
     // Of the workers of a unit the first takes its slot 1, the others slot 0.
     float* part = p.part + (static_cast<long long>(w) * 2 + (s.t0 == 0 ? 1 : 0)) * kRows * kPartRow;
@@ -737,7 +743,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
     for (int row = tid >> 3; row < rows; row += kWarps * 4) {
       const int d0 = (tid & 7) * 8;
       float M = -INFINITY;
-      bool any_bad = false;
+      bool any_bad = !ok;
 #pragma unroll
       for (int v = 0; v < kWarps; ++v) {
         const float* src = red + (v * kRows + row) * L::kRedRow;
@@ -898,16 +904,16 @@ int paged_ctas(long long B, int H, int Hkv, int max_seqlen, bool e4m3, int sms) 
   return static_cast<int>(tiles < full ? tiles : full);
 }
 
-template <bool kE4m3, int kRows>
+template <bool kE4m3, int kRows, bool kDrop = false>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int ctas,
                    cudaStream_t stream) {
   constexpr int bytes = Cfg<kE4m3, kRows>::BYTES;
   static_assert(Cfg<kE4m3, kRows>::kCtas * (bytes + 1024) <= 233472,
                 "CTAs of an SM share its 228 KiB");
   static bool done[64] = {};
-  const cudaError_t e = allow_smem(ne_attn_paged_kernel<kE4m3, kRows>, bytes, done);
+  const cudaError_t e = allow_smem(ne_attn_paged_kernel<kE4m3, kRows, kDrop>, bytes, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(ne_attn_paged_kernel<kE4m3, kRows>, dim3(ctas), dim3(kThreads), bytes, stream,
+  return launch_pdl(ne_attn_paged_kernel<kE4m3, kRows, kDrop>, dim3(ctas), dim3(kThreads), bytes, stream,
                     tk, tv, p);
 }
 }  // namespace
@@ -936,12 +942,14 @@ unsigned paged_box_rows(int page_size) {
 size_t paged_counter_bytes() { return kPagedSms * Cfg<false, 8>::kCtas * sizeof(int); }
 
 // tmK, tmV: the bf16 pools as [rows, 64] in boxes of paged_box_rows rows
-// (unused for e4m3).  arrived: paged_counter_bytes of zeros.
+// (unused for e4m3).  arrived: paged_counter_bytes of zeros.  drop_cta: -1, or (bf16,
+// groups of at most 8) the CTA whose first tile is never loaded.
 cudaError_t launch_decode_paged(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                 const __nv_bfloat16* q, const PagedCache& pc, bool e4m3,
                                 const int* seq_lens, int B, int H, const RopeTable& rope,
                                 float scale_log2, float* part, int* arrived, __nv_bfloat16* out,
-                                float* lse, int sms, int* status, cudaStream_t stream) {
+                                float* lse, int sms, int* status, cudaStream_t stream,
+                                int drop_cta) {
   if (sms > kPagedSms) sms = kPagedSms;
   Params p;
   p.pc = pc;
@@ -954,6 +962,8 @@ cudaError_t launch_decode_paged(const CUtensorMap& tmK, const CUtensorMap& tmV,
   p.part = part;
   p.arrived = arrived;
   p.status = status;
+  p.drop_cta = drop_cta;
+  if (drop_cta >= 0 && (e4m3 || rows != 8)) return cudaErrorInvalidValue;
   const int batch = paged_batch(H, pc.Hkv, pc.max_seqlen);
   for (int b0 = 0; b0 < B; b0 += batch) {
     p.B = B - b0 < batch ? B - b0 : batch;
@@ -964,7 +974,8 @@ cudaError_t launch_decode_paged(const CUtensorMap& tmK, const CUtensorMap& tmV,
     p.lse = lse + static_cast<long long>(b0) * H;
     const int ctas = paged_ctas(p.B, H, pc.Hkv, pc.max_seqlen, e4m3, sms);
     const cudaError_t e =
-        e4m3 ? (rows == 8 ? launch<true, 8>(tmK, tmV, p, ctas, stream)
+        drop_cta >= 0 ? launch<false, 8, true>(tmK, tmV, p, ctas, stream)
+        : e4m3 ? (rows == 8 ? launch<true, 8>(tmK, tmV, p, ctas, stream)
                           : launch<true, 16>(tmK, tmV, p, ctas, stream))
              : (rows == 8 ? launch<false, 8>(tmK, tmV, p, ctas, stream)
                           : launch<false, 16>(tmK, tmV, p, ctas, stream));

@@ -37,7 +37,8 @@ EXPORTED = ("ne_attn_fwd", "ne_attn_fwd_f32out", "ne_attn_bwd", "ne_attn_bwd_wor
             "ne_attn_set_fwd_phase_event", "ne_mtp_head", "ne_mtp_head_workspace_bytes",
             "ne_debug_schedule", "ne_attn_gqa_varlen_fwd", "ne_attn_gqa_varlen_bwd",
             "ne_attn_gqa_bwd_workspace_bytes", "ne_kv_append", "ne_kv_read",
-            "ne_attn_decode_paged", "ne_attn_decode_paged_workspace_bytes", "ne_debug_kv_place")
+            "ne_attn_decode_paged", "ne_attn_decode_paged_workspace_bytes", "ne_debug_kv_place",
+            "ne_debug_decode_drop")
 
 
 class NeAttnError(RuntimeError):
@@ -860,6 +861,23 @@ def ne_debug_kv_place(cu_seqlens, start_pos, block_table, Hkv, n_pages, page_siz
               int(max_seqlen), int(pair), ctypes.byref(src), ctypes.byref(slot),
               ctypes.byref(pos))
     return code, src.value, slot.value, pos.value
+
+
+def ne_debug_decode_drop(q, k_pages, v_pages, block_table, seq_lens, max_seqlen, drop_cta,
+                         scale=0.125):
+    """:func:`ne_attn_decode_paged` (bfloat16 cache, ``rope_base=0``) with a tile
+    that never arrives, see include/ne_attn_debug.h.  Returns ``(out, lse)``."""
+    P, I = ctypes.c_void_p, ctypes.c_int
+    fn = lib().ne_debug_decode_drop
+    fn.argtypes = [P, P, P, P, I, I, I, I, P, I, I, I, ctypes.c_float, P, P, I, P]
+    B, H, _ = q.shape
+    n_pages, Hkv, page_size, _ = k_pages.shape
+    out, lse = torch.empty_like(q), torch.empty((B, H), dtype=_F32, device=q.device)
+    _check("ne_debug_decode_drop", fn(
+        _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), block_table.shape[1], n_pages,
+        page_size, int(max_seqlen), _ptr(seq_lens), B, H, Hkv, scale, _ptr(out), _ptr(lse),
+        int(drop_cta), torch.cuda.current_stream().cuda_stream))
+    return out, lse
 
 
 def ne_debug_pipeline(src, n_items, drop_item=-1, wait_limit_cycles=2_000_000_000, stream=None):

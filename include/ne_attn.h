@@ -380,7 +380,8 @@ ne_status ne_kv_read(int kv_type, const void* k_pages, const void* v_pages,
  * H is a multiple of Hkv; query head h reads cached head h / (H / Hkv).
  * B, H <= 65535.  A sequence whose seq_lens entry or a page is bad is reported
  * as above and its outputs are zero and -inf.  What the cache holds beyond a
- * sequence's length never reaches its outputs.  How the work is split depends
+ * sequence's length never reaches its outputs.  Where a wait ran out (NE_ERR_TIMEOUT)
+ * the outputs of the heads concerned are zero and -inf, too.  How the work is split depends
  * on the whole batch's lengths, and with it the last bits of a result; the
  * same call gives the same bits.  workspace:
  * ne_attn_decode_paged_workspace_bytes(B, H, Hkv, max_seqlen) bytes, 16-byte

@@ -61,6 +61,16 @@ ne_status ne_debug_umma(int form, const ne_bf16* a, const ne_bf16* b, float* d, 
 ne_status ne_debug_pipeline(const ne_bf16* src, int n_rows, int H, int n_items, int drop_item,
                             long long wait_limit_cycles, float* d, void* stream);
 
+/* ne_attn_decode_paged on a bf16 cache and rotated queries (H / Hkv <= 8; no
+ * workspace), of which the CTA `drop_cta` never gets the first tile of its share:
+ * its wait runs out after about a second.  The device status becomes a timeout,
+ * the outputs of the heads that had a part there are zero and -inf, the others'
+ * are those of ne_attn_decode_paged, and so are those of later calls. */
+ne_status ne_debug_decode_drop(const ne_bf16* q, const ne_bf16* k_pages, const ne_bf16* v_pages,
+                               const int* block_table, int max_pages, int n_pages, int page_size,
+                               int max_seqlen, const int* seq_lens, int B, int H, int Hkv,
+                               float scale, ne_bf16* out, float* lse, int drop_cta, void* stream);
+
 /* Host only: where ne_kv_append and ne_kv_read place (row, head) pair `pair`
  * = row * Hkv + head of a packed batch, from HOST arrays.  Returns 0 (*src: the
  * row's element offset in the packed tensors, *slot: its row in the pools,
