@@ -176,15 +176,33 @@ ne_status cuda_status(cudaError_t e) {
   return NE_ERR_CUDA;
 }
 
+// A block of zeroed memory, also while this thread or another one captures a
+// stream: in the relaxed mode an allocation is allowed then and is no part of the
+// graph, and the clearing runs on a stream of its own.
+ne_status zeroed_block(size_t bytes, void** out) {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return NE_ERR_CUDA;
+  void* block = nullptr;
+  cudaStream_t own = nullptr;
+  e = cudaMalloc(&block, bytes);
+  if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+  if (e == cudaSuccess) e = cudaMemsetAsync(block, 0, bytes, own);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(own);  // any stream may use the block
+  if (own) cudaStreamDestroy(own);
+  if (e != cudaSuccess && block) cudaFree(block);
+  const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e == cudaSuccess) *out = block;
+  return cuda_status(e == cudaSuccess ? back : e);
+}
+
 // Arrival counters, in sets of `bytes` that are zero between launches (every
 // launch leaves them so).  A set belongs to one stream, whose launches run one
 // after the other, or to one captured call, whose replays do.  Sets come in
-// blocks, cleared before first use; *out = nullptr when none is left during a
-// capture, which allows no new block (caller holds g_mutex).
+// blocks, cleared before first use (caller holds g_mutex).
 constexpr int kCounterSets = 128;
 ne_status counter_set(DeviceState& st, cudaStream_t stream, bool captured, size_t bytes,
                       int** out) {
-  *out = nullptr;
   unsigned long long id = 0;
   const ne_status rc = captured ? NE_OK : per_thread_id(stream, &id);
   if (rc != NE_OK) return rc;
@@ -194,18 +212,17 @@ ne_status counter_set(DeviceState& st, cudaStream_t stream, bool captured, size_
         *out = static_cast<int*>(e.ptr);
         return NE_OK;
       }
+  try {  // (room first: nothing below throws)
+    st.counter_blocks.reserve(st.counter_blocks.size() + 1);
+    st.counters.reserve(st.counters.size() + 1);
+  } catch (const std::bad_alloc&) {
+    return NE_ERR_OOM;
+  }
   if (st.counter_sets_left == 0) {
-    if (captured) return NE_OK;
     void* block = nullptr;
-    cudaError_t r = cudaMalloc(&block, kCounterSets * bytes);
-    if (r != cudaSuccess) return cuda_status(r);
-    r = cudaMemsetAsync(block, 0, kCounterSets * bytes, stream);
-    if (r == cudaSuccess) r = cudaStreamSynchronize(stream);  // other streams use the block too
-    if (r != cudaSuccess) {
-      cudaFree(block);
-      return cuda_status(r);
-    }
-    st.counter_blocks.push_back(block);
+    const ne_status r = zeroed_block(kCounterSets * bytes, &block);
+    if (block) st.counter_blocks.push_back(block);
+    if (r != NE_OK) return r;
     st.counter_sets_left = kCounterSets;
   }
   --st.counter_sets_left;
@@ -1150,8 +1167,7 @@ ne_status ne_kv_read(int kv_type, const void* k_pages, const void* v_pages,
 
 size_t ne_attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int max_seqlen) {
   if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || max_seqlen <= 0) return 0;
-  // The arrival counters of a captured call, then the parts.
-  return align256(ne::paged_counter_bytes()) + ne::paged_part_bytes(B, H, Hkv, max_seqlen);
+  return ne::paged_part_bytes(B, H, Hkv, max_seqlen);
 }
 
 namespace {
@@ -1206,17 +1222,11 @@ ne_status decode_paged(const ne_bf16* q, int kv_type, const void* k_pages, const
   cudaError_t e = cudaSuccess;
   if (owned && (e = cudaMallocAsync(&ws, need, cs)) != cudaSuccess) return cuda_status(e);
   if (!ws && (rc = stream_scratch(*st, cs, need, &ws)) != NE_OK) return rc;
-  if (!arrived) {  // counters in the workspace, cleared by a node of the graph
-    arrived = static_cast<int*>(ws);
-    e = cudaMemsetAsync(arrived, 0, ne::paged_counter_bytes(), cs);
-  }
-  if (e == cudaSuccess)
-    e = ne::launch_decode_paged(
-        tk, tv, reinterpret_cast<const __nv_bfloat16*>(q), pc, kv_type == NE_KV_E4M3, seq_lens, B,
-        H, rope, scale * 1.4426950408889634f,
-        reinterpret_cast<float*>(static_cast<char*>(ws) + align256(ne::paged_counter_bytes())),
-        arrived, reinterpret_cast<__nv_bfloat16*>(out), lse, st->sm_count, st->status, cs,
-        drop_cta);
+  e = ne::launch_decode_paged(tk, tv, reinterpret_cast<const __nv_bfloat16*>(q), pc,
+                              kv_type == NE_KV_E4M3, seq_lens, B, H, rope,
+                              scale * 1.4426950408889634f, static_cast<float*>(ws), arrived,
+                              reinterpret_cast<__nv_bfloat16*>(out), lse, st->sm_count, st->status,
+                              cs, drop_cta);
   if (owned) {
     const cudaError_t e2 = cudaFreeAsync(ws, cs);
     if (e == cudaSuccess) e = e2;

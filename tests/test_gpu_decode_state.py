@@ -1,5 +1,7 @@
 """What the paged decode keeps between calls: the arrival counters of streams and of
 captured calls."""
+import ctypes
+
 import pytest
 import torch
 
@@ -30,6 +32,10 @@ def _decode(na, c, q, lens, **kw):
     return na.ne_attn_decode_paged(q, c.k, c.v, c.table, lens, max(c.lens), c.ks, c.vs, **kw)
 
 
+def _driver(name, *args):
+    assert getattr(ctypes.CDLL("libcuda.so.1"), name)(*args) == 0, name
+
+
 @pytest.mark.parametrize("drop", [7, 20, 100])
 def test_a_call_after_one_whose_wait_ran_out(na, drop):
     """A tile never arrives at one CTA.  That is reported, the heads that it concerns
@@ -52,3 +58,49 @@ def test_a_call_after_one_whose_wait_ran_out(na, drop):
             got = _decode(na, c, x, lens, rope_base=0.0)
             assert na.ne_attn_get_device_status() == 0
             assert all(torch.equal(a, b) for a, b in zip(got, w))
+
+
+KERNEL_NODE = 0  # CU_GRAPH_NODE_TYPE_KERNEL
+
+
+def test_any_number_of_captured_calls_are_a_kernel_each(na):
+    """As many as a model's layers times its batch sizes make, with a workspace: each is
+    its kernel and nothing in front of it, and each has counters of its own."""
+    P, n = ctypes.c_void_p, 400
+    c = Cache([900, 300], 2, 64, False, seed=1).fill_random(2)
+    q, lens = _randn(3, 2, 6, 64), _i32(c.lens)
+    want = [t.clone() for t in _decode(na, c, q, lens)]
+    ws = torch.empty(na.ne_attn_decode_paged_workspace_bytes(2, 6, 2, 900), dtype=torch.uint8,
+                     device="cuda")
+    outs = torch.zeros((n, 2, 6, 64), dtype=torch.bfloat16, device="cuda")
+    lses = torch.zeros((n, 2, 6), device="cuda")
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    raw, graph, executable = P(stream.cuda_stream), P(), P()
+    with torch.cuda.stream(stream):
+        _driver("cuStreamBeginCapture_v2", raw, 0)  # of the global mode, the strictest
+        for i in range(n):
+            _decode(na, c, q, lens, out=outs[i], lse=lses[i], workspace=ws)
+        _driver("cuStreamEndCapture", raw, ctypes.byref(graph))
+    count = ctypes.c_size_t()
+    _driver("cuGraphGetNodes", graph, None, ctypes.byref(count))
+    nodes = (P * count.value)()
+    _driver("cuGraphGetNodes", graph, nodes, ctypes.byref(count))
+    kinds = []
+    for node in nodes:
+        kind = ctypes.c_int()
+        _driver("cuGraphNodeGetType", P(node), ctypes.byref(kind))
+        kinds.append(kind.value)
+    assert kinds == [KERNEL_NODE] * n
+    _driver("cuGraphInstantiateWithFlags", ctypes.byref(executable), graph, ctypes.c_ulonglong(0))
+    for _ in range(2):
+        outs.zero_()
+        lses.zero_()
+        torch.cuda.synchronize()
+        _driver("cuGraphLaunch", executable, raw)
+        torch.cuda.synchronize()
+        assert bool((outs == want[0]).all()) and bool((lses == want[1]).all())
+    _driver("cuGraphExecDestroy", executable)
+    _driver("cuGraphDestroy", graph)
+    assert all(torch.equal(a, b) for a, b in zip(_decode(na, c, q, lens), want))
+    assert na.ne_attn_get_device_status() == 0
