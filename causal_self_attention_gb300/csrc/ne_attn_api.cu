@@ -114,6 +114,7 @@ struct SchedEntry {
 
 struct DeviceState {
   bool ready = false;
+  CUcontext ctx = nullptr;  // where everything below lives
   int* status = nullptr;  // device address of g_device_status on this device
   bool supported = false;
   int sm_count = 0;
@@ -169,6 +170,19 @@ DeviceState g_dev[kMaxDevices];
 int g_last_code = 0;
 cudaEvent_t g_ev_pre = nullptr, g_ev_main = nullptr, g_ev_rot = nullptr;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+PFN_cuCtxGetCurrent_v4000 g_current = nullptr;
+
+// A driver function, as of the given version.
+template <typename Fn>
+ne_status entry_point(const char* name, unsigned version, Fn* fn) {
+  void* at = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion(name, &at, version, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess || !at)
+    return NE_ERR_CUDA;
+  *fn = reinterpret_cast<Fn>(at);
+  return NE_OK;
+}
 
 ne_status cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return NE_OK;
@@ -244,13 +258,16 @@ ne_status device_state(DeviceState** out) {
   if (cudaGetDevice(&dev) != cudaSuccess) return NE_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return NE_ERR_UNSUPPORTED;
   // A host thread that has made no CUDA call has no context yet, and the tensor
-  // maps come from a driver call, which makes none.
-  static thread_local int bound = -1;
-  if (bound != dev) {
-    if (cudaSetDevice(dev) != cudaSuccess) return NE_ERR_CUDA;
-    bound = dev;
-  }
+  // maps come from a driver call, which makes none.  A context that is current
+  // stays so, whoever made it.
+  if (!g_current && entry_point("cuCtxGetCurrent", 4000, &g_current) != NE_OK) return NE_ERR_CUDA;
+  CUcontext ctx = nullptr;
+  if (g_current(&ctx) != CUDA_SUCCESS) return NE_ERR_CUDA;
+  if (!ctx && (cudaSetDevice(dev) != cudaSuccess || g_current(&ctx) != CUDA_SUCCESS))
+    return NE_ERR_CUDA;
   DeviceState& st = g_dev[dev];
+  // What the library keeps lives in the context of the first call on the device.
+  if (st.ready && st.ctx != ctx) return NE_ERR_UNSUPPORTED;
   if (!st.ready) {
     int major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
@@ -262,6 +279,7 @@ ne_status device_state(DeviceState** out) {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_device_status) != cudaSuccess) return NE_ERR_CUDA;
     st.status = static_cast<int*>(p);
+    st.ctx = ctx;
     st.ready = true;
   }
   if (!st.supported) return NE_ERR_UNSUPPORTED;
@@ -270,15 +288,7 @@ ne_status device_state(DeviceState** out) {
 }
 
 ne_status get_encoder() {
-  if (g_encode) return NE_OK;
-  void* fn = nullptr;
-  cudaDriverEntryPointQueryResult q;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                       &q) != cudaSuccess ||
-      q != cudaDriverEntryPointSuccess || !fn)
-    return NE_ERR_CUDA;
-  g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  return NE_OK;
+  return g_encode ? NE_OK : entry_point("cuTensorMapEncodeTiled", 12000, &g_encode);
 }
 
 RopeTable table_view(float2* dev, int cap) {

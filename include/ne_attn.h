@@ -56,7 +56,10 @@
  *    sequence longer than max_seqlen, a pipeline wait that timed out) are
  *    recorded in a device status word read by ne_attn_get_device_status.
  *  - Nothing here calls exit, abort or traps the GPU.
- *  - Calls are thread-safe; the RoPE table cache is per device.  A workspace
+ *  - Calls are thread-safe; the RoPE table cache is per device.  A call runs in
+ *    the calling thread's current context (the device's primary one where there
+ *    is none yet) and leaves it current; on one device every call comes from one
+ *    context (NE_ERR_UNSUPPORTED from another).  A workspace
  *    belongs to one call at a time: calls (or graphs) that may run at once
  *    need one each.
  */
