@@ -671,7 +671,7 @@ def ne_kv_append(k, v, cu_seqlens, start_pos, k_pages, v_pages, block_table, max
     64]``, bfloat16, or float8_e4m3fn with ``k_scale``, ``v_scale`` uint8
     ``[n_pages, Hkv, page_size]``; ``block_table`` int32 ``[nseq, max_pages]``.
     ``rope_base=0``: ``k`` is rotated already.  Returns ``(k_pages, v_pages)``,
-    written in place."""
+    written in place (with no rows at all, ``n_tot = 0``, as they are)."""
     dev = _device(k, "k")
     _need_on(k, _BF16, dev, "k")
     _need_on(v, _BF16, dev, "v")
@@ -681,6 +681,8 @@ def ne_kv_append(k, v, cu_seqlens, start_pos, k_pages, v_pages, block_table, max
     shape = k.shape
     if len(shape) != 3 or shape[1] != Hkv or shape[2] != 64 or shape != v.shape:
         raise ValueError("k, v must be [n_tot, Hkv, 64] with the pages' Hkv")
+    if shape[0] == 0:  # a step in which no sequence has a row
+        return k_pages, v_pages
     raw, ctx = _on(stream, dev)
     try:
         rc = lib().ne_kv_append(
@@ -717,6 +719,8 @@ def ne_kv_read(k_pages, v_pages, block_table, cu_seqlens, start_pos, n_tot, k_sc
     try:
         k = torch.empty(shape, dtype=_BF16, device=k_pages.device) if k is None else k
         v = torch.empty_like(k) if v is None else v
+        if n_tot == 0:  # no sequence has a row
+            return k, v
         rc = lib().ne_kv_read(
             kv_type, k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scale), _addr(v_scale),
             block_table.data_ptr(), max_pages, n_pages, page_size,

@@ -347,7 +347,8 @@ ne_status ne_attn_gqa_varlen_bwd(const ne_bf16* qr, const ne_bf16* kr, const ne_
  *
  * ne_kv_append writes new rows: row i of sequence s of k, v [n_tot, Hkv, 64]
  * bf16 (rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1; DEVICE int32 [nseq + 1],
- * nondecreasing; a sequence may have none) goes to position start_pos[s] + i
+ * nondecreasing; a sequence may have none, but n_tot is at least 1: a step in
+ * which no sequence has a row makes no call) goes to position start_pos[s] + i
  * (DEVICE int32 [nseq]): a whole prompt, part of one, or a token per sequence.
  * rope_base > 0: k is rotated at its position (the fp32 rule of
  * ne_attn_fwd); rope_base = 0: k is k' already.  e4m3: with a row's largest
