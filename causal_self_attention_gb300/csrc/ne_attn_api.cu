@@ -657,6 +657,15 @@ ne_status run_fwd(const Shape& s, const void* q, const void* k, const void* v, f
   return cuda_status(e);
 }
 
+// What the backward with shared heads keeps: dQ', D and, where groups are split,
+// the partials of dK' and dV.
+size_t gqa_bwd_need(int n_tot, int max_seqlen, int H, int Hkv) {
+  const size_t s = ne::bwd_group_splits(n_tot, max_seqlen, H, H / Hkv);
+  return align256(static_cast<size_t>(n_tot) * H * 64 * sizeof(float)) +
+         align256(static_cast<size_t>(n_tot) * H * sizeof(float)) +
+         (s > 1 ? align256(2 * s * n_tot * Hkv * 64 * sizeof(float)) : 0);
+}
+
 // kRotate: q, k as given; kPreRotated: q, k are q', k' and the gradients
 // returned are w.r.t. them; kTrain: q, k are q', k' (from the training
 // forward) and the gradients returned are w.r.t. the un-rotated q, k.
@@ -676,7 +685,7 @@ ne_status run_bwd(const Shape& s, const void* q, const void* k, const void* v, c
     return NE_ERR_MISALIGNED;
   const int Hkv = s.H / s.group;
   const size_t need =
-      s.grouped ? ne_attn_gqa_bwd_workspace_bytes(s.n_tot, s.max_len, s.H, Hkv, s.D)
+      s.grouped ? gqa_bwd_need(s.n_tot, s.max_len, s.H, Hkv)
                 : ne_attn_bwd_workspace_bytes(s.n_tot, s.H, s.D);
   if (workspace && workspace_bytes < need) return NE_ERR_INVALID_ARG;
   if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return NE_ERR_MISALIGNED;
@@ -1024,11 +1033,9 @@ ne_status ne_attn_varlen_bwd(const ne_bf16* q, const ne_bf16* k, const ne_bf16* 
 
 size_t ne_attn_gqa_bwd_workspace_bytes(int n_tot, int max_seqlen, int H, int Hkv, int D) {
   if (n_tot <= 0 || max_seqlen <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || D != 64) return 0;
+  // A head each: the size that serves ne_attn_varlen_bwd, too.
   if (H == Hkv) return ne_attn_bwd_workspace_bytes(n_tot, H, D);
-  const size_t s = ne::bwd_group_splits(n_tot, max_seqlen, H, H / Hkv);
-  return align256(static_cast<size_t>(n_tot) * H * 64 * sizeof(float)) +
-         align256(static_cast<size_t>(n_tot) * H * sizeof(float)) +
-         (s > 1 ? align256(2 * s * n_tot * Hkv * 64 * sizeof(float)) : 0);
+  return gqa_bwd_need(n_tot, max_seqlen, H, Hkv);
 }
 
 namespace {

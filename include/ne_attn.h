@@ -311,7 +311,10 @@ ne_status ne_attn_decode_rotated(const ne_bf16* qr, const ne_bf16* kr_cache,
  * the same 128, counted from the sequence's first.)
  * nseq <= 65535, and ceil(max_seqlen / 128) * nseq * H < 2^31.
  * workspace: ne_attn_gqa_bwd_workspace_bytes(n_tot, max_seqlen, H, Hkv, D)
- * bytes, 256-byte aligned, or NULL for a stream-ordered temporary. */
+ * bytes, 256-byte aligned, or NULL for a stream-ordered temporary.  (With
+ * Hkv = H the query gives the size that serves ne_attn_varlen_bwd, too; the call
+ * itself asks for dQ' and D alone, 260 bytes a token and head, each part in whole
+ * 256 bytes.) */
 ne_status ne_attn_gqa_varlen_fwd(const ne_bf16* q, const ne_bf16* k, const ne_bf16* v,
                                  const int* cu_seqlens, int nseq, int n_tot, int max_seqlen,
                                  int H, int Hkv, int D, float rope_base, float scale,
