@@ -140,6 +140,24 @@ def test_backward_beside_a_bad_neighbour(na, H, Hkv, name, stale):
         _check_backward(f, g, v, do, LENS, [s for s in range(len(LENS)) if s != bad])
 
 
+@pytest.mark.parametrize("H,Hkv", [(12, 4), (12, 1)])
+def test_backward_of_a_larger_batch_beside_a_bad_neighbour(na, H, Hkv):
+    """So many rows that a group stays whole (12 on 4), or is split in shares of
+    several heads (12 on 1): a unit then walks a sequence's last tile once a head."""
+    lens = [1000 - 9 * i for i in range(8)]
+    q, k, v, do = _inputs(71, sum(lens), H, Hkv)
+    cu = _cu(lens)
+    f = _forward(na, q, k, v, cu, 1000, 0.0)
+    for bad in (0, 3, 7):
+        r = slice(sum(lens[:bad]), sum(lens[:bad + 1]))
+        ff, vv, dd = [t.clone() for t in f], v.clone(), do.clone()
+        for t in (ff[0], ff[1].T, ff[2], ff[3], vv, dd):
+            t[r] = NAN
+        g = _backward(na, ff, vv, dd, cu, 1000, 0.0)
+        assert na.ne_attn_get_device_status() == 0
+        _check_backward(f, g, v, do, lens, [s for s in range(8) if s != bad])
+
+
 def test_backward_beside_a_skipped_sequence(na):
     """A sequence longer than the bound is reported and skipped by the forward, which
     leaves its rotated operands unwritten; the backward of the same call gives the
