@@ -1582,14 +1582,18 @@ int ne_attn_last_device_code(void) {
 
 void ne_attn_release(void) {
   std::lock_guard<std::mutex> lock(g_mutex);
-  int cur = 0;
-  cudaGetDevice(&cur);
+  PFN_cuCtxSetCurrent_v4000 set_current = nullptr;
+  CUcontext before = nullptr;
+  if (!g_current) return;  // no call has kept anything
+  if (g_current(&before) != CUDA_SUCCESS ||
+      entry_point("cuCtxSetCurrent", 4000, &set_current) != NE_OK)
+    return;
   for (int d = 0; d < kMaxDevices; ++d) {
     DeviceState& st = g_dev[d];
     if (st.tables.empty() && st.retired.empty() && st.scratch.empty() && st.scheds.empty() &&
         st.counter_blocks.empty())
       continue;
-    cudaSetDevice(d);
+    set_current(st.ctx);
     for (auto& t : st.tables) cudaFree(t.dev);
     for (auto& e : st.scheds)
       if (e.dev) cudaFree(e.dev);
@@ -1605,7 +1609,7 @@ void ne_attn_release(void) {
     st.retired.clear();
     st.scratch.clear();
   }
-  cudaSetDevice(cur);
+  set_current(before);
 }
 
 // ------------------------------------------------------------ debug entries --

@@ -1308,10 +1308,13 @@ __global__ void __launch_bounds__(kPostThreads)
 // many sequences of max_len as they can.  The busiest CTA has the longest unit
 // (the first key tile of a sequence) or the mean plus an eighth of it, at 1.75
 // a query tile; a unit's ends cost 2.6; and the partials of split groups are
-// written and read at 5 TB/s.  (Measured: 8 x 1024, 12 query heads on 4: one
-// unit 72, three 98; on 1: four 74, three 83, twelve 101; 1 x 16384, 12 on 2:
-// one 1342, two 1240, three 1213; 2 x 4096, 12 on 4: one 190, three 198.
-// Uneven shares lose: two of three heads 218.)  152: the SMs of the part -- the
+// written and read at 5 TB/s.  (Measured, the choice first: 8 x 1024, 12 query
+// heads on 4: one unit 67, three 94; on 1: four 71, three 79, twelve 98; 1 x
+// 16384, 12 on 2: three 1134, two 1152, one 1240; 2 x 4096, 12 on 4: one 178,
+// three 191; on 2: three 188, two 181.  Ragged batches, reckoned as sequences of
+// the longest: 32 of 64 to 2048, 12 on 4: one 188, three 227; on 2: one 284, two
+// 273; on 1: three 213, four 209; 4 of 16 to 4096, 16 on 1: eight 151, sixteen 157,
+// four 228.  Uneven shares lose.)  152: the SMs of the part -- the
 // reckoning is the host's that sizes the workspace, too.
 int bwd_group_splits(int n_tot, int max_len, int H, int group) {
   const double nt = static_cast<double>((static_cast<long long>(max_len) + kBM - 1) / kBM);
