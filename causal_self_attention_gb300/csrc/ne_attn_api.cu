@@ -144,7 +144,8 @@ ne_status stream_scratch(DeviceState& st, cudaStream_t stream, size_t bytes, voi
     if (e.stream == stream && e.thread_id == id) {
       if (e.bytes < bytes) {
         // Enqueued after every earlier use of the old buffer on this stream.
-        if (cudaFreeAsync(e.ptr, stream) != cudaSuccess) return NE_ERR_CUDA;
+        // (Null where an allocation failed before.)
+        if (e.ptr && cudaFreeAsync(e.ptr, stream) != cudaSuccess) return NE_ERR_CUDA;
         e.ptr = nullptr;
         e.bytes = 0;
         cudaError_t r = cudaMallocAsync(&e.ptr, bytes, stream);
@@ -154,6 +155,11 @@ ne_status stream_scratch(DeviceState& st, cudaStream_t stream, size_t bytes, voi
       *out = e.ptr;
       return NE_OK;
     }
+  try {
+    st.scratch.reserve(st.scratch.size() + 1);  // nothing below throws
+  } catch (const std::bad_alloc&) {
+    return NE_ERR_OOM;
+  }
   StreamScratch e;
   e.stream = stream;
   e.thread_id = id;
@@ -1599,7 +1605,8 @@ void ne_attn_release(void) {
       if (e.dev) cudaFree(e.dev);
     st.scheds.clear();
     for (auto* p : st.retired) cudaFree(p);
-    for (auto& e : st.scratch) cudaFreeAsync(e.ptr, e.stream);
+    for (auto& e : st.scratch)
+      if (e.ptr) cudaFreeAsync(e.ptr, e.stream);
     for (auto* b : st.counter_blocks) cudaFree(b);
     if (!st.scratch.empty()) cudaDeviceSynchronize();
     st.counters.clear();
