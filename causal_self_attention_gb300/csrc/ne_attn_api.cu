@@ -301,6 +301,14 @@ RopeTable table_view(float2* dev, int cap) {
   return RopeTable{dev, reinterpret_cast<const float4*>(dev + static_cast<size_t>(cap) * 32), cap};
 }
 
+// A table that kernels on any stream read next.  (cudaMemcpy of pageable memory may
+// return when the data is staged, with the copy into place still under way on the
+// legacy stream, which a non-blocking stream does not wait for.)
+cudaError_t copy_to_device(void* dst, const void* src, size_t bytes) {
+  const cudaError_t e = cudaMemcpy(dst, src, bytes, cudaMemcpyHostToDevice);
+  return e == cudaSuccess ? cudaStreamSynchronize(cudaStreamLegacy) : e;
+}
+
 // RoPE table for (base, D = 64) covering at least `positions` positions:
 // cs[p * 32 + i] = ((float)cos(p * theta_i), (float)sin(p * theta_i)),
 // theta_i = base^(-(2i)/64), all in double before the final fp32 rounding;
@@ -342,7 +350,7 @@ ne_status rope_table(DeviceState& st, float base, int positions, cudaStream_t st
   float2* dev = nullptr;
   cudaError_t e = cudaMalloc(&dev, host.size() * sizeof(float2));
   if (e != cudaSuccess) return cuda_status(e);
-  e = cudaMemcpy(dev, host.data(), host.size() * sizeof(float2), cudaMemcpyHostToDevice);
+  e = copy_to_device(dev, host.data(), host.size() * sizeof(float2));
   if (e != cudaSuccess) {
     cudaFree(dev);
     return cuda_status(e);
@@ -400,7 +408,7 @@ ne_status work_schedule(DeviceState& st, bool fixed, int nseq, int H, int T, cud
   if (!tab.empty()) {
     cudaError_t r = cudaMalloc(&e.dev, tab.size() * sizeof(int));
     if (r == cudaSuccess)
-      r = cudaMemcpy(e.dev, tab.data(), tab.size() * sizeof(int), cudaMemcpyHostToDevice);
+      r = copy_to_device(e.dev, tab.data(), tab.size() * sizeof(int));
     if (r != cudaSuccess) {
       if (e.dev) cudaFree(e.dev);
       return cuda_status(r);
