@@ -42,7 +42,8 @@
 //   warp 14     MMA: its elected lane issues S^T and dP^T of every tile (8
 //               MMAs).  Two issuing warps: one warp issuing all 32 MMAs of a
 //               tile was measured to pace the whole loop (its instructions
-//               compete with the softmax warps for issue slots).
+//               compete with the softmax warps for issue slots).  With shared
+//               heads it clears rows behind a sequence's end before them
 //   warp 15     TMA: lane 0 loads each unit's K'_j into the K' buffer the
 //               unit before the previous one has released, and V_j once the
 //               previous unit's last dP^T has completed
@@ -442,7 +443,7 @@ __device__ __forceinline__ int next_unit(const BwdParams& p, int n_units, int c,
 // sums the postprocess adds in a fixed order.
 //
 // Measured with shared heads (12 on 4, 8 x 1024 / 12 on 2, 16384 tokens): 55 /
-// 1096 us of 67 / 1140 with the passes.  A tile takes about 3,450 cycles: the
+// 1090 us of 67.5 / 1132 with the passes.  A tile takes about 3,450 cycles: the
 // softmax warps' arithmetic 2,400 and their stores 525, the rest waits (clock
 // stamps); the five products take 1,280 of them, and what a tile moves through
 // shared memory -- operands, dS^T, dQ' in and out of its staging, loads: 300 KB

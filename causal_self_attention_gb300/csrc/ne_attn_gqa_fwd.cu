@@ -41,9 +41,12 @@
 // the maximum of a half row while the other half loads (380), the two tiles'
 // exponentials in turns (457 against 413), sixteen softmax warps of half a row
 // (507 against 410), the softmax first in the code (424 against 413).
-// 351 us for 16384 tokens, 12 heads on 2 (1,170 TFLOP/s with the pass); 55 us for
-// the packed prompts, 12 heads on 4, of which the pass is 16, the way to the
-// first scores 3, and a CTA's six items of four steps each the rest.
+// 357-361 us for 16384 tokens, 12 heads on 2 (1,150 TFLOP/s with the pass); 57 us
+// for the packed prompts, 12 heads on 4, of which the pass is 16, the way to the
+// first scores 3, and a CTA's six items of four steps each the rest.  (Clearing V
+// behind a sequence's end took 55.7 to 57.0, by the test's presence alone: the
+// same where it is never true, 57.1 with the epilogue warps clearing, 57.7 before
+// the scores.)
 //
 // Warp roles (512 threads, registers re-split per warpgroup with setmaxnreg):
 //   warps 0-3   softmax A: thread t owns row t of tile A (TMEM lane t), 192 regs
@@ -52,7 +55,8 @@
 //   warp 12     MMA: allocates TMEM; one elected lane issues S_X = Q_X K^T
 //   warp 13     TMA: lane 0 takes the items, loads Q_A, Q_B and the K' ring
 //   warp 14     TMA: lane 0 loads the V ring; lane 1 stores whole O tiles
-//   warp 15     MMA: one elected lane issues O_X += P_X V; warps 12-15 at 48 regs
+//   warp 15     MMA: clears V behind a sequence's end; one elected lane issues
+//               O_X += P_X V; warps 12-15 at 48 regs
 // TMEM columns: S_A 0-127, S_B 128-255, O_A 256-319, O_B 320-383,
 // P_A 384-447, P_B 448-511 (bf16 pairs: P is the TMEM A operand of P V).
 //
@@ -765,7 +769,7 @@ cudaError_t launch_gqa_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
 // persistent form with the next block's loads and search ahead was no faster.
 // Rows of no sequence, or of one with bad bounds (the attention kernel reports
 // it), are left alone.  (The queries rotated by the attention kernel's epilogue
-// warps instead, an item ahead: the first scores wait for it, 59.5 us against 55
+// warps instead, an item ahead: the first scores wait for it, 59.5 us against 55.1
 // for the packed prompts, 13.6 against 10.9 for short ones.)
 //
 // Four lanes take a (row, head), lane c the 16-byte chunks c and c + 4; a CTA's
