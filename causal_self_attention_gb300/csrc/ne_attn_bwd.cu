@@ -42,8 +42,8 @@
 //   warp 14     MMA: its elected lane issues S^T and dP^T of every tile (8
 //               MMAs).  Two issuing warps: one warp issuing all 32 MMAs of a
 //               tile was measured to pace the whole loop (its instructions
-//               compete with the softmax warps for issue slots).  With shared
-//               heads it clears rows behind a sequence's end before them
+//               compete with the softmax warps for issue slots).  It clears
+//               rows behind a sequence's end before them
 //   warp 15     TMA: lane 0 loads each unit's K'_j into the K' buffer the
 //               unit before the previous one has released, and V_j once the
 //               previous unit's last dP^T has completed
@@ -653,35 +653,30 @@ __global__ void __launch_bounds__(512, 1)
           ok = false;
           break;
         }
-        // Shared heads: where the sequence ends inside a tile, the rows behind it (a
-        // neighbour's, or padding that may hold anything) are cleared before any
-        // product, as the products that sum over rows take them with a weight of
-        // zero, and 0 * NaN would show.  Here, as this warp has time: it waits for
-        // the softmax in most tiles.
-        int to_last = 0;  // tiles to the last one of the query head
-        if constexpr (kShared) {
-          const int keys = u.len - u.kt * kBN;
-          if (keys < kBN) {
-            clear_rows(sK + b * kTileBytes, keys);
-            clear_rows(sV, keys);
-          }
-          to_last = u.n_qt - 1;
+        // Where the sequence ends inside a tile, the rows behind it (a neighbour's, or
+        // padding that may hold anything) are cleared before any product, as the
+        // products that sum over rows take them with a weight of zero, and 0 * NaN
+        // would show.  Here, as this warp has time: it waits for the softmax in
+        // most tiles.
+        const int keys = u.len - u.kt * kBN;
+        if (keys < kBN) {
+          clear_rows(sK + b * kTileBytes, keys);
+          clear_rows(sV, keys);
         }
+        int to_last = u.n_qt - 1;  // tiles to the last one of the query head
         for (int it = 0; it < u.n_it; ++it, ++g) {
           const int sn = g % kQStages;
           if (!mbar_poll_warp(&bars[B_QDO_FULL + sn], (g / kQStages) & 1, abort_flag, p.status, 33)) {
             ok = false;
             break;
           }
-          if constexpr (kShared) {
-            if (--to_last < 0) {
-              const int rows = u.len - (u.kt + u.n_qt - 1) * kBM;
-              if (rows < kBM) {
-                clear_rows(sQ + sn * kTileBytes, rows);
-                clear_rows(sDO + sn * kTileBytes, rows);
-              }
-              to_last = u.n_qt - 1;
+          if (--to_last < 0) {
+            const int rows = u.len - (u.kt + u.n_qt - 1) * kBM;
+            if (rows < kBM) {
+              clear_rows(sQ + sn * kTileBytes, rows);
+              clear_rows(sDO + sn * kTileBytes, rows);
             }
+            to_last = u.n_qt - 1;
           }
           if (g >= 1 && !mbar_poll_warp(&bars[B_S_FREE], (g - 1) & 1, abort_flag, p.status, 34)) {
             ok = false;
@@ -803,8 +798,8 @@ __global__ void __launch_bounds__(512, 1)
     };
     next(0);
     // LSE (log2 units) and D of query row r of the cursor's tile; rows past
-    // the sequence get LSE = +inf, hence P = 0 (with shared heads, where q' and
-    // dO are cleared there, whatever the rows hold).  The loads always address a
+    // the sequence get LSE = +inf, hence P = 0 (q' and dO are cleared there,
+    // whatever the rows hold).  The loads always address a
     // row of the sequence (read-only loads may run ahead of the condition
     // that guards them).
     auto load_rowstats = [&](float& l2, float& dl) {
@@ -863,7 +858,7 @@ __global__ void __launch_bounds__(512, 1)
         if (!(ok = named_bar_and(1, 128, ok && wok))) break;
         // Rows past the sequence's end add nothing to what lies there (their dS is
         // zero, but a key of the sequence may be NaN).
-        if (kShared && w.row + r >= u.start + u.len) {
+        if (w.row + r >= u.start + u.len) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) v0[c] = v1[c] = 0u;
         }
