@@ -32,8 +32,8 @@
 //   warp 12     MMA: allocates TMEM; one elected lane issues S_X = Q_X K^T
 //   warp 13     TMA: lane 0 loads each item's Q_A, Q_B and the K' ring (5 stages)
 //   warp 14     TMA: lane 0 loads the V ring (5 stages)
-//   warp 15     MMA: one elected lane issues O_X += P_X V; warps 12-15 run at
-//               56 regs
+//   warp 15     MMA: clears V behind a sequence's end; one elected lane issues
+//               O_X += P_X V; warps 12-15 run at 56 regs
 // TMEM columns: S_A 0-127, S_B 128-255, O_A 256-319, O_B 320-383,
 // P_A 384-447, P_B 448-511 (bf16 pairs: P is the TMEM A operand of P V).
 // A softmax thread loads its whole S row with one TMEM round trip and frees
@@ -361,6 +361,9 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
             ok = false;
             break;
           }
+          // The sequence's last tile: rows of V behind it (a neighbour's) are cleared,
+          // as their weight is zero and 0 * NaN would show.
+          if (it.len - jj * kBN < kBN) clear_rows(sV + s * kTileBytes, it.len - jj * kBN);
           const uint64_t dV = dV0 + kTileD * s;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {

@@ -109,3 +109,46 @@ def test_packed_backward_beside_a_skipped_sequence(na, train):
     got = step(399)
     assert na.ne_attn_get_device_status() == 7
     _same(got, want, others, dq=0)
+
+
+# -------------------------------------------------------------------- forward
+
+@pytest.mark.parametrize("stale", [NAN, INF])
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+@pytest.mark.parametrize("form", ["plain", "f32out", "train"])
+def test_packed_forward_beside_a_bad_neighbour(na, form, name, stale):
+    q, k, v, _ = _inputs(4, sum(LENS), 3, 64)
+    cu = _cu(LENS)
+
+    def fwd(q, k, v):
+        if form == "train":
+            f = na.ne_attn_varlen_fwd_train(q, k, v, cu, 400)
+        else:
+            f = na.ne_attn_varlen_fwd(q, k, v, cu, 400, out_f32=form == "f32out")
+        return (f[0], f[1].T) + tuple(f[2:])
+
+    want = fwd(q, k, v)
+    for bad in range(len(LENS)):
+        r = slice(sum(LENS[:bad]), sum(LENS[:bad + 1]))
+        x = dict(q=q, k=k, v=v)
+        x[name] = x[name].clone()
+        x[name][r] = stale
+        others = torch.ones(sum(LENS), dtype=torch.bool, device="cuda")
+        others[r] = False
+        _same(fwd(**x), want, others)
+        assert na.ne_attn_get_device_status() == 0
+
+
+@pytest.mark.parametrize("T", [1, 200, 256, 2100])
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+def test_fixed_length_forward_beside_a_bad_neighbour(na, name, T):
+    """Short sequences rotate their keys in the tiles, long ones (2100) in a pass."""
+    q, k, v, _ = _inputs(5, 3, T, 2, 64)
+    for fwd in (na.ne_attn_fwd, na.ne_attn_fwd_train, na.ne_attn_fwd_rotated):
+        want = fwd(q, k, v)
+        for bad in range(3):
+            x = dict(q=q, k=k, v=v)
+            x[name] = x[name].clone()
+            x[name][bad] = NAN
+            _same(fwd(*x.values()), want, [b for b in range(3) if b != bad])
+            assert na.ne_attn_get_device_status() == 0
