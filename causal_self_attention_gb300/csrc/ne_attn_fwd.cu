@@ -506,7 +506,9 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
         }
         // P = 2^(x - m_ref) in bf16 pairs, computed before P_X / O_X are touched.
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
-        const uint64_t negm2 = f2_pack(-m_ref, -m_ref);
+        // (-inf: no finite score yet, nor a weight; not -inf + inf.)
+        const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
+        const uint64_t negm2 = f2_pack(neg, neg);
         uint64_t acc[4] = {0, 0, 0, 0};  // packed partial row sums (0 = +0.f, +0.f)
         uint32_t pw[64];
 #pragma unroll

@@ -70,6 +70,28 @@ def test_prompt_with_nothing_but_infinite_scores(na):
     within(lse[:, rest], l[:, rest], le[:, rest], "lse")
 
 
+@pytest.mark.parametrize("n,bad", [(500, 128), (500, 300), (2300, 150), (2300, 2200)])
+@pytest.mark.parametrize("form", ["fixed", "train", "packed", "rotated"])
+def test_a_head_each_whose_first_keys_have_infinite_scores(na, form, n, bad):
+    """The forwards without shared heads (from 2048 positions on they rotate their keys in
+    a pass); the rotated operands as the training forward gives them."""
+    q, k, v = _qkv(15, n, n, 3, 3, bad)
+    q[bad:, :, 31] = 16
+    _, _, qr, kr = na.ne_attn_fwd_train(q[None], k[None], v[None])
+    if form == "packed":
+        out, lse = na.ne_attn_varlen_fwd(q, k, v, _i32([0, n]), n)
+    elif form == "rotated":
+        out, lse = (t[0] for t in na.ne_attn_fwd_rotated(qr, kr, v[None]))
+    else:
+        fwd = na.ne_attn_fwd_train if form == "train" else na.ne_attn_fwd
+        out, lse = (t[0] for t in fwd(q[None], k[None], v[None])[:2])
+    assert na.ne_attn_get_device_status() == 0
+    for r in (slice(0, bad), slice(bad, n)):
+        o, l, oe, le = attention(qr[0][r], kr[0][r], v[r], 0.125)
+        within(out[r], o, oe, "out")
+        within(lse[:, r], l, le, "lse")
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("n,bad", [(60, 40), (700, 100), (700, 650), (20000, 5000), (20000, 19990)])
 @pytest.mark.parametrize("low", [False, True])
