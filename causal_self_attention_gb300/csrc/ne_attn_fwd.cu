@@ -487,8 +487,13 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
           for (int cc = 0; cc < 128; ++cc)
             if (cc > r) sr[cc] = 0xff800000u;  // -inf
         }
-        // Row max of the raw scores (the scale is positive), four chains.
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // Row max of the raw scores (the scale is positive), four chains.  From the
+        // lowest number on, not -inf: where all of a step's scores are -inf the
+        // reference stays finite (up to a scale of 1 / log2(e); 0.125 by default), the
+        // weights are zero, and later keys start the row.  (A select on the reference
+        // would do it for any scale, and costs the plain forward 3%.)
+        constexpr float kLow = -3.402823466e38f;
+        float m4[4] = {kLow, kLow, kLow, kLow};
 #pragma unroll
         for (int cc = 0; cc < 128; cc += 8)
 #pragma unroll
@@ -506,9 +511,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
         }
         // P = 2^(x - m_ref) in bf16 pairs, computed before P_X / O_X are touched.
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
-        // (-inf: no finite score yet, nor a weight; not -inf + inf.)
-        const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-        const uint64_t negm2 = f2_pack(neg, neg);
+        const uint64_t negm2 = f2_pack(-m_ref, -m_ref);
         uint64_t acc[4] = {0, 0, 0, 0};  // packed partial row sums (0 = +0.f, +0.f)
         uint32_t pw[64];
 #pragma unroll
