@@ -41,7 +41,7 @@
 // the maximum of a half row while the other half loads (380), the two tiles'
 // exponentials in turns (457 against 413), sixteen softmax warps of half a row
 // (507 against 410), the softmax first in the code (424 against 413).
-// 357-361 us for 16384 tokens, 12 heads on 2 (1,150 TFLOP/s with the pass); 57 us
+// 357-363 us for 16384 tokens, 12 heads on 2 (1,145 TFLOP/s with the pass); 57 us
 // for the packed prompts, 12 heads on 4, of which the pass is 16, the way to the
 // first scores 3, and a CTA's six items of four steps each the rest.  (Clearing V
 // behind a sequence's end took 55.7 to 57.0, by the test's presence alone: the
