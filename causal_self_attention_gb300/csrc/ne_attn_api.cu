@@ -39,6 +39,7 @@ cudaError_t launch_bwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUt
 cudaError_t launch_gqa_rotate(const __nv_bfloat16* q, __nv_bfloat16* qr, const __nv_bfloat16* k,
                               __nv_bfloat16* kr, const Problem& pb, const RopeTable& rope,
                               const ItemList& list, cudaStream_t stream);
+cudaError_t launch_gqa_items(const Problem& pb, const ItemList& list, cudaStream_t stream);
 cudaError_t launch_debug_tile(const CUtensorMap& tm, int h, int row0, int rotate, int pos0,
                               RopeTable rope, void* dst_raw, __nv_bfloat16* dst_rows,
                               int* status, cudaStream_t stream);
@@ -58,16 +59,21 @@ cudaError_t launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, const 
                           bool rot);
 cudaError_t launch_kv_append(const __nv_bfloat16* k, const __nv_bfloat16* v, const int* cu,
                              const int* start_pos, int nseq, int n_tot, const PagedCache& pc,
-                             bool e4m3, const RopeTable& rope, int* status, cudaStream_t stream);
+                             Kv type, const RopeTable& rope, int* status, cudaStream_t stream);
 cudaError_t launch_kv_read(__nv_bfloat16* k, __nv_bfloat16* v, const int* cu,
                            const int* start_pos, int nseq, int n_tot, const PagedCache& pc,
-                           bool e4m3, int* status, cudaStream_t stream);
+                           Kv type, int* status, cudaStream_t stream);
+cudaError_t launch_kv_reserve(const PagesParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_kv_release(const PagesParams& p, int sms, cudaStream_t stream);
+size_t qk_norm_part_bytes();
+cudaError_t launch_qk_norm(const QkNormParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_qk_norm_bwd(const QkNormParams& p, int sms, cudaStream_t stream);
 size_t paged_part_bytes(int B, int H, int Hkv, int max_seqlen);
 size_t paged_counter_bytes();
 unsigned paged_box_rows(int page_size);
 int paged_batch(int H, int Hkv, int max_seqlen);
 cudaError_t launch_decode_paged(const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                const __nv_bfloat16* q, const PagedCache& pc, bool e4m3,
+                                const __nv_bfloat16* q, const PagedCache& pc, Kv type,
                                 const int* seq_lens, int B, int H, const RopeTable& rope,
                                 float scale_log2, float* part, int* arrived, __nv_bfloat16* out,
                                 float* lse, int sms, int* status, cudaStream_t stream,
@@ -636,11 +642,14 @@ ne_status run_fwd(const Shape& s, const void* q, const void* k, const void* v, f
     // Shared heads: the rotation pass builds the work list too.
     items.out = list;
     items.counter = static_cast<int*>(tmp) + (compact ? n_items + 1 : 0);
-    e = ne::launch_gqa_rotate(static_cast<const __nv_bfloat16*>(q),
+    if (pre_rotated)
+      e = ne::launch_gqa_items(p.pb, items, cs);
+    else
+      e = ne::launch_gqa_rotate(static_cast<const __nv_bfloat16*>(q),
                               static_cast<__nv_bfloat16*>(qr_out),
                               static_cast<const __nv_bfloat16*>(k),
                               static_cast<__nv_bfloat16*>(kr_out), p.pb, p.rope, items, cs);
-    if (e == cudaSuccess && g_ev_rot) e = cudaEventRecord(g_ev_rot, cs);
+    if (e == cudaSuccess && g_ev_rot && !pre_rotated) e = cudaEventRecord(g_ev_rot, cs);
     if (e == cudaSuccess)
       e = ne::launch_gqa_fwd(tq, tk, tv, to, p.pb, static_cast<__nv_bfloat16*>(out), lse,
                              p.scale_log2, items, static_cast<int>(n_items), st->sm_count,
@@ -856,6 +865,7 @@ const char* ne_status_string(ne_status s) {
     case NE_ERR_BAD_SEQLEN: return "NE_ERR_BAD_SEQLEN";
     case NE_ERR_TOO_LARGE: return "NE_ERR_TOO_LARGE";
     case NE_ERR_BAD_PAGE: return "NE_ERR_BAD_PAGE";
+    case NE_ERR_NO_PAGES: return "NE_ERR_NO_PAGES";
     default: return "NE_ERR_UNKNOWN";
   }
 }
@@ -1099,7 +1109,41 @@ ne_status ne_attn_gqa_varlen_bwd(const ne_bf16* qr, const ne_bf16* kr, const ne_
                  workspace_bytes, stream, Rot::kTrain);
 }
 
+ne_status ne_attn_gqa_varlen_fwd_rotated(const ne_bf16* qr, const ne_bf16* kr, const ne_bf16* v,
+                                         const int* cu_seqlens, int nseq, int n_tot,
+                                         int max_seqlen, int H, int Hkv, int D, float scale,
+                                         ne_bf16* out, float* lse, void* stream) {
+  Shape s;
+  const ne_status rc = gqa_shape(cu_seqlens, nseq, n_tot, max_seqlen, H, Hkv, D, &s);
+  if (rc != NE_OK) return rc;
+  return run_fwd(s, qr, kr, v, 0.f, scale, out, 0, lse, stream, Rot::kPreRotated);
+}
+
+ne_status ne_attn_gqa_varlen_bwd_rotated(const ne_bf16* qr, const ne_bf16* kr, const ne_bf16* v,
+                                         const ne_bf16* out, const ne_bf16* dout,
+                                         const float* lse, const int* cu_seqlens, int nseq,
+                                         int n_tot, int max_seqlen, int H, int Hkv, int D,
+                                         float scale, ne_bf16* dqr, ne_bf16* dkr, ne_bf16* dv,
+                                         void* workspace, size_t workspace_bytes, void* stream) {
+  Shape s;
+  const ne_status rc = gqa_shape(cu_seqlens, nseq, n_tot, max_seqlen, H, Hkv, D, &s);
+  if (rc != NE_OK) return rc;
+  return run_bwd(s, qr, kr, v, out, dout, lse, 0.f, scale, dqr, dkr, dv, workspace,
+                 workspace_bytes, stream, Rot::kPreRotated);
+}
+
 namespace {
+// log2 of a page's positions, -1 for a size that is not supported.
+int page_shift_of(int page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+ne::Kv kv_of(int kv_type) {
+  return kv_type == NE_KV_E2M1 ? ne::Kv::kE2m1 : kv_type == NE_KV_E4M3 ? ne::Kv::kE4m3 : ne::Kv::kBf16;
+}
+
 // The checks that every call on a paged cache shares; fills *pc.
 ne_status paged_cache(const void* k_pages, const void* v_pages, const uint8_t* k_scale,
                       const uint8_t* v_scale, int kv_type, const int* block_table, int max_pages,
@@ -1107,10 +1151,10 @@ ne_status paged_cache(const void* k_pages, const void* v_pages, const uint8_t* k
                       ne::PagedCache* pc) {
   if (!k_pages || !v_pages || !block_table) return NE_ERR_INVALID_ARG;
   if (D != 64) return NE_ERR_UNSUPPORTED;
-  if (kv_type != NE_KV_BF16 && kv_type != NE_KV_E4M3) return NE_ERR_UNSUPPORTED;
-  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 &&
-      page_size != 256)
+  if (kv_type != NE_KV_BF16 && kv_type != NE_KV_E4M3 && kv_type != NE_KV_E2M1)
     return NE_ERR_UNSUPPORTED;
+  const int page_shift = page_shift_of(page_size);
+  if (page_shift < 0) return NE_ERR_UNSUPPORTED;
   if (max_pages <= 0 || n_pages <= 0 || Hkv <= 0 || max_seqlen <= 0) return NE_ERR_INVALID_ARG;
   if (max_seqlen > static_cast<long long>(max_pages) * page_size) return NE_ERR_INVALID_ARG;
   // Rows of a pool are numbered in 32 bits by the tile loads (their
@@ -1118,20 +1162,20 @@ ne_status paged_cache(const void* k_pages, const void* v_pages, const uint8_t* k
   if (static_cast<long long>(n_pages) * Hkv > ((1LL << 31) - 1 - 256) / page_size)
     return NE_ERR_INVALID_ARG;
   if ((max_seqlen + 127) / 128 > 65535) return NE_ERR_INVALID_ARG;
-  if (kv_type == NE_KV_E4M3 && (!k_scale || !v_scale)) return NE_ERR_INVALID_ARG;
+  const bool scaled = kv_type != NE_KV_BF16;
+  if (scaled && (!k_scale || !v_scale)) return NE_ERR_INVALID_ARG;
   if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(block_table))
     return NE_ERR_MISALIGNED;
-  if (kv_type == NE_KV_E4M3 && (!aligned16(k_scale) || !aligned16(v_scale)))
+  if (scaled && (!aligned16(k_scale) || !aligned16(v_scale)))
     return NE_ERR_MISALIGNED;
   pc->k = const_cast<void*>(k_pages);
   pc->v = const_cast<void*>(v_pages);
-  pc->k_scale = kv_type == NE_KV_E4M3 ? const_cast<uint8_t*>(k_scale) : nullptr;
-  pc->v_scale = kv_type == NE_KV_E4M3 ? const_cast<uint8_t*>(v_scale) : nullptr;
+  pc->k_scale = scaled ? const_cast<uint8_t*>(k_scale) : nullptr;
+  pc->v_scale = scaled ? const_cast<uint8_t*>(v_scale) : nullptr;
   pc->block_table = block_table;
   pc->max_pages = max_pages;
   pc->n_pages = n_pages;
-  pc->page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6
-                   : page_size == 128 ? 7 : 8;
+  pc->page_shift = page_shift;
   pc->Hkv = Hkv;
   pc->max_seqlen = max_seqlen;
   return NE_OK;
@@ -1172,7 +1216,7 @@ ne_status ne_kv_append(const ne_bf16* k, const ne_bf16* v, const int* cu_seqlens
     return rc;
   return cuda_status(ne::launch_kv_append(reinterpret_cast<const __nv_bfloat16*>(k),
                                           reinterpret_cast<const __nv_bfloat16*>(v), cu_seqlens,
-                                          start_pos, nseq, n_tot, pc, kv_type == NE_KV_E4M3, rope,
+                                          start_pos, nseq, n_tot, pc, kv_of(kv_type), rope,
                                           st->status, cs));
 }
 
@@ -1192,7 +1236,7 @@ ne_status ne_kv_read(int kv_type, const void* k_pages, const void* v_pages,
   if ((rc = device_state(&st)) != NE_OK) return rc;
   return cuda_status(ne::launch_kv_read(reinterpret_cast<__nv_bfloat16*>(k),
                                         reinterpret_cast<__nv_bfloat16*>(v), cu_seqlens,
-                                        start_pos, nseq, n_tot, pc, kv_type == NE_KV_E4M3,
+                                        start_pos, nseq, n_tot, pc, kv_of(kv_type),
                                         st->status, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1254,7 +1298,7 @@ ne_status decode_paged(const ne_bf16* q, int kv_type, const void* k_pages, const
   if (owned && (e = cudaMallocAsync(&ws, need, cs)) != cudaSuccess) return cuda_status(e);
   if (!ws && (rc = stream_scratch(*st, cs, need, &ws)) != NE_OK) return rc;
   e = ne::launch_decode_paged(tk, tv, reinterpret_cast<const __nv_bfloat16*>(q), pc,
-                              kv_type == NE_KV_E4M3, seq_lens, B, H, rope,
+                              kv_of(kv_type), seq_lens, B, H, rope,
                               scale * 1.4426950408889634f, static_cast<float*>(ws), arrived,
                               reinterpret_cast<__nv_bfloat16*>(out), lse, st->sm_count, st->status,
                               cs, drop_cta);
@@ -1286,6 +1330,212 @@ ne_status ne_debug_decode_drop(const ne_bf16* q, const ne_bf16* k_pages, const n
   return decode_paged(q, NE_KV_BF16, k_pages, v_pages, nullptr, nullptr, block_table, max_pages,
                       n_pages, page_size, max_seqlen, seq_lens, B, H, Hkv, 64, 0.f, scale, out,
                       lse, nullptr, 0, stream, drop_cta);
+}
+
+namespace {
+// Whether a call is being captured, and an arrival counter for it.
+ne_status arrival_counter(DeviceState& st, cudaStream_t cs, int** arrived) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(cs, &capture) != cudaSuccess) return NE_ERR_CUDA;
+  return counter_set(st, cs, capture != cudaStreamCaptureStatusNone, ne::paged_counter_bytes(),
+                     arrived);
+}
+
+// The checks that ne_kv_reserve and ne_kv_release share; fills what they share.
+ne_status pages_params(const int* seq_lens, int nseq, const int* block_table, int max_pages,
+                       const int* free_pages, const int* n_free, int n_pages, int page_size,
+                       int max_seqlen, ne::PagesParams* p) {
+  if (!seq_lens || !block_table || !free_pages || !n_free) return NE_ERR_INVALID_ARG;
+  p->page_shift = page_shift_of(page_size);
+  if (p->page_shift < 0) return NE_ERR_UNSUPPORTED;
+  if (nseq <= 0 || max_pages <= 0 || n_pages <= 0 || max_seqlen <= 0) return NE_ERR_INVALID_ARG;
+  if (nseq > ne::kMaxPagedSequences) return NE_ERR_INVALID_ARG;
+  if (max_seqlen > static_cast<long long>(max_pages) * page_size) return NE_ERR_INVALID_ARG;
+  if ((max_seqlen + 127LL) / 128 > 65535) return NE_ERR_INVALID_ARG;
+  if (n_pages > ((1LL << 31) - 1) / page_size) return NE_ERR_INVALID_ARG;  // slots in 31 bits
+  if (!aligned4(seq_lens) || !aligned4(block_table) || !aligned4(free_pages) || !aligned4(n_free))
+    return NE_ERR_MISALIGNED;
+  p->seq_lens = seq_lens;
+  p->nseq = nseq;
+  p->max_pages = max_pages;
+  p->free_pages = free_pages;
+  p->n_free = n_free;
+  p->n_pages = n_pages;
+  p->max_seqlen = max_seqlen;
+  return NE_OK;
+}
+}  // namespace
+
+ne_status ne_kv_reserve(const int* new_lens, const int* seq_lens, int nseq, int* block_table,
+                        int max_pages, const int* free_pages, const int* n_free, int n_pages,
+                        int page_size, int max_seqlen, int n_tot, int* cu_seqlens, int* start_pos,
+                        int* positions, int* slots, int* seq_lens_out, int* n_free_out,
+                        void* stream) {
+  ne::PagesParams p = {};
+  if (!new_lens || !seq_lens_out || !n_free_out) return NE_ERR_INVALID_ARG;
+  ne_status rc = pages_params(seq_lens, nseq, block_table, max_pages, free_pages, n_free, n_pages,
+                              page_size, max_seqlen, &p);
+  if (rc != NE_OK) return rc;
+  if (n_tot < 0 || n_tot > 1 << 30) return NE_ERR_INVALID_ARG;
+  if (!aligned4(new_lens) || !aligned4(cu_seqlens) || !aligned4(start_pos) ||
+      !aligned4(positions) || !aligned4(slots) || !aligned4(seq_lens_out) || !aligned4(n_free_out))
+    return NE_ERR_MISALIGNED;
+  p.new_lens = new_lens;
+  p.block_table = block_table;
+  p.n_tot = positions || slots ? n_tot : 0;
+  p.max_rows = positions || slots ? n_tot : 0x7fffffff;
+  p.cu_seqlens = cu_seqlens;
+  p.start_pos = start_pos;
+  p.positions = positions;
+  p.slots = slots;
+  p.seq_lens_out = seq_lens_out;
+  p.n_free_out = n_free_out;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != NE_OK) return rc;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if ((rc = arrival_counter(*st, cs, &p.arrived)) != NE_OK) return rc;
+  p.status = st->status;
+  return cuda_status(ne::launch_kv_reserve(p, st->sm_count, cs));
+}
+
+ne_status ne_kv_release(const uint8_t* finished, int* seq_lens, int nseq, int* block_table,
+                        int max_pages, int* free_pages, int* n_free, int n_pages, int page_size,
+                        int max_seqlen, void* stream) {
+  ne::PagesParams p = {};
+  if (!finished) return NE_ERR_INVALID_ARG;
+  ne_status rc = pages_params(seq_lens, nseq, block_table, max_pages, free_pages, n_free, n_pages,
+                              page_size, max_seqlen, &p);
+  if (rc != NE_OK) return rc;
+  p.finished = finished;
+  p.seq_lens_out = seq_lens;
+  p.block_table = block_table;
+  p.free_pages_out = free_pages;
+  p.n_free_out = n_free;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != NE_OK) return rc;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if ((rc = arrival_counter(*st, cs, &p.arrived)) != NE_OK) return rc;
+  p.status = st->status;
+  return cuda_status(ne::launch_kv_release(p, st->sm_count, cs));
+}
+
+namespace {
+// The checks that ne_qk_norm_rope_fwd and ..._bwd share; fills what they share.
+ne_status qk_norm_params(const ne_bf16* q, const ne_bf16* k, long long q_stride,
+                         long long k_stride, const ne_bf16* q_weight, const ne_bf16* k_weight,
+                         const int* positions, int n_tot, int H, int Hkv, int D, int max_seqlen,
+                         float eps, float rope_base, ne::QkNormParams* p) {
+  if (!q || !k || !q_weight || !k_weight) return NE_ERR_INVALID_ARG;
+  if (D != 64) return NE_ERR_UNSUPPORTED;
+  if (n_tot <= 0 || H <= 0 || Hkv <= 0 || max_seqlen <= 0) return NE_ERR_INVALID_ARG;
+  if (static_cast<long long>(n_tot) * (static_cast<long long>(H) + Hkv) > (1LL << 31) - 1)
+    return NE_ERR_INVALID_ARG;
+  if ((max_seqlen + 127LL) / 128 > 65535) return NE_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.f || bad_base_or_none(rope_base)) return NE_ERR_INVALID_ARG;
+  if (!positions && rope_base > 0.f) return NE_ERR_INVALID_ARG;
+  if (q_stride < 64LL * H || k_stride < 64LL * Hkv || q_stride > 1LL << 31 || k_stride > 1LL << 31)
+    return NE_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_weight) || !aligned16(k_weight) ||
+      q_stride % 8 != 0 || k_stride % 8 != 0 || !aligned4(positions))
+    return NE_ERR_MISALIGNED;
+  p->q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p->k = reinterpret_cast<const __nv_bfloat16*>(k);
+  p->q_stride = q_stride;
+  p->k_stride = k_stride;
+  p->qw = reinterpret_cast<const __nv_bfloat16*>(q_weight);
+  p->kw = reinterpret_cast<const __nv_bfloat16*>(k_weight);
+  p->positions = positions;
+  p->n_tot = n_tot;
+  p->H = H;
+  p->Hkv = Hkv;
+  p->max_seqlen = max_seqlen;
+  p->eps = eps;
+  return NE_OK;
+}
+}  // namespace
+
+ne_status ne_qk_norm_rope_fwd(const ne_bf16* q, const ne_bf16* k, long long q_stride,
+                              long long k_stride, const ne_bf16* q_weight,
+                              const ne_bf16* k_weight, const int* positions, int n_tot, int H,
+                              int Hkv, int D, int max_seqlen, float eps, float rope_base,
+                              ne_bf16* qr, ne_bf16* kr, void* stream) {
+  ne::QkNormParams p = {};
+  ne_status rc = qk_norm_params(q, k, q_stride, k_stride, q_weight, k_weight, positions, n_tot, H,
+                                Hkv, D, max_seqlen, eps, rope_base, &p);
+  if (rc != NE_OK) return rc;
+  if (!qr || !kr) return NE_ERR_INVALID_ARG;
+  if (!aligned16(qr) || !aligned16(kr)) return NE_ERR_MISALIGNED;
+  p.qr = reinterpret_cast<__nv_bfloat16*>(qr);
+  p.kr = reinterpret_cast<__nv_bfloat16*>(kr);
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != NE_OK) return rc;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (rope_base > 0.f && (rc = rope_table(*st, rope_base, max_seqlen, cs, &p.rope)) != NE_OK)
+    return rc;
+  p.status = st->status;
+  return cuda_status(ne::launch_qk_norm(p, st->sm_count, cs));
+}
+
+size_t ne_qk_norm_rope_bwd_workspace_bytes(void) { return ne::qk_norm_part_bytes(); }
+
+ne_status ne_qk_norm_rope_bwd(const ne_bf16* dqr, const ne_bf16* dkr, const ne_bf16* q,
+                              const ne_bf16* k, long long q_stride, long long k_stride,
+                              const ne_bf16* q_weight, const ne_bf16* k_weight,
+                              const int* positions, int n_tot, int H, int Hkv, int D,
+                              int max_seqlen, float eps, float rope_base, ne_bf16* dq, ne_bf16* dk,
+                              long long dq_stride, long long dk_stride, float* dq_weight,
+                              float* dk_weight, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  ne::QkNormParams p = {};
+  ne_status rc = qk_norm_params(q, k, q_stride, k_stride, q_weight, k_weight, positions, n_tot, H,
+                                Hkv, D, max_seqlen, eps, rope_base, &p);
+  if (rc != NE_OK) return rc;
+  if (!dqr || !dkr || !dq || !dk || !dq_weight || !dk_weight) return NE_ERR_INVALID_ARG;
+  if (dq_stride < 64LL * H || dk_stride < 64LL * Hkv || dq_stride > 1LL << 31 ||
+      dk_stride > 1LL << 31)
+    return NE_ERR_INVALID_ARG;
+  if (!aligned16(dqr) || !aligned16(dkr) || !aligned16(dq) || !aligned16(dk) ||
+      dq_stride % 8 != 0 || dk_stride % 8 != 0 || !aligned16(dq_weight) || !aligned16(dk_weight))
+    return NE_ERR_MISALIGNED;
+  const size_t need = ne::qk_norm_part_bytes();
+  if (workspace && workspace_bytes < need) return NE_ERR_INVALID_ARG;
+  if (workspace && !aligned16(workspace)) return NE_ERR_MISALIGNED;
+  p.dqr = reinterpret_cast<const __nv_bfloat16*>(dqr);
+  p.dkr = reinterpret_cast<const __nv_bfloat16*>(dkr);
+  p.dq = reinterpret_cast<__nv_bfloat16*>(dq);
+  p.dk = reinterpret_cast<__nv_bfloat16*>(dk);
+  p.dq_stride = dq_stride;
+  p.dk_stride = dk_stride;
+  p.dqw = dq_weight;
+  p.dkw = dk_weight;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st)) != NE_OK) return rc;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (rope_base > 0.f && (rc = rope_table(*st, rope_base, max_seqlen, cs, &p.rope)) != NE_OK)
+    return rc;
+  p.status = st->status;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(cs, &capture) != cudaSuccess) return NE_ERR_CUDA;
+  const bool captured = capture != cudaStreamCaptureStatusNone;
+  if ((rc = counter_set(*st, cs, captured, ne::paged_counter_bytes(), &p.arrived)) != NE_OK)
+    return rc;
+  // As the paged decode: the library's temporary for this stream, or nodes of the graph.
+  void* ws = workspace;
+  const bool owned = !ws && captured;
+  cudaError_t e = cudaSuccess;
+  if (owned && (e = cudaMallocAsync(&ws, need, cs)) != cudaSuccess) return cuda_status(e);
+  if (!ws && (rc = stream_scratch(*st, cs, need, &ws)) != NE_OK) return rc;
+  p.part = static_cast<float*>(ws);
+  e = ne::launch_qk_norm_bwd(p, st->sm_count, cs);
+  if (owned) {
+    const cudaError_t e2 = cudaFreeAsync(ws, cs);
+    if (e == cudaSuccess) e = e2;
+  }
+  return cuda_status(e);
 }
 
 size_t ne_attn_decode_workspace_bytes(int B, int H, int Tmax) {
@@ -1585,6 +1835,7 @@ ne_status ne_attn_get_device_status(void* stream) {
   if (code == ne::NE_DEV_OK) return NE_OK;
   if (code == ne::NE_DEV_BAD_SEQLEN) return NE_ERR_BAD_SEQLEN;
   if (code == ne::NE_DEV_BAD_PAGE) return NE_ERR_BAD_PAGE;
+  if (code == ne::NE_DEV_NO_PAGES) return NE_ERR_NO_PAGES;
   if (code >= ne::NE_DEV_TIMEOUT_BASE) return NE_ERR_TIMEOUT;
   return NE_ERR_CUDA;
 }

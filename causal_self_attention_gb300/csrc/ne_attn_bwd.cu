@@ -1030,7 +1030,8 @@ __global__ void __launch_bounds__(512, 1)
         // table in the layout whose lines are a warp's 32 positions (the table has
         // every position of a tile).  The other form's postprocess rotates.  (8 x 1024, a
         // head each, 78 us as in that form; by rows of the table, a line a lane, 83.)
-        if (half) {
+        // No table: the gradient w.r.t. k' is asked for.
+        if (half && p.rope.csw) {
           const float4* cs = p.rope.csw + 16LL * 32 * (4 * u.kt + wq) + lane;
 #pragma unroll
           for (int i0 = 0; i0 < 16; i0 += 8) {
@@ -1275,7 +1276,7 @@ __global__ void __launch_bounds__(kPostThreads)
       const float sc = is_q ? scale : 1.f;
       float a[4] = {lo[u].x * sc, lo[u].y * sc, lo[u].z * sc, lo[u].w * sc};
       float b[4] = {hi[u].x * sc, hi[u].y * sc, hi[u].z * sc, hi[u].w * sc};
-      if (!is_v) {
+      if (!is_v && rope.cs) {  // (no table: the gradients w.r.t. q', k' themselves)
         const float4* cs4 =
             reinterpret_cast<const float4*>(rope.cs + static_cast<long long>(pos) * 32 + part * 4);
         const float4 t0 = __ldg(cs4), t1 = __ldg(cs4 + 1);  // (cos, sin) of dims 4c .. 4c + 3

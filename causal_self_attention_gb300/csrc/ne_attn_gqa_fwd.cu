@@ -874,4 +874,15 @@ cudaError_t launch_gqa_rotate(const __nv_bfloat16* q, __nv_bfloat16* qr, const _
                     k, kr, pb, rope, rows, list);
 }
 
+// The pass's other work alone, for operands that come rotated: the work list (that
+// CTA of it), or, where none is wanted, the counter.
+cudaError_t launch_gqa_items(const Problem& pb, const ItemList& list, cudaStream_t stream) {
+  if (!list.out) return cudaMemsetAsync(list.counter, 0, sizeof(int), stream);
+  return launch_pdl(ne_attn_gqa_rotate_kernel, dim3(1), dim3(kRopeThreads),
+                    sizeof(int) * list.n_buckets, stream,
+                    static_cast<const __nv_bfloat16*>(nullptr), static_cast<__nv_bfloat16*>(nullptr),
+                    static_cast<const __nv_bfloat16*>(nullptr), static_cast<__nv_bfloat16*>(nullptr),
+                    pb, RopeTable{nullptr, nullptr, 0}, 1, list);
+}
+
 }  // namespace ne

@@ -74,21 +74,23 @@ constexpr float kBad = INFINITY;               // lse of a part that met a page 
 constexpr int kQRow = 144;                     // bytes of a q row in shared memory (banks)
 constexpr int kQSlots = 2;
 
-template <bool kE4m3>
+template <Kv kType>
 struct Tile {
-  static constexpr int kKeys = kE4m3 ? 32 : 16;         // of a warp
-  static constexpr int kTile = kWarps * kKeys;          // 128 / 64 keys
-  static constexpr int kRowBytes = kE4m3 ? kHD : 2 * kHD;
-  static constexpr int kPool = kTile * kRowBytes;       // 8 KiB of K, and of V
-  static constexpr int kStageBytes = 2 * kPool + (kE4m3 ? 2 * kTile : 0);
+  static constexpr int kKeys = kType == Kv::kBf16 ? 16 : 32;  // of a warp
+  static constexpr int kTile = kWarps * kKeys;                // 128 / 64 keys
+  static constexpr int kRowBytes = kType == Kv::kE2m1 ? kHD / 2 : kType == Kv::kE4m3 ? kHD : 2 * kHD;
+  static constexpr int kScales = kType == Kv::kE2m1 ? 2 : kType == Kv::kE4m3 ? 1 : 0;  // of a row
+  static constexpr int kPool = kTile * kRowBytes;             // 8 KiB (e2m1: 4) of K, and of V
+  static constexpr int kStageBytes = 2 * kPool + 2 * kScales * kTile;
 };
 
-template <bool kE4m3, int kRows>
+template <Kv kType, int kRows>
 struct Cfg {
   static constexpr int kCtas = kRows == 8 ? 3 : 2;      // per SM
-  static constexpr int kStages = kRows == 8 ? 3 : 4;
-  static constexpr int OFF_RED = kStages * Tile<kE4m3>::kStageBytes;
-  static constexpr int kRedRow = kHD + 4;                // m, l, m2, bad, o[64]
+  static constexpr int kStages = (kRows == 8 ? 3 : 4) * (kType == Kv::kE2m1 ? 2 : 1);
+  static constexpr int OFF_RED = kStages * Tile<kType>::kStageBytes;
+  // m, l, m2, bad, o[64]; e2m1: the other half's m2
+  static constexpr int kRedRow = kHD + (kType == Kv::kE2m1 ? 8 : 4);
   static constexpr int OFF_Q = OFF_RED + kWarps * kRows * kRedRow * 4;
   static constexpr int kQBytes = kRows * kQRow + 256;    // q rows, one row of the RoPE table
   static constexpr int OFF_PREFIX = OFF_Q + kQSlots * kQBytes;
@@ -206,16 +208,43 @@ __device__ __forceinline__ int e4m3_key(int mt, int x) {
   const int c = (x & 7) >> 1;
   return 16 * mt + (x & 8) + ((x & 1) ? 4 + (c ^ 1) : c);
 }
+// The same for e2m1, whose rows are 32 bytes: the four rows that a half warp reads
+// of K (8 bytes a lane) and the four lanes c of V (4 bytes) differ mod 4.
+__device__ __forceinline__ int e2m1_key(int mt, int x) {
+  const int c = (x & 7) >> 1;
+  return 16 * mt + (x & 8) + ((x & 1) ? 4 + (c ^ 2) : c);
+}
+template <Kv kType>
+__device__ __forceinline__ int key_of(int mt, int x) {
+  return kType == Kv::kBf16 ? 16 * mt + x : kType == Kv::kE4m3 ? e4m3_key(mt, x) : e2m1_key(mt, x);
+}
+// Two scale bytes -> 2^(byte - 127) as two bf16 (exact; 255: NaN).
+__device__ __forceinline__ uint32_t scales_bf16x2(uint32_t two) {
+  uint32_t b = two & 255u, c = two >> 8;
+  b = b == 255u ? 0x7fc0u : b == 0u ? 0x40u : b << 7;
+  c = c == 255u ? 0x7fc0u : c == 0u ? 0x40u : c << 7;
+  return b | (c << 16);
+}
+// ... and their exponents (byte - 127), as two bf16 (exact; 255: NaN).
+__device__ __forceinline__ uint32_t exponents_bf16x2(uint32_t two) {
+  const uint32_t b = two & 255u, c = two >> 8;
+  const uint32_t e = pack_bf16x2(static_cast<float>(static_cast<int>(b) - 127),
+                                 static_cast<float>(static_cast<int>(c) - 127));
+  return (b == 255u ? 0x7fc0u : e & 0xffffu) | (c == 255u ? 0x7fc00000u : e & 0xffff0000u);
+}
 }  // namespace paged
 
 // kDrop: a tile of one CTA never arrives, for the tests of a wait that runs out.
-template <bool kE4m3, int kRows, bool kDrop>
-__global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCtas)
+template <Kv kType, int kRows, bool kDrop>
+__global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCtas)
     ne_attn_paged_kernel(const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const paged::Params p) {
   using namespace paged;
-  using T = Tile<kE4m3>;
-  using L = Cfg<kE4m3, kRows>;
+  using T = Tile<kType>;
+  using L = Cfg<kType, kRows>;
+  constexpr bool kE2m1 = kType == Kv::kE2m1;
+  constexpr bool kF16 = kType != Kv::kBf16;  // products of halves, scales per row
+  constexpr int kParts = kE2m1 ? 2 : 1;      // parts of a row with a scale each
   constexpr int kStages = L::kStages;
   constexpr int kNT = kRows / 8;           // column tiles: 8 query heads each
   constexpr int kMT = T::kKeys / 16;       // row tiles of a warp's keys
@@ -296,7 +325,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ the loads
-    if constexpr (!kE4m3) {
+    if constexpr (!kF16) {
       if (lane == 0) {
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
@@ -362,19 +391,21 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
           stage_bad[st] = bad;
           if (bad) atomicCAS(p.status, 0, NE_DEV_BAD_PAGE);
           const uint32_t copies = pg1 - pg0 + 1;
-          mbar_arrive_expect_tx(&full[st], copies * box * (2 * T::kRowBytes + (kE4m3 ? 2 : 0)));
+          mbar_arrive_expect_tx(&full[st], copies * box * 2 * (T::kRowBytes + T::kScales));
         }
         __syncwarp();
         if (mine) {
           const int off = lane * box;  // first key of the copy in the tile
           const long long row = kv::pool_row(p.pc, page, hk, page_size < T::kTile ? 0 : key0);
-          if constexpr (kE4m3) {
-            bulk_load(sk + off * kHD, static_cast<const uint8_t*>(p.pc.k) + row * kHD, box * kHD,
+          if constexpr (kF16) {
+            constexpr int kB = T::kRowBytes, kS = T::kScales;
+            bulk_load(sk + off * kB, static_cast<const uint8_t*>(p.pc.k) + row * kB, box * kB,
                       &full[st]);
-            bulk_load(sv + off * kHD, static_cast<const uint8_t*>(p.pc.v) + row * kHD, box * kHD,
+            bulk_load(sv + off * kB, static_cast<const uint8_t*>(p.pc.v) + row * kB, box * kB,
                       &full[st]);
-            bulk_load(sv + T::kPool + off, p.pc.k_scale + row, box, &full[st]);
-            bulk_load(sv + T::kPool + T::kTile + off, p.pc.v_scale + row, box, &full[st]);
+            bulk_load(sv + T::kPool + off * kS, p.pc.k_scale + row * kS, box * kS, &full[st]);
+            bulk_load(sv + T::kPool + (T::kTile + off) * kS, p.pc.v_scale + row * kS, box * kS,
+                      &full[st]);
           } else {
             tma_load_2d(sk + off * 128, &tmK, &full[st], 0, static_cast<int>(row));
             tma_load_2d(sv + off * 128, &tmV, &full[st], 0, static_cast<int>(row));
@@ -439,8 +470,11 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
         for (int u = 0; u < 2; ++u) {
           // bf16: k-step k holds dims 16 k + 2 c (+ 1) and + 8 (+ 9).  e4m3:
           // dims 16 c + 4 k .. + 3 (any order of the contraction will do, if
-          // K's has it too).
-          const int d = kE4m3 ? 16 * c + 4 * k + 2 * u : 16 * k + 2 * c + 8 * u;
+          // K's has it too).  e2m1: k-steps 0, 1 the first half, dims 8 c + 4 k ..,
+          // 2, 3 the second.
+          const int d = kE2m1 ? 32 * (k >> 1) + 8 * c + 4 * (k & 1) + 2 * u
+                        : kF16 ? 16 * c + 4 * k + 2 * u
+                               : 16 * k + 2 * c + 8 * u;
           const uint32_t me = *reinterpret_cast<const uint32_t*>(row + 2 * d);
           float v0 = bf16lo_to_f32(me), v1 = bf16hi_to_f32(me);
           if (p.rope.cs) {
@@ -451,7 +485,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
             v1 = __fmaf_rn(v1, t.z, sg * __fmul_rn(bf16hi_to_f32(other), t.w));
           }
           const uint32_t w2 = pack_bf16x2(v0, v1);  // the operator's q'
-          if constexpr (kE4m3) {
+          if constexpr (kF16) {
             a[k][2 * u] = bf16lo_to_f32(w2);
             a[k][2 * u + 1] = bf16hi_to_f32(w2);
             top = fmaxf(top, fmaxf(fabsf(a[k][2 * u]), fabsf(a[k][2 * u + 1])));
@@ -460,7 +494,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
           }
         }
       f[nt][0] = f[nt][1] = p.scale_log2;
-      if constexpr (kE4m3) {
+      if constexpr (kF16) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 2^-e with 2^e <= top < 2^(e+1): |q' 2^-e| < 2.  (0 and what is not
@@ -482,13 +516,16 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
     if (ok && lane == 0) mbar_arrive(&qempty[slot]);
 
     // References (the same in every lane of a column), sums (this lane's keys).
-    float m[kNT][2], m2[kNT][2], l[kNT][2];
+    // (m2: of the weights with their value rows' scales, for each scale of a row.)
+    float m[kNT][2], m2[kNT][2][kParts], l[kNT][2];
     float o[kNT][4][4];
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[nt][e] = m2[nt][e] = -INFINITY;
+        m[nt][e] = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) m2[nt][e][h] = -INFINITY;
         l[nt][e] = 0.f;
       }
 #pragma unroll
@@ -507,7 +544,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
       uint8_t* sk = smem + st * T::kStageBytes + warp * T::kKeys * T::kRowBytes;
       uint8_t* sv = sk + T::kPool;
       const int live = n - t * T::kTile - warp * T::kKeys;  // of this warp's keys, from the first
-      if (live < T::kKeys) {
+      if (!kE2m1 && live < T::kKeys) {  // (an e2m1 row is finite whatever its bytes)
         // Past the end: clear the value rows (16 bytes a lane and step).
         const int first = max(live, 0) * T::kRowBytes;
         for (int i = first + 16 * lane; i < T::kKeys * T::kRowBytes; i += 512)
@@ -517,14 +554,61 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
       }
       // Scores: [row tile][column tile][key r: heads 2c, 2c+1; key r + 8: the same].
       float sc[kMT][kNT][4];
-      float ev[kMT][2];  // e4m3: exponents of the value rows' scales
+      float ev[kMT][2][kParts];  // exponents of the value rows' scales
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
-      if constexpr (kE4m3) {
+      if constexpr (kE2m1) {
+        const uint16_t* scales =
+            reinterpret_cast<const uint16_t*>(smem + st * T::kStageBytes + 2 * T::kPool) +
+            warp * T::kKeys;
+        const uint32_t ks2 = scales_bf16x2(scales[lane]);
+        const uint32_t vs2 = exponents_bf16x2(scales[T::kTile + lane]);
+        // Products with each half of a row, then their sum with the halves' scales.
+        float s2[kMT][kNT][4];
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+          const uint2 w0 = *reinterpret_cast<const uint2*>(sk + e2m1_key(mt, r) * T::kRowBytes + 8 * c);
+          const uint2 w1 = *reinterpret_cast<const uint2*>(sk + e2m1_key(mt, r + 8) * T::kRowBytes + 8 * c);
+          uint32_t x0[2][4], x1[2][4];  // [word][byte]: halves of rows r, r + 8
+          kv::e2m1x8_to_f16x2(w0.x, x0[0]);
+          kv::e2m1x8_to_f16x2(w0.y, x0[1]);
+          kv::e2m1x8_to_f16x2(w1.x, x1[0]);
+          kv::e2m1x8_to_f16x2(w1.y, x1[1]);
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s2[mt][nt][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t lo[4] = {x0[k][0], x1[k][0], x0[k][1], x1[k][1]};
+              const uint32_t hi[4] = {x0[k][2], x1[k][2], x0[k][3], x1[k][3]};
+              mma16816<true>(sc[mt][nt], lo, qb[nt][k][0], qb[nt][k][1]);
+              mma16816<true>(s2[mt][nt], hi, qb[nt][2 + k][0], qb[nt][2 + k][1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int key = e2m1_key(mt, r + 8 * hf);
+            const uint32_t ks = __shfl_sync(0xffffffffu, ks2, key);
+            const uint32_t vs = __shfl_sync(0xffffffffu, vs2, key);
+            ev[mt][hf][0] = bf16lo_to_f32(vs);
+            ev[mt][hf][kParts - 1] = bf16hi_to_f32(vs);
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& x = sc[mt][nt][2 * hf + e];
+                x = __fmaf_rn(s2[mt][nt][2 * hf + e], bf16hi_to_f32(ks), x * bf16lo_to_f32(ks)) * f[nt][e];
+              }
+          }
+      } else if constexpr (kF16) {
         const uint8_t* scales = smem + st * T::kStageBytes + 2 * T::kPool + warp * T::kKeys;
         const int kb = scales[lane], vb = scales[T::kTile + lane];
 #pragma unroll
@@ -550,7 +634,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
           for (int hf = 0; hf < 2; ++hf) {
             const int key = e4m3_key(mt, r + 8 * hf);
             const float ks = __shfl_sync(0xffffffffu, kf, key);
-            ev[mt][hf] = __shfl_sync(0xffffffffu, vf, key);
+            ev[mt][hf][0] = __shfl_sync(0xffffffffu, vf, key);
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -580,44 +664,54 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const int key = kE4m3 ? e4m3_key(mt, r + 8 * hf) : 16 * mt + r + 8 * hf;
-            if (key >= live) {
+            if (key_of<kType>(mt, r + 8 * hf) >= live) {
 #pragma unroll
               for (int nt = 0; nt < kNT; ++nt)
                 sc[mt][nt][2 * hf] = sc[mt][nt][2 * hf + 1] = -INFINITY;
-              if (kE4m3) ev[mt][hf] = 0.f;
+#pragma unroll
+              for (int h = 0; h < kParts; ++h)
+                if (kF16) ev[mt][hf][h] = 0.f;
             }
           }
       }
       // A score above its reference by more than 2^8 anywhere in the warp (the
       // first keys: m = -inf): move the references to the maxima.
-      float mx[kNT][2], mx2[kNT][2];
+      float mx[kNT][2], mx2[kNT][2][kParts];
       bool over = false;
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[nt][e] = mx2[nt][e] = -INFINITY;
+          mx[nt][e] = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < kParts; ++h) mx2[nt][e][h] = -INFINITY;
 #pragma unroll
           for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               mx[nt][e] = fmaxf(mx[nt][e], sc[mt][nt][2 * hf + e]);
-              if (kE4m3) mx2[nt][e] = fmaxf(mx2[nt][e], sc[mt][nt][2 * hf + e] + ev[mt][hf]);
+#pragma unroll
+              for (int h = 0; h < kParts; ++h)
+                if (kF16) mx2[nt][e][h] = fmaxf(mx2[nt][e][h], sc[mt][nt][2 * hf + e] + ev[mt][hf][h]);
             }
           over |= mx[nt][e] > m[nt][e] + 8.f;
-          if (kE4m3) over |= mx2[nt][e] > m2[nt][e] + 8.f;
+#pragma unroll
+          for (int h = 0; h < kParts; ++h)
+            if (kF16) over |= mx2[nt][e][h] > m2[nt][e][h] + 8.f;
         }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float a = mx[nt][e], b = mx2[nt][e];
+            float a = mx[nt][e];
 #pragma unroll
             for (int sh = 4; sh < 32; sh <<= 1) {
               a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, sh));
-              if (kE4m3) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, sh));
+#pragma unroll
+              for (int h = 0; h < kParts; ++h)
+                if (kF16)
+                  mx2[nt][e][h] = fmaxf(mx2[nt][e][h], __shfl_xor_sync(0xffffffffu, mx2[nt][e][h], sh));
             }
             // (-inf stays until a finite score comes; a factor of 0 / 0 = NaN
             // cannot come up: the new reference is finite or +inf.)
@@ -627,30 +721,35 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
               l[nt][e] *= up;
               m[nt][e] = a;
             }
-            if (kE4m3) {
-              up = 1.f;
-              if (b > m2[nt][e]) {
-                up = ex2_approx(m2[nt][e] - b);
-                m2[nt][e] = b;
-              }
-            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              o[nt][i][e] *= up;
-              o[nt][i][2 + e] *= up;
+            for (int h = 0; h < kParts; ++h) {
+              if (kF16) {
+                const float b = mx2[nt][e][h];
+                up = 1.f;
+                if (b > m2[nt][e][h]) {
+                  up = ex2_approx(m2[nt][e][h] - b);
+                  m2[nt][e][h] = b;
+                }
+              }
+#pragma unroll
+              for (int i = 4 / kParts * h; i < 4 / kParts * (h + 1); ++i) {
+                o[nt][i][e] *= up;
+                o[nt][i][2 + e] *= up;
+              }
             }
           }
       }
       // Weights, transposed into B fragments (keys x heads); a column none of
       // whose keys is live yet (m = -inf) takes none.
-      uint32_t pb[kMT][kNT][2];
+      uint32_t pb[kMT][kNT][kParts][2];
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
-        float ref[2], ref2[2];
+        float ref[2], ref2[2][kParts];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           ref[e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-          ref2[e] = m2[nt][e] == -INFINITY ? 0.f : m2[nt][e];
+#pragma unroll
+          for (int h = 0; h < kParts; ++h) ref2[e][h] = m2[nt][e][h] == -INFINITY ? 0.f : m2[nt][e][h];
         }
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
@@ -660,19 +759,45 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
             const float p0 = ex2_approx(s0 - ref[0]), p1 = ex2_approx(s1 - ref[1]);
             l[nt][0] += p0;
             l[nt][1] += p1;
-            uint32_t w2;
-            if constexpr (kE4m3)
-              w2 = pack_f16x2(ex2_approx(s0 + ev[mt][hf] - ref2[0]),
-                              ex2_approx(s1 + ev[mt][hf] - ref2[1]));
-            else
-              w2 = pack_bf16x2(p0, p1);
-            pb[mt][nt][hf] = transpose8x8(w2);
+#pragma unroll
+            for (int h = 0; h < kParts; ++h) {
+              uint32_t w2;
+              if constexpr (kF16)
+                w2 = pack_f16x2(ex2_approx(s0 + ev[mt][hf][h] - ref2[0][h]),
+                                ex2_approx(s1 + ev[mt][hf][h] - ref2[1][h]));
+              else
+                w2 = pack_bf16x2(p0, p1);
+              pb[mt][nt][h][hf] = transpose8x8(w2);
+            }
           }
       }
       // o^T += V^T P^T, 16 keys a step.
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
-        if constexpr (kE4m3) {
+        if constexpr (kE2m1) {
+          // A word is dims 4 r .. 4 r + 3 of each half of the lane's four keys: row
+          // tile i holds the word's byte i, its low value (row r) and its high one (row
+          // r + 8).  Two keys' low values make a byte, and two keys' high ones.
+          uint32_t vw[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            vw[i] = *reinterpret_cast<const uint32_t*>(
+                sv + e2m1_key(mt, 8 * (i >> 1) + 2 * c + (i & 1)) * T::kRowBytes + 4 * r);
+          uint32_t va[4][4];  // [operand register][row tile]
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t a = vw[2 * j], b = vw[2 * j + 1];
+            kv::e2m1x8_to_f16x2((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), va[2 * j]);
+            kv::e2m1x8_to_f16x2(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), va[2 * j + 1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t v4[4] = {va[0][i], va[1][i], va[2][i], va[3][i]};
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+              mma16816<true>(o[nt][i], v4, pb[mt][nt][(i >> 1) % kParts][0], pb[mt][nt][(i >> 1) % kParts][1]);
+          }
+        } else if constexpr (kF16) {
           // Dims 8 r .. 8 r + 7 of the lane's four keys: row tile i holds dims
           // 8 r + 2 i (row r) and 8 r + 2 i + 1 (row r + 8).
           uint2 vw[4];
@@ -691,7 +816,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
                                     kv::e4m3x2_to_f16x2(hi), kv::e4m3x2_to_f16x2(hi >> 16)};
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
-              mma16816<true>(o[nt][i], va, pb[mt][nt][0], pb[mt][nt][1]);
+              mma16816<true>(o[nt][i], va, pb[mt][nt][0][0], pb[mt][nt][0][1]);
           }
         } else {
           const uint32_t vbase = smem_u32(sv);
@@ -703,7 +828,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
                           va);
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
-              mma16816<false>(o[nt][i], va, pb[mt][nt][0], pb[mt][nt][1]);
+              mma16816<false>(o[nt][i], va, pb[mt][nt][0][0], pb[mt][nt][0][1]);
           }
         }
       }
@@ -723,14 +848,17 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
         if (r == 0) {
           dst[0] = m[nt][e];
           dst[1] = sum;
-          dst[2] = kE4m3 ? m2[nt][e] : m[nt][e];
+          dst[2] = kF16 ? m2[nt][e][0] : m[nt][e];
           dst[3] = bad ? 1.f : 0.f;
+          if (kE2m1) dst[4 + kHD] = m2[nt][e][kParts - 1];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
-            dst[4 + (kE4m3 ? 8 * r + 2 * i + hf : 16 * i + r + 8 * hf)] = o[nt][i][2 * hf + e];
+            dst[4 + (kE2m1 ? 32 * (i >> 1) + 4 * r + 2 * (i & 1) + hf
+                     : kF16 ? 8 * r + 2 * i + hf
+                            : 16 * i + r + 8 * hf)] = o[nt][i][2 * hf + e];
       }
     // A wait that gave up (reported): this segment and the CTA's later ones have no
     // result.  They still count as arrived, as bad parts, so that the counters are
@@ -757,7 +885,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kE4m3, kRows>::kCt
         const float* src = red + (v * kRows + row) * L::kRedRow;
         if (src[2] == -INFINITY && src[0] == -INFINITY && src[1] == 0.f) continue;  // no keys
         sum += src[1] * ex2_approx(src[0] - ref);
-        const float wt = ex2_approx(src[2] - ref);
+        const float wt = ex2_approx(src[kE2m1 && d0 >= kHD / 2 ? 4 + kHD : 2] - ref);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] += src[4 + d0 + e] * wt;
       }
@@ -895,25 +1023,28 @@ using namespace paged;
 int paged_rows(int H, int Hkv) { return H / Hkv <= 8 ? 8 : 16; }
 
 // Launched CTAs: no more than the batch can have tiles.
-int paged_ctas(long long B, int H, int Hkv, int max_seqlen, bool e4m3, int sms) {
-  const int rows = paged_rows(H, Hkv), tile = e4m3 ? Tile<true>::kTile : Tile<false>::kTile;
+int paged_ctas(long long B, int H, int Hkv, int max_seqlen, Kv type, int sms) {
+  const int rows = paged_rows(H, Hkv);
+  const int tile = type == Kv::kE2m1   ? Tile<Kv::kE2m1>::kTile
+                   : type == Kv::kE4m3 ? Tile<Kv::kE4m3>::kTile
+                                       : Tile<Kv::kBf16>::kTile;
   const long long units = B * Hkv * ((H / Hkv + rows - 1) / rows);
   const long long tiles = units * ((max_seqlen + tile - 1) / tile);
   const long long full =
-      static_cast<long long>(rows == 8 ? Cfg<false, 8>::kCtas : Cfg<false, 16>::kCtas) * sms;
+      static_cast<long long>(rows == 8 ? Cfg<Kv::kBf16, 8>::kCtas : Cfg<Kv::kBf16, 16>::kCtas) * sms;
   return static_cast<int>(tiles < full ? tiles : full);
 }
 
-template <bool kE4m3, int kRows, bool kDrop = false>
+template <Kv kType, int kRows, bool kDrop = false>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int ctas,
                    cudaStream_t stream) {
-  constexpr int bytes = Cfg<kE4m3, kRows>::BYTES;
-  static_assert(Cfg<kE4m3, kRows>::kCtas * (bytes + 1024) <= 233472,
+  constexpr int bytes = Cfg<kType, kRows>::BYTES;
+  static_assert(Cfg<kType, kRows>::kCtas * (bytes + 1024) <= 233472,
                 "CTAs of an SM share its 228 KiB");
   static bool done[64] = {};
-  const cudaError_t e = allow_smem(ne_attn_paged_kernel<kE4m3, kRows, kDrop>, bytes, done);
+  const cudaError_t e = allow_smem(ne_attn_paged_kernel<kType, kRows, kDrop>, bytes, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(ne_attn_paged_kernel<kE4m3, kRows, kDrop>, dim3(ctas), dim3(kThreads), bytes, stream,
+  return launch_pdl(ne_attn_paged_kernel<kType, kRows, kDrop>, dim3(ctas), dim3(kThreads), bytes, stream,
                     tk, tv, p);
 }
 }  // namespace
@@ -921,7 +1052,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p
 // Sequences that a launch takes: what its shared memory holds, and so many that
 // their tiles and overheads are numbered in 31 bits (0: not one).
 int paged_batch(int H, int Hkv, int max_seqlen) {
-  const int rows = paged_rows(H, Hkv), tile = Tile<false>::kTile;  // the smaller tile
+  const int rows = paged_rows(H, Hkv), tile = Tile<Kv::kBf16>::kTile;  // the smaller tile
   const long long J = static_cast<long long>(Hkv) * ((H / Hkv + rows - 1) / rows);
   const long long one = J * ((max_seqlen + tile - 1) / tile + kOverhead);
   return static_cast<int>(std::min<long long>(kMaxBatch, ((1LL << 31) - (1 << 25)) / one));
@@ -931,21 +1062,21 @@ constexpr int kPagedSms = 160;  // an upper bound on the part's SMs (152), for t
 
 size_t paged_part_bytes(int B, int H, int Hkv, int max_seqlen) {
   const long long b = B < kMaxBatch ? B : kMaxBatch;
-  const long long n = paged_ctas(b, H, Hkv, max_seqlen, false, kPagedSms);  // the smaller tile
+  const long long n = paged_ctas(b, H, Hkv, max_seqlen, Kv::kBf16, kPagedSms);  // the smaller tile
   return static_cast<size_t>(n) * 2 * paged_rows(H, Hkv) * kPartRow * sizeof(float);
 }
 
 unsigned paged_box_rows(int page_size) {
-  return page_size < Tile<false>::kTile ? page_size : Tile<false>::kTile;
+  return page_size < Tile<Kv::kBf16>::kTile ? page_size : Tile<Kv::kBf16>::kTile;
 }
 
-size_t paged_counter_bytes() { return kPagedSms * Cfg<false, 8>::kCtas * sizeof(int); }
+size_t paged_counter_bytes() { return kPagedSms * Cfg<Kv::kBf16, 8>::kCtas * sizeof(int); }
 
 // tmK, tmV: the bf16 pools as [rows, 64] in boxes of paged_box_rows rows
-// (unused for e4m3).  arrived: paged_counter_bytes of zeros.  drop_cta: -1, or (bf16,
+// (unused for the others).  arrived: paged_counter_bytes of zeros.  drop_cta: -1, or (bf16,
 // groups of at most 8) the CTA whose first tile is never loaded.
 cudaError_t launch_decode_paged(const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                const __nv_bfloat16* q, const PagedCache& pc, bool e4m3,
+                                const __nv_bfloat16* q, const PagedCache& pc, Kv type,
                                 const int* seq_lens, int B, int H, const RopeTable& rope,
                                 float scale_log2, float* part, int* arrived, __nv_bfloat16* out,
                                 float* lse, int sms, int* status, cudaStream_t stream,
@@ -963,7 +1094,7 @@ cudaError_t launch_decode_paged(const CUtensorMap& tmK, const CUtensorMap& tmV,
   p.arrived = arrived;
   p.status = status;
   p.drop_cta = drop_cta;
-  if (drop_cta >= 0 && (e4m3 || rows != 8)) return cudaErrorInvalidValue;
+  if (drop_cta >= 0 && (type != Kv::kBf16 || rows != 8)) return cudaErrorInvalidValue;
   const int batch = paged_batch(H, pc.Hkv, pc.max_seqlen);
   for (int b0 = 0; b0 < B; b0 += batch) {
     p.B = B - b0 < batch ? B - b0 : batch;
@@ -972,13 +1103,15 @@ cudaError_t launch_decode_paged(const CUtensorMap& tmK, const CUtensorMap& tmV,
     p.pc.block_table = pc.block_table + static_cast<long long>(b0) * pc.max_pages;
     p.out = out + static_cast<long long>(b0) * H * kHD;
     p.lse = lse + static_cast<long long>(b0) * H;
-    const int ctas = paged_ctas(p.B, H, pc.Hkv, pc.max_seqlen, e4m3, sms);
+    const int ctas = paged_ctas(p.B, H, pc.Hkv, pc.max_seqlen, type, sms);
     const cudaError_t e =
-        drop_cta >= 0 ? launch<false, 8, true>(tmK, tmV, p, ctas, stream)
-        : e4m3 ? (rows == 8 ? launch<true, 8>(tmK, tmV, p, ctas, stream)
-                          : launch<true, 16>(tmK, tmV, p, ctas, stream))
-             : (rows == 8 ? launch<false, 8>(tmK, tmV, p, ctas, stream)
-                          : launch<false, 16>(tmK, tmV, p, ctas, stream));
+        drop_cta >= 0 ? launch<Kv::kBf16, 8, true>(tmK, tmV, p, ctas, stream)
+        : type == Kv::kE2m1 ? (rows == 8 ? launch<Kv::kE2m1, 8>(tmK, tmV, p, ctas, stream)
+                                         : launch<Kv::kE2m1, 16>(tmK, tmV, p, ctas, stream))
+        : type == Kv::kE4m3 ? (rows == 8 ? launch<Kv::kE4m3, 8>(tmK, tmV, p, ctas, stream)
+                                         : launch<Kv::kE4m3, 16>(tmK, tmV, p, ctas, stream))
+                            : (rows == 8 ? launch<Kv::kBf16, 8>(tmK, tmV, p, ctas, stream)
+                                         : launch<Kv::kBf16, 16>(tmK, tmV, p, ctas, stream));
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -21,6 +21,8 @@ constexpr int NE_DEV_OK = 0;
 constexpr int NE_DEV_BAD_SEQLEN = 1;        // a sequence longer than max_seqlen, or
                                             // cu_seqlens outside [0, n_tot]
 constexpr int NE_DEV_BAD_PAGE = 2;          // a block table entry outside [0, n_pages)
+constexpr int NE_DEV_NO_PAGES = 3;          // more pages wanted than are free, or given back
+                                            // than there are
 constexpr int NE_DEV_TIMEOUT_BASE = 0x100;  // + wait site id
 
 // RoPE table: for position p and frequency i < 32, rope[p * 32 + i] = (cos, sin)
@@ -47,12 +49,18 @@ struct Problem {
   int group = 1;          // query heads per key/value head (k, v, dk, dv: [N_tot, H / group, 64])
 };
 
+// What a paged cache's rows are held in.
+enum class Kv { kBf16, kE4m3, kE2m1 };
+
 // A paged key/value cache: n_pages pages of 2^page_shift positions, each
 // [Hkv, page, 64] in both pools (a head's positions of a page are contiguous,
-// so that one copy fetches them), bf16 or e4m3.  Position n of sequence s
+// so that one copy fetches them), bf16, e4m3 or e2m1.  Position n of sequence s
 // lies in slot n % page of page block_table[s * max_pages + n / page].  e4m3
 // rows have a scale byte each (scale [n_pages, Hkv, page]): the row's values
 // are e4m3 * 2^(byte - 127); byte 255 marks a row that held an infinity or NaN.
+// e2m1 rows are 32 bytes with a scale byte for each half of the dims (scale
+// [n_pages, Hkv, page, 2]), and their word w of four bytes holds dims 4 w .. 4 w
+// + 3 (two to a byte, the even one low), then dims 32 + 4 w .. 32 + 4 w + 3.
 struct PagedCache {
   void* k;
   void* v;
@@ -64,6 +72,54 @@ struct PagedCache {
   int page_shift;
   int Hkv;
   int max_seqlen;  // every position is below this (<= max_pages pages)
+};
+
+// Norms of queries and keys for each head, with the rotation (ne_qk_norm.cu).
+struct QkNormParams {
+  const __nv_bfloat16* q;  // [n_tot, H, 64], rows q_stride elements apart
+  const __nv_bfloat16* k;  // [n_tot, Hkv, 64], rows k_stride apart
+  long long q_stride, k_stride;
+  const __nv_bfloat16* qw;  // [64]
+  const __nv_bfloat16* kw;
+  const int* positions;  // [n_tot], -1: a row to leave alone; nullptr: none (no rotation)
+  int n_tot, H, Hkv;
+  int max_seqlen;
+  float eps;
+  RopeTable rope;  // cs == nullptr: no rotation
+  __nv_bfloat16* qr;  // forward: [n_tot, H, 64], [n_tot, Hkv, 64]
+  __nv_bfloat16* kr;
+  const __nv_bfloat16* dqr;  // backward: gradients of qr, kr ...
+  const __nv_bfloat16* dkr;
+  __nv_bfloat16* dq;  // ... and of q, k, rows dq_stride, dk_stride apart
+  __nv_bfloat16* dk;
+  long long dq_stride, dk_stride;
+  float* dqw;  // [64]
+  float* dkw;
+  float* part;   // [CTAs][2][64]: the CTAs' sums for dqw, dkw
+  int* arrived;  // zero before and after the launch
+  int* status;
+};
+
+// Pages handed out and taken back, and the places of a step's rows (ne_kv_pages.cu).
+constexpr int kMaxPagedSequences = 16384;  // a CTA's shared memory holds their sums
+struct PagesParams {
+  const int* new_lens;      // reserve: [nseq] rows that each sequence gets
+  const uint8_t* finished;  // release: [nseq]
+  const int* seq_lens;      // [nseq] positions held
+  int* seq_lens_out;        // (may be seq_lens)
+  int* block_table;         // [nseq, max_pages]
+  const int* free_pages;    // [n_pages], the first *n_free valid: the last is the top
+  int* free_pages_out;      // release
+  const int* n_free;
+  int* n_free_out;          // (may be n_free)
+  int nseq, n_tot, max_pages, n_pages, page_shift, max_seqlen;
+  int max_rows;     // reserve: n_tot, or no bound where neither positions nor slots are wanted
+  int* cu_seqlens;  // reserve: [nseq + 1], [nseq], [n_tot], [n_tot], each or nullptr
+  int* start_pos;
+  int* positions;
+  int* slots;
+  int* arrived;  // zero before and after the launch
+  int* status;
 };
 
 struct FwdParams {

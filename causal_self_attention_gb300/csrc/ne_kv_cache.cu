@@ -11,10 +11,12 @@
 // once (at most half an e4m3 step, 2^-4 of it; below 2^-6 * 2^e half of
 // 2^-9 * 2^e), the scale is a single byte, and dequantised values are exact
 // in bf16.  The key is quantised from its fp32 rotation, not from the bf16
-// rounding of it.  Read: the mirror image, bf16 out.
+// rounding of it.  e2m1: the same for each half of a row, the 32 dims that the
+// other 32 are rotated with, with max |x| <= 6 * 2^e and e <= 125 (so that 6 * 2^e
+// is finite in bf16; larger values become that).  Read: the mirror image, bf16 out.
 //
-// Both move bytes and nothing else: per (row, head) 256 in and 256 (bf16) or
-// 130 (e4m3) out, or the reverse.  Four lanes take the 64 dims of a (row,
+// Both move bytes and nothing else: per (row, head) 256 in and 256 (bf16), 130
+// (e4m3) or 68 (e2m1) out, or the reverse.  Four lanes take the 64 dims of a (row,
 // head), lane c the 16-byte chunks c and c + 4 of K and of V, so that each
 // rotation pair (i, i + 32) sits in one lane, a warp moves eight neighbouring
 // 128-byte rows of each tensor, and every thread has four loads in flight.
@@ -89,10 +91,49 @@ __device__ __forceinline__ void store_e4m3(const float (&lo)[8], const float (&h
                  pack_e4m3x4(hi[4] * inv, hi[5] * inv, hi[6] * inv, hi[7] * inv));
   if (c == 0) scale[slot] = static_cast<uint8_t>(byte);
 }
+// The scale of 32 values in e2m1.
+__device__ __forceinline__ int scale_byte_e2m1(uint32_t top) {
+  if (top >= 0x7f800000u) return 255;
+  const int e = static_cast<int>(top >> 23) - 127 - 2 + ((top & 0x7fffffu) > 0x400000u ? 1 : 0);
+  return min(max(e, -100), 125) + 127;
+}
+
+// One row's 16 values of a lane, 8 of each half, into the e2m1 pool, and the
+// row's two scales (lane 0 of the four).  Every lane of the warp calls this.
+__device__ __forceinline__ void store_e2m1(float (&lo)[8], float (&hi)[8], int c, bool valid,
+                                           long long slot, uint8_t* pool, uint8_t* scale) {
+  uint32_t top0 = 0, top1 = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    top0 = max(top0, __float_as_uint(lo[i]) & 0x7fffffffu);
+    top1 = max(top1, __float_as_uint(hi[i]) & 0x7fffffffu);
+  }
+#pragma unroll
+  for (int sh = 1; sh < kParts; sh <<= 1) {
+    top0 = max(top0, __shfl_xor_sync(0xffffffffu, top0, sh));
+    top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, sh));
+  }
+  const int b0 = scale_byte_e2m1(top0), b1 = scale_byte_e2m1(top1);
+  // 2^-e, e = byte - 127; a half marked 255 stores zeros.
+  const float inv0 = b0 == 255 ? 0.f : __uint_as_float(static_cast<uint32_t>(254 - b0) << 23);
+  const float inv1 = b1 == 255 ? 0.f : __uint_as_float(static_cast<uint32_t>(254 - b1) << 23);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lo[i] = b0 == 255 ? 0.f : lo[i] * inv0;
+    hi[i] = b1 == 255 ? 0.f : hi[i] * inv1;
+  }
+  if (!valid) return;
+  // Words 2c and 2c + 1: four values of each half.
+  const uint32_t l = pack_e2m1x8(lo), h = pack_e2m1x8(hi);
+  reinterpret_cast<uint2*>(pool + slot * (kHD / 2))[c] =
+      make_uint2(__byte_perm(l, h, 0x5410), __byte_perm(l, h, 0x7632));
+  if (c == 0)
+    reinterpret_cast<uint16_t*>(scale)[slot] = static_cast<uint16_t>(b0 | (b1 << 8));
+}
 }  // namespace kv
 
-// kE4m3: the pools' type.  rope.cs == nullptr: the keys come rotated.
-template <bool kE4m3>
+// kType: the pools' type.  rope.cs == nullptr: the keys come rotated.
+template <Kv kType>
 __global__ void __launch_bounds__(kv::kThreads)
     ne_kv_append_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                         const int* __restrict__ cu, const int* __restrict__ start_pos, int nseq,
@@ -132,11 +173,16 @@ __global__ void __launch_bounds__(kv::kThreads)
       b[2 * u + 1] = hi1;
     }
   }
-  if constexpr (kE4m3) {
+  if constexpr (kType == Kv::kE4m3) {
     store_e4m3(a, b, c, valid, pl.slot, static_cast<uint8_t*>(pc.k), pc.k_scale);
     unpack8(v0, a);
     unpack8(v1, b);
     store_e4m3(a, b, c, valid, pl.slot, static_cast<uint8_t*>(pc.v), pc.v_scale);
+  } else if constexpr (kType == Kv::kE2m1) {
+    store_e2m1(a, b, c, valid, pl.slot, static_cast<uint8_t*>(pc.k), pc.k_scale);
+    unpack8(v0, a);
+    unpack8(v1, b);
+    store_e2m1(a, b, c, valid, pl.slot, static_cast<uint8_t*>(pc.v), pc.v_scale);
   } else if (valid) {
     uint4* ko = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pc.k) + pl.slot * kHD);
     uint4* vo = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pc.v) + pl.slot * kHD);
@@ -147,7 +193,7 @@ __global__ void __launch_bounds__(kv::kThreads)
   }
 }
 
-template <bool kE4m3>
+template <Kv kType>
 __global__ void __launch_bounds__(kv::kThreads)
     ne_kv_read_kernel(__nv_bfloat16* __restrict__ k, __nv_bfloat16* __restrict__ v,
                       const int* __restrict__ cu, const int* __restrict__ start_pos, int nseq,
@@ -164,7 +210,31 @@ __global__ void __launch_bounds__(kv::kThreads)
   if (code != 0) return;
   uint4* ko = reinterpret_cast<uint4*>(k + pl.src);
   uint4* vo = reinterpret_cast<uint4*>(v + pl.src);
-  if constexpr (kE4m3) {
+  if constexpr (kType == Kv::kE2m1) {
+    auto row = [&](const void* pool, const uint8_t* scale, uint4* out) {
+      const uint2 w = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) +
+                                                     pl.slot * (kHD / 2))[c];
+      const int bytes = reinterpret_cast<const uint16_t*>(scale)[pl.slot];
+      // (low halves of the two words: dims 8c .. 8c + 7; high halves: 32 + 8c ..)
+      const uint32_t half[2] = {__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632)};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float f = scale_value(u ? bytes >> 8 : bytes & 255);
+        uint32_t h[4];
+        e2m1x8_to_f16x2(half[u], h);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f16x2_to_f32(h[i], x[2 * i], x[2 * i + 1]);
+          x[2 * i] *= f;
+          x[2 * i + 1] *= f;
+        }
+        out[c + 4 * u] = pack8(x);
+      }
+    };
+    row(pc.k, pc.k_scale, ko);
+    row(pc.v, pc.v_scale, vo);
+  } else if constexpr (kType == Kv::kE4m3) {
     auto row = [&](const void* pool, const uint8_t* scale, uint4* out) {
       const uint2* src =
           reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) + pl.slot * kHD);
@@ -206,16 +276,20 @@ dim3 kv_grid(int n_tot, int Hkv) {
 
 cudaError_t launch_kv_append(const __nv_bfloat16* k, const __nv_bfloat16* v, const int* cu,
                              const int* start_pos, int nseq, int n_tot, const PagedCache& pc,
-                             bool e4m3, const RopeTable& rope, int* status, cudaStream_t stream) {
-  return launch_pdl(e4m3 ? ne_kv_append_kernel<true> : ne_kv_append_kernel<false>,
+                             Kv type, const RopeTable& rope, int* status, cudaStream_t stream) {
+  return launch_pdl(type == Kv::kE2m1   ? ne_kv_append_kernel<Kv::kE2m1>
+                    : type == Kv::kE4m3 ? ne_kv_append_kernel<Kv::kE4m3>
+                                        : ne_kv_append_kernel<Kv::kBf16>,
                     kv_grid(n_tot, pc.Hkv), dim3(kv::kThreads), 0, stream, k, v, cu, start_pos,
                     nseq, n_tot, pc, rope, status);
 }
 
 cudaError_t launch_kv_read(__nv_bfloat16* k, __nv_bfloat16* v, const int* cu,
                            const int* start_pos, int nseq, int n_tot, const PagedCache& pc,
-                           bool e4m3, int* status, cudaStream_t stream) {
-  return launch_pdl(e4m3 ? ne_kv_read_kernel<true> : ne_kv_read_kernel<false>,
+                           Kv type, int* status, cudaStream_t stream) {
+  return launch_pdl(type == Kv::kE2m1   ? ne_kv_read_kernel<Kv::kE2m1>
+                    : type == Kv::kE4m3 ? ne_kv_read_kernel<Kv::kE4m3>
+                                        : ne_kv_read_kernel<Kv::kBf16>,
                     kv_grid(n_tot, pc.Hkv), dim3(kv::kThreads), 0, stream, k, v, cu, start_pos,
                     nseq, n_tot, pc, status);
 }

@@ -1,0 +1,248 @@
+// ne_kv_pages.cu -- the pages of a paged key/value cache handed out and taken
+// back on the GPU, and the positions and slots of a step's new rows, sm_103a.
+//
+// The free pages are a stack.  Reserve: sequence s, holding n_s positions, gets
+// m_s new rows; with had(s) = ceil(n_s / P) and take(s) = ceil((n_s + m_s) / P) -
+// had(s) pages of P positions, the t-th page taken (in the order of the sequences,
+// within one of its positions) is the t-th from the top of the stack:
+//   first(s) = sum_{s' < s} take(s'),   cu(s) = sum_{s' < s} m_s',
+//   block_table[s, had(s) + j] = free[n_free - 1 - (first(s) + j)],
+//   row cu(s) + i: position n_s + i, slot page * P + position % P.
+// Release: the pages of finished sequences go onto the stack in the same order.
+//
+// Both are a prefix sum over the sequences and a few words for every row.  Every
+// CTA forms the sums itself, in shared memory (16384 sequences take 192 KB: the
+// limit), so that nothing has to wait for another CTA; then each takes its share
+// of the rows and of the pages, finding a row's sequence by bisection.  What is
+// kept for the next step (lengths, the stack's height) may be updated in place:
+// the CTA that has read it last does that (one CTA: itself), so that no CTA reads
+// a new value for an old one.
+#include "ne_paged.cuh"
+#include "ne_sm100.cuh"
+
+namespace ne {
+
+namespace pages {
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRowsPerThread = 4;
+
+struct Shared {
+  long long warp_rows[kWarps], warp_pages[kWarps];
+  int last;
+};
+
+__device__ __forceinline__ long long scan_warp(long long v, int lane) {
+#pragma unroll
+  for (int sh = 1; sh < 32; sh <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, sh);
+    if (lane >= sh) v += u;
+  }
+  return v;
+}
+
+// The last s with first[s] <= x (first[0] = 0, nondecreasing, first[n] > x).
+__device__ __forceinline__ int find(const int* first, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Exclusive prefix sums of rows(s) and pages(s) over the sequences into shared
+// memory, [nseq + 1] each, and their totals (64 bits: the entries hold where the
+// totals fit).  one(s, rows, pages): what sequence s adds.  Every thread calls it.
+template <typename One>
+__device__ __forceinline__ void prefix_sums(int nseq, int* row_at, int* page_at, Shared& sh,
+                                            long long& rows, long long& pages, One one) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  rows = pages = 0;
+  for (int s0 = 0; s0 < nseq; s0 += kThreads) {
+    const int s = s0 + threadIdx.x;
+    int m = 0, t = 0;
+    if (s < nseq) one(s, m, t);
+    const long long a = scan_warp(m, lane), b = scan_warp(t, lane);
+    if (lane == 31) {
+      sh.warp_rows[warp] = a;
+      sh.warp_pages[warp] = b;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      sh.warp_rows[lane] = scan_warp(sh.warp_rows[lane], lane);
+      sh.warp_pages[lane] = scan_warp(sh.warp_pages[lane], lane);
+    }
+    __syncthreads();
+    if (s < nseq) {
+      row_at[s] = static_cast<int>(rows + (warp ? sh.warp_rows[warp - 1] : 0) + a - m);
+      page_at[s] = static_cast<int>(pages + (warp ? sh.warp_pages[warp - 1] : 0) + b - t);
+    }
+    rows += sh.warp_rows[kWarps - 1];
+    pages += sh.warp_pages[kWarps - 1];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    row_at[nseq] = static_cast<int>(rows);
+    page_at[nseq] = static_cast<int>(pages);
+  }
+  __syncthreads();
+}
+
+// Whether this CTA is the last of the launch to come here (with its reads of what
+// is updated in place behind it).  Every thread calls it.
+__device__ __forceinline__ bool last_to_read(int* arrived, Shared& sh) {
+  if (gridDim.x == 1) return true;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    sh.last = atomicAdd(arrived, 1) == static_cast<int>(gridDim.x) - 1;
+    if (sh.last) *arrived = 0;  // as the next launch wants it
+    __threadfence();
+  }
+  __syncthreads();
+  return sh.last != 0;
+}
+}  // namespace pages
+
+__global__ void __launch_bounds__(pages::kThreads) ne_kv_reserve_kernel(const PagesParams p) {
+  using namespace pages;
+  extern __shared__ int dyn[];
+  __shared__ Shared sh;
+  int* row_at = dyn;                  // [nseq + 1] first row of each sequence
+  int* page_at = row_at + p.nseq + 1; // [nseq + 1] first page taken for it
+  int* lens = page_at + p.nseq + 1;   // [nseq] positions that it holds
+  pdl_wait();
+  const int P1 = (1 << p.page_shift) - 1;
+  const int n_free = __ldcg(p.n_free);
+  bool bad = false;
+  long long rows, taken;
+  prefix_sums(p.nseq, row_at, page_at, sh, rows, taken, [&](int s, int& m, int& t) {
+    const int n = __ldcg(p.seq_lens + s);
+    m = __ldg(p.new_lens + s);
+    lens[s] = n;
+    if (n < 0 || m < 0 || n > p.max_seqlen || m > p.max_seqlen - n) {
+      bad = true;
+      m = 0;
+      return;
+    }
+    t = ((n + m + P1) >> p.page_shift) - ((n + P1) >> p.page_shift);
+  });
+  bad = __syncthreads_or(bad) || rows > p.max_rows;
+  const bool short_of = taken > n_free || n_free > p.n_pages || n_free < 0;
+  const bool ok = !bad && !short_of;
+  if (!ok && blockIdx.x == 0 && threadIdx.x == 0)
+    atomicCAS(p.status, 0, bad ? NE_DEV_BAD_SEQLEN : NE_DEV_NO_PAGES);
+
+  const int id = blockIdx.x * kThreads + threadIdx.x, all = gridDim.x * kThreads;
+  // The pages taken, into the block table.
+  if (ok)
+    for (int t = id; t < static_cast<int>(taken); t += all) {
+      const int s = find(page_at, p.nseq, t);
+      const int at = ((lens[s] + P1) >> p.page_shift) + t - page_at[s];
+      p.block_table[static_cast<long long>(s) * p.max_pages + at] = __ldg(p.free_pages + n_free - 1 - t);
+    }
+  // Positions and slots, neighbouring rows in a thread's hands.
+  const int n_rows = ok ? static_cast<int>(rows) : 0;
+  for (int r0 = id * kRowsPerThread; r0 < p.n_tot; r0 += all * kRowsPerThread) {
+    int s = r0 < n_rows ? find(row_at, p.nseq, r0) : 0;
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      const int r = r0 + i;
+      if (r >= p.n_tot) break;
+      int pos = -1, slot = -1;
+      if (r < n_rows) {
+        while (row_at[s + 1] <= r) ++s;
+        pos = lens[s] + r - row_at[s];
+        const int had = (lens[s] + P1) >> p.page_shift, at = pos >> p.page_shift;
+        const int page =
+            at < had ? __ldcg(p.block_table + static_cast<long long>(s) * p.max_pages + at)
+                     : __ldg(p.free_pages + n_free - 1 - (page_at[s] + at - had));
+        if (page >= 0 && page < p.n_pages)
+          slot = (page << p.page_shift) + (pos & P1);
+        else
+          atomicCAS(p.status, 0, NE_DEV_BAD_PAGE);
+      }
+      if (p.positions) p.positions[r] = pos;
+      if (p.slots) p.slots[r] = slot;
+    }
+  }
+  for (int s = id; s <= p.nseq; s += all) {
+    if (p.cu_seqlens) p.cu_seqlens[s] = ok ? row_at[s] : 0;
+    if (p.start_pos && s < p.nseq) p.start_pos[s] = lens[s];
+  }
+  if (!last_to_read(p.arrived, sh)) return;
+  for (int s = threadIdx.x; s < p.nseq; s += kThreads)
+    p.seq_lens_out[s] = ok ? lens[s] + row_at[s + 1] - row_at[s] : lens[s];
+  if (threadIdx.x == 0) *p.n_free_out = ok ? n_free - static_cast<int>(taken) : n_free;
+}
+
+__global__ void __launch_bounds__(pages::kThreads) ne_kv_release_kernel(const PagesParams p) {
+  using namespace pages;
+  extern __shared__ int dyn[];
+  __shared__ Shared sh;
+  int* row_at = dyn;                   // (finished sequences before each)
+  int* page_at = row_at + p.nseq + 1;  // [nseq + 1] first page given back by it
+  pdl_wait();
+  const int P1 = (1 << p.page_shift) - 1;
+  const int n_free = __ldcg(p.n_free);
+  bool bad = false;
+  long long done, given;
+  prefix_sums(p.nseq, row_at, page_at, sh, done, given, [&](int s, int& m, int& t) {
+    m = __ldg(p.finished + s) != 0;
+    if (!m) return;
+    const int n = __ldcg(p.seq_lens + s);
+    if (n < 0 || n > p.max_seqlen) {
+      bad = true;
+      return;
+    }
+    t = (n + P1) >> p.page_shift;
+  });
+  bad = __syncthreads_or(bad);
+  const bool over = n_free < 0 || n_free > p.n_pages || given > p.n_pages - n_free;
+  const bool ok = !bad && !over;
+  if (!ok && blockIdx.x == 0 && threadIdx.x == 0)
+    atomicCAS(p.status, 0, bad ? NE_DEV_BAD_SEQLEN : NE_DEV_NO_PAGES);
+  const int id = blockIdx.x * kThreads + threadIdx.x, all = gridDim.x * kThreads;
+  if (ok)
+    for (int t = id; t < static_cast<int>(given); t += all) {
+      const int s = find(page_at, p.nseq, t);
+      int* entry = p.block_table + static_cast<long long>(s) * p.max_pages + t - page_at[s];
+      p.free_pages_out[n_free + t] = *entry;
+      *entry = -1;
+    }
+  if (!last_to_read(p.arrived, sh) || !ok) return;
+  for (int s = threadIdx.x; s < p.nseq; s += kThreads)
+    if (row_at[s + 1] != row_at[s]) p.seq_lens_out[s] = 0;
+  if (threadIdx.x == 0) *p.n_free_out = n_free + static_cast<int>(given);
+}
+
+namespace {
+cudaError_t launch(void (*kernel)(const PagesParams), int arrays, long long work,
+                   const PagesParams& p, int sms, bool (&done)[64], cudaStream_t stream) {
+  const int bytes = arrays * (p.nseq + 1) * static_cast<int>(sizeof(int));
+  if (bytes > 48 * 1024 - static_cast<int>(sizeof(pages::Shared))) {
+    const cudaError_t e =
+        allow_smem(kernel, arrays * (kMaxPagedSequences + 1) * static_cast<int>(sizeof(int)), done);
+    if (e != cudaSuccess) return e;
+  }
+  long long ctas = (work + pages::kThreads * pages::kRowsPerThread - 1) /
+                   (pages::kThreads * pages::kRowsPerThread);
+  ctas = ctas < 1 ? 1 : ctas > sms ? sms : ctas;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(pages::kThreads), bytes, stream,
+                    p);
+}
+}  // namespace
+
+cudaError_t launch_kv_reserve(const PagesParams& p, int sms, cudaStream_t stream) {
+  static bool done[64] = {};
+  return launch(ne_kv_reserve_kernel, 3, p.n_tot, p, sms, done, stream);
+}
+
+// (The pages given back are not known on the host: a CTA for every 1024 sequences.)
+cudaError_t launch_kv_release(const PagesParams& p, int sms, cudaStream_t stream) {
+  static bool done[64] = {};
+  return launch(ne_kv_release_kernel, 2, static_cast<long long>(p.nseq) * pages::kRowsPerThread, p,
+                sms, done, stream);
+}
+
+}  // namespace ne

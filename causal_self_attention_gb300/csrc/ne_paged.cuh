@@ -1,4 +1,4 @@
-// ne_paged.cuh -- addressing of the paged key/value cache, and its 8-bit type.
+// ne_paged.cuh -- addressing of the paged key/value cache, and its 8-bit and 4-bit types.
 #pragma once
 
 #include "ne_common.cuh"
@@ -55,11 +55,37 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
   return h;
 }
-// Two e4m3 bytes -> two fp32 (exact).
-__device__ __forceinline__ void unpack_e4m3x2(uint32_t two, float& a, float& b) {
+// Two halves -> two fp32 (exact).
+__device__ __forceinline__ void f16x2_to_f32(uint32_t h, float& a, float& b) {
   asm("{\n\t.reg .f16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
       : "=f"(a), "=f"(b)
-      : "r"(e4m3x2_to_f16x2(two)));
+      : "r"(h));
+}
+// Two e4m3 bytes -> two fp32 (exact).
+__device__ __forceinline__ void unpack_e4m3x2(uint32_t two, float& a, float& b) {
+  f16x2_to_f32(e4m3x2_to_f16x2(two), a, b);
+}
+
+// The four bytes of a word, two e2m1 values each -> halves (exact), the low one
+// first.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// Eight fp32 of magnitude at most 6 -> e2m1 (round to nearest, ties to even), two to
+// a byte, the first in the low half.
+__device__ __forceinline__ uint32_t pack_e2m1x8(const float (&x)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return w;
 }
 
 }  // namespace kv

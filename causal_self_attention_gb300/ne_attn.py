@@ -21,8 +21,9 @@ _lib = None
 NE_OK = 0
 STATUS_NAMES = {0: "NE_OK", 1: "NE_ERR_INVALID_ARG", 2: "NE_ERR_UNSUPPORTED",
                 3: "NE_ERR_MISALIGNED", 4: "NE_ERR_CUDA", 5: "NE_ERR_TIMEOUT", 6: "NE_ERR_OOM",
-                7: "NE_ERR_BAD_SEQLEN", 8: "NE_ERR_TOO_LARGE", 9: "NE_ERR_BAD_PAGE"}
-KV_BF16, KV_E4M3 = 0, 1  # types of a paged cache's pools
+                7: "NE_ERR_BAD_SEQLEN", 8: "NE_ERR_TOO_LARGE", 9: "NE_ERR_BAD_PAGE",
+                10: "NE_ERR_NO_PAGES"}
+KV_BF16, KV_E4M3, KV_E2M1 = 0, 1, 4  # types of a paged cache's pools
 
 EXPORTED = ("ne_attn_fwd", "ne_attn_fwd_f32out", "ne_attn_bwd", "ne_attn_bwd_workspace_bytes",
             "ne_attn_bwd_noalloc", "ne_attn_decode", "ne_attn_decode_rotated",
@@ -38,7 +39,9 @@ EXPORTED = ("ne_attn_fwd", "ne_attn_fwd_f32out", "ne_attn_bwd", "ne_attn_bwd_wor
             "ne_debug_schedule", "ne_attn_gqa_varlen_fwd", "ne_attn_gqa_varlen_bwd",
             "ne_attn_gqa_bwd_workspace_bytes", "ne_kv_append", "ne_kv_read",
             "ne_attn_decode_paged", "ne_attn_decode_paged_workspace_bytes", "ne_debug_kv_place",
-            "ne_debug_decode_drop")
+            "ne_debug_decode_drop", "ne_attn_gqa_varlen_fwd_rotated",
+            "ne_attn_gqa_varlen_bwd_rotated", "ne_kv_reserve", "ne_kv_release",
+            "ne_qk_norm_rope_fwd", "ne_qk_norm_rope_bwd", "ne_qk_norm_rope_bwd_workspace_bytes")
 
 
 class NeAttnError(RuntimeError):
@@ -62,6 +65,7 @@ def lib():
                            "`python -m causal_self_attention_gb300.build`")
     L = ctypes.CDLL(path)
     P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    LL = ctypes.c_longlong
     sig = {
         "ne_attn_fwd": [P, P, P, I, I, I, I, F, F, P, P, P],
         "ne_attn_fwd_f32out": [P, P, P, I, I, I, I, F, F, P, P, P],
@@ -94,6 +98,14 @@ def lib():
         "ne_debug_schedule": [I, I, I, I, P, I],
         "ne_attn_gqa_varlen_fwd": [P, P, P, P, I, I, I, I, I, I, F, F, P, P, P, P, P],
         "ne_attn_gqa_varlen_bwd": [P, P, P, P, P, P, P, I, I, I, I, I, I, F, F, P, P, P, P, Z, P],
+        "ne_attn_gqa_varlen_fwd_rotated": [P, P, P, P, I, I, I, I, I, I, F, P, P, P],
+        "ne_attn_gqa_varlen_bwd_rotated": [P, P, P, P, P, P, P, I, I, I, I, I, I, F, P, P, P, P, Z,
+                                           P],
+        "ne_kv_reserve": [P, P, I, P, I, P, P, I, I, I, I, P, P, P, P, P, P, P],
+        "ne_kv_release": [P, P, I, P, I, P, P, I, I, I, P],
+        "ne_qk_norm_rope_fwd": [P, P, LL, LL, P, P, P, I, I, I, I, I, F, F, P, P, P],
+        "ne_qk_norm_rope_bwd": [P, P, P, P, LL, LL, P, P, P, I, I, I, I, I, F, F, P, P, LL, LL, P,
+                                P, P, Z, P],
         "ne_kv_append": [P, P, P, P, I, I, I, I, F, I, P, P, P, P, P, I, I, I, I, P],
         "ne_kv_read": [I, P, P, P, P, P, I, I, I, I, P, P, I, I, I, I, P, P, P],
         "ne_attn_decode_paged": [P, I, P, P, P, P, P, I, I, I, I, P, I, I, I, I, F, F, P, P, P, Z,
@@ -113,6 +125,8 @@ def lib():
     L.ne_attn_gqa_bwd_workspace_bytes.restype = Z
     L.ne_attn_decode_paged_workspace_bytes.argtypes = [I, I, I, I]
     L.ne_attn_decode_paged_workspace_bytes.restype = Z
+    L.ne_qk_norm_rope_bwd_workspace_bytes.argtypes = []
+    L.ne_qk_norm_rope_bwd_workspace_bytes.restype = Z
     L.ne_status_string.argtypes = [I]
     L.ne_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -629,17 +643,258 @@ def ne_attn_gqa_varlen_bwd(qr, kr, v, out, dout, lse, cu_seqlens, max_seqlen, ro
     return dq, dk, dv
 
 
+def ne_attn_gqa_varlen_fwd_rotated(qr, kr, v, cu_seqlens, max_seqlen, scale=None, out=None,
+                                   lse=None, stream=None):
+    """:func:`ne_attn_gqa_varlen_fwd` on operands that are rotated already
+    (:func:`ne_qk_norm_rope_fwd`'s, for instance).  Returns ``(out, lse)``."""
+    dev, N, H, Hkv, D, nseq = _gqa_shapes(qr, kr, v, cu_seqlens, ("qr", "kr", "v"))
+    if out is not None:
+        _given(out, qr.shape, _BF16, dev, "out")
+    if lse is not None:
+        _given(lse, (H, N), _F32, dev, "lse")
+    raw, ctx = _on(stream, dev)
+    try:
+        out = torch.empty_like(qr) if out is None else out
+        lse = torch.empty((H, N), dtype=_F32, device=qr.device) if lse is None else lse
+        rc = lib().ne_attn_gqa_varlen_fwd_rotated(
+            qr.data_ptr(), kr.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), nseq, N,
+            int(max_seqlen), H, Hkv, D, D ** -0.5 if scale is None else scale, out.data_ptr(),
+            lse.data_ptr(), raw)
+    finally:
+        _leave(ctx)
+    _check("ne_attn_gqa_varlen_fwd_rotated", rc)
+    return out, lse
+
+
+def ne_attn_gqa_varlen_bwd_rotated(qr, kr, v, out, dout, lse, cu_seqlens, max_seqlen, scale=None,
+                                   dqr=None, dkr=None, dv=None, workspace=None, stream=None):
+    """Backward of :func:`ne_attn_gqa_varlen_fwd_rotated`.  Returns ``(dqr, dkr, dv)``:
+    gradients w.r.t. ``qr``, ``kr`` and ``v``.  ``workspace`` as for
+    :func:`ne_attn_gqa_varlen_bwd`."""
+    dev, N, H, Hkv, D, nseq = _gqa_shapes(qr, kr, v, cu_seqlens, ("qr", "kr", "v"))
+    _given(out, qr.shape, _BF16, dev, "out")
+    _given(dout, qr.shape, _BF16, dev, "dout")
+    _given(lse, (H, N), _F32, dev, "lse")
+    for t, like, name in ((dqr, qr, "dqr"), (dkr, kr, "dkr"), (dv, v, "dv")):
+        if t is not None:
+            _given(t, like.shape, _BF16, dev, name)
+    ws_bytes = _ws_bytes(workspace, dev)
+    raw, ctx = _on(stream, dev)
+    try:
+        dqr = torch.empty_like(qr) if dqr is None else dqr
+        dkr = torch.empty_like(kr) if dkr is None else dkr
+        dv = torch.empty_like(v) if dv is None else dv
+        rc = lib().ne_attn_gqa_varlen_bwd_rotated(
+            qr.data_ptr(), kr.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
+            lse.data_ptr(), cu_seqlens.data_ptr(), nseq, N, int(max_seqlen), H, Hkv, D,
+            D ** -0.5 if scale is None else scale, dqr.data_ptr(), dkr.data_ptr(), dv.data_ptr(),
+            _addr(workspace), ws_bytes, raw)
+    finally:
+        _leave(ctx)
+    _check("ne_attn_gqa_varlen_bwd_rotated", rc)
+    return dqr, dkr, dv
+
+
+# ------------------------------------------------- norms of queries and keys
+
+def _rows_of(t, shape, dev, name):
+    """Checks [N, heads, 64] bf16 rows whose heads are contiguous; returns the elements
+    from one row to the next."""
+    if not (t.dtype is _BF16 and t.get_device() == dev):
+        raise ValueError(f"{name} must be a CUDA {_BF16} tensor on cuda:{dev}")
+    if t.dim() != 3 or t.shape[2] != 64 or (shape is not None and t.shape != shape):
+        want = "[N, heads, 64]" if shape is None else str(tuple(shape))
+        raise ValueError(f"{name} must have the shape {want}")
+    row, head, one = t.stride()
+    heads = t.shape[1]
+    if one != 1 or (heads > 1 and head != 64):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return row if t.shape[0] > 1 else 64 * heads
+
+
+def _qk_norm_shapes(q, k, q_weight, k_weight, positions, rope_base):
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    q_row, k_row = _rows_of(q, None, dev, "q"), _rows_of(k, None, dev, "k")
+    N, H, D = q.shape
+    if k.shape[0] != N:
+        raise ValueError("q, k must be [N, H, 64] and [N, Hkv, 64]")
+    _given(q_weight, (D,), _BF16, dev, "q_weight")
+    _given(k_weight, (D,), _BF16, dev, "k_weight")
+    if positions is not None:
+        _given(positions, (N,), _I32, dev, "positions")
+    elif rope_base:
+        raise ValueError("positions: needed unless rope_base is 0")
+    return dev, N, H, k.shape[1], D, q_row, k_row
+
+
+def ne_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, max_seqlen, eps=1e-5,
+                        rope_base=10000.0, qr=None, kr=None, stream=None):
+    """RMS norm of every head of ``q`` ``[N, H, 64]`` and ``k`` ``[N, Hkv, 64]`` (bf16;
+    rows any multiple of 8 elements apart: slices of a joint projection's output) with
+    weights ``[64]`` bf16, then RoPE at ``positions`` (int32 CUDA ``[N]``; -1: a row of
+    no sequence, left alone), in one pass.  ``rope_base=0``: the norms alone, and
+    ``positions`` may be None.  Returns ``(qr, kr)``, contiguous, for the ``_rotated``
+    attention calls and, with ``rope_base=0``, the paged cache's."""
+    dev, N, H, Hkv, D, q_row, k_row = _qk_norm_shapes(q, k, q_weight, k_weight, positions,
+                                                      rope_base)
+    if qr is not None:
+        _given(qr, q.shape, _BF16, dev, "qr")
+    if kr is not None:
+        _given(kr, k.shape, _BF16, dev, "kr")
+    raw, ctx = _on(stream, dev)
+    try:
+        qr = torch.empty((N, H, D), dtype=_BF16, device=q.device) if qr is None else qr
+        kr = torch.empty((N, Hkv, D), dtype=_BF16, device=q.device) if kr is None else kr
+        if N == 0:  # a step in which no sequence has a row
+            return qr, kr
+        rc = lib().ne_qk_norm_rope_fwd(
+            q.data_ptr(), k.data_ptr(), q_row, k_row, q_weight.data_ptr(), k_weight.data_ptr(),
+            _addr(positions), N, H, Hkv, D, int(max_seqlen), eps, rope_base, qr.data_ptr(),
+            kr.data_ptr(), raw)
+    finally:
+        _leave(ctx)
+    _check("ne_qk_norm_rope_fwd", rc)
+    return qr, kr
+
+
+def ne_qk_norm_rope_bwd_workspace_bytes() -> int:
+    return int(lib().ne_qk_norm_rope_bwd_workspace_bytes())
+
+
+def ne_qk_norm_rope_bwd(dqr, dkr, q, k, q_weight, k_weight, positions, max_seqlen, eps=1e-5,
+                        rope_base=10000.0, dq=None, dk=None, dq_weight=None, dk_weight=None,
+                        workspace=None, stream=None):
+    """Backward of :func:`ne_qk_norm_rope_fwd` from the gradients of ``qr``, ``kr`` and
+    the forward's ``q``, ``k``.  Returns ``(dq, dk, dq_weight, dk_weight)``: bf16 ``[N, H,
+    64]``, ``[N, Hkv, 64]`` (contiguous unless given, as slices of a joint gradient, say)
+    and fp32 ``[64]``."""
+    dev, N, H, Hkv, D, q_row, k_row = _qk_norm_shapes(q, k, q_weight, k_weight, positions,
+                                                      rope_base)
+    _given(dqr, q.shape, _BF16, dev, "dqr")
+    _given(dkr, k.shape, _BF16, dev, "dkr")
+    dq_row = 64 * H if dq is None else _rows_of(dq, q.shape, dev, "dq")
+    dk_row = 64 * Hkv if dk is None else _rows_of(dk, k.shape, dev, "dk")
+    for t, name in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+        if t is not None:
+            _given(t, (D,), _F32, dev, name)
+    ws_bytes = _ws_bytes(workspace, dev)
+    raw, ctx = _on(stream, dev)
+    try:
+        dq = torch.empty((N, H, D), dtype=_BF16, device=q.device) if dq is None else dq
+        dk = torch.empty((N, Hkv, D), dtype=_BF16, device=q.device) if dk is None else dk
+        if dq_weight is None:
+            dq_weight = torch.empty(D, dtype=_F32, device=q.device)
+        if dk_weight is None:
+            dk_weight = torch.empty(D, dtype=_F32, device=q.device)
+        if N == 0:
+            return dq, dk, dq_weight.zero_(), dk_weight.zero_()
+        rc = lib().ne_qk_norm_rope_bwd(
+            dqr.data_ptr(), dkr.data_ptr(), q.data_ptr(), k.data_ptr(), q_row, k_row,
+            q_weight.data_ptr(), k_weight.data_ptr(), _addr(positions), N, H, Hkv, D,
+            int(max_seqlen), eps, rope_base, dq.data_ptr(), dk.data_ptr(), dq_row, dk_row,
+            dq_weight.data_ptr(), dk_weight.data_ptr(), _addr(workspace), ws_bytes, raw)
+    finally:
+        _leave(ctx)
+    _check("ne_qk_norm_rope_bwd", rc)
+    return dq, dk, dq_weight, dk_weight
+
+
+# ------------------------------------------------------- the paged cache's pages
+
+def _pages(seq_lens, block_table, free_pages, n_free, first, name):
+    """Checks what ne_kv_reserve and ne_kv_release share; returns (device, nseq,
+    max_pages, n_pages)."""
+    dev = _device(first, name)
+    _need_on(seq_lens, _I32, dev, "seq_lens")
+    _need_on(block_table, _I32, dev, "block_table")
+    _need_on(free_pages, _I32, dev, "free_pages")
+    _given(n_free, (1,), _I32, dev, "n_free")
+    nseq = seq_lens.numel()
+    if first.shape != (nseq,) or seq_lens.dim() != 1:
+        raise ValueError(f"{name}, seq_lens must be [nseq]")
+    if block_table.dim() != 2 or block_table.shape[0] != nseq:
+        raise ValueError(f"block_table must be [{nseq}, max_pages]")
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be [n_pages]")
+    return dev, nseq, block_table.shape[1], free_pages.shape[0]
+
+
+def ne_kv_reserve(new_lens, seq_lens, block_table, free_pages, n_free, n_tot, page_size,
+                  max_seqlen, cu_seqlens=None, start_pos=None, positions=None, slots=None,
+                  seq_lens_out=None, n_free_out=None, stream=None):
+    """Room in a paged cache for ``new_lens[s]`` more rows of each sequence (int32 CUDA
+    ``[nseq]``), its pages taken from the stack ``free_pages`` (int32 ``[n_pages]``, the
+    first ``n_free[0]`` of them free, the last of these the top) into ``block_table``
+    ``[nseq, max_pages]``.  ``seq_lens`` ``[nseq]`` (positions held) and ``n_free`` ``[1]``
+    are updated in place, or left as they are with the new values in ``seq_lens_out``,
+    ``n_free_out``.  Returns ``(cu_seqlens [nseq + 1], start_pos [nseq], positions
+    [n_tot], slots [n_tot])`` of the packed new rows, -1 from the last of them on:
+    :func:`ne_kv_append` takes the first two, :func:`ne_qk_norm_rope_fwd` the third; a
+    slot is page * page_size + position % page_size.  Nothing comes to the host: too few
+    pages (``NE_ERR_NO_PAGES``), rows (more than ``n_tot``) or positions
+    (``NE_ERR_BAD_SEQLEN``) show in :func:`ne_attn_get_device_status`, and then nothing
+    is handed out and there are no rows."""
+    dev, nseq, max_pages, n_pages = _pages(seq_lens, block_table, free_pages, n_free, new_lens,
+                                           "new_lens")
+    _need_on(new_lens, _I32, dev, "new_lens")
+    n_tot = int(n_tot)
+    for t, shape, name in ((cu_seqlens, (nseq + 1,), "cu_seqlens"), (start_pos, (nseq,), "start_pos"),
+                           (positions, (n_tot,), "positions"), (slots, (n_tot,), "slots"),
+                           (seq_lens_out, (nseq,), "seq_lens_out"),
+                           (n_free_out, (1,), "n_free_out")):
+        if t is not None:
+            _given(t, shape, _I32, dev, name)
+    raw, ctx = _on(stream, dev)
+    try:
+        new = lambda n: torch.empty(n, dtype=_I32, device=seq_lens.device)  # noqa: E731
+        cu_seqlens = new(nseq + 1) if cu_seqlens is None else cu_seqlens
+        start_pos = new(nseq) if start_pos is None else start_pos
+        positions = new(n_tot) if positions is None else positions
+        slots = new(n_tot) if slots is None else slots
+        rc = lib().ne_kv_reserve(
+            new_lens.data_ptr(), seq_lens.data_ptr(), nseq, block_table.data_ptr(), max_pages,
+            free_pages.data_ptr(), n_free.data_ptr(), n_pages, int(page_size), int(max_seqlen),
+            n_tot, cu_seqlens.data_ptr(), start_pos.data_ptr(), positions.data_ptr(),
+            slots.data_ptr(), _addr(seq_lens if seq_lens_out is None else seq_lens_out),
+            _addr(n_free if n_free_out is None else n_free_out), raw)
+    finally:
+        _leave(ctx)
+    _check("ne_kv_reserve", rc)
+    return cu_seqlens, start_pos, positions, slots
+
+
+def ne_kv_release(finished, seq_lens, block_table, free_pages, n_free, page_size, max_seqlen,
+                  stream=None):
+    """Take back the pages of every sequence with ``finished[s]`` (bool or uint8 CUDA
+    ``[nseq]``): they go onto the stack of :func:`ne_kv_reserve`, their entries of
+    ``block_table`` become -1 and ``seq_lens[s]`` 0, all in place.  Returns None."""
+    dev, nseq, max_pages, n_pages = _pages(seq_lens, block_table, free_pages, n_free, finished,
+                                           "finished")
+    _need_on(finished, torch.bool if finished.dtype is torch.bool else _U8, dev, "finished")
+    raw, ctx = _on(stream, dev)
+    try:
+        rc = lib().ne_kv_release(
+            finished.data_ptr(), seq_lens.data_ptr(), nseq, block_table.data_ptr(), max_pages,
+            free_pages.data_ptr(), n_free.data_ptr(), n_pages, int(page_size), int(max_seqlen),
+            raw)
+    finally:
+        _leave(ctx)
+    _check("ne_kv_release", rc)
+
+
 def _paged(k_pages, v_pages, k_scale, v_scale, block_table, nseq, dev):
     """Checks a paged cache; returns (kv_type, n_pages, Hkv, page_size, max_pages)."""
     dtype = k_pages.dtype
-    if dtype is not _BF16 and dtype is not _E4M3:
-        raise ValueError("k_pages must be bfloat16 or float8_e4m3fn")
+    if dtype is not _BF16 and dtype is not _E4M3 and dtype is not _U8:
+        raise ValueError("k_pages must be bfloat16, float8_e4m3fn or uint8 (two e2m1 each)")
     _need_on(k_pages, dtype, dev, "k_pages")
     _need_on(v_pages, dtype, dev, "v_pages")
     _need_on(block_table, _I32, dev, "block_table")
     shape = k_pages.shape
-    if len(shape) != 4 or shape != v_pages.shape or shape[3] != 64:
-        raise ValueError("k_pages, v_pages must be [n_pages, Hkv, page_size, 64]")
+    if len(shape) != 4 or shape != v_pages.shape or shape[3] != (32 if dtype is _U8 else 64):
+        raise ValueError("k_pages, v_pages must be [n_pages, Hkv, page_size, 64] (uint8: 32)")
     table = block_table.shape
     if len(table) != 2 or table[0] != nseq:
         raise ValueError(f"block_table must be [{nseq}, max_pages]")
@@ -647,11 +902,13 @@ def _paged(k_pages, v_pages, k_scale, v_scale, block_table, nseq, dev):
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale, v_scale: a bfloat16 cache has no scales")
     elif k_scale is None or v_scale is None:
-        raise ValueError("k_scale, v_scale: a float8_e4m3fn cache needs its scales")
+        raise ValueError("k_scale, v_scale: a float8_e4m3fn or uint8 cache needs its scales")
     else:
-        _given(k_scale, shape[:3], _U8, dev, "k_scale")
-        _given(v_scale, shape[:3], _U8, dev, "v_scale")
-    return (KV_BF16 if dtype is _BF16 else KV_E4M3,) + shape[:3] + table[1:]
+        scales = shape[:3] if dtype is _E4M3 else (*shape[:3], 2)
+        _given(k_scale, scales, _U8, dev, "k_scale")
+        _given(v_scale, scales, _U8, dev, "v_scale")
+    kv_type = KV_BF16 if dtype is _BF16 else KV_E4M3 if dtype is _E4M3 else KV_E2M1
+    return (kv_type,) + shape[:3] + table[1:]
 
 
 def _row_places(cu_seqlens, start_pos, dev):
@@ -669,7 +926,9 @@ def ne_kv_append(k, v, cu_seqlens, start_pos, k_pages, v_pages, block_table, max
     (``[n_tot, Hkv, 64]`` bf16, packed by ``cu_seqlens``) goes to position
     ``start_pos[s] + i``.  ``k_pages``, ``v_pages``: ``[n_pages, Hkv, page_size,
     64]``, bfloat16, or float8_e4m3fn with ``k_scale``, ``v_scale`` uint8
-    ``[n_pages, Hkv, page_size]``; ``block_table`` int32 ``[nseq, max_pages]``.
+    ``[n_pages, Hkv, page_size]``, or, in 4 bits, uint8 ``[n_pages, Hkv, page_size,
+    32]`` (two e2m1 values each; include/ne_attn.h has their order) with scales
+    ``[n_pages, Hkv, page_size, 2]``; ``block_table`` int32 ``[nseq, max_pages]``.
     ``rope_base=0``: ``k`` is rotated already.  Returns ``(k_pages, v_pages)``,
     written in place (with no rows at all, ``n_tot = 0``, as they are)."""
     dev = _device(k, "k")

@@ -39,8 +39,9 @@
  *    the first call on that stream outside graph capture and grown when
  *    needed; inside a capture each call allocates and frees its own), the
  *    backward's work-schedule tables (one per fixed-length shape, a few KB,
- *    made on first use outside graph capture), the paged decode's arrival
- *    counters (in blocks; 2 KB for each stream and each captured call) -- all released by
+ *    made on first use outside graph capture), the arrival counters of the paged
+ *    decode, the norms' backward and the calls that hand pages out and take them
+ *    back (in blocks; 2 KB for each stream and each captured call) -- all released by
  *    ne_attn_release -- and, when a backward is given no workspace, a
  *    stream-ordered temporary it frees itself.
  *  - `stream` is a cudaStream_t (NULL = legacy default stream).  Work is
@@ -85,6 +86,8 @@ typedef int ne_status;
                                 (device-detected) */
 #define NE_ERR_TOO_LARGE 8   /* problem exceeds the fixed scratch of ne_attn_bwd_noalloc */
 #define NE_ERR_BAD_PAGE 9    /* a block table entry outside the page pool (device-detected) */
+#define NE_ERR_NO_PAGES 10   /* ne_kv_reserve wants more pages than are free, or ne_kv_release
+                                gives back more than there are (device-detected) */
 
 typedef uint16_t ne_bf16; /* raw bfloat16 bits */
 
@@ -328,6 +331,20 @@ ne_status ne_attn_gqa_varlen_bwd(const ne_bf16* qr, const ne_bf16* kr, const ne_
                                  ne_bf16* dk, ne_bf16* dv, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* The same on operands that are rotated already (ne_qk_norm_rope_fwd's, for instance):
+ * qr, kr replace q, k, nothing is rotated, and the gradients are w.r.t. qr and kr.
+ * Otherwise as above. */
+ne_status ne_attn_gqa_varlen_fwd_rotated(const ne_bf16* qr, const ne_bf16* kr, const ne_bf16* v,
+                                         const int* cu_seqlens, int nseq, int n_tot,
+                                         int max_seqlen, int H, int Hkv, int D, float scale,
+                                         ne_bf16* out, float* lse, void* stream);
+ne_status ne_attn_gqa_varlen_bwd_rotated(const ne_bf16* qr, const ne_bf16* kr, const ne_bf16* v,
+                                         const ne_bf16* out, const ne_bf16* dout,
+                                         const float* lse, const int* cu_seqlens, int nseq,
+                                         int n_tot, int max_seqlen, int H, int Hkv, int D,
+                                         float scale, ne_bf16* dqr, ne_bf16* dkr, ne_bf16* dv,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
 /* A paged key/value cache for generation.  Two pools of n_pages pages, each
  * page [Hkv, page_size, 64] (a head's positions of a page are contiguous),
  * page_size 16, 32, 64, 128 or 256 (NE_ERR_UNSUPPORTED otherwise), of type
@@ -335,7 +352,16 @@ ne_status ne_attn_gqa_varlen_bwd(const ne_bf16* qr, const ne_bf16* kr, const ne_
  *   NE_KV_E4M3  8-bit e4m3, each row of 64 values with a scale byte of its
  *               own (k_scale, v_scale: uint8 [n_pages, Hkv, page_size]):
  *               value = e4m3 * 2^(byte - 127); byte 255 marks a row that held
- *               an infinity or NaN and reads back as NaN.
+ *               an infinity or NaN and reads back as NaN;
+ *   NE_KV_E2M1  4-bit e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives;
+ *               bit 3 the sign), rows of 32 bytes: a page is [Hkv, page_size,
+ *               32] bytes.  The 64 values are two halves of 32, dims 0 .. 31 and
+ *               those that RoPE pairs them with, 32 .. 63, with a scale byte each
+ *               (k_scale, v_scale: uint8 [n_pages, Hkv, page_size, 2]): value =
+ *               e2m1 * 2^(byte - 127), byte 255 as above, for the half.  Two values to a byte,
+ *               the even dim in the low four bits; of a row's eight words of four
+ *               bytes, word w holds dims 4 w .. 4 w + 3, then 32 + 4 w .. 32 + 4 w +
+ *               3 (dim d in byte 4 (d % 32 / 4) + 2 (d / 32) + d % 4 / 2).
  * Position n of sequence s lies in slot n % page_size of page
  * block_table[s * max_pages + n / page_size] (DEVICE int32 [nseq, max_pages];
  * entries past a sequence's positions are not read).  The keys of the cache
@@ -356,8 +382,9 @@ ne_status ne_attn_gqa_varlen_bwd(const ne_bf16* qr, const ne_bf16* kr, const ne_
  * rope_base > 0: k is rotated at its position (the fp32 rule of
  * ne_attn_fwd); rope_base = 0: k is k' already.  e4m3: with a row's largest
  * magnitude a, the scale is 2^e with the smallest e >= -100 that has
- * a <= 448 * 2^e, and the values are rounded to nearest even.  Two rows of one
- * call must not go to the same slot.
+ * a <= 448 * 2^e, and the values are rounded to nearest even.  e2m1: the same for
+ * each half of the row, with a <= 6 * 2^e and e <= 125 (values beyond 6 * 2^125
+ * become that).  Two rows of one call must not go to the same slot.
  *
  * ne_kv_read reads rows back, as bf16 (exact): row i of sequence s of k, v
  * from position start_pos[s] + i; the keys come as the cache holds them (k').
@@ -365,6 +392,7 @@ ne_status ne_attn_gqa_varlen_bwd(const ne_bf16* qr, const ne_bf16* kr, const ne_
  * are left as they are. */
 #define NE_KV_BF16 0
 #define NE_KV_E4M3 1
+#define NE_KV_E2M1 4
 ne_status ne_kv_append(const ne_bf16* k, const ne_bf16* v, const int* cu_seqlens,
                        const int* start_pos, int nseq, int n_tot, int Hkv, int D,
                        float rope_base, int kv_type, void* k_pages, void* v_pages,
@@ -375,6 +403,95 @@ ne_status ne_kv_read(int kv_type, const void* k_pages, const void* v_pages,
                      int max_pages, int n_pages, int page_size, int max_seqlen,
                      const int* cu_seqlens, const int* start_pos, int nseq, int n_tot, int Hkv,
                      int D, ne_bf16* k, ne_bf16* v, void* stream);
+
+/* The pages of a paged cache handed out and taken back on the GPU, and the places of a
+ * step's new rows: what ne_kv_append, ne_qk_norm_rope_fwd and ne_attn_decode_paged
+ * take, from the requests' lengths, so that a step (or a graph of it) needs no word
+ * from the host.
+ *   block_table: DEVICE int32 [nseq, max_pages], as above.  seq_lens: DEVICE int32
+ *     [nseq], the positions that each sequence holds.  free_pages: DEVICE int32
+ *     [n_pages], a stack of the pages in no sequence's hands: entries 0 .. *n_free -
+ *     1, the last the top.  n_free: DEVICE int32 [1].
+ *   nseq <= 16384; page_size as above; max_seqlen <= max_pages * page_size and 65535 *
+ *   128; n_pages * page_size < 2^31.
+ *
+ * ne_kv_reserve: sequence s gets new_lens[s] >= 0 rows (DEVICE int32 [nseq]), at
+ * positions seq_lens[s] on, and the pages that they need beyond those it has,
+ * ceil(seq_lens[s] / page_size): the stack's top goes to the first page of the first
+ * sequence that needs one, the next to the next.  Written:
+ *   block_table   the entries of the new pages (the others stay);
+ *   cu_seqlens    [nseq + 1], the prefix sums of new_lens;
+ *   start_pos     [nseq], seq_lens as it came;
+ *   positions     [n_tot], of each packed row its position in its sequence;
+ *   slots         [n_tot], its place in a pool of positions: block_table entry *
+ *                 page_size + position % page_size (-1 where the entry is outside [0,
+ *                 n_pages), reported as NE_ERR_BAD_PAGE; entries are handed out as
+ *                 they are);
+ *   seq_lens_out  [nseq], seq_lens + new_lens (may be seq_lens itself);
+ *   n_free_out    [1], n_free less the pages taken (may be n_free itself).
+ * cu_seqlens, start_pos, positions, slots: NULL where not wanted.  Rows from the sum
+ * of new_lens on have position and slot -1.  n_tot: 0 .. 2^30; 0 where neither
+ * positions nor slots are wanted leaves the number of rows unbounded.  All or nothing:
+ * a length out of place (seq_lens[s] or new_lens[s] negative, their sum beyond
+ * max_seqlen, more rows than n_tot) is reported as NE_ERR_BAD_SEQLEN, more pages than
+ * are free as NE_ERR_NO_PAGES; then no page is handed out, cu_seqlens is zero,
+ * positions and slots are -1, and seq_lens_out and n_free_out are as before, so that
+ * the calls that follow find no rows.
+ *
+ * ne_kv_release: the pages of every sequence s with finished[s] != 0 (DEVICE uint8
+ * [nseq]), ceil(seq_lens[s] / page_size) of them, go onto the stack, the first page
+ * of the first such sequence first; their entries of the block table become -1 and
+ * seq_lens[s] 0.  All or nothing, too: NE_ERR_BAD_SEQLEN for a length outside [0,
+ * max_seqlen], NE_ERR_NO_PAGES where the stack would hold more than n_pages.
+ *
+ * The arrays written must not overlap the others or each other but as stated. */
+ne_status ne_kv_reserve(const int* new_lens, const int* seq_lens, int nseq, int* block_table,
+                        int max_pages, const int* free_pages, const int* n_free, int n_pages,
+                        int page_size, int max_seqlen, int n_tot, int* cu_seqlens, int* start_pos,
+                        int* positions, int* slots, int* seq_lens_out, int* n_free_out,
+                        void* stream);
+ne_status ne_kv_release(const uint8_t* finished, int* seq_lens, int nseq, int* block_table,
+                        int max_pages, int* free_pages, int* n_free, int n_pages, int page_size,
+                        int max_seqlen, void* stream);
+
+/* RMS norm of every head of the queries and keys, with RoPE in the same pass, and
+ * its gradients (what many models do between the projections and the attention):
+ *   y = x / sqrt(mean(x^2) + eps) * w,  out = R(p) y
+ * over the 64 dims of a head; w: bf16 [64], one for all query heads and one for all
+ * key heads; fp32 inside, each output rounded once.
+ *   q, k:      [n_tot, H, 64], [n_tot, Hkv, 64] bf16, a row's heads contiguous, rows
+ *              q_stride, k_stride elements apart (multiples of 8, at least H * 64, Hkv *
+ *              64; at most 2^31): slices of a joint projection's output will do.
+ *   positions: DEVICE int32 [n_tot].  -1 marks a row of no sequence: its outputs are
+ *              left as they are and it adds nothing to the gradients of the weights.
+ *              Other positions outside [0, max_seqlen) are treated the same and
+ *              reported as NE_ERR_BAD_SEQLEN.  May be NULL with rope_base = 0.
+ *   rope_base: 0: the norms alone (for an attention that rotates).
+ *   qr, kr:    [n_tot, H, 64], [n_tot, Hkv, 64] bf16 (written): what the *_rotated
+ *              attention calls, and with rope_base = 0 ne_kv_append and
+ *              ne_attn_decode_paged, take.
+ * H and Hkv are independent; n_tot * (H + Hkv) < 2^31.  (The squares are summed in
+ * fp32: magnitudes from 2^60 on may overflow there.)
+ * The backward takes the gradients dqr, dkr of qr, kr and the forward's q and k, and
+ * returns dq, dk (bf16, rows dq_stride, dk_stride apart) and dq_weight, dk_weight
+ * (fp32 [64], 16-byte aligned, written: sums over all rows and heads in an order that
+ * the sizes fix: the same call gives the same bits).
+ * workspace: ne_qk_norm_rope_bwd_workspace_bytes() bytes, 16-byte aligned, or NULL for
+ * the library's temporary.  Outputs must not overlap inputs. */
+ne_status ne_qk_norm_rope_fwd(const ne_bf16* q, const ne_bf16* k, long long q_stride,
+                              long long k_stride, const ne_bf16* q_weight,
+                              const ne_bf16* k_weight, const int* positions, int n_tot, int H,
+                              int Hkv, int D, int max_seqlen, float eps, float rope_base,
+                              ne_bf16* qr, ne_bf16* kr, void* stream);
+size_t ne_qk_norm_rope_bwd_workspace_bytes(void);
+ne_status ne_qk_norm_rope_bwd(const ne_bf16* dqr, const ne_bf16* dkr, const ne_bf16* q,
+                              const ne_bf16* k, long long q_stride, long long k_stride,
+                              const ne_bf16* q_weight, const ne_bf16* k_weight,
+                              const int* positions, int n_tot, int H, int Hkv, int D,
+                              int max_seqlen, float eps, float rope_base, ne_bf16* dq, ne_bf16* dk,
+                              long long dq_stride, long long dk_stride, float* dq_weight,
+                              float* dk_weight, void* workspace, size_t workspace_bytes,
+                              void* stream);
 
 /* Decode attention over a paged cache: one new token per sequence attends to
  * every cached position, its own included (already appended).
@@ -462,8 +579,8 @@ ne_status ne_mtp_head(const ne_bf16* h, const ne_bf16* w, const int* targets, in
                       void* workspace, size_t workspace_bytes, void* stream);
 
 /* Synchronize `stream`, then return and clear the device status word of the
- * current device: NE_OK, NE_ERR_TIMEOUT, NE_ERR_BAD_SEQLEN or NE_ERR_BAD_PAGE
- * (or NE_ERR_CUDA if the synchronization itself failed). */
+ * current device: NE_OK, NE_ERR_TIMEOUT, NE_ERR_BAD_SEQLEN, NE_ERR_BAD_PAGE or
+ * NE_ERR_NO_PAGES (or NE_ERR_CUDA if the synchronization itself failed). */
 ne_status ne_attn_get_device_status(void* stream);
 
 /* Detail of the last device status read by ne_attn_get_device_status: the raw
