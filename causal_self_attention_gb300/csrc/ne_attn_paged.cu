@@ -76,22 +76,24 @@ constexpr int kQSlots = 2;
 
 template <Kv kType>
 struct Tile {
-  static constexpr int kKeys = kType == Kv::kBf16 ? 16 : 32;  // of a warp
-  static constexpr int kTile = kWarps * kKeys;                // 128 / 64 keys
+  static constexpr int kKeys = kType == Kv::kBf16 ? 16 : kType == Kv::kE4m3 ? 32 : 64;  // of a warp
+  static constexpr int kTile = kWarps * kKeys;                // 64, 128, 256 keys
   static constexpr int kRowBytes = kType == Kv::kE2m1 ? kHD / 2 : kType == Kv::kE4m3 ? kHD : 2 * kHD;
   static constexpr int kScales = kType == Kv::kE2m1 ? 2 : kType == Kv::kE4m3 ? 1 : 0;  // of a row
-  static constexpr int kPool = kTile * kRowBytes;             // 8 KiB (e2m1: 4) of K, and of V
+  static constexpr int kPool = kTile * kRowBytes;             // 8 KiB of K, and of V
   static constexpr int kStageBytes = 2 * kPool + 2 * kScales * kTile;
 };
 
 template <Kv kType, int kRows>
 struct Cfg {
   static constexpr int kCtas = kRows == 8 ? 3 : 2;      // per SM
-  static constexpr int kStages = (kRows == 8 ? 3 : 4) * (kType == Kv::kE2m1 ? 2 : 1);
+  static constexpr int kStages = kRows == 8 ? 3 : 4;
   static constexpr int OFF_RED = kStages * Tile<kType>::kStageBytes;
   // m, l, m2, bad, o[64]; e2m1: the other half's m2
   static constexpr int kRedRow = kHD + (kType == Kv::kE2m1 ? 8 : 4);
-  static constexpr int OFF_Q = OFF_RED + kWarps * kRows * kRedRow * 4;
+  static constexpr int kScratch = kType == Kv::kE2m1 ? 768 : 0;  // of a warp: FourBit's
+  static constexpr int OFF_SCRATCH = OFF_RED + kWarps * kRows * kRedRow * 4;
+  static constexpr int OFF_Q = OFF_SCRATCH + kWarps * kScratch;
   static constexpr int kQBytes = kRows * kQRow + 256;    // q rows, one row of the RoPE table
   static constexpr int OFF_PREFIX = OFF_Q + kQSlots * kQBytes;
   static constexpr int OFF_LEN = OFF_PREFIX + (kMaxBatch + 2) * 4;
@@ -199,6 +201,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Key of a warp's e4m3 slice that stands in row x of score tile mt (16 rows
 // each).  The rows of a lane are then c, 4 + (c ^ 1), 8 + c, 12 + (c ^ 1) as the
 // contraction with v wants them in pairs 2 c, 2 c + 1: the two rows that a
@@ -214,24 +222,387 @@ __device__ __forceinline__ int e2m1_key(int mt, int x) {
   const int c = (x & 7) >> 1;
   return 16 * mt + (x & 8) + ((x & 1) ? 4 + (c ^ 2) : c);
 }
-template <Kv kType>
-__device__ __forceinline__ int key_of(int mt, int x) {
-  return kType == Kv::kBf16 ? 16 * mt + x : kType == Kv::kE4m3 ? e4m3_key(mt, x) : e2m1_key(mt, x);
-}
-// Two scale bytes -> 2^(byte - 127) as two bf16 (exact; 255: NaN).
-__device__ __forceinline__ uint32_t scales_bf16x2(uint32_t two) {
-  uint32_t b = two & 255u, c = two >> 8;
-  b = b == 255u ? 0x7fc0u : b == 0u ? 0x40u : b << 7;
-  c = c == 255u ? 0x7fc0u : c == 0u ? 0x40u : c << 7;
-  return b | (c << 16);
-}
-// ... and their exponents (byte - 127), as two bf16 (exact; 255: NaN).
-__device__ __forceinline__ uint32_t exponents_bf16x2(uint32_t two) {
-  const uint32_t b = two & 255u, c = two >> 8;
-  const uint32_t e = pack_bf16x2(static_cast<float>(static_cast<int>(b) - 127),
-                                 static_cast<float>(static_cast<int>(c) - 127));
-  return (b == 255u ? 0x7fc0u : e & 0xffffu) | (c == 255u ? 0x7fc00000u : e & 0xffff0000u);
-}
+
+// The state of a warp's softmax over 4-bit rows, and a tile of 64 keys, two a lane.
+//
+// Scores: the products with the two halves of a key's row, each with its scale: x =
+// s0 a0 + s1 a1, f x in log2 units.  Weights p = 2^(f x - m) with a reference m, in
+// halves; for a value row's half h they take its scale, 2 p 2^(e_h - E_h), E_h an
+// exponent that the warp keeps, so that a weight is formed once and scaled by a product
+// of two halves.  (E_h - e_h is 0 .. 15: what that costs is half's smallest step, 2^-26 of
+// 2^E_h, 2^-11 of the largest term that the sum has.)  Where a score exceeds its
+// reference by more than 2^8, or an exponent this range, or the sequence ends in the
+// tile -- one vote tells --, the tile takes a longer way, on which the references move.
+// Rows whose scales differ by more (never mind zeros) put the warp into another mode
+// for the rest of the segment: a reference of its own for every (query head, half),
+// 2^(f x + e_h - m2), which loses nothing however far the scales are apart.
+//
+// What bounds a tile is the integer pipe: 128 of its conversions take two cycles each,
+// so that choices are made by masks and pairs of bytes are looked at together.
+template <int kNT>
+struct FourBit {
+  static constexpr float kNone = -1e30f;  // no score yet: a finite one exceeds it by any measure
+  static constexpr int kMT = 4;           // row tiles of 16 keys
+  static constexpr int kRange = 15;
+  static constexpr int kZero = 27;        // the scale byte of zeros
+  static constexpr int kUnset = -1000;
+  static constexpr int kScratch = 16 * kMT * 12;  // a warp's: key scales (float2), value factors
+  float m[kNT][2], l[kNT][2];             // l: of this lane's keys
+  float o[kNT][4][4];                     // row tiles 0, 1: the first half's dims; 2, 3: the second's
+  int eb[2];                              // E_h + 127
+  bool slow;
+  float m2[kNT][2][2];                    // slow: o's references
+
+  __device__ __forceinline__ void begin() {
+    slow = false;
+    eb[0] = eb[1] = kUnset;
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[nt][e] = m2[nt][e][0] = m2[nt][e][1] = kNone;
+        l[nt][e] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+    }
+  }
+  // The references as the segment's end wants them.
+  __device__ __forceinline__ float ref(int nt, int e) const {
+    return m[nt][e] > 0.5f * kNone ? m[nt][e] : -INFINITY;
+  }
+  __device__ __forceinline__ float of_o(int nt, int e, int h) const {
+    return slow ? m2[nt][e][h] : m[nt][e] + static_cast<float>(eb[h] - 128);
+  }
+  __device__ __forceinline__ float ref2(int nt, int e, int h) const {
+    const float x = of_o(nt, e, h);
+    return x > 0.5f * kNone ? x : -INFINITY;
+  }
+
+  // Where the keys of a lane, j and j + 32, stand: rows r of tiles t = 2 mt + hf and t + 4
+  // (row r + 8 hf of score tile mt).
+  struct Slots {
+    int k, v;  // in a warp's scratch: of its key scales (float2), of its value factors (uint16)
+    __device__ __forceinline__ explicit Slots(int lane) {
+      const int t = lane >> 3, y = lane & 7;
+      const int r = y < 4 ? 2 * y : 2 * ((y - 4) ^ 2) + 1;  // e2m1_key's inverse
+      k = 2 * kMT * r + t;
+      v = 2 * (2 * kMT * (r >> 1) + t) + (r & 1);
+    }
+  };
+  static constexpr int kOther = 16 * kMT;  // from a half's factors to the other's (uint16)
+
+  // 2 * 2^(byte - 127 - E_h) as a half: NaN for a row marked so, zero for zeros far below.
+  __device__ __forceinline__ uint32_t factor(int byte, int h) const {
+    const int u = byte - eb[h] + kRange;
+    return byte == 255 ? 0x7e00u : u >= 0 && u <= kRange ? static_cast<uint32_t>(u + 1) << 10 : 0u;
+  }
+  static __device__ __forceinline__ float column_max(float v) {
+#pragma unroll
+    for (int sh = 4; sh < 32; sh <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, sh));
+    return v;
+  }
+
+  // Moves the references to what this tile holds (vb: the scale bytes of this lane's value
+  // rows, -1 for none).  Returns whether the mode changed.
+  __device__ __forceinline__ bool move(const float (&x)[kMT][kNT][4], const float (&f)[kNT][2],
+                                       const int (&vb)[2][2]) {
+    bool turned = false;
+    if (!slow) {
+      int hi[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        int most = eb[h], least = 1000;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (vb[i][h] >= 0 && vb[i][h] != 255) {
+            most = max(most, vb[i][h]);
+            if (vb[i][h] > kZero) least = min(least, vb[i][h]);
+          }
+        }
+        hi[h] = __reduce_max_sync(0xffffffffu, most);
+        turned |= __reduce_min_sync(0xffffffffu, least) < hi[h] - kRange;
+      }
+      if (turned) {  // o stays as it is, under the references that it has
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) m2[nt][e][h] = of_o(nt, e, h);
+        slow = true;
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float down = ex2_approx(static_cast<float>(eb[h] - hi[h]));
+          eb[h] = hi[h];
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int i = 2 * h; i < 2 * h + 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][i][e] *= down;
+        }
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float a = -INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) a = fmaxf(a, fmaxf(x[mt][nt][e], x[mt][nt][2 + e]));
+        a = column_max(a) * f[nt][e];
+        if (a > m[nt][e]) {
+          const float up = ex2_approx(m[nt][e] - a);
+          m[nt][e] = a;
+          l[nt][e] *= up;
+          if (!slow) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o[nt][i][e] *= up;
+              o[nt][i][2 + e] *= up;
+            }
+          }
+        }
+      }
+    return turned;
+  }
+
+  // The other mode: o's references for this tile, ev its value rows' exponents in half h.
+  // first: the mode's first tile, where a reference may be far above o's size (exponents of
+  // rows without weight made it): there it comes down to that size.
+  __device__ __forceinline__ void far_references(const float (&x)[kMT][kNT][4],
+                                                 const float (&f)[kNT][2],
+                                                 const float (&ev)[kMT][2], int h, bool first) {
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t = -INFINITY, size = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            t = fmaxf(t, __fmaf_rn(x[mt][nt][2 * hf + e], f[nt][e], ev[mt][hf]));
+#pragma unroll
+        for (int i = 2 * h; i < 2 * h + 2; ++i)
+          size = fmaxf(size, fmaxf(fabsf(o[nt][i][e]), fabsf(o[nt][i][2 + e])));
+        t = column_max(t);
+        const float old = m2[nt][e][h];
+        float now = fmaxf(t, old);
+        if (first) {
+          size = column_max(size);
+          now = fmaxf(t, size > 0.f ? old + __log2f(size) : kNone);
+        }
+        m2[nt][e][h] = now;
+        const float part = ex2_approx(0.5f * (old - now));  // (2^(old - now) may leave fp32's range)
+#pragma unroll
+        for (int i = 2 * h; i < 2 * h + 2; ++i) {
+          o[nt][i][e] = o[nt][i][e] * part * part;
+          o[nt][i][2 + e] = o[nt][i][2 + e] * part * part;
+        }
+      }
+  }
+
+  // o^T += V^T P^T, 16 keys.  A word is dims 4 r .. 4 r + 3 of each half of a key's row: row
+  // tile i holds the word's byte i, its low value (row r) and its high one (row r + 8).
+  // Two keys' low values make a byte, and two keys' high ones.  b: the weights as B
+  // fragments (keys x heads) for each half.
+  __device__ __forceinline__ void add_values(const uint8_t* sv, int mt, int r, int c,
+                                             const uint32_t (&b)[2][kNT][2]) {
+    uint32_t vw[4], va[4][4];  // [operand register][row tile]
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      vw[i] = *reinterpret_cast<const uint32_t*>(
+          sv + e2m1_key(mt, 8 * (i >> 1) + 2 * c + (i & 1)) * (kHD / 2) + 4 * r);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t x = vw[2 * j], y = vw[2 * j + 1];
+      kv::e2m1x8_to_f16x2((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), va[2 * j]);
+      kv::e2m1x8_to_f16x2(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), va[2 * j + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v4[4] = {va[0][i], va[1][i], va[2][i], va[3][i]};
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+        mma16816<true>(o[nt][i], v4, b[i >> 1][nt][0], b[i >> 1][nt][1]);
+    }
+  }
+
+  // 64 keys: rows sk, sv of 32 bytes, scale bytes ks, vs, the first `live` of them the
+  // sequence's (what the others hold is finite but for their scales, which are not
+  // used).  scratch: kScratch bytes of the warp's own.
+  __device__ __forceinline__ void tile(const uint8_t* sk, const uint8_t* sv, const uint16_t* ks,
+                                       const uint16_t* vs, uint8_t* scratch, const Slots& at,
+                                       int live, const uint32_t (&qb)[kNT][4][2],
+                                       const float (&f)[kNT][2], int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    uint16_t* factors = reinterpret_cast<uint16_t*>(scratch + 128 * kMT);
+    uint32_t bytes[2];
+    bool longer = live < 16 * kMT;
+    // (Both halves' exponents in one word: 0 .. 15 fits.)
+    const uint32_t base = static_cast<uint32_t>(eb[0] - kRange) +
+                          (static_cast<uint32_t>(eb[1] - kRange) << 16);
+    longer |= slow;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t kb = ks[lane + 32 * i];
+      bytes[i] = vs[lane + 32 * i];
+      reinterpret_cast<float2*>(scratch)[at.k + 4 * i] =
+          make_float2(kv::scale_value(kb & 255u), kv::scale_value(kb >> 8));
+      const uint32_t u = __byte_perm(bytes[i], 0u, 0x4140) - base;
+      longer |= (u & 0xfff0fff0u) != 0u;
+      const uint32_t two = (u << 10) + 0x04000400u;
+      factors[at.v + 8 * i] = static_cast<uint16_t>(two);
+      factors[at.v + 8 * i + kOther] = static_cast<uint16_t>(two >> 16);
+    }
+    __syncwarp();
+    float x[kMT][kNT][4];
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+      const uint2 w0 = *reinterpret_cast<const uint2*>(sk + e2m1_key(mt, r) * (kHD / 2) + 8 * c);
+      const uint2 w1 = *reinterpret_cast<const uint2*>(sk + e2m1_key(mt, r + 8) * (kHD / 2) + 8 * c);
+      uint32_t x0[2][4], x1[2][4];  // [word][byte]: halves of rows r, r + 8
+      kv::e2m1x8_to_f16x2(w0.x, x0[0]);
+      kv::e2m1x8_to_f16x2(w0.y, x0[1]);
+      kv::e2m1x8_to_f16x2(w1.x, x1[0]);
+      kv::e2m1x8_to_f16x2(w1.y, x1[1]);
+      // (s0, s1) of row r, of row r + 8
+      const float4 s = reinterpret_cast<const float4*>(scratch)[kMT * r + mt];
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        float a[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t lo[4] = {x0[k][0], x1[k][0], x0[k][1], x1[k][1]};
+          const uint32_t hi[4] = {x0[k][2], x1[k][2], x0[k][3], x1[k][3]};
+          mma16816<true>(a[0], lo, qb[nt][k][0], qb[nt][k][1]);
+          mma16816<true>(a[1], hi, qb[nt][2 + k][0], qb[nt][2 + k][1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[mt][nt][e] = __fmaf_rn(a[1][e], e < 2 ? s.y : s.w, a[0][e] * (e < 2 ? s.x : s.z));
+      }
+    }
+    uint32_t w[kMT][kNT][2];
+    float sum[kNT][2];
+    uint32_t top;  // halves that are not negative compare as their bits do
+    auto weigh = [&]() {
+      top = 0u;
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        sum[nt][0] = sum[nt][1] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float p[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              p[e] = ex2_approx(__fmaf_rn(x[mt][nt][2 * hf + e], f[nt][e], -m[nt][e]));
+              sum[nt][e] += p[e];
+            }
+            w[mt][nt][hf] = pack_f16x2(p[0], p[1]);
+            top = __vmaxu2(top, w[mt][nt][hf]);
+          }
+      }
+    };
+    weigh();
+    longer |= ((top + 0x23ff23ffu) & 0x80008000u) != 0u;  // above 2^8 = 0x5c00
+    if (__any_sync(0xffffffffu, longer)) {
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+          if (e2m1_key(mt, r + 8 * hf) >= live) {
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) x[mt][nt][2 * hf] = x[mt][nt][2 * hf + 1] = -INFINITY;
+          }
+      int vb[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool mine = lane + 32 * i < live;
+        vb[i][0] = mine ? static_cast<int>(bytes[i] & 255u) : -1;
+        vb[i][1] = mine ? static_cast<int>(bytes[i] >> 8) : -1;
+      }
+      const bool first = move(x, f, vb);
+      weigh();
+      if (slow) {
+        far_values(x, f, sv, vs, live, first, r, c);
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) l[nt][e] += sum[nt][e];
+        return;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          factors[at.v + 8 * i + kOther * h] =
+              static_cast<uint16_t>(vb[i][h] < 0 ? 0u : factor(vb[i][h], h));
+      __syncwarp();
+    }
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) l[nt][e] += sum[nt][e];
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+      uint32_t b[2][kNT][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint2 fw = reinterpret_cast<const uint2*>(factors + kOther * h)[kMT * c + mt];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          if (h == 0) {
+            w[mt][nt][0] = transpose8x8(w[mt][nt][0]);
+            w[mt][nt][1] = transpose8x8(w[mt][nt][1]);
+          }
+          b[h][nt][0] = mul_f16x2(w[mt][nt][0], fw.x);
+          b[h][nt][1] = mul_f16x2(w[mt][nt][1], fw.y);
+        }
+      }
+      add_values(sv, mt, r, c, b);
+    }
+  }
+
+  __device__ __forceinline__ void far_values(const float (&x)[kMT][kNT][4], const float (&f)[kNT][2],
+                                             const uint8_t* sv, const uint16_t* vs, int live,
+                                             bool first, int r, int c) {
+    float ev[2][kMT][2];
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = e2m1_key(mt, r + 8 * hf);
+          const int byte = h ? vs[key] >> 8 : vs[key] & 255;
+          ev[h][mt][hf] = key >= live ? 0.f : byte == 255 ? NAN : static_cast<float>(byte - 127);
+        }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) far_references(x, f, ev[h], h, first);
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+      uint32_t b[2][kNT][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            b[h][nt][hf] = transpose8x8(pack_f16x2(
+                ex2_approx(__fmaf_rn(x[mt][nt][2 * hf], f[nt][0], ev[h][mt][hf]) - m2[nt][0][h]),
+                ex2_approx(__fmaf_rn(x[mt][nt][2 * hf + 1], f[nt][1], ev[h][mt][hf]) - m2[nt][1][h])));
+      add_values(sv, mt, r, c, b);
+    }
+  }
+};
 }  // namespace paged
 
 // kDrop: a tile of one CTA never arrives, for the tests of a wait that runs out.
@@ -242,15 +613,16 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
   using namespace paged;
   using T = Tile<kType>;
   using L = Cfg<kType, kRows>;
-  constexpr bool kE2m1 = kType == Kv::kE2m1;
-  constexpr bool kF16 = kType != Kv::kBf16;  // products of halves, scales per row
-  constexpr int kParts = kE2m1 ? 2 : 1;      // parts of a row with a scale each
   constexpr int kStages = L::kStages;
   constexpr int kNT = kRows / 8;           // column tiles: 8 query heads each
+  constexpr bool kE4m3 = kType == Kv::kE4m3, kE2m1 = kType == Kv::kE2m1;
+  constexpr bool kF16 = kE4m3 || kE2m1;  // products of halves
+  static_assert(!kE2m1 || (L::kScratch == FourBit<kNT>::kScratch && T::kKeys == 16 * FourBit<kNT>::kMT),
+                "FourBit's tile");
   constexpr int kMT = T::kKeys / 16;       // row tiles of a warp's keys
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  // (An offset, not a rounded address: the loads below stay loads of shared memory.)
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   int* prefix = reinterpret_cast<int*>(smem + L::OFF_PREFIX);
   int* lens = reinterpret_cast<int*>(smem + L::OFF_LEN);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
@@ -436,6 +808,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
   // tile and heads 2 c and 2 c + 1 of each column tile; of the output, two dims
   // of each of four row tiles and the same heads.
   const int r = lane >> 2, c = lane & 3;
+  const typename FourBit<kNT>::Slots slots(lane);
   bool ok = true;
   int g = 0, nq = 0;
   Segment s = first_segment(prefix, B, J, x0, x1);
@@ -472,9 +845,9 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
           // dims 16 c + 4 k .. + 3 (any order of the contraction will do, if
           // K's has it too).  e2m1: k-steps 0, 1 the first half, dims 8 c + 4 k ..,
           // 2, 3 the second.
-          const int d = kE2m1 ? 32 * (k >> 1) + 8 * c + 4 * (k & 1) + 2 * u
-                        : kF16 ? 16 * c + 4 * k + 2 * u
-                               : 16 * k + 2 * c + 8 * u;
+          const int d = kE2m1   ? 32 * (k >> 1) + 8 * c + 4 * (k & 1) + 2 * u
+                        : kE4m3 ? 16 * c + 4 * k + 2 * u
+                                : 16 * k + 2 * c + 8 * u;
           const uint32_t me = *reinterpret_cast<const uint32_t*>(row + 2 * d);
           float v0 = bf16lo_to_f32(me), v1 = bf16hi_to_f32(me);
           if (p.rope.cs) {
@@ -505,6 +878,10 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
         const float up = p.scale_log2 * (plain ? __uint_as_float(eb << 23) : 1.f);  // of head r
         f[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
         f[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+        if (kE2m1) {  // (positive: FourBit multiplies scores of -inf by it)
+          f[nt][0] = fmaxf(f[nt][0], 1.17549435e-38f);
+          f[nt][1] = fmaxf(f[nt][1], 1.17549435e-38f);
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -516,16 +893,13 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
     if (ok && lane == 0) mbar_arrive(&qempty[slot]);
 
     // References (the same in every lane of a column), sums (this lane's keys).
-    // (m2: of the weights with their value rows' scales, for each scale of a row.)
-    float m[kNT][2], m2[kNT][2][kParts], l[kNT][2];
+    float m[kNT][2], m2[kNT][2], l[kNT][2];
     float o[kNT][4][4];
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[nt][e] = -INFINITY;
-#pragma unroll
-        for (int h = 0; h < kParts; ++h) m2[nt][e][h] = -INFINITY;
+        m[nt][e] = m2[nt][e] = -INFINITY;
         l[nt][e] = 0.f;
       }
 #pragma unroll
@@ -534,6 +908,8 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
     }
     bool bad = false;
+    FourBit<kNT> four;
+    if constexpr (kE2m1) four.begin();
 
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const int st = g % kStages;
@@ -544,7 +920,17 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
       uint8_t* sk = smem + st * T::kStageBytes + warp * T::kKeys * T::kRowBytes;
       uint8_t* sv = sk + T::kPool;
       const int live = n - t * T::kTile - warp * T::kKeys;  // of this warp's keys, from the first
-      if (!kE2m1 && live < T::kKeys) {  // (an e2m1 row is finite whatever its bytes)
+      if constexpr (kE2m1) {
+        const uint16_t* scales =
+            reinterpret_cast<const uint16_t*>(smem + st * T::kStageBytes + 2 * T::kPool) +
+            warp * T::kKeys;
+        four.tile(sk, sv, scales, scales + T::kTile,
+                  smem + L::OFF_SCRATCH + warp * L::kScratch, slots, live, qb, f, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+        continue;
+      }
+      if (live < T::kKeys) {
         // Past the end: clear the value rows (16 bytes a lane and step).
         const int first = max(live, 0) * T::kRowBytes;
         for (int i = first + 16 * lane; i < T::kKeys * T::kRowBytes; i += 512)
@@ -554,61 +940,14 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
       }
       // Scores: [row tile][column tile][key r: heads 2c, 2c+1; key r + 8: the same].
       float sc[kMT][kNT][4];
-      float ev[kMT][2][kParts];  // exponents of the value rows' scales
+      float ev[kMT][2];  // e4m3: exponents of the value rows' scales
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[mt][nt][e] = 0.f;
-      if constexpr (kE2m1) {
-        const uint16_t* scales =
-            reinterpret_cast<const uint16_t*>(smem + st * T::kStageBytes + 2 * T::kPool) +
-            warp * T::kKeys;
-        const uint32_t ks2 = scales_bf16x2(scales[lane]);
-        const uint32_t vs2 = exponents_bf16x2(scales[T::kTile + lane]);
-        // Products with each half of a row, then their sum with the halves' scales.
-        float s2[kMT][kNT][4];
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-          const uint2 w0 = *reinterpret_cast<const uint2*>(sk + e2m1_key(mt, r) * T::kRowBytes + 8 * c);
-          const uint2 w1 = *reinterpret_cast<const uint2*>(sk + e2m1_key(mt, r + 8) * T::kRowBytes + 8 * c);
-          uint32_t x0[2][4], x1[2][4];  // [word][byte]: halves of rows r, r + 8
-          kv::e2m1x8_to_f16x2(w0.x, x0[0]);
-          kv::e2m1x8_to_f16x2(w0.y, x0[1]);
-          kv::e2m1x8_to_f16x2(w1.x, x1[0]);
-          kv::e2m1x8_to_f16x2(w1.y, x1[1]);
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s2[mt][nt][e] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t lo[4] = {x0[k][0], x1[k][0], x0[k][1], x1[k][1]};
-              const uint32_t hi[4] = {x0[k][2], x1[k][2], x0[k][3], x1[k][3]};
-              mma16816<true>(sc[mt][nt], lo, qb[nt][k][0], qb[nt][k][1]);
-              mma16816<true>(s2[mt][nt], hi, qb[nt][2 + k][0], qb[nt][2 + k][1]);
-            }
-          }
-        }
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const int key = e2m1_key(mt, r + 8 * hf);
-            const uint32_t ks = __shfl_sync(0xffffffffu, ks2, key);
-            const uint32_t vs = __shfl_sync(0xffffffffu, vs2, key);
-            ev[mt][hf][0] = bf16lo_to_f32(vs);
-            ev[mt][hf][kParts - 1] = bf16hi_to_f32(vs);
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float& x = sc[mt][nt][2 * hf + e];
-                x = __fmaf_rn(s2[mt][nt][2 * hf + e], bf16hi_to_f32(ks), x * bf16lo_to_f32(ks)) * f[nt][e];
-              }
-          }
-      } else if constexpr (kF16) {
+      if constexpr (kE4m3) {
         const uint8_t* scales = smem + st * T::kStageBytes + 2 * T::kPool + warp * T::kKeys;
         const int kb = scales[lane], vb = scales[T::kTile + lane];
 #pragma unroll
@@ -634,7 +973,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
           for (int hf = 0; hf < 2; ++hf) {
             const int key = e4m3_key(mt, r + 8 * hf);
             const float ks = __shfl_sync(0xffffffffu, kf, key);
-            ev[mt][hf][0] = __shfl_sync(0xffffffffu, vf, key);
+            ev[mt][hf] = __shfl_sync(0xffffffffu, vf, key);
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -664,54 +1003,44 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            if (key_of<kType>(mt, r + 8 * hf) >= live) {
+            const int key = kE4m3 ? e4m3_key(mt, r + 8 * hf) : 16 * mt + r + 8 * hf;
+            if (key >= live) {
 #pragma unroll
               for (int nt = 0; nt < kNT; ++nt)
                 sc[mt][nt][2 * hf] = sc[mt][nt][2 * hf + 1] = -INFINITY;
-#pragma unroll
-              for (int h = 0; h < kParts; ++h)
-                if (kF16) ev[mt][hf][h] = 0.f;
+              if (kE4m3) ev[mt][hf] = 0.f;
             }
           }
       }
       // A score above its reference by more than 2^8 anywhere in the warp (the
       // first keys: m = -inf): move the references to the maxima.
-      float mx[kNT][2], mx2[kNT][2][kParts];
+      float mx[kNT][2], mx2[kNT][2];
       bool over = false;
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[nt][e] = -INFINITY;
-#pragma unroll
-          for (int h = 0; h < kParts; ++h) mx2[nt][e][h] = -INFINITY;
+          mx[nt][e] = mx2[nt][e] = -INFINITY;
 #pragma unroll
           for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
               mx[nt][e] = fmaxf(mx[nt][e], sc[mt][nt][2 * hf + e]);
-#pragma unroll
-              for (int h = 0; h < kParts; ++h)
-                if (kF16) mx2[nt][e][h] = fmaxf(mx2[nt][e][h], sc[mt][nt][2 * hf + e] + ev[mt][hf][h]);
+              if (kE4m3) mx2[nt][e] = fmaxf(mx2[nt][e], sc[mt][nt][2 * hf + e] + ev[mt][hf]);
             }
           over |= mx[nt][e] > m[nt][e] + 8.f;
-#pragma unroll
-          for (int h = 0; h < kParts; ++h)
-            if (kF16) over |= mx2[nt][e][h] > m2[nt][e][h] + 8.f;
+          if (kE4m3) over |= mx2[nt][e] > m2[nt][e] + 8.f;
         }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float a = mx[nt][e];
+            float a = mx[nt][e], b = mx2[nt][e];
 #pragma unroll
             for (int sh = 4; sh < 32; sh <<= 1) {
               a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, sh));
-#pragma unroll
-              for (int h = 0; h < kParts; ++h)
-                if (kF16)
-                  mx2[nt][e][h] = fmaxf(mx2[nt][e][h], __shfl_xor_sync(0xffffffffu, mx2[nt][e][h], sh));
+              if (kE4m3) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, sh));
             }
             // (-inf stays until a finite score comes; a factor of 0 / 0 = NaN
             // cannot come up: the new reference is finite or +inf.)
@@ -721,35 +1050,30 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
               l[nt][e] *= up;
               m[nt][e] = a;
             }
-#pragma unroll
-            for (int h = 0; h < kParts; ++h) {
-              if (kF16) {
-                const float b = mx2[nt][e][h];
-                up = 1.f;
-                if (b > m2[nt][e][h]) {
-                  up = ex2_approx(m2[nt][e][h] - b);
-                  m2[nt][e][h] = b;
-                }
+            if (kE4m3) {
+              up = 1.f;
+              if (b > m2[nt][e]) {
+                up = ex2_approx(m2[nt][e] - b);
+                m2[nt][e] = b;
               }
+            }
 #pragma unroll
-              for (int i = 4 / kParts * h; i < 4 / kParts * (h + 1); ++i) {
-                o[nt][i][e] *= up;
-                o[nt][i][2 + e] *= up;
-              }
+            for (int i = 0; i < 4; ++i) {
+              o[nt][i][e] *= up;
+              o[nt][i][2 + e] *= up;
             }
           }
       }
       // Weights, transposed into B fragments (keys x heads); a column none of
       // whose keys is live yet (m = -inf) takes none.
-      uint32_t pb[kMT][kNT][kParts][2];
+      uint32_t pb[kMT][kNT][2];
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
-        float ref[2], ref2[2][kParts];
+        float ref[2], ref2[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           ref[e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
-#pragma unroll
-          for (int h = 0; h < kParts; ++h) ref2[e][h] = m2[nt][e][h] == -INFINITY ? 0.f : m2[nt][e][h];
+          ref2[e] = m2[nt][e] == -INFINITY ? 0.f : m2[nt][e];
         }
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
@@ -759,45 +1083,19 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
             const float p0 = ex2_approx(s0 - ref[0]), p1 = ex2_approx(s1 - ref[1]);
             l[nt][0] += p0;
             l[nt][1] += p1;
-#pragma unroll
-            for (int h = 0; h < kParts; ++h) {
-              uint32_t w2;
-              if constexpr (kF16)
-                w2 = pack_f16x2(ex2_approx(s0 + ev[mt][hf][h] - ref2[0][h]),
-                                ex2_approx(s1 + ev[mt][hf][h] - ref2[1][h]));
-              else
-                w2 = pack_bf16x2(p0, p1);
-              pb[mt][nt][h][hf] = transpose8x8(w2);
-            }
+            uint32_t w2;
+            if constexpr (kE4m3)
+              w2 = pack_f16x2(ex2_approx(s0 + ev[mt][hf] - ref2[0]),
+                              ex2_approx(s1 + ev[mt][hf] - ref2[1]));
+            else
+              w2 = pack_bf16x2(p0, p1);
+            pb[mt][nt][hf] = transpose8x8(w2);
           }
       }
       // o^T += V^T P^T, 16 keys a step.
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
-        if constexpr (kE2m1) {
-          // A word is dims 4 r .. 4 r + 3 of each half of the lane's four keys: row
-          // tile i holds the word's byte i, its low value (row r) and its high one (row
-          // r + 8).  Two keys' low values make a byte, and two keys' high ones.
-          uint32_t vw[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            vw[i] = *reinterpret_cast<const uint32_t*>(
-                sv + e2m1_key(mt, 8 * (i >> 1) + 2 * c + (i & 1)) * T::kRowBytes + 4 * r);
-          uint32_t va[4][4];  // [operand register][row tile]
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t a = vw[2 * j], b = vw[2 * j + 1];
-            kv::e2m1x8_to_f16x2((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), va[2 * j]);
-            kv::e2m1x8_to_f16x2(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), va[2 * j + 1]);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t v4[4] = {va[0][i], va[1][i], va[2][i], va[3][i]};
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
-              mma16816<true>(o[nt][i], v4, pb[mt][nt][(i >> 1) % kParts][0], pb[mt][nt][(i >> 1) % kParts][1]);
-          }
-        } else if constexpr (kF16) {
+        if constexpr (kE4m3) {
           // Dims 8 r .. 8 r + 7 of the lane's four keys: row tile i holds dims
           // 8 r + 2 i (row r) and 8 r + 2 i + 1 (row r + 8).
           uint2 vw[4];
@@ -816,7 +1114,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
                                     kv::e4m3x2_to_f16x2(hi), kv::e4m3x2_to_f16x2(hi >> 16)};
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
-              mma16816<true>(o[nt][i], va, pb[mt][nt][0][0], pb[mt][nt][0][1]);
+              mma16816<true>(o[nt][i], va, pb[mt][nt][0], pb[mt][nt][1]);
           }
         } else {
           const uint32_t vbase = smem_u32(sv);
@@ -828,7 +1126,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
                           va);
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
-              mma16816<false>(o[nt][i], va, pb[mt][nt][0][0], pb[mt][nt][0][1]);
+              mma16816<false>(o[nt][i], va, pb[mt][nt][0], pb[mt][nt][1]);
           }
         }
       }
@@ -841,24 +1139,25 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
     for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float sum = l[nt][e];
+        float sum = kE2m1 ? four.l[nt][e] : l[nt][e];
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sh);
         float* dst = red + (warp * kRows + 8 * nt + 2 * c + e) * L::kRedRow;
         if (r == 0) {
-          dst[0] = m[nt][e];
+          dst[0] = kE2m1 ? four.ref(nt, e) : m[nt][e];
           dst[1] = sum;
-          dst[2] = kF16 ? m2[nt][e][0] : m[nt][e];
+          dst[2] = kE2m1 ? four.ref2(nt, e, 0) : kE4m3 ? m2[nt][e] : m[nt][e];
           dst[3] = bad ? 1.f : 0.f;
-          if (kE2m1) dst[4 + kHD] = m2[nt][e][kParts - 1];
+          if (kE2m1) dst[4 + kHD] = four.ref2(nt, e, 1);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
-            dst[4 + (kE2m1 ? 32 * (i >> 1) + 4 * r + 2 * (i & 1) + hf
-                     : kF16 ? 8 * r + 2 * i + hf
-                            : 16 * i + r + 8 * hf)] = o[nt][i][2 * hf + e];
+            dst[4 + (kE2m1   ? 32 * (i >> 1) + 4 * r + 2 * (i & 1) + hf
+                     : kE4m3 ? 8 * r + 2 * i + hf
+                             : 16 * i + r + 8 * hf)] =
+                kE2m1 ? four.o[nt][i][2 * hf + e] : o[nt][i][2 * hf + e];
       }
     // A wait that gave up (reported): this segment and the CTA's later ones have no
     // result.  They still count as arrived, as bad parts, so that the counters are

@@ -42,11 +42,13 @@ __host__ __device__ __forceinline__ int place(const PagedCache& pc, const int* c
   return 0;
 }
 
-// The value of a scale byte: 2^(byte - 127), NaN for 255.
-__device__ __forceinline__ float scale_value(int byte) {
-  return __uint_as_float(byte == 255 ? 0x7fc00000u
-                                     : byte == 0 ? 0x00400000u
-                                                 : static_cast<uint32_t>(byte) << 23);
+// The value of a scale byte: 2^(byte - 127), NaN for 255.  (Both ends differ from the
+// exponent alone by the mantissa's first bit: 2^-127 and a NaN.  Without branches: a
+// choice here became a second copy of what follows it, 128 instructions a tile of the
+// 4-bit decode.)
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  const uint32_t ends = static_cast<uint32_t>(static_cast<int>((byte + 1u) & 0xfeu) - 1) >> 31;
+  return __uint_as_float((byte << 23) | (ends << 22));
 }
 
 // Two e4m3 bytes (low half of `two`) -> two halves (exact).
