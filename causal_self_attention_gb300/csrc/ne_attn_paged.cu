@@ -736,6 +736,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
       if (lane == 31 && p.rope.cs)
         bulk_load(sq + kRows * kQRow, p.rope.cs + static_cast<long long>(n - 1) * 32, 256,
                   &qfull[slot]);
+      bool seg_bad = false;  // (lane 0's; the consumers ask for it at the segment's last tile)
       for (int t = s.t0; t < s.t1; ++t, ++g) {
         const int key0 = t * T::kTile;
         const int pg0 = key0 >> p.pc.page_shift;
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
         uint8_t* sk = smem + st * T::kStageBytes;
         uint8_t* sv = sk + T::kPool;
         if (lane == 0) {
-          stage_bad[st] = bad;
+          stage_bad[st] = seg_bad |= bad;
           if (bad) atomicCAS(p.status, 0, NE_DEV_BAD_PAGE);
           const uint32_t copies = pg1 - pg0 + 1;
           mbar_arrive_expect_tx(&full[st], copies * box * 2 * (T::kRowBytes + T::kScales));
@@ -810,7 +811,8 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
   const int r = lane >> 2, c = lane & 3;
   const typename FourBit<kNT>::Slots slots(lane);
   bool ok = true;
-  int g = 0, nq = 0;
+  int st = 0, nq = 0;
+  uint32_t phase = 0u;  // of the ring's slot st
   Segment s = first_segment(prefix, B, J, x0, x1);
   for (bool begun = false;; begun = true) {
     if (begun) {
@@ -911,12 +913,16 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
     FourBit<kNT> four;
     if constexpr (kE2m1) four.begin();
 
-    for (int t = s.t0; t < s.t1; ++t, ++g) {
-      const int st = g % kStages;
+    auto advance = [&]() {
+      const bool wrap = ++st == kStages;
+      st = wrap ? 0 : st;
+      phase ^= wrap ? 1u : 0u;
+    };
+    for (int t = s.t0; t < s.t1; ++t, advance()) {
       // (A wait that gave up is carried to the segment's vote.)
-      if (!ok || !(ok = mbar_wait_warp(&full[st], (g / kStages) & 1, abort_flag, p.status, 61)))
+      if (!ok || !(ok = mbar_wait_warp(&full[st], phase, abort_flag, p.status, 61)))
         continue;
-      bad |= stage_bad[st] != 0;
+      if (t + 1 == s.t1) bad = stage_bad[st] != 0;
       uint8_t* sk = smem + st * T::kStageBytes + warp * T::kKeys * T::kRowBytes;
       uint8_t* sv = sk + T::kPool;
       const int live = n - t * T::kTile - warp * T::kKeys;  // of this warp's keys, from the first

@@ -44,14 +44,13 @@ __device__ __forceinline__ float rstd_of(const float (&a)[8], const float (&b)[8
   for (int i = 0; i < 8; ++i) ss += a[i] * a[i] + b[i] * b[i];
   return rsqrtf(head_sum(ss) * (1.f / kHD) + eps);
 }
-// The lane's 8 rotation pairs (a, b) turned by their position's angles, or back.
+// The lane's 8 rotation pairs (a, b) turned by their position's angles, or back.  cs[u]:
+// (cos, sin) of dims 8c + 2u and 8c + 2u + 1.
 template <bool kBack>
-__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float2* table_row,
-                                     int c) {
-  const float4* cs = reinterpret_cast<const float4*>(table_row + 8 * c);
+__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float4 (&cs)[4]) {
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const float4 t = __ldg(cs + u);  // (cos, sin) of dims 8c + 2u and 8c + 2u + 1
+    const float4 t = cs[u];
     const float s0 = kBack ? -t.y : t.y, s1 = kBack ? -t.w : t.w;
     const float lo0 = __fmaf_rn(a[2 * u], t.x, -__fmul_rn(b[2 * u], s0));
     const float hi0 = __fmaf_rn(b[2 * u], t.x, __fmul_rn(a[2 * u], s0));
@@ -77,53 +76,66 @@ __device__ __forceinline__ int position(const QkNormParams& p, int row) {
 namespace qkn {
 constexpr int kFwdThreads = 256;
 constexpr int kFwdQuads = kFwdThreads / kParts;
+
+// The lane's chunks of w, 8 dims each, times r.
+__device__ __forceinline__ void scale8(float (&x)[8], const uint4& w, float r) {
+  float v[8];
+  unpack8(w, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = x[i] * r * v[i];
+}
 }  // namespace qkn
 
-// kItems (row, head) pairs per quad, all their loads in flight at once.
-template <int kItems>
-__global__ void __launch_bounds__(qkn::kFwdThreads) ne_qk_norm_rope_kernel(const QkNormParams p) {
+// A quad takes kHeads heads of a row, `groups` apart (so that neighbouring quads read
+// neighbouring heads), all their loads in flight at once: the row's position and its row of
+// the table are fetched once for them.
+template <int kHeads>
+__global__ void __launch_bounds__(qkn::kFwdThreads) ne_qk_norm_rope_kernel(const QkNormParams p,
+                                                                           uint32_t groups) {
   using namespace qkn;
   pdl_wait();
-  const int c = threadIdx.x % kParts, quad = threadIdx.x / kParts;
-  const int heads = p.H + p.Hkv;
-  const long long items = static_cast<long long>(p.n_tot) * heads;
-  const long long first = static_cast<long long>(blockIdx.x) * (kItems * kFwdQuads) + quad;
-  uint4 lo[kItems], hi[kItems];
-  int row[kItems], head[kItems], pos[kItems];
+  const int c = threadIdx.x % kParts;
+  const uint32_t unit = blockIdx.x * kFwdQuads + threadIdx.x / kParts;
+  const uint32_t at = unit / groups;
+  const bool live = at < static_cast<uint32_t>(p.n_tot);
+  const long long row = live ? at : p.n_tot - 1;  // (past the end: read, not written)
+  const int heads = p.H + p.Hkv, h0 = static_cast<int>(unit - at * groups);
+  const int pos = live ? position(p, static_cast<int>(row)) : -1;
+  const uint4* q = reinterpret_cast<const uint4*>(p.q + row * p.q_stride) + c;
+  const uint4* k = reinterpret_cast<const uint4*>(p.k + row * p.k_stride) + c;
+  uint4 lo[kHeads], hi[kHeads];
 #pragma unroll
-  for (int u = 0; u < kItems; ++u) {
-    const long long i = min(first + u * kFwdQuads, items - 1);  // (past the end: not written)
-    row[u] = static_cast<int>(i / heads);
-    head[u] = static_cast<int>(i - static_cast<long long>(row[u]) * heads);
-    const bool is_k = head[u] >= p.H;
-    const __nv_bfloat16* x =
-        is_k ? p.k + row[u] * p.k_stride + (head[u] - p.H) * kHD : p.q + row[u] * p.q_stride + head[u] * kHD;
-    const uint4* src = reinterpret_cast<const uint4*>(x);
-    lo[u] = __ldg(src + c);
-    hi[u] = __ldg(src + c + 4);
-    pos[u] = first + u * kFwdQuads < items ? position(p, row[u]) : -1;
+  for (int j = 0; j < kHeads; ++j) {
+    const int h = min(h0 + j * static_cast<int>(groups), heads - 1);
+    const uint4* src = h < p.H ? q + h * (kHD / 8) : k + (h - p.H) * (kHD / 8);
+    lo[j] = __ldg(src);
+    hi[j] = __ldg(src + 4);
+  }
+  const uint4* qw = reinterpret_cast<const uint4*>(p.qw) + c;
+  const uint4* kw = reinterpret_cast<const uint4*>(p.kw) + c;
+  const uint4 qw0 = __ldg(qw), qw1 = __ldg(qw + 4), kw0 = __ldg(kw), kw1 = __ldg(kw + 4);
+  float4 cs[4];  // (cos, sin) of dims 8c + 2u and 8c + 2u + 1
+  if (p.rope.cs) {
+    const float4* t = reinterpret_cast<const float4*>(p.rope.cs + static_cast<long long>(max(pos, 0)) * 32) + 4 * c;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) cs[u] = __ldg(t + u);
   }
 #pragma unroll
-  for (int u = 0; u < kItems; ++u) {
-    const bool is_k = head[u] >= p.H;
-    const uint4* wr = reinterpret_cast<const uint4*>(is_k ? p.kw : p.qw);
-    float a[8], b[8], w[8];
-    unpack8(lo[u], a);
-    unpack8(hi[u], b);
+  for (int j = 0; j < kHeads; ++j) {
+    const int h = h0 + j * static_cast<int>(groups);
+    const bool is_k = h >= p.H;
+    float a[8], b[8];
+    unpack8(lo[j], a);
+    unpack8(hi[j], b);
     const float r = rstd_of(a, b, p.eps);
-    unpack8(__ldg(wr + c), w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = a[i] * r * w[i];
-    unpack8(__ldg(wr + c + 4), w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = b[i] * r * w[i];
-    if (pos[u] < 0) continue;
-    if (p.rope.cs) turn<false>(a, b, p.rope.cs + static_cast<long long>(pos[u]) * 32, c);
-    __nv_bfloat16* y = is_k ? p.kr + (static_cast<long long>(row[u]) * p.Hkv + (head[u] - p.H)) * kHD
-                            : p.qr + (static_cast<long long>(row[u]) * p.H + head[u]) * kHD;
-    uint4* dst = reinterpret_cast<uint4*>(y);
-    dst[c] = pack8(a);
-    dst[c + 4] = pack8(b);
+    scale8(a, is_k ? kw0 : qw0, r);
+    scale8(b, is_k ? kw1 : qw1, r);
+    if (p.rope.cs) turn<false>(a, b, cs);
+    if (pos < 0 || h >= heads) continue;
+    uint4* dst = reinterpret_cast<uint4*>(is_k ? p.kr + (row * p.Hkv + (h - p.H)) * kHD
+                                               : p.qr + (row * p.H + h) * kHD) + c;
+    dst[0] = pack8(a);
+    dst[4] = pack8(b);
   }
 }
 
@@ -133,60 +145,84 @@ constexpr int kBwdQuads = kBwdThreads / kParts;
 constexpr int kBwdWarps = kBwdThreads / 32;
 
 // One tensor's rows (the queries' or the keys'): gradients dx, and this lane's
-// part of dw in acc[16] (dims 8c .. 8c + 7, then 32 + 8c ..).
+// part of dw in acc[16] (dims 8c .. 8c + 7, then 32 + 8c ..).  A quad takes kHeads heads of a
+// row at a time, as in the forward.
+template <int kHeads>
 __device__ __forceinline__ void grad_rows(const QkNormParams& p, const __nv_bfloat16* __restrict__ dr,
                                           const __nv_bfloat16* __restrict__ x, long long x_stride,
                                           const __nv_bfloat16* __restrict__ w, int H,
                                           __nv_bfloat16* __restrict__ dx, long long dx_stride,
                                           int c, int quad, float (&acc)[16]) {
-  const uint4* wr = reinterpret_cast<const uint4*>(w);
-  const uint4 wl = __ldg(wr + c), wh = __ldg(wr + c + 4);
-  const long long items = static_cast<long long>(p.n_tot) * H;
-  const long long step = static_cast<long long>(gridDim.x) * kBwdQuads;
+  const uint4* wr = reinterpret_cast<const uint4*>(w) + c;
+  const uint4 wl = __ldg(wr), wh = __ldg(wr + 4);
+  const uint32_t groups = (H + kHeads - 1) / kHeads, units = groups * p.n_tot;
+  const uint32_t step = gridDim.x * kBwdQuads;
   // (Whole warps take part in the sums over the heads: a quad past the end reads
   // the last row and adds nothing.)
-  for (long long i0 = static_cast<long long>(blockIdx.x) * kBwdQuads; i0 < items; i0 += step) {
-    const long long i = min(i0 + quad, items - 1);
-    const int row = static_cast<int>(i / H), head = static_cast<int>(i - static_cast<long long>(row) * H);
-    const uint4* xs = reinterpret_cast<const uint4*>(x + row * x_stride + head * kHD);
-    const uint4* gs = reinterpret_cast<const uint4*>(dr + i * kHD);
-    const uint4 x0 = __ldg(xs + c), x1 = __ldg(xs + c + 4);
-    const uint4 g0 = __ldg(gs + c), g1 = __ldg(gs + c + 4);
-    const int pos = i0 + quad < items ? position(p, row) : -1;
-    float a[8], b[8], ga[8], gb[8], v[8];
-    unpack8(x0, a);
-    unpack8(x1, b);
-    unpack8(g0, ga);
-    unpack8(g1, gb);
-    const float r = rstd_of(a, b, p.eps);
-    if (p.rope.cs) turn<true>(ga, gb, p.rope.cs + static_cast<long long>(max(pos, 0)) * 32, c);
-    float along = 0.f;
-    unpack8(wl, v);
+  for (uint32_t u0 = blockIdx.x * kBwdQuads; u0 < units; u0 += step) {
+    const uint32_t unit = u0 + quad, at = unit / groups;
+    const bool live = at < static_cast<uint32_t>(p.n_tot);
+    const long long row = live ? at : p.n_tot - 1;
+    const int h0 = static_cast<int>(unit - at * groups);
+    const int pos = live ? position(p, static_cast<int>(row)) : -1;
+    uint4 xl[kHeads], xh[kHeads], gl[kHeads], gh[kHeads];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a[j] *= r;
-      if (pos >= 0) acc[j] += ga[j] * a[j];
-      ga[j] *= v[j];
-      along += ga[j] * a[j];
+    for (int j = 0; j < kHeads; ++j) {
+      const int h = min(h0 + j * static_cast<int>(groups), H - 1);
+      const uint4* xs = reinterpret_cast<const uint4*>(x + row * x_stride + h * kHD) + c;
+      const uint4* gs = reinterpret_cast<const uint4*>(dr + (row * H + h) * kHD) + c;
+      xl[j] = __ldg(xs);
+      xh[j] = __ldg(xs + 4);
+      gl[j] = __ldg(gs);
+      gh[j] = __ldg(gs + 4);
     }
-    unpack8(wh, v);
+    float4 cs[4];
+    if (p.rope.cs) {
+      const float4* t = reinterpret_cast<const float4*>(p.rope.cs + static_cast<long long>(max(pos, 0)) * 32) + 4 * c;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      b[j] *= r;
-      if (pos >= 0) acc[8 + j] += gb[j] * b[j];
-      gb[j] *= v[j];
-      along += gb[j] * b[j];
+      for (int u = 0; u < 4; ++u) cs[u] = __ldg(t + u);
     }
-    along = head_sum(along) * (1.f / kHD);
-    if (pos < 0) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a[j] = r * (ga[j] - a[j] * along);
-      b[j] = r * (gb[j] - b[j] * along);
+    for (int j = 0; j < kHeads; ++j) {
+      const int h = h0 + j * static_cast<int>(groups);
+      const bool there = pos >= 0 && h < H;
+      float a[8], b[8], ga[8], gb[8], v[8];
+      unpack8(xl[j], a);
+      unpack8(xh[j], b);
+      unpack8(gl[j], ga);
+      unpack8(gh[j], gb);
+      const float r = rstd_of(a, b, p.eps);
+      if (p.rope.cs) turn<true>(ga, gb, cs);
+      float along = 0.f;
+      unpack8(wl, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] *= r;
+        const float d = ga[i] * a[i];
+        acc[i] += there ? d : 0.f;
+        ga[i] *= v[i];
+        along += d * v[i];
+      }
+      unpack8(wh, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        b[i] *= r;
+        const float d = gb[i] * b[i];
+        acc[8 + i] += there ? d : 0.f;
+        gb[i] *= v[i];
+        along += d * v[i];
+      }
+      along = head_sum(along) * (1.f / kHD);
+      if (!there) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] = r * (ga[i] - a[i] * along);
+        b[i] = r * (gb[i] - b[i] * along);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(dx + row * dx_stride + h * kHD) + c;
+      dst[0] = pack8(a);
+      dst[4] = pack8(b);
     }
-    uint4* dst = reinterpret_cast<uint4*>(dx + row * dx_stride + head * kHD);
-    dst[c] = pack8(a);
-    dst[c + 4] = pack8(b);
   }
 }
 
@@ -224,9 +260,9 @@ __global__ void __launch_bounds__(qkn::kBwdThreads) ne_qk_norm_rope_bwd_kernel(c
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = 0.f;
   float* part = p.part + static_cast<long long>(blockIdx.x) * 2 * kHD;
-  grad_rows(p, p.dqr, p.q, p.q_stride, p.qw, p.H, p.dq, p.dq_stride, c, quad, acc);
+  grad_rows<2>(p, p.dqr, p.q, p.q_stride, p.qw, p.H, p.dq, p.dq_stride, c, quad, acc);
   cta_sum(acc, c, sum, part);
-  grad_rows(p, p.dkr, p.k, p.k_stride, p.kw, p.Hkv, p.dk, p.dk_stride, c, quad, acc);
+  grad_rows<2>(p, p.dkr, p.k, p.k_stride, p.kw, p.Hkv, p.dk, p.dk_stride, c, quad, acc);
   cta_sum(acc, c, sum, part + kHD);
   if (threadIdx.x == 0) {
     __threadfence();  // the CTA's partials (ordered before this by the barrier), then the arrival
@@ -271,21 +307,27 @@ constexpr int kQkNormSms = 160;  // an upper bound on the part's SMs (152), for 
 
 size_t qk_norm_part_bytes() { return kQkNormSms * 2 * kHD * sizeof(float); }
 
+namespace {
+template <int kHeads>
+cudaError_t launch_forward(const QkNormParams& p, cudaStream_t stream) {
+  const uint32_t groups = (p.H + p.Hkv + kHeads - 1) / kHeads;
+  const long long units = static_cast<long long>(p.n_tot) * groups;
+  return launch_pdl(ne_qk_norm_rope_kernel<kHeads>,
+                    dim3(static_cast<unsigned>((units + qkn::kFwdQuads - 1) / qkn::kFwdQuads)),
+                    dim3(qkn::kFwdThreads), 0, stream, p, groups);
+}
+}  // namespace
+
+// Four heads a quad once that fills the GPU (and there are as many).
 cudaError_t launch_qk_norm(const QkNormParams& p, int sms, cudaStream_t stream) {
-  const long long items = static_cast<long long>(p.n_tot) * (p.H + p.Hkv);
-  if (items >= 4LL * sms * qkn::kFwdQuads) {
-    const long long per = 4 * qkn::kFwdQuads;
-    return launch_pdl(ne_qk_norm_rope_kernel<4>, dim3(static_cast<unsigned>((items + per - 1) / per)),
-                      dim3(qkn::kFwdThreads), 0, stream, p);
-  }
-  return launch_pdl(ne_qk_norm_rope_kernel<1>,
-                    dim3(static_cast<unsigned>((items + qkn::kFwdQuads - 1) / qkn::kFwdQuads)),
-                    dim3(qkn::kFwdThreads), 0, stream, p);
+  const long long pairs = static_cast<long long>(p.n_tot) * (p.H + p.Hkv);
+  return pairs >= 8LL * sms * qkn::kFwdQuads && p.H + p.Hkv >= 4 ? launch_forward<4>(p, stream)
+                                                                 : launch_forward<1>(p, stream);
 }
 
 cudaError_t launch_qk_norm_bwd(const QkNormParams& p, int sms, cudaStream_t stream) {
-  const long long items = static_cast<long long>(p.n_tot) * (p.H > p.Hkv ? p.H : p.Hkv);
-  long long ctas = (items + qkn::kBwdQuads - 1) / qkn::kBwdQuads;
+  const long long pairs = static_cast<long long>(p.n_tot) * (p.H > p.Hkv ? p.H : p.Hkv);
+  long long ctas = (pairs + qkn::kBwdQuads - 1) / qkn::kBwdQuads;
   if (sms > kQkNormSms) sms = kQkNormSms;
   if (ctas > sms) ctas = sms;
   return launch_pdl(ne_qk_norm_rope_bwd_kernel, dim3(static_cast<unsigned>(ctas)),
