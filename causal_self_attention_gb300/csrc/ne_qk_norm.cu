@@ -89,8 +89,8 @@ __device__ __forceinline__ void scale8(float (&x)[8], const uint4& w, float r) {
 // A quad takes kHeads heads of a row, `groups` apart (so that neighbouring quads read
 // neighbouring heads), all their loads in flight at once: the row's position and its row of
 // the table are fetched once for them.
-template <int kHeads>
-__global__ void __launch_bounds__(qkn::kFwdThreads) ne_qk_norm_rope_kernel(const QkNormParams p,
+template <int kHeads, int kCtas>
+__global__ void __launch_bounds__(qkn::kFwdThreads, kCtas) ne_qk_norm_rope_kernel(const QkNormParams p,
                                                                            uint32_t groups) {
   using namespace qkn;
   pdl_wait();
@@ -140,26 +140,24 @@ __global__ void __launch_bounds__(qkn::kFwdThreads) ne_qk_norm_rope_kernel(const
 }
 
 namespace qkn {
-constexpr int kBwdThreads = 512;
-constexpr int kBwdQuads = kBwdThreads / kParts;
-constexpr int kBwdWarps = kBwdThreads / 32;
 
 // One tensor's rows (the queries' or the keys'): gradients dx, and this lane's
 // part of dw in acc[16] (dims 8c .. 8c + 7, then 32 + 8c ..).  A quad takes kHeads heads of a
 // row at a time, as in the forward.
-template <int kHeads>
+template <int kThreads, int kHeads>
 __device__ __forceinline__ void grad_rows(const QkNormParams& p, const __nv_bfloat16* __restrict__ dr,
                                           const __nv_bfloat16* __restrict__ x, long long x_stride,
                                           const __nv_bfloat16* __restrict__ w, int H,
                                           __nv_bfloat16* __restrict__ dx, long long dx_stride,
                                           int c, int quad, float (&acc)[16]) {
+  constexpr uint32_t kQuads = kThreads / kParts;
   const uint4* wr = reinterpret_cast<const uint4*>(w) + c;
   const uint4 wl = __ldg(wr), wh = __ldg(wr + 4);
   const uint32_t groups = (H + kHeads - 1) / kHeads, units = groups * p.n_tot;
-  const uint32_t step = gridDim.x * kBwdQuads;
+  const uint32_t step = gridDim.x * kQuads;
   // (Whole warps take part in the sums over the heads: a quad past the end reads
   // the last row and adds nothing.)
-  for (uint32_t u0 = blockIdx.x * kBwdQuads; u0 < units; u0 += step) {
+  for (uint32_t u0 = blockIdx.x * kQuads; u0 < units; u0 += step) {
     const uint32_t unit = u0 + quad, at = unit / groups;
     const bool live = at < static_cast<uint32_t>(p.n_tot);
     const long long row = live ? at : p.n_tot - 1;
@@ -227,6 +225,7 @@ __device__ __forceinline__ void grad_rows(const QkNormParams& p, const __nv_bflo
 }
 
 // The CTA's sum of acc into row[64] (a partial of dw), in a fixed order.
+template <int kWarps>
 __device__ __forceinline__ void cta_sum(float (&acc)[16], int c, float (*sum)[kHD], float* row) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
@@ -240,7 +239,7 @@ __device__ __forceinline__ void cta_sum(float (&acc)[16], int c, float (*sum)[kH
   if (threadIdx.x < kHD) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kBwdWarps; ++w) s += sum[w][threadIdx.x];
+    for (int w = 0; w < kWarps; ++w) s += sum[w][threadIdx.x];
     row[threadIdx.x] = s;
   }
   __syncthreads();
@@ -250,9 +249,11 @@ __device__ __forceinline__ void cta_sum(float (&acc)[16], int c, float (*sum)[kH
 // Each CTA takes its share of the queries' (row, head) pairs, then of the keys',
 // and leaves a partial of each dw; the CTA that arrives last adds them up, in
 // their order: one launch, and the same bits whichever CTA is last.
-__global__ void __launch_bounds__(qkn::kBwdThreads) ne_qk_norm_rope_bwd_kernel(const QkNormParams p) {
+template <int kThreads, int kHeads, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) ne_qk_norm_rope_bwd_kernel(const QkNormParams p) {
   using namespace qkn;
-  __shared__ float sum[kBwdWarps][kHD];
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float sum[kWarps][kHD];
   __shared__ int last;
   pdl_wait();
   const int c = threadIdx.x % kParts, quad = threadIdx.x / kParts;
@@ -260,10 +261,10 @@ __global__ void __launch_bounds__(qkn::kBwdThreads) ne_qk_norm_rope_bwd_kernel(c
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = 0.f;
   float* part = p.part + static_cast<long long>(blockIdx.x) * 2 * kHD;
-  grad_rows<2>(p, p.dqr, p.q, p.q_stride, p.qw, p.H, p.dq, p.dq_stride, c, quad, acc);
-  cta_sum(acc, c, sum, part);
-  grad_rows<2>(p, p.dkr, p.k, p.k_stride, p.kw, p.Hkv, p.dk, p.dk_stride, c, quad, acc);
-  cta_sum(acc, c, sum, part + kHD);
+  grad_rows<kThreads, kHeads>(p, p.dqr, p.q, p.q_stride, p.qw, p.H, p.dq, p.dq_stride, c, quad, acc);
+  cta_sum<kWarps>(acc, c, sum, part);
+  grad_rows<kThreads, kHeads>(p, p.dkr, p.k, p.k_stride, p.kw, p.Hkv, p.dk, p.dk_stride, c, quad, acc);
+  cta_sum<kWarps>(acc, c, sum, part + kHD);
   if (threadIdx.x == 0) {
     __threadfence();  // the CTA's partials (ordered before this by the barrier), then the arrival
     last = atomicAdd(p.arrived, 1) == static_cast<int>(gridDim.x) - 1;
@@ -277,19 +278,19 @@ __global__ void __launch_bounds__(qkn::kBwdThreads) ne_qk_norm_rope_bwd_kernel(c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = gridDim.x;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int i = warp; i < n; i += kBwdWarps) {
+  for (int i = warp; i < n; i += kWarps) {
     const float4 v = __ldcg(src + i * 32 + lane);
     s.x += v.x;
     s.y += v.y;
     s.z += v.z;
     s.w += v.w;
   }
-  __shared__ float4 all[kBwdWarps][32];
+  __shared__ float4 all[kWarps][32];
   all[warp][lane] = s;
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < kBwdWarps; ++w) {
+    for (int w = 1; w < kWarps; ++w) {
       const float4 v = all[w][lane];
       s.x += v.x;
       s.y += v.y;
@@ -308,30 +309,45 @@ constexpr int kQkNormSms = 160;  // an upper bound on the part's SMs (152), for 
 size_t qk_norm_part_bytes() { return kQkNormSms * 2 * kHD * sizeof(float); }
 
 namespace {
-template <int kHeads>
+template <int kHeads, int kCtas>
 cudaError_t launch_forward(const QkNormParams& p, cudaStream_t stream) {
   const uint32_t groups = (p.H + p.Hkv + kHeads - 1) / kHeads;
   const long long units = static_cast<long long>(p.n_tot) * groups;
-  return launch_pdl(ne_qk_norm_rope_kernel<kHeads>,
+  return launch_pdl(ne_qk_norm_rope_kernel<kHeads, kCtas>,
                     dim3(static_cast<unsigned>((units + qkn::kFwdQuads - 1) / qkn::kFwdQuads)),
                     dim3(qkn::kFwdThreads), 0, stream, p, groups);
 }
 }  // namespace
 
-// Four heads a quad once that fills the GPU (and there are as many).
+// What a quad takes decides how many bytes are on their way: 80,000 rows of 40 heads take
+// 135 us by eight heads (6.1 TB/s), 163 by four, 169 by two, 187 by one (each with
+// the registers and CTAs that suit it best).  Few rows are spread wide instead, and eight
+// where they leave four slots or more empty are four: 8192 rows of 16 heads 7.5 us by
+// eight, 7.9 by four, 9.1 by one.
 cudaError_t launch_qk_norm(const QkNormParams& p, int sms, cudaStream_t stream) {
-  const long long pairs = static_cast<long long>(p.n_tot) * (p.H + p.Hkv);
-  return pairs >= 8LL * sms * qkn::kFwdQuads && p.H + p.Hkv >= 4 ? launch_forward<4>(p, stream)
-                                                                 : launch_forward<1>(p, stream);
+  const int heads = p.H + p.Hkv;
+  const long long pairs = static_cast<long long>(p.n_tot) * heads;
+  if (pairs < 8LL * sms * qkn::kFwdQuads || heads < 4) return launch_forward<1, 4>(p, stream);
+  return (heads + 7) / 8 * 8 - heads < 4 ? launch_forward<8, 2>(p, stream)
+                                         : launch_forward<4, 2>(p, stream);
 }
 
-cudaError_t launch_qk_norm_bwd(const QkNormParams& p, int sms, cudaStream_t stream) {
-  const long long pairs = static_cast<long long>(p.n_tot) * (p.H > p.Hkv ? p.H : p.Hkv);
-  long long ctas = (pairs + qkn::kBwdQuads - 1) / qkn::kBwdQuads;
+namespace {
+template <int kThreads, int kHeads, int kCtas>
+cudaError_t launch_backward(const QkNormParams& p, int sms, cudaStream_t stream) {
+  constexpr int kQuads = kThreads / qkn::kParts;
+  const int H = p.H > p.Hkv ? p.H : p.Hkv;
+  const long long units = static_cast<long long>(p.n_tot) * ((H + kHeads - 1) / kHeads);
+  long long ctas = (units + kQuads - 1) / kQuads;
   if (sms > kQkNormSms) sms = kQkNormSms;
-  if (ctas > sms) ctas = sms;
-  return launch_pdl(ne_qk_norm_rope_bwd_kernel, dim3(static_cast<unsigned>(ctas)),
-                    dim3(qkn::kBwdThreads), 0, stream, p);
+  if (ctas > kCtas * sms) ctas = kCtas * sms;
+  return launch_pdl(ne_qk_norm_rope_bwd_kernel<kThreads, kHeads, kCtas>, dim3(static_cast<unsigned>(ctas)),
+                    dim3(kThreads), 0, stream, p);
+}
+}  // namespace
+
+cudaError_t launch_qk_norm_bwd(const QkNormParams& p, int sms, cudaStream_t stream) {
+  return launch_backward<512, 2, 1>(p, sms, stream);
 }
 
 }  // namespace ne

@@ -501,7 +501,22 @@ def ne_attn_varlen_bwd_train(qr, kr, v, out, dout, lse, cu_seqlens, max_seqlen,
 # ------------------------------------------- grouped heads and the paged cache
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-_E4M3 = torch.float8_e4m3fn
+_E4M3, _ROWS = torch.float8_e4m3fn, torch.contiguous_format
+
+
+def _current_device():
+    return torch.cuda.current_device()
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+# (The step's calls take 10 to 20 us of host time, most of it in what marshals them: the
+# checks below look at everything in one expression, and call the functions that say
+# what is wrong only where something is.)
+if hasattr(torch._C, "_cuda_getDevice"):
+    _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _need_on(t, dtype, dev, name):
@@ -526,8 +541,8 @@ def _on(stream, dev):
     ``stream``: a torch stream, a raw ``cudaStream_t``, or None for the device's
     current stream.  The context is entered; the caller leaves it."""
     if stream is None:
-        if dev == torch.cuda.current_device():
-            return torch._C._cuda_getCurrentRawStream(dev), None
+        if dev == _current_device():
+            return _raw_stream(dev), None
         stream = torch.cuda.current_stream(dev)
     elif not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
@@ -702,31 +717,35 @@ def _rows_of(t, shape, dev, name):
     from one row to the next."""
     if not (t.dtype is _BF16 and t.get_device() == dev):
         raise ValueError(f"{name} must be a CUDA {_BF16} tensor on cuda:{dev}")
-    if t.dim() != 3 or t.shape[2] != 64 or (shape is not None and t.shape != shape):
+    have = t.shape
+    if len(have) != 3 or have[2] != 64 or (shape is not None and have != shape):
         want = "[N, heads, 64]" if shape is None else str(tuple(shape))
         raise ValueError(f"{name} must have the shape {want}")
     row, head, one = t.stride()
-    heads = t.shape[1]
+    heads = have[1]
     if one != 1 or (heads > 1 and head != 64):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return row if t.shape[0] > 1 else 64 * heads
+    return row if have[0] > 1 else 64 * heads
 
 
 def _qk_norm_shapes(q, k, q_weight, k_weight, positions, rope_base):
-    dev = q.get_device()
-    if dev < 0:
-        raise ValueError("q must be a CUDA tensor")
+    dev, N, H = _device(q, "q"), q.shape[0], q.shape[1]
     q_row, k_row = _rows_of(q, None, dev, "q"), _rows_of(k, None, dev, "k")
-    N, H, D = q.shape
     if k.shape[0] != N:
         raise ValueError("q, k must be [N, H, 64] and [N, Hkv, 64]")
-    _given(q_weight, (D,), _BF16, dev, "q_weight")
-    _given(k_weight, (D,), _BF16, dev, "k_weight")
+    if not (q_weight.dtype is _BF16 and k_weight.dtype is _BF16
+            and dev == q_weight.get_device() == k_weight.get_device()
+            and q_weight.is_contiguous() and k_weight.is_contiguous()
+            and q_weight.shape == (64,) and k_weight.shape == (64,)):
+        _given(q_weight, (64,), _BF16, dev, "q_weight")
+        _given(k_weight, (64,), _BF16, dev, "k_weight")
     if positions is not None:
-        _given(positions, (N,), _I32, dev, "positions")
+        if not (positions.dtype is _I32 and dev == positions.get_device()
+                and positions.is_contiguous() and positions.shape == (N,)):
+            _given(positions, (N,), _I32, dev, "positions")
     elif rope_base:
         raise ValueError("positions: needed unless rope_base is 0")
-    return dev, N, H, k.shape[1], D, q_row, k_row
+    return dev, N, H, k.shape[1], 64, q_row, k_row
 
 
 def ne_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, max_seqlen, eps=1e-5,
@@ -745,8 +764,9 @@ def ne_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, max_seqlen, eps=1e-
         _given(kr, k.shape, _BF16, dev, "kr")
     raw, ctx = _on(stream, dev)
     try:
-        qr = torch.empty((N, H, D), dtype=_BF16, device=q.device) if qr is None else qr
-        kr = torch.empty((N, Hkv, D), dtype=_BF16, device=q.device) if kr is None else kr
+        # (contiguous, whatever the distance of q's rows)
+        qr = torch.empty_like(q, memory_format=_ROWS) if qr is None else qr
+        kr = torch.empty_like(k, memory_format=_ROWS) if kr is None else kr
         if N == 0:  # a step in which no sequence has a row
             return qr, kr
         rc = lib().ne_qk_norm_rope_fwd(
@@ -772,8 +792,11 @@ def ne_qk_norm_rope_bwd(dqr, dkr, q, k, q_weight, k_weight, positions, max_seqle
     and fp32 ``[64]``."""
     dev, N, H, Hkv, D, q_row, k_row = _qk_norm_shapes(q, k, q_weight, k_weight, positions,
                                                       rope_base)
-    _given(dqr, q.shape, _BF16, dev, "dqr")
-    _given(dkr, k.shape, _BF16, dev, "dkr")
+    if not (dqr.dtype is _BF16 and dkr.dtype is _BF16
+            and dev == dqr.get_device() == dkr.get_device() and dqr.is_contiguous()
+            and dkr.is_contiguous() and dqr.shape == q.shape and dkr.shape == k.shape):
+        _given(dqr, q.shape, _BF16, dev, "dqr")
+        _given(dkr, k.shape, _BF16, dev, "dkr")
     dq_row = 64 * H if dq is None else _rows_of(dq, q.shape, dev, "dq")
     dk_row = 64 * Hkv if dk is None else _rows_of(dk, k.shape, dev, "dk")
     for t, name in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
@@ -782,12 +805,12 @@ def ne_qk_norm_rope_bwd(dqr, dkr, q, k, q_weight, k_weight, positions, max_seqle
     ws_bytes = _ws_bytes(workspace, dev)
     raw, ctx = _on(stream, dev)
     try:
-        dq = torch.empty((N, H, D), dtype=_BF16, device=q.device) if dq is None else dq
-        dk = torch.empty((N, Hkv, D), dtype=_BF16, device=q.device) if dk is None else dk
+        dq = torch.empty_like(dqr) if dq is None else dq
+        dk = torch.empty_like(dkr) if dk is None else dk
         if dq_weight is None:
-            dq_weight = torch.empty(D, dtype=_F32, device=q.device)
+            dq_weight = torch.empty_like(q_weight, dtype=_F32)
         if dk_weight is None:
-            dk_weight = torch.empty(D, dtype=_F32, device=q.device)
+            dk_weight = torch.empty_like(k_weight, dtype=_F32)
         if N == 0:
             return dq, dk, dq_weight.zero_(), dk_weight.zero_()
         rc = lib().ne_qk_norm_rope_bwd(
@@ -806,19 +829,24 @@ def ne_qk_norm_rope_bwd(dqr, dkr, q, k, q_weight, k_weight, positions, max_seqle
 def _pages(seq_lens, block_table, free_pages, n_free, first, name):
     """Checks what ne_kv_reserve and ne_kv_release share; returns (device, nseq,
     max_pages, n_pages)."""
-    dev = _device(first, name)
-    _need_on(seq_lens, _I32, dev, "seq_lens")
-    _need_on(block_table, _I32, dev, "block_table")
-    _need_on(free_pages, _I32, dev, "free_pages")
-    _given(n_free, (1,), _I32, dev, "n_free")
-    nseq = seq_lens.numel()
-    if first.shape != (nseq,) or seq_lens.dim() != 1:
+    dev, nseq, table, free = _device(first, name), seq_lens.numel(), block_table.shape, free_pages.shape
+    if not (seq_lens.dtype is _I32 and block_table.dtype is _I32 and free_pages.dtype is _I32
+            and n_free.dtype is _I32
+            and dev == seq_lens.get_device() == block_table.get_device() == free_pages.get_device()
+            == n_free.get_device() and seq_lens.is_contiguous() and block_table.is_contiguous()
+            and free_pages.is_contiguous() and n_free.shape == (1,)
+            and first.shape == seq_lens.shape == (nseq,) and len(table) == 2 and table[0] == nseq
+            and len(free) == 1):
+        _need_on(seq_lens, _I32, dev, "seq_lens")
+        _need_on(block_table, _I32, dev, "block_table")
+        _need_on(free_pages, _I32, dev, "free_pages")
+        _given(n_free, (1,), _I32, dev, "n_free")
+        if len(table) != 2 or table[0] != nseq:
+            raise ValueError(f"block_table must be [{nseq}, max_pages]")
+        if len(free) != 1:
+            raise ValueError("free_pages must be [n_pages]")
         raise ValueError(f"{name}, seq_lens must be [nseq]")
-    if block_table.dim() != 2 or block_table.shape[0] != nseq:
-        raise ValueError(f"block_table must be [{nseq}, max_pages]")
-    if free_pages.dim() != 1:
-        raise ValueError("free_pages must be [n_pages]")
-    return dev, nseq, block_table.shape[1], free_pages.shape[0]
+    return dev, nseq, table[1], free[0]
 
 
 def ne_kv_reserve(new_lens, seq_lens, block_table, free_pages, n_free, n_tot, page_size,
@@ -840,25 +868,29 @@ def ne_kv_reserve(new_lens, seq_lens, block_table, free_pages, n_free, n_tot, pa
                                            "new_lens")
     _need_on(new_lens, _I32, dev, "new_lens")
     n_tot = int(n_tot)
-    for t, shape, name in ((cu_seqlens, (nseq + 1,), "cu_seqlens"), (start_pos, (nseq,), "start_pos"),
-                           (positions, (n_tot,), "positions"), (slots, (n_tot,), "slots"),
-                           (seq_lens_out, (nseq,), "seq_lens_out"),
-                           (n_free_out, (1,), "n_free_out")):
+    for t, n, name in ((cu_seqlens, nseq + 1, "cu_seqlens"), (start_pos, nseq, "start_pos"),
+                       (positions, n_tot, "positions"), (slots, n_tot, "slots"),
+                       (seq_lens_out, nseq, "seq_lens_out"), (n_free_out, 1, "n_free_out")):
         if t is not None:
-            _given(t, shape, _I32, dev, name)
+            _given(t, (n,), _I32, dev, name)
     raw, ctx = _on(stream, dev)
     try:
-        new = lambda n: torch.empty(n, dtype=_I32, device=seq_lens.device)  # noqa: E731
-        cu_seqlens = new(nseq + 1) if cu_seqlens is None else cu_seqlens
-        start_pos = new(nseq) if start_pos is None else start_pos
-        positions = new(n_tot) if positions is None else positions
-        slots = new(n_tot) if slots is None else slots
+        device = seq_lens.device
+        if cu_seqlens is None:
+            cu_seqlens = torch.empty(nseq + 1, dtype=_I32, device=device)
+        if start_pos is None:
+            start_pos = torch.empty_like(seq_lens)
+        if positions is None:
+            positions = torch.empty(n_tot, dtype=_I32, device=device)
+        if slots is None:
+            slots = torch.empty_like(positions)
         rc = lib().ne_kv_reserve(
             new_lens.data_ptr(), seq_lens.data_ptr(), nseq, block_table.data_ptr(), max_pages,
             free_pages.data_ptr(), n_free.data_ptr(), n_pages, int(page_size), int(max_seqlen),
-            n_tot, cu_seqlens.data_ptr(), start_pos.data_ptr(), positions.data_ptr(),
-            slots.data_ptr(), _addr(seq_lens if seq_lens_out is None else seq_lens_out),
-            _addr(n_free if n_free_out is None else n_free_out), raw)
+            n_tot, cu_seqlens.data_ptr(), start_pos.data_ptr(), positions.data_ptr() if n_tot else None,
+            slots.data_ptr() if n_tot else None,
+            (seq_lens if seq_lens_out is None else seq_lens_out).data_ptr(),
+            (n_free if n_free_out is None else n_free_out).data_ptr(), raw)
     finally:
         _leave(ctx)
     _check("ne_kv_reserve", rc)
@@ -886,6 +918,34 @@ def ne_kv_release(finished, seq_lens, block_table, free_pages, n_free, page_size
 
 def _paged(k_pages, v_pages, k_scale, v_scale, block_table, nseq, dev):
     """Checks a paged cache; returns (kv_type, n_pages, Hkv, page_size, max_pages)."""
+    dtype, shape, table = k_pages.dtype, k_pages.shape, block_table.shape
+    if dtype is _U8:
+        kv_type, scales, last = KV_E2M1, (*shape[:3], 2), 32
+    else:
+        kv_type, scales, last = (KV_BF16 if dtype is _BF16 else KV_E4M3), shape[:3], 64
+    if not ((dtype is _BF16 or dtype is _E4M3 or dtype is _U8) and v_pages.dtype is dtype
+            and block_table.dtype is _I32
+            and dev == k_pages.get_device() == v_pages.get_device() == block_table.get_device()
+            and k_pages.is_contiguous() and v_pages.is_contiguous() and block_table.is_contiguous()
+            and len(shape) == 4 and shape == v_pages.shape and shape[3] == last
+            and len(table) == 2 and table[0] == nseq):
+        _bad_pages(k_pages, v_pages, block_table, nseq, dev, last)
+    if kv_type == KV_BF16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale, v_scale: a bfloat16 cache has no scales")
+    elif k_scale is None or v_scale is None:
+        raise ValueError("k_scale, v_scale: a float8_e4m3fn or uint8 cache needs its scales")
+    elif not (k_scale.dtype is _U8 and v_scale.dtype is _U8
+              and dev == k_scale.get_device() == v_scale.get_device()
+              and k_scale.is_contiguous() and v_scale.is_contiguous()
+              and k_scale.shape == scales and v_scale.shape == scales):
+        _given(k_scale, scales, _U8, dev, "k_scale")
+        _given(v_scale, scales, _U8, dev, "v_scale")
+    return kv_type, shape[0], shape[1], shape[2], table[1]
+
+
+def _bad_pages(k_pages, v_pages, block_table, nseq, dev, last):
+    """Says what _paged found wrong."""
     dtype = k_pages.dtype
     if dtype is not _BF16 and dtype is not _E4M3 and dtype is not _U8:
         raise ValueError("k_pages must be bfloat16, float8_e4m3fn or uint8 (two e2m1 each)")
@@ -893,27 +953,17 @@ def _paged(k_pages, v_pages, k_scale, v_scale, block_table, nseq, dev):
     _need_on(v_pages, dtype, dev, "v_pages")
     _need_on(block_table, _I32, dev, "block_table")
     shape = k_pages.shape
-    if len(shape) != 4 or shape != v_pages.shape or shape[3] != (32 if dtype is _U8 else 64):
+    if len(shape) != 4 or shape != v_pages.shape or shape[3] != last:
         raise ValueError("k_pages, v_pages must be [n_pages, Hkv, page_size, 64] (uint8: 32)")
-    table = block_table.shape
-    if len(table) != 2 or table[0] != nseq:
-        raise ValueError(f"block_table must be [{nseq}, max_pages]")
-    if dtype is _BF16:
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("k_scale, v_scale: a bfloat16 cache has no scales")
-    elif k_scale is None or v_scale is None:
-        raise ValueError("k_scale, v_scale: a float8_e4m3fn or uint8 cache needs its scales")
-    else:
-        scales = shape[:3] if dtype is _E4M3 else (*shape[:3], 2)
-        _given(k_scale, scales, _U8, dev, "k_scale")
-        _given(v_scale, scales, _U8, dev, "v_scale")
-    kv_type = KV_BF16 if dtype is _BF16 else KV_E4M3 if dtype is _E4M3 else KV_E2M1
-    return (kv_type,) + shape[:3] + table[1:]
+    raise ValueError(f"block_table must be [{nseq}, max_pages]")
 
 
 def _row_places(cu_seqlens, start_pos, dev):
-    _need_on(cu_seqlens, _I32, dev, "cu_seqlens")
-    _need_on(start_pos, _I32, dev, "start_pos")
+    if not (cu_seqlens.dtype is _I32 and start_pos.dtype is _I32
+            and dev == cu_seqlens.get_device() == start_pos.get_device()
+            and cu_seqlens.is_contiguous() and start_pos.is_contiguous()):
+        _need_on(cu_seqlens, _I32, dev, "cu_seqlens")
+        _need_on(start_pos, _I32, dev, "start_pos")
     nseq = start_pos.numel()
     if cu_seqlens.numel() != nseq + 1:
         raise ValueError("cu_seqlens must be [nseq + 1] for start_pos [nseq]")
@@ -932,8 +982,10 @@ def ne_kv_append(k, v, cu_seqlens, start_pos, k_pages, v_pages, block_table, max
     ``rope_base=0``: ``k`` is rotated already.  Returns ``(k_pages, v_pages)``,
     written in place (with no rows at all, ``n_tot = 0``, as they are)."""
     dev = _device(k, "k")
-    _need_on(k, _BF16, dev, "k")
-    _need_on(v, _BF16, dev, "v")
+    if not (k.dtype is _BF16 and v.dtype is _BF16 and dev == v.get_device()
+            and k.is_contiguous() and v.is_contiguous()):
+        _need_on(k, _BF16, dev, "k")
+        _need_on(v, _BF16, dev, "v")
     nseq = _row_places(cu_seqlens, start_pos, dev)
     kv_type, n_pages, Hkv, page_size, max_pages = _paged(k_pages, v_pages, k_scale, v_scale,
                                                          block_table, nseq, dev)
@@ -1005,8 +1057,10 @@ def ne_attn_decode_paged(q, k_pages, v_pages, block_table, seq_lens, max_seqlen,
     ``[B]`` on the device (positions 0 .. seq_lens[b] - 1 are attended; 0 gives
     zeros and -inf).  Returns ``(out [B, H, 64] bf16, lse [B, H] fp32)``."""
     dev = _device(q, "q")
-    _need_on(q, _BF16, dev, "q")
-    _need_on(seq_lens, _I32, dev, "seq_lens")
+    if not (q.dtype is _BF16 and seq_lens.dtype is _I32 and dev == seq_lens.get_device()
+            and q.is_contiguous() and seq_lens.is_contiguous()):
+        _need_on(q, _BF16, dev, "q")
+        _need_on(seq_lens, _I32, dev, "seq_lens")
     B, H, D = q.shape
     if seq_lens.numel() != B:
         raise ValueError("seq_lens must be [B]")
