@@ -68,11 +68,11 @@ constexpr int kWarps = 4;                      // consumers
 constexpr int kThreads = (kWarps + 1) * 32;    // and the loading warp
 constexpr int kMaxBatch = 512;                 // sequences per launch (prefix sums in shared memory)
 constexpr int kMaxParts = 96;                  // parts of one (sequence, head), about
-constexpr int kOverhead = 4;                   // tiles that a segment's start and end cost
 constexpr int kPartRow = 68;                   // floats: lse (log2 units), 3 pad, o[64]
 constexpr float kBad = INFINITY;               // lse of a part that met a page outside the pool
 constexpr int kQRow = 144;                     // bytes of a q row in shared memory (banks)
 constexpr int kQSlots = 2;
+constexpr int kBulkShift = 7;                  // e2m1: pages from 2^7 keys on come as bulk copies
 
 template <Kv kType>
 struct Tile {
@@ -82,6 +82,7 @@ struct Tile {
   static constexpr int kScales = kType == Kv::kE2m1 ? 2 : kType == Kv::kE4m3 ? 1 : 0;  // of a row
   static constexpr int kPool = kTile * kRowBytes;             // 8 KiB of K, and of V
   static constexpr int kStageBytes = 2 * kPool + 2 * kScales * kTile;
+  static constexpr int kOverhead = kType == Kv::kE2m1 ? 2 : 4;  // tiles that a segment's start and end cost
 };
 
 template <Kv kType, int kRows>
@@ -130,12 +131,14 @@ struct Segment {
 // The flat order: sequence b's units start at prefix[b] * J, unit j's at + j *
 // cost(b), cost(b) = kOverhead + its tiles, the overhead first.  (Positions are
 // below 2^31: the launch sees to it.)
+template <int kOverhead>
 __device__ __forceinline__ void clip_segment(Segment& s, int unit, int x, int end) {
   s.at = unit + kOverhead;
   s.next = min(s.at + s.n_tiles, end);
   s.t0 = max(x - s.at, 0);
   s.t1 = max(s.next - s.at, 0);
 }
+template <int kOverhead>
 __device__ __forceinline__ Segment first_segment(const int* prefix, int B, int J, int x, int end) {
   const int y = x / J;
   int lo = 0, hi = B;  // prefix[lo] <= y < prefix[hi]: the last such lo has tiles
@@ -148,17 +151,18 @@ __device__ __forceinline__ Segment first_segment(const int* prefix, int B, int J
   const int cost = prefix[lo + 1] - prefix[lo], first = prefix[lo] * J;
   s.j = (x - first) / cost;
   s.n_tiles = cost - kOverhead;
-  clip_segment(s, first + s.j * cost, x, end);
+  clip_segment<kOverhead>(s, first + s.j * cost, x, end);
   return s;
 }
 // The segment that starts where s ends (s.next < end).
+template <int kOverhead>
 __device__ __forceinline__ void next_segment(Segment& s, const int* prefix, int J, int end) {
   if (++s.j == J) {
     s.j = 0;
     do ++s.b; while (prefix[s.b + 1] == prefix[s.b]);
     s.n_tiles = prefix[s.b + 1] - prefix[s.b] - kOverhead;
   }
-  clip_segment(s, s.next, s.next, end);
+  clip_segment<kOverhead>(s, s.next, s.next, end);
 }
 
 // D += A * B, m16n8k16, fp32 accumulators; A row-major, B column-major.
@@ -201,6 +205,30 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// 16 bytes into shared memory, asynchronously; the lane's arrival once its copies are there.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -303,6 +331,14 @@ struct FourBit {
 #pragma unroll
     for (int sh = 4; sh < 32; sh <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, sh));
     return v;
+  }
+
+  __device__ __forceinline__ void add_sums(const float2 (&sum)[kNT]) {
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      l[nt][0] += sum[nt].x;
+      l[nt][1] += sum[nt].y;
+    }
   }
 
   // Moves the references to what this tile holds (vb: the scale bytes of this lane's value
@@ -489,24 +525,22 @@ struct FourBit {
       }
     }
     uint32_t w[kMT][kNT][2];
-    float sum[kNT][2];
+    float2 sum[kNT];
     uint32_t top;  // halves that are not negative compare as their bits do
     auto weigh = [&]() {
       top = 0u;
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
-        sum[nt][0] = sum[nt][1] = 0.f;
+        sum[nt] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            float p[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              p[e] = ex2_approx(__fmaf_rn(x[mt][nt][2 * hf + e], f[nt][e], -m[nt][e]));
-              sum[nt][e] += p[e];
-            }
-            w[mt][nt][hf] = pack_f16x2(p[0], p[1]);
+            const float2 y = fma2(make_float2(x[mt][nt][2 * hf], x[mt][nt][2 * hf + 1]),
+                                  make_float2(f[nt][0], f[nt][1]), make_float2(-m[nt][0], -m[nt][1]));
+            const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            sum[nt] = add2(sum[nt], p);
+            w[mt][nt][hf] = pack_f16x2(p.x, p.y);
             top = __vmaxu2(top, w[mt][nt][hf]);
           }
       }
@@ -533,10 +567,7 @@ struct FourBit {
       weigh();
       if (slow) {
         far_values(x, f, sv, vs, live, first, r, c);
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) l[nt][e] += sum[nt][e];
+        add_sums(sum);
         return;
       }
 #pragma unroll
@@ -547,10 +578,7 @@ struct FourBit {
               static_cast<uint16_t>(vb[i][h] < 0 ? 0u : factor(vb[i][h], h));
       __syncwarp();
     }
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) l[nt][e] += sum[nt][e];
+    add_sums(sum);
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
       uint32_t b[2][kNT][2];
@@ -635,9 +663,11 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
   float* red = reinterpret_cast<float*>(smem + L::OFF_RED);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // Pages far below a tile of e2m1 come by copies of 16 bytes a lane.
+  const bool by_lanes = kE2m1 && p.pc.page_shift < kBulkShift;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], by_lanes ? 33 : 1);  // (32 lanes' copies, and what lane 0 says)
       mbar_init(&empty[s], kWarps);
     }
     for (int s = 0; s < kQSlots; ++s) {
@@ -656,7 +686,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
     const bool ok = n >= 0 && n <= p.pc.max_seqlen;
     if (!ok && blockIdx.x == 0) atomicCAS(p.status, 0, NE_DEV_BAD_SEQLEN);
     lens[b] = n;
-    prefix[b + 1] = ok && n > 0 ? (n + T::kTile - 1) / T::kTile + kOverhead : 0;
+    prefix[b + 1] = ok && n > 0 ? (n + T::kTile - 1) / T::kTile + T::kOverhead : 0;
   }
   __syncthreads();
   if (warp == 0) {
@@ -707,7 +737,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
     const int box = page_size < T::kTile ? page_size : T::kTile;  // keys per copy
     bool ok = true;
     int g = 0, nq = 0;  // tiles, segments loaded
-    for (Segment s = first_segment(prefix, B, J, x0, x1);; next_segment(s, prefix, J, x1)) {
+    for (Segment s = first_segment<T::kOverhead>(prefix, B, J, x0, x1);; next_segment<T::kOverhead>(s, prefix, J, x1)) {
       if (s.t0 >= s.t1) {
         if (s.next >= x1) break;
         continue;
@@ -750,6 +780,40 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
                                             p.status, 60)) {
           ok = false;
           break;
+        }
+        if constexpr (kE2m1) {
+          if (by_lanes) {
+            // Lane i: the pool's row of key key0 + 16 i (16 keys are 512 bytes, 16 a lane).
+            const int key = key0 + 16 * (lane & 15), pg = min(key >> p.pc.page_shift, pg1);
+            int page = __shfl_sync(0xffffffffu, id, (pg - have) & 31);
+            const bool page_ok = page >= 0 && page < p.pc.n_pages;
+            if (!page_ok) page = 0;  // reported; its rows are not used
+            const bool bad = __any_sync(0xffffffffu, !page_ok);
+            if (lane == 0) {
+              stage_bad[st] = seg_bad |= bad;
+              if (bad) atomicCAS(p.status, 0, NE_DEV_BAD_PAGE);
+            }
+            // (Rows of a pool are numbered in 31 bits.)
+            const int row = ((page * p.pc.Hkv + hk) << p.pc.page_shift) + (key & (page_size - 1));
+            const uint32_t to = smem_u32(smem + st * T::kStageBytes) + 16 * lane;
+            const uint8_t* k_from = static_cast<const uint8_t*>(p.pc.k) + 16 * lane;
+            const uint8_t* v_from = static_cast<const uint8_t*>(p.pc.v) + 16 * lane;
+            const int some = min(T::kTile, (pages << p.pc.page_shift) - key0) >> 4;
+#pragma unroll 4
+            for (int i = 0; i < some; ++i) {
+              const long long from = static_cast<long long>(__shfl_sync(0xffffffffu, row, i)) * T::kRowBytes;
+              copy16(to + 512 * i, k_from + from);
+              copy16(to + T::kPool + 512 * i, v_from + from);
+            }
+            // Scales: 8 keys a lane.
+            const long long scale = 2LL * (__shfl_sync(0xffffffffu, row, lane >> 1) + 8 * (lane & 1));
+            copy16(to + 2 * T::kPool, p.pc.k_scale + scale);
+            copy16(to + 2 * T::kPool + 2 * T::kTile, p.pc.v_scale + scale);
+            copies_arrive(&full[st]);
+            if (lane == 0) mbar_arrive(&full[st]);
+            __syncwarp();
+            continue;
+          }
         }
         // Lane i copies page pg0 + i.
         int page = __shfl_sync(0xffffffffu, id, (pg0 - have + lane) & 31);
@@ -813,11 +877,11 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
   bool ok = true;
   int st = 0, nq = 0;
   uint32_t phase = 0u;  // of the ring's slot st
-  Segment s = first_segment(prefix, B, J, x0, x1);
+  Segment s = first_segment<T::kOverhead>(prefix, B, J, x0, x1);
   for (bool begun = false;; begun = true) {
     if (begun) {
       if (s.next >= x1) break;
-      next_segment(s, prefix, J, x1);
+      next_segment<T::kOverhead>(s, prefix, J, x1);
     }
     if (s.t0 >= s.t1) continue;
     const int n = lens[s.b];
@@ -1226,7 +1290,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
       const bool last = atomicAdd(p.arrived + w_first, 1) == n_parts - 1;
       if (last) p.arrived[w_first] = 0;  // as the next launch wants it
       *last_flag = last;
-      __threadfence();  // and the other parts after it
+      if (last) __threadfence();  // and the other parts after it
     }
     named_bar_sync(1, kWarps * 32);
     if (!*last_flag) continue;
@@ -1359,7 +1423,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p
 int paged_batch(int H, int Hkv, int max_seqlen) {
   const int rows = paged_rows(H, Hkv), tile = Tile<Kv::kBf16>::kTile;  // the smaller tile
   const long long J = static_cast<long long>(Hkv) * ((H / Hkv + rows - 1) / rows);
-  const long long one = J * ((max_seqlen + tile - 1) / tile + kOverhead);
+  const long long one = J * ((max_seqlen + tile - 1) / tile + Tile<Kv::kBf16>::kOverhead);
   return static_cast<int>(std::min<long long>(kMaxBatch, ((1LL << 31) - (1 << 25)) / one));
 }
 

@@ -132,8 +132,9 @@ __device__ __forceinline__ void store_e2m1(float (&lo)[8], float (&hi)[8], int c
 }
 }  // namespace kv
 
-// kType: the pools' type.  rope.cs == nullptr: the keys come rotated.
-template <Kv kType>
+// kType: the pools' type.  kHeads: neighbouring heads of a row that a quad takes, whose
+// place is found once (Hkv is a multiple of it).  rope.cs == nullptr: the keys come rotated.
+template <Kv kType, int kHeads>
 __global__ void __launch_bounds__(kv::kThreads)
     ne_kv_append_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                         const int* __restrict__ cu, const int* __restrict__ start_pos, int nseq,
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kv::kThreads)
   pdl_wait();  // the kernel that wrote k, v (and anything before it) has completed
   const long long w = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   const int c = static_cast<int>(w % kParts);
-  const long long rh = w / kParts;
+  const long long rh = w / kParts * kHeads;
   Place pl = {0, 0, 0};
   int code = -1;
   if (rh < static_cast<long long>(n_tot) * pc.Hkv)
@@ -150,50 +151,65 @@ __global__ void __launch_bounds__(kv::kThreads)
   if (code > 0) atomicCAS(status, 0, code);
   const bool valid = code == 0;
   // A lane with nothing to do reads row 0 of each tensor and discards it.
-  const uint4* kr = reinterpret_cast<const uint4*>(k + pl.src);
-  const uint4* vr = reinterpret_cast<const uint4*>(v + pl.src);
-  const uint4 k0 = __ldg(kr + c), k1 = __ldg(kr + c + 4);
-  const uint4 v0 = __ldg(vr + c), v1 = __ldg(vr + c + 4);
-  float a[8], b[8];
-  unpack8(k0, a);
-  unpack8(k1, b);
+  const uint4* kr = reinterpret_cast<const uint4*>(k + pl.src) + c;
+  const uint4* vr = reinterpret_cast<const uint4*>(v + pl.src) + c;
+  uint4 k0[kHeads], k1[kHeads], v0[kHeads], v1[kHeads];
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    k0[h] = __ldg(kr + 8 * h);
+    k1[h] = __ldg(kr + 8 * h + 4);
+    v0[h] = __ldg(vr + 8 * h);
+    v1[h] = __ldg(vr + 8 * h + 4);
+  }
+  float4 cs[4];  // (cos, sin) of dims 8c + 2u and 8c + 2u + 1
   if (rope.cs) {
-    const float4* cs =
+    const float4* t =
         reinterpret_cast<const float4*>(rope.cs + static_cast<long long>(pl.pos) * 32 + 8 * c);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float4 t = __ldg(cs + u);  // (cos, sin) of dims 8c + 2u and 8c + 2u + 1
-      const float lo0 = __fmaf_rn(a[2 * u], t.x, -__fmul_rn(b[2 * u], t.y));
-      const float hi0 = __fmaf_rn(b[2 * u], t.x, __fmul_rn(a[2 * u], t.y));
-      const float lo1 = __fmaf_rn(a[2 * u + 1], t.z, -__fmul_rn(b[2 * u + 1], t.w));
-      const float hi1 = __fmaf_rn(b[2 * u + 1], t.z, __fmul_rn(a[2 * u + 1], t.w));
-      a[2 * u] = lo0;
-      b[2 * u] = hi0;
-      a[2 * u + 1] = lo1;
-      b[2 * u + 1] = hi1;
-    }
+    for (int u = 0; u < 4; ++u) cs[u] = __ldg(t + u);
   }
-  if constexpr (kType == Kv::kE4m3) {
-    store_e4m3(a, b, c, valid, pl.slot, static_cast<uint8_t*>(pc.k), pc.k_scale);
-    unpack8(v0, a);
-    unpack8(v1, b);
-    store_e4m3(a, b, c, valid, pl.slot, static_cast<uint8_t*>(pc.v), pc.v_scale);
-  } else if constexpr (kType == Kv::kE2m1) {
-    store_e2m1(a, b, c, valid, pl.slot, static_cast<uint8_t*>(pc.k), pc.k_scale);
-    unpack8(v0, a);
-    unpack8(v1, b);
-    store_e2m1(a, b, c, valid, pl.slot, static_cast<uint8_t*>(pc.v), pc.v_scale);
-  } else if (valid) {
-    uint4* ko = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pc.k) + pl.slot * kHD);
-    uint4* vo = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pc.v) + pl.slot * kHD);
-    ko[c] = pack8(a);
-    ko[c + 4] = pack8(b);
-    vo[c] = v0;
-    vo[c + 4] = v1;
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    const long long slot = pl.slot + (static_cast<long long>(h) << pc.page_shift);
+    float a[8], b[8];
+    unpack8(k0[h], a);
+    unpack8(k1[h], b);
+    if (rope.cs) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float4 t = cs[u];
+        const float lo0 = __fmaf_rn(a[2 * u], t.x, -__fmul_rn(b[2 * u], t.y));
+        const float hi0 = __fmaf_rn(b[2 * u], t.x, __fmul_rn(a[2 * u], t.y));
+        const float lo1 = __fmaf_rn(a[2 * u + 1], t.z, -__fmul_rn(b[2 * u + 1], t.w));
+        const float hi1 = __fmaf_rn(b[2 * u + 1], t.z, __fmul_rn(a[2 * u + 1], t.w));
+        a[2 * u] = lo0;
+        b[2 * u] = hi0;
+        a[2 * u + 1] = lo1;
+        b[2 * u + 1] = hi1;
+      }
+    }
+    if constexpr (kType == Kv::kE4m3) {
+      store_e4m3(a, b, c, valid, slot, static_cast<uint8_t*>(pc.k), pc.k_scale);
+      unpack8(v0[h], a);
+      unpack8(v1[h], b);
+      store_e4m3(a, b, c, valid, slot, static_cast<uint8_t*>(pc.v), pc.v_scale);
+    } else if constexpr (kType == Kv::kE2m1) {
+      store_e2m1(a, b, c, valid, slot, static_cast<uint8_t*>(pc.k), pc.k_scale);
+      unpack8(v0[h], a);
+      unpack8(v1[h], b);
+      store_e2m1(a, b, c, valid, slot, static_cast<uint8_t*>(pc.v), pc.v_scale);
+    } else if (valid) {
+      uint4* ko = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pc.k) + slot * kHD);
+      uint4* vo = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pc.v) + slot * kHD);
+      ko[c] = pack8(a);
+      ko[c + 4] = pack8(b);
+      vo[c] = v0[h];
+      vo[c + 4] = v1[h];
+    }
   }
 }
 
-template <Kv kType>
+template <Kv kType, int kHeads>
 __global__ void __launch_bounds__(kv::kThreads)
     ne_kv_read_kernel(__nv_bfloat16* __restrict__ k, __nv_bfloat16* __restrict__ v,
                       const int* __restrict__ cu, const int* __restrict__ start_pos, int nseq,
@@ -202,96 +218,133 @@ __global__ void __launch_bounds__(kv::kThreads)
   pdl_wait();  // the kernel that filled the cache has completed
   const long long w = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   const int c = static_cast<int>(w % kParts);
-  const long long rh = w / kParts;
+  const long long rh = w / kParts * kHeads;
   if (rh >= static_cast<long long>(n_tot) * pc.Hkv) return;
   Place pl = {0, 0, 0};
   const int code = place(pc, cu, start_pos, nseq, static_cast<int>(rh), pl);
   if (code > 0) atomicCAS(status, 0, code);
   if (code != 0) return;
-  uint4* ko = reinterpret_cast<uint4*>(k + pl.src);
-  uint4* vo = reinterpret_cast<uint4*>(v + pl.src);
-  if constexpr (kType == Kv::kE2m1) {
-    auto row = [&](const void* pool, const uint8_t* scale, uint4* out) {
-      const uint2 w = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) +
-                                                     pl.slot * (kHD / 2))[c];
-      const int bytes = reinterpret_cast<const uint16_t*>(scale)[pl.slot];
-      // (low halves of the two words: dims 8c .. 8c + 7; high halves: 32 + 8c ..)
-      const uint32_t half[2] = {__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632)};
+  // Loads of all heads first.
+  constexpr int kWords = kType == Kv::kBf16 ? 4 : kType == Kv::kE4m3 ? 2 : 1;  // uint2 of a lane
+  uint2 kw[kHeads][kWords], vw[kHeads][kWords];
+  int ks[kHeads], vs[kHeads];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float f = scale_value(u ? bytes >> 8 : bytes & 255);
-        uint32_t h[4];
-        e2m1x8_to_f16x2(half[u], h);
-        float x[8];
+  for (int h = 0; h < kHeads; ++h) {
+    const long long slot = pl.slot + (static_cast<long long>(h) << pc.page_shift);
+    auto load = [&](const void* pool, const uint8_t* scale, uint2 (&to)[kWords], int& byte) {
+      if constexpr (kType == Kv::kBf16) {
+        const uint4* src =
+            reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pool) + slot * kHD);
+        const uint4 x = src[c], y = src[c + 4];
+        to[0] = make_uint2(x.x, x.y);
+        to[1] = make_uint2(x.z, x.w);
+        to[2] = make_uint2(y.x, y.y);
+        to[3] = make_uint2(y.z, y.w);
+        byte = 0;
+      } else if constexpr (kType == Kv::kE4m3) {
+        const uint2* src =
+            reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) + slot * kHD);
+        to[0] = src[c];
+        to[1] = src[c + 4];
+        byte = scale[slot];
+      } else {
+        to[0] = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) + slot * (kHD / 2))[c];
+        byte = reinterpret_cast<const uint16_t*>(scale)[slot];
+      }
+    };
+    load(pc.k, pc.k_scale, kw[h], ks[h]);
+    load(pc.v, pc.v_scale, vw[h], vs[h]);
+  }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f16x2_to_f32(h[i], x[2 * i], x[2 * i + 1]);
-          x[2 * i] *= f;
-          x[2 * i + 1] *= f;
+  for (int h = 0; h < kHeads; ++h) {
+    auto store = [&](const uint2 (&w)[kWords], int byte, uint4* out) {
+      if constexpr (kType == Kv::kBf16) {
+        out[0] = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+        out[4] = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+      } else if constexpr (kType == Kv::kE4m3) {
+        const float f = scale_value(byte);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float x[8];
+          unpack_e4m3x2(w[u].x, x[0], x[1]);
+          unpack_e4m3x2(w[u].x >> 16, x[2], x[3]);
+          unpack_e4m3x2(w[u].y, x[4], x[5]);
+          unpack_e4m3x2(w[u].y >> 16, x[6], x[7]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] *= f;
+          out[4 * u] = pack8(x);
         }
-        out[c + 4 * u] = pack8(x);
+      } else {
+        // (low halves of the two words: dims 8c .. 8c + 7; high halves: 32 + 8c ..)
+        const uint32_t half[2] = {__byte_perm(w[0].x, w[0].y, 0x5410),
+                                  __byte_perm(w[0].x, w[0].y, 0x7632)};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float f = scale_value(u ? byte >> 8 : byte & 255);
+          uint32_t two[4];
+          e2m1x8_to_f16x2(half[u], two);
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f16x2_to_f32(two[i], x[2 * i], x[2 * i + 1]);
+            x[2 * i] *= f;
+            x[2 * i + 1] *= f;
+          }
+          out[4 * u] = pack8(x);
+        }
       }
     };
-    row(pc.k, pc.k_scale, ko);
-    row(pc.v, pc.v_scale, vo);
-  } else if constexpr (kType == Kv::kE4m3) {
-    auto row = [&](const void* pool, const uint8_t* scale, uint4* out) {
-      const uint2* src =
-          reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pool) + pl.slot * kHD);
-      const uint2 w[2] = {src[c], src[c + 4]};
-      const float f = scale_value(scale[pl.slot]);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float x[8];
-        unpack_e4m3x2(w[u].x, x[0], x[1]);
-        unpack_e4m3x2(w[u].x >> 16, x[2], x[3]);
-        unpack_e4m3x2(w[u].y, x[4], x[5]);
-        unpack_e4m3x2(w[u].y >> 16, x[6], x[7]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= f;
-        out[c + 4 * u] = pack8(x);
-      }
-    };
-    row(pc.k, pc.k_scale, ko);
-    row(pc.v, pc.v_scale, vo);
-  } else {
-    const uint4* kr =
-        reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pc.k) + pl.slot * kHD);
-    const uint4* vr =
-        reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pc.v) + pl.slot * kHD);
-    const uint4 k0 = kr[c], k1 = kr[c + 4], v0 = vr[c], v1 = vr[c + 4];
-    ko[c] = k0;
-    ko[c + 4] = k1;
-    vo[c] = v0;
-    vo[c + 4] = v1;
+    store(kw[h], ks[h], reinterpret_cast<uint4*>(k + pl.src + h * kHD) + c);
+    store(vw[h], vs[h], reinterpret_cast<uint4*>(v + pl.src + h * kHD) + c);
   }
 }
 
 namespace {
-dim3 kv_grid(int n_tot, int Hkv) {
-  const long long items = static_cast<long long>(n_tot) * Hkv * kv::kParts;
-  return dim3(static_cast<unsigned>((items + kv::kThreads - 1) / kv::kThreads));
+template <Kv kType, int kHeads>
+cudaError_t append(const __nv_bfloat16* k, const __nv_bfloat16* v, const int* cu,
+                   const int* start_pos, int nseq, int n_tot, const PagedCache& pc,
+                   const RopeTable& rope, int* status, cudaStream_t stream) {
+  const long long items = static_cast<long long>(n_tot) * (pc.Hkv / kHeads) * kv::kParts;
+  return launch_pdl(ne_kv_append_kernel<kType, kHeads>,
+                    dim3(static_cast<unsigned>((items + kv::kThreads - 1) / kv::kThreads)),
+                    dim3(kv::kThreads), 0, stream, k, v, cu, start_pos, nseq, n_tot, pc, rope, status);
+}
+template <Kv kType, int kHeads>
+cudaError_t read(__nv_bfloat16* k, __nv_bfloat16* v, const int* cu, const int* start_pos, int nseq,
+                 int n_tot, const PagedCache& pc, int* status, cudaStream_t stream) {
+  const long long items = static_cast<long long>(n_tot) * (pc.Hkv / kHeads) * kv::kParts;
+  return launch_pdl(ne_kv_read_kernel<kType, kHeads>,
+                    dim3(static_cast<unsigned>((items + kv::kThreads - 1) / kv::kThreads)),
+                    dim3(kv::kThreads), 0, stream, k, v, cu, start_pos, nseq, n_tot, pc, status);
+}
+
+// Two heads a quad for rows with scales, once they fill the GPU: what finds a row's place is
+// half of the instructions of a (row, head) otherwise.  (69,524 rows of 12 heads, a head and
+// two: e2m1 written 70.2 and 60.6 us, read 51.8 and 44.3; e4m3 63.7 and 59.2, 53.6 and 51.4;
+// bf16, which only moves bytes, 67.3 and 65.5, 65.5 and 66.5.  Four: as two, or slower.)
+bool two_heads(int n_tot, int Hkv) {
+  return Hkv % 2 == 0 && static_cast<long long>(n_tot) * Hkv >= 1 << 16;
 }
 }  // namespace
 
 cudaError_t launch_kv_append(const __nv_bfloat16* k, const __nv_bfloat16* v, const int* cu,
                              const int* start_pos, int nseq, int n_tot, const PagedCache& pc,
                              Kv type, const RopeTable& rope, int* status, cudaStream_t stream) {
-  return launch_pdl(type == Kv::kE2m1   ? ne_kv_append_kernel<Kv::kE2m1>
-                    : type == Kv::kE4m3 ? ne_kv_append_kernel<Kv::kE4m3>
-                                        : ne_kv_append_kernel<Kv::kBf16>,
-                    kv_grid(n_tot, pc.Hkv), dim3(kv::kThreads), 0, stream, k, v, cu, start_pos,
-                    nseq, n_tot, pc, rope, status);
+  const bool two = two_heads(n_tot, pc.Hkv);
+  auto* go = type == Kv::kE2m1   ? (two ? append<Kv::kE2m1, 2> : append<Kv::kE2m1, 1>)
+             : type == Kv::kE4m3 ? (two ? append<Kv::kE4m3, 2> : append<Kv::kE4m3, 1>)
+                                 : append<Kv::kBf16, 1>;
+  return go(k, v, cu, start_pos, nseq, n_tot, pc, rope, status, stream);
 }
 
 cudaError_t launch_kv_read(__nv_bfloat16* k, __nv_bfloat16* v, const int* cu,
                            const int* start_pos, int nseq, int n_tot, const PagedCache& pc,
                            Kv type, int* status, cudaStream_t stream) {
-  return launch_pdl(type == Kv::kE2m1   ? ne_kv_read_kernel<Kv::kE2m1>
-                    : type == Kv::kE4m3 ? ne_kv_read_kernel<Kv::kE4m3>
-                                        : ne_kv_read_kernel<Kv::kBf16>,
-                    kv_grid(n_tot, pc.Hkv), dim3(kv::kThreads), 0, stream, k, v, cu, start_pos,
-                    nseq, n_tot, pc, status);
+  const bool two = two_heads(n_tot, pc.Hkv);
+  auto* go = type == Kv::kE2m1   ? (two ? read<Kv::kE2m1, 2> : read<Kv::kE2m1, 1>)
+             : type == Kv::kE4m3 ? (two ? read<Kv::kE4m3, 2> : read<Kv::kE4m3, 1>)
+                                 : read<Kv::kBf16, 1>;
+  return go(k, v, cu, start_pos, nseq, n_tot, pc, status, stream);
 }
 
 }  // namespace ne

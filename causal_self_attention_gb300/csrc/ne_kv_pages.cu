@@ -28,14 +28,16 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRowsPerThread = 4;
 
 struct Shared {
-  long long warp_rows[kWarps], warp_pages[kWarps];
+  uint32_t warp_rows[kWarps], warp_pages[kWarps];
   int last;
 };
 
-__device__ __forceinline__ long long scan_warp(long long v, int lane) {
+// Inclusive sums over the lanes.
+template <typename T>
+__device__ __forceinline__ T scan_warp(T v, int lane) {
 #pragma unroll
   for (int sh = 1; sh < 32; sh <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, sh);
+    const T u = __shfl_up_sync(0xffffffffu, v, sh);
     if (lane >= sh) v += u;
   }
   return v;
@@ -53,34 +55,45 @@ __device__ __forceinline__ int find(const int* first, int n, int x) {
 
 // Exclusive prefix sums of rows(s) and pages(s) over the sequences into shared
 // memory, [nseq + 1] each, and their totals (64 bits: the entries hold where the
-// totals fit).  one(s, rows, pages): what sequence s adds.  Every thread calls it.
+// totals fit).  one(s, rows, pages): what sequence s adds, at most 65535 * 128 rows, so that
+// a warp's 512 sequences fit 32 bits.  Every thread calls it, with neighbouring sequences of
+// its own: one exchange between the warps, however many there are.
 template <typename One>
 __device__ __forceinline__ void prefix_sums(int nseq, int* row_at, int* page_at, Shared& sh,
                                             long long& rows, long long& pages, One one) {
+  static_assert(kMaxPagedSequences <= 16 * kThreads, "32 bits for a warp's sums");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  rows = pages = 0;
-  for (int s0 = 0; s0 < nseq; s0 += kThreads) {
-    const int s = s0 + threadIdx.x;
+  const int per = (nseq + kThreads - 1) / kThreads;
+  const int s0 = min(static_cast<int>(threadIdx.x) * per, nseq), s1 = min(s0 + per, nseq);
+  uint32_t m_sum = 0, t_sum = 0;
+#pragma unroll 4
+  for (int s = s0; s < s1; ++s) {
     int m = 0, t = 0;
-    if (s < nseq) one(s, m, t);
-    const long long a = scan_warp(m, lane), b = scan_warp(t, lane);
-    if (lane == 31) {
-      sh.warp_rows[warp] = a;
-      sh.warp_pages[warp] = b;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      sh.warp_rows[lane] = scan_warp(sh.warp_rows[lane], lane);
-      sh.warp_pages[lane] = scan_warp(sh.warp_pages[lane], lane);
-    }
-    __syncthreads();
-    if (s < nseq) {
-      row_at[s] = static_cast<int>(rows + (warp ? sh.warp_rows[warp - 1] : 0) + a - m);
-      page_at[s] = static_cast<int>(pages + (warp ? sh.warp_pages[warp - 1] : 0) + b - t);
-    }
-    rows += sh.warp_rows[kWarps - 1];
-    pages += sh.warp_pages[kWarps - 1];
-    __syncthreads();
+    one(s, m, t);
+    row_at[s] = m;
+    page_at[s] = t;
+    m_sum += m;
+    t_sum += t;
+  }
+  const uint32_t a = scan_warp(m_sum, lane), b = scan_warp(t_sum, lane);
+  if (lane == 31) {
+    sh.warp_rows[warp] = a;
+    sh.warp_pages[warp] = b;
+  }
+  __syncthreads();
+  const long long wr = scan_warp(static_cast<long long>(sh.warp_rows[lane]), lane);
+  const long long wp = scan_warp(static_cast<long long>(sh.warp_pages[lane]), lane);
+  rows = __shfl_sync(0xffffffffu, wr, 31);
+  pages = __shfl_sync(0xffffffffu, wp, 31);
+  long long r = __shfl_sync(0xffffffffu, wr, max(warp - 1, 0)), p = __shfl_sync(0xffffffffu, wp, max(warp - 1, 0));
+  r = (warp ? r : 0) + a - m_sum;
+  p = (warp ? p : 0) + b - t_sum;
+  for (int s = s0; s < s1; ++s) {
+    const int m = row_at[s], t = page_at[s];
+    row_at[s] = static_cast<int>(r);
+    page_at[s] = static_cast<int>(p);
+    r += m;
+    p += t;
   }
   if (threadIdx.x == 0) {
     row_at[nseq] = static_cast<int>(rows);
@@ -89,15 +102,18 @@ __device__ __forceinline__ void prefix_sums(int nseq, int* row_at, int* page_at,
   __syncthreads();
 }
 
-// Whether this CTA is the last of the launch to come here (with its reads of what
-// is updated in place behind it).  Every thread calls it.
+// Whether this CTA is the last of the launch to come here, with its reads of what is
+// updated in place behind it (and no store, which the fence would wait for).  Every
+// thread calls it.
 __device__ __forceinline__ bool last_to_read(int* arrived, Shared& sh) {
   if (gridDim.x == 1) return true;
   if (threadIdx.x == 0) {
     __threadfence();
     sh.last = atomicAdd(arrived, 1) == static_cast<int>(gridDim.x) - 1;
-    if (sh.last) *arrived = 0;  // as the next launch wants it
-    __threadfence();
+    if (sh.last) {
+      *arrived = 0;  // as the next launch wants it
+      __threadfence();
+    }
   }
   __syncthreads();
   return sh.last != 0;
@@ -127,6 +143,7 @@ __global__ void __launch_bounds__(pages::kThreads) ne_kv_reserve_kernel(const Pa
     }
     t = ((n + m + P1) >> p.page_shift) - ((n + P1) >> p.page_shift);
   });
+  const bool updates = last_to_read(p.arrived, sh);
   bad = __syncthreads_or(bad) || rows > p.max_rows;
   const bool short_of = taken > n_free || n_free > p.n_pages || n_free < 0;
   const bool ok = !bad && !short_of;
@@ -141,36 +158,50 @@ __global__ void __launch_bounds__(pages::kThreads) ne_kv_reserve_kernel(const Pa
       const int at = ((lens[s] + P1) >> p.page_shift) + t - page_at[s];
       p.block_table[static_cast<long long>(s) * p.max_pages + at] = __ldg(p.free_pages + n_free - 1 - t);
     }
-  // Positions and slots, neighbouring rows in a thread's hands.
+  // Positions and slots, neighbouring rows in a thread's hands (a page looked up once).
   const int n_rows = ok ? static_cast<int>(rows) : 0;
+  const bool aligned = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15) == 0;
   for (int r0 = id * kRowsPerThread; r0 < p.n_tot; r0 += all * kRowsPerThread) {
     int s = r0 < n_rows ? find(row_at, p.nseq, r0) : 0;
+    int pos[kRowsPerThread], slot[kRowsPerThread], seen = -1, page = -1;
 #pragma unroll
     for (int i = 0; i < kRowsPerThread; ++i) {
       const int r = r0 + i;
-      if (r >= p.n_tot) break;
-      int pos = -1, slot = -1;
-      if (r < n_rows) {
-        while (row_at[s + 1] <= r) ++s;
-        pos = lens[s] + r - row_at[s];
-        const int had = (lens[s] + P1) >> p.page_shift, at = pos >> p.page_shift;
-        const int page =
-            at < had ? __ldcg(p.block_table + static_cast<long long>(s) * p.max_pages + at)
-                     : __ldg(p.free_pages + n_free - 1 - (page_at[s] + at - had));
-        if (page >= 0 && page < p.n_pages)
-          slot = (page << p.page_shift) + (pos & P1);
-        else
-          atomicCAS(p.status, 0, NE_DEV_BAD_PAGE);
+      pos[i] = slot[i] = -1;
+      if (r >= n_rows) continue;
+      while (row_at[s + 1] <= r) {
+        ++s;
+        seen = -1;
       }
-      if (p.positions) p.positions[r] = pos;
-      if (p.slots) p.slots[r] = slot;
+      pos[i] = lens[s] + r - row_at[s];
+      const int at = pos[i] >> p.page_shift;
+      if (at != seen) {
+        const int had = (lens[s] + P1) >> p.page_shift;
+        page = at < had ? __ldcg(p.block_table + static_cast<long long>(s) * p.max_pages + at)
+                        : __ldg(p.free_pages + n_free - 1 - (page_at[s] + at - had));
+        seen = at;
+      }
+      if (page >= 0 && page < p.n_pages)
+        slot[i] = (page << p.page_shift) + (pos[i] & P1);
+      else
+        atomicCAS(p.status, 0, NE_DEV_BAD_PAGE);
+    }
+    if (aligned && r0 + kRowsPerThread <= p.n_tot) {
+      if (p.positions) *reinterpret_cast<int4*>(p.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      if (p.slots) *reinterpret_cast<int4*>(p.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRowsPerThread; ++i) {
+        if (p.positions && r0 + i < p.n_tot) p.positions[r0 + i] = pos[i];
+        if (p.slots && r0 + i < p.n_tot) p.slots[r0 + i] = slot[i];
+      }
     }
   }
   for (int s = id; s <= p.nseq; s += all) {
     if (p.cu_seqlens) p.cu_seqlens[s] = ok ? row_at[s] : 0;
     if (p.start_pos && s < p.nseq) p.start_pos[s] = lens[s];
   }
-  if (!last_to_read(p.arrived, sh)) return;
+  if (!updates) return;
   for (int s = threadIdx.x; s < p.nseq; s += kThreads)
     p.seq_lens_out[s] = ok ? lens[s] + row_at[s + 1] - row_at[s] : lens[s];
   if (threadIdx.x == 0) *p.n_free_out = ok ? n_free - static_cast<int>(taken) : n_free;
@@ -197,6 +228,7 @@ __global__ void __launch_bounds__(pages::kThreads) ne_kv_release_kernel(const Pa
     }
     t = (n + P1) >> p.page_shift;
   });
+  const bool updates = last_to_read(p.arrived, sh);
   bad = __syncthreads_or(bad);
   const bool over = n_free < 0 || n_free > p.n_pages || given > p.n_pages - n_free;
   const bool ok = !bad && !over;
@@ -210,7 +242,7 @@ __global__ void __launch_bounds__(pages::kThreads) ne_kv_release_kernel(const Pa
       p.free_pages_out[n_free + t] = *entry;
       *entry = -1;
     }
-  if (!last_to_read(p.arrived, sh) || !ok) return;
+  if (!updates || !ok) return;
   for (int s = threadIdx.x; s < p.nseq; s += kThreads)
     if (row_at[s + 1] != row_at[s]) p.seq_lens_out[s] = 0;
   if (threadIdx.x == 0) *p.n_free_out = n_free + static_cast<int>(given);
@@ -227,7 +259,8 @@ cudaError_t launch(void (*kernel)(const PagesParams), int arrays, long long work
   }
   long long ctas = (work + pages::kThreads * pages::kRowsPerThread - 1) /
                    (pages::kThreads * pages::kRowsPerThread);
-  ctas = ctas < 1 ? 1 : ctas > sms ? sms : ctas;
+  const long long most = bytes <= 96 * 1024 ? 2LL * sms : sms;  // (resident at once)
+  ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(pages::kThreads), bytes, stream,
                     p);
 }
