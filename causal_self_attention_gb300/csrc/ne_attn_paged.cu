@@ -254,16 +254,18 @@ __device__ __forceinline__ int e2m1_key(int mt, int x) {
 // The state of a warp's softmax over 4-bit rows, and a tile of 64 keys, two a lane.
 //
 // Scores: the products with the two halves of a key's row, each with its scale: x =
-// s0 a0 + s1 a1, f x in log2 units.  Weights p = 2^(f x - m) with a reference m, in
-// halves; for a value row's half h they take its scale, 2 p 2^(e_h - E_h), E_h an
-// exponent that the warp keeps, so that a weight is formed once and scaled by a product
-// of two halves.  (E_h - e_h is 0 .. 15: what that costs is half's smallest step, 2^-26 of
-// 2^E_h, 2^-11 of the largest term that the sum has.)  Where a score exceeds its
-// reference by more than 2^8, or an exponent this range, or the sequence ends in the
-// tile -- one vote tells --, the tile takes a longer way, on which the references move.
-// Rows whose scales differ by more (never mind zeros) put the warp into another mode
-// for the rest of the segment: a reference of its own for every (query head, half),
-// 2^(f x + e_h - m2), which loses nothing however far the scales are apart.
+// s0 a0 + s1 a1, f x in log2 units.  Weights p = 2^(f x - m), in halves, with a reference
+// m that was kHeadroom below the largest score when it was set; for a value row's half h
+// they take its scale, p 2^(e_h - E_h), E_h an exponent that the warp keeps, so that a
+// weight is formed once and scaled by a product of two halves.  E_h - e_h is 0 .. 7 for
+// every row that the warp has seen.  What halves cost is their smallest step, two
+// roundings of at most 2^-25 + 2^-26 of 2^(m + E_h) for a key; the key of the largest score
+// alone has a term of 2^(m + 8 + E_h - 7), so that it is less than 2^-25 of the largest term.
+// Where a score exceeds the reference's by more than 2^7, or an exponent its range, or the
+// sequence ends in the tile -- one vote tells --, the tile takes a longer way, on which the
+// references move.  Rows whose scales differ by more (never mind zeros) put the warp into
+// another mode for the rest of the segment: a reference of its own for every (query head,
+// half), 2^(f x + e_h - m2), which loses nothing however far the scales are apart.
 //
 // What bounds a tile is the integer pipe: 128 of its conversions take two cycles each,
 // so that choices are made by masks and pairs of bytes are looked at together.
@@ -271,19 +273,22 @@ template <int kNT>
 struct FourBit {
   static constexpr float kNone = -1e30f;  // no score yet: a finite one exceeds it by any measure
   static constexpr int kMT = 4;           // row tiles of 16 keys
-  static constexpr int kRange = 15;
+  static constexpr int kRange = 7;
+  static constexpr float kHeadroom = 8.f;  // weights of 2^15 at most: within a half
   static constexpr int kZero = 27;        // the scale byte of zeros
   static constexpr int kUnset = -1000;
   static constexpr int kScratch = 16 * kMT * 12;  // a warp's: key scales (float2), value factors
   float m[kNT][2], l[kNT][2];             // l: of this lane's keys
   float o[kNT][4][4];                     // row tiles 0, 1: the first half's dims; 2, 3: the second's
-  int eb[2];                              // E_h + 127
+  uint32_t base;                          // E_h + 127 - kRange, as one word's halves
+  uint32_t lowest;                        // smallest scale bytes of this lane's rows, 16 bits each
   bool slow;
   float m2[kNT][2][2];                    // slow: o's references
 
   __device__ __forceinline__ void begin() {
     slow = false;
-    eb[0] = eb[1] = kUnset;
+    set_base(kUnset, kUnset);
+    lowest = 0xffffffffu;
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
@@ -297,12 +302,19 @@ struct FourBit {
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
     }
   }
+  __device__ __forceinline__ void set_base(int b0, int b1) {
+    base = static_cast<uint32_t>(b0 - kRange) + (static_cast<uint32_t>(b1 - kRange) << 16);
+  }
+  __device__ __forceinline__ int eb(int h) const {  // E_h + 127
+    const int low = static_cast<int16_t>(base & 0xffffu);
+    return (h ? static_cast<int>(base - static_cast<uint32_t>(low)) >> 16 : low) + kRange;
+  }
   // The references as the segment's end wants them.
   __device__ __forceinline__ float ref(int nt, int e) const {
     return m[nt][e] > 0.5f * kNone ? m[nt][e] : -INFINITY;
   }
   __device__ __forceinline__ float of_o(int nt, int e, int h) const {
-    return slow ? m2[nt][e][h] : m[nt][e] + static_cast<float>(eb[h] - 128);
+    return slow ? m2[nt][e][h] : m[nt][e] + static_cast<float>(eb(h) - 127);
   }
   __device__ __forceinline__ float ref2(int nt, int e, int h) const {
     const float x = of_o(nt, e, h);
@@ -322,10 +334,11 @@ struct FourBit {
   };
   static constexpr int kOther = 16 * kMT;  // from a half's factors to the other's (uint16)
 
-  // 2 * 2^(byte - 127 - E_h) as a half: NaN for a row marked so, zero for zeros far below.
+  // 2^(byte - 127 - E_h) as a half: NaN for a row marked so, zero for zeros far below.
   __device__ __forceinline__ uint32_t factor(int byte, int h) const {
-    const int u = byte - eb[h] + kRange;
-    return byte == 255 ? 0x7e00u : u >= 0 && u <= kRange ? static_cast<uint32_t>(u + 1) << 10 : 0u;
+    const int u = byte - eb(h) + kRange;
+    return byte == 255 ? 0x7e00u
+                       : u >= 0 && u <= kRange ? static_cast<uint32_t>(u + 15 - kRange) << 10 : 0u;
   }
   static __device__ __forceinline__ float column_max(float v) {
 #pragma unroll
@@ -348,9 +361,10 @@ struct FourBit {
     bool turned = false;
     if (!slow) {
       int hi[2];
+      uint32_t low[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        int most = eb[h], least = 1000;
+        int most = eb(h), least = static_cast<int>(h ? lowest >> 16 : lowest & 0xffffu);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (vb[i][h] >= 0 && vb[i][h] != 255) {
@@ -360,7 +374,9 @@ struct FourBit {
         }
         hi[h] = __reduce_max_sync(0xffffffffu, most);
         turned |= __reduce_min_sync(0xffffffffu, least) < hi[h] - kRange;
+        low[h] = static_cast<uint32_t>(least);
       }
+      lowest = low[0] | low[1] << 16;
       if (turned) {  // o stays as it is, under the references that it has
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
@@ -372,8 +388,7 @@ struct FourBit {
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float down = ex2_approx(static_cast<float>(eb[h] - hi[h]));
-          eb[h] = hi[h];
+          const float down = ex2_approx(static_cast<float>(eb(h) - hi[h]));
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -381,6 +396,7 @@ struct FourBit {
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[nt][i][e] *= down;
         }
+        set_base(hi[0], hi[1]);
       }
     }
 #pragma unroll
@@ -390,7 +406,7 @@ struct FourBit {
         float a = -INFINITY;
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt) a = fmaxf(a, fmaxf(x[mt][nt][e], x[mt][nt][2 + e]));
-        a = column_max(a) * f[nt][e];
+        a = column_max(a) * f[nt][e] - kHeadroom;
         if (a > m[nt][e]) {
           const float up = ex2_approx(m[nt][e] - a);
           m[nt][e] = a;
@@ -426,7 +442,7 @@ struct FourBit {
 #pragma unroll
         for (int i = 2 * h; i < 2 * h + 2; ++i)
           size = fmaxf(size, fmaxf(fabsf(o[nt][i][e]), fabsf(o[nt][i][2 + e])));
-        t = column_max(t);
+        t = column_max(t) - kHeadroom;
         const float old = m2[nt][e][h];
         float now = fmaxf(t, old);
         if (first) {
@@ -480,9 +496,6 @@ struct FourBit {
     uint16_t* factors = reinterpret_cast<uint16_t*>(scratch + 128 * kMT);
     uint32_t bytes[2];
     bool longer = live < 16 * kMT;
-    // (Both halves' exponents in one word: 0 .. 15 fits.)
-    const uint32_t base = static_cast<uint32_t>(eb[0] - kRange) +
-                          (static_cast<uint32_t>(eb[1] - kRange) << 16);
     longer |= slow;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -491,8 +504,9 @@ struct FourBit {
       reinterpret_cast<float2*>(scratch)[at.k + 4 * i] =
           make_float2(kv::scale_value(kb & 255u), kv::scale_value(kb >> 8));
       const uint32_t u = __byte_perm(bytes[i], 0u, 0x4140) - base;
-      longer |= (u & 0xfff0fff0u) != 0u;
-      const uint32_t two = (u << 10) + 0x04000400u;
+      static_assert(kRange == 7, "three bits, and 2^-7 as a half: 8 << 10");
+      longer |= (u & 0xfff8fff8u) != 0u;
+      const uint32_t two = (u << 10) + 0x20002000u;
       factors[at.v + 8 * i] = static_cast<uint16_t>(two);
       factors[at.v + 8 * i + kOther] = static_cast<uint16_t>(two >> 16);
     }
@@ -546,7 +560,7 @@ struct FourBit {
       }
     };
     weigh();
-    longer |= ((top + 0x23ff23ffu) & 0x80008000u) != 0u;  // above 2^8 = 0x5c00
+    longer |= ((top + 0x07ff07ffu) & 0x80008000u) != 0u;  // above 2^15 = 0x7800
     if (__any_sync(0xffffffffu, longer)) {
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt)
@@ -577,6 +591,10 @@ struct FourBit {
           factors[at.v + 8 * i + kOther * h] =
               static_cast<uint16_t>(vb[i][h] < 0 ? 0u : factor(vb[i][h], h));
       __syncwarp();
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        lowest = __vminu2(lowest, __byte_perm(bytes[i], 0u, 0x4140));
     }
     add_sums(sum);
 #pragma unroll

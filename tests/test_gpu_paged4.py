@@ -283,6 +283,26 @@ def test_decode_values_of_very_different_scales(na, halves):
     _check_sequence(c, 0, 200, q, out[0], lse[0])
 
 
+@pytest.mark.parametrize("up", [6, 9, 20, 40])
+def test_decode_values_whose_scales_rise_along_the_sequence(na, up):
+    """The weight on early keys with small values, and tiles of much larger ones behind
+    them, each tile's scales alike: what the later keys add counts by its size, not by its
+    weight."""
+    lens = [320, 1500]
+    c = Cache4(lens, 1, 64, seed=71).fill_random(72)
+    for s, n in enumerate(lens):
+        page, slot = (t.cuda() for t in c.where(s, torch.arange(n)))
+        late = (torch.arange(n) >= 64).cuda()
+        c.vs[page, 0, slot] = torch.where(late, 127 + up, 127).to(torch.uint8)[:, None].expand(n, 2)
+        # Scores of 0 for the first keys, -0.125 * 64 * 2.25 = -18 (2^-26) for the others.
+        c.k[page, 0, slot] = torch.where(late, 0xcc, 0x00).to(torch.uint8)[:, None].expand(n, 32)
+        c.ks[page, 0, slot] = 127
+    q = torch.full((2, 4, 64), 1.125, dtype=torch.bfloat16, device="cuda")
+    out, lse = _decode(na, c, q, _i32(lens), 1500, 0.0)
+    for s, n in enumerate(lens):
+        _check_sequence(c, s, n, q[s:s + 1], out[s], lse[s])
+
+
 def test_decode_halves_of_a_key_with_scales_far_apart(na):
     """A score is the sum of its halves', each with its own scale."""
     lens = [150]
