@@ -275,7 +275,8 @@ struct FourBit {
   static constexpr int kMT = 4;           // row tiles of 16 keys
   static constexpr int kRange = 7;
   static constexpr float kHeadroom = 8.f;  // weights of 2^15 at most: within a half
-  static constexpr int kZero = 27;        // the scale byte of zeros
+  // The scale byte of zeros, 2^-100; rows of it or less count as zeros beside rows 2^7 above.
+  static constexpr int kZero = 27;
   static constexpr int kUnset = -1000;
   static constexpr int kScratch = 16 * kMT * 12;  // a warp's: key scales (float2), value factors
   float m[kNT][2], l[kNT][2];             // l: of this lane's keys

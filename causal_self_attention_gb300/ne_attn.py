@@ -860,7 +860,8 @@ def ne_kv_reserve(new_lens, seq_lens, block_table, free_pages, n_free, n_tot, pa
     ``n_free_out``.  Returns ``(cu_seqlens [nseq + 1], start_pos [nseq], positions
     [n_tot], slots [n_tot])`` of the packed new rows, -1 from the last of them on:
     :func:`ne_kv_append` takes the first two, :func:`ne_qk_norm_rope_fwd` the third; a
-    slot is page * page_size + position % page_size.  Nothing comes to the host: too few
+    slot is page * page_size + position % page_size.  ``n_tot = 0``: neither positions nor
+    slots are wanted, and the rows have no bound.  Nothing comes to the host: too few
     pages (``NE_ERR_NO_PAGES``), rows (more than ``n_tot``) or positions
     (``NE_ERR_BAD_SEQLEN``) show in :func:`ne_attn_get_device_status`, and then nothing
     is handed out and there are no rows."""

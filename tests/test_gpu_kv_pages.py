@@ -168,6 +168,30 @@ def test_a_page_outside_the_pool(na):
     assert na.ne_attn_get_device_status() == 9 and slots.tolist() == [-1] * 5
 
 
+def test_slots_up_to_31_bits(na):
+    """The largest pool: its last pages' slots, and rows of a long sequence of them."""
+    n_pages = (2 ** 31 - 1) // 256
+    free = torch.arange(n_pages, dtype=torch.int32, device="cuda")
+    lens, n_free = _i32([0, 3]), _i32([n_pages])
+    table = torch.full((2, 5000), -1, dtype=torch.int32, device="cuda")
+    table[1, 0] = 7
+    m = 1000 * 256 + 5
+    cu, start, pos, slots = na.ne_kv_reserve(_i32([m, 2]), lens, table, free, n_free, m + 2, 256,
+                                             5000 * 256)
+    assert na.ne_attn_get_device_status() == 0
+    assert cu.tolist() == [0, m, m + 2] and start.tolist() == [0, 3] and lens.tolist() == [m, 5]
+    assert n_free.tolist() == [n_pages - 1001]
+    i = torch.arange(m, device="cuda")
+    assert torch.equal(pos[:m].long(), i)
+    assert torch.equal(slots[:m].long(), (n_pages - 1 - i // 256) * 256 + i % 256)
+    assert slots[m:].tolist() == [7 * 256 + 3, 7 * 256 + 4]
+    na.ne_kv_release(torch.tensor([1, 0], dtype=torch.uint8, device="cuda"), lens, table, free,
+                     n_free, 256, 5000 * 256)
+    assert na.ne_attn_get_device_status() == 0
+    assert n_free.tolist() == [n_pages] and lens.tolist() == [0, 5]
+    assert torch.equal(free[-1001:].flip(0), torch.arange(n_pages - 1001, n_pages, device="cuda"))
+
+
 def test_giving_back_too_much(na):
     """A stack that would hold more than there is stays as it was."""
     plain = step.Pages(2, 4, 4, 16, range(4))

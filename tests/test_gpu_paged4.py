@@ -4,9 +4,10 @@ import pytest
 import torch
 
 import step
-from grouped import F64, U16, attention, rotate, rotate_bound, within
+from grouped import F64, U16, Cache, attention, rotate, rotate_bound, within
 from step import Cache4, quantise4
 from test_gpu_paged import BASE, LENS, _append, _cu, _decode, _i32, _randn
+from test_gpu_paged import _check_append as check_append_e4m3
 
 pytestmark = pytest.mark.gpu
 
@@ -66,6 +67,48 @@ def test_append_one_token_each_and_parts_of_prompts(na, Hkv):
     rows = [1] * 8 + [40]
     lens = [s + r for s, r in zip(start, rows)]
     _check_append(na, Cache4(lens, Hkv, 16, seed=2), rows, start, BASE, 12)
+
+
+@pytest.mark.parametrize("Hkv,lens", [(2, [20000, 0, 13001]), (4, [9000, 9001]), (10, [7001])])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append_and_read_many_rows(na, Hkv, lens, e4m3):
+    """Rows enough to fill the GPU, with an even number of heads; e4m3's likewise."""
+    if e4m3:
+        c = Cache(lens, Hkv, 64, True, seed=9)
+        check_append_e4m3(na, c, lens, [0] * len(lens), BASE, 14)
+    else:
+        c = Cache4(lens, Hkv, 64, seed=9)
+        _check_append(na, c, lens, [0] * len(lens), BASE, 14)
+    tot = sum(lens)
+    k, v = na.ne_kv_read(c.k, c.v, c.table, _cu(lens), _i32([0] * len(lens)), tot, c.ks, c.vs)
+    assert na.ne_attn_get_device_status() == 0
+    at = 0
+    for s, n in enumerate(lens):
+        for got, want in zip((k, v), c.rows(s) if n else ()):
+            assert torch.equal(got[at:at + n].to(F64), want)
+        at += n
+
+
+@pytest.mark.parametrize("page", [16, 256])
+def test_pools_past_32_bits(na, page):
+    """Pages at the end of pools of more than 4 GiB: written, read, attended to."""
+    lens, Hkv, H = [700, 33], 4, 12
+    c = Cache4(lens, Hkv, page, seed=10)
+    many = (2 ** 27 + 2 ** 24) // (Hkv * page)
+    c.table[c.table >= 0] += many - c.n_pages
+    c.n_pages = many
+    c.k, c.v = (torch.zeros((many, Hkv, page, 32), dtype=torch.uint8, device="cuda") for _ in range(2))
+    c.ks, c.vs = (torch.zeros((many, Hkv, page, 2), dtype=torch.uint8, device="cuda")
+                  for _ in range(2))
+    tot = sum(lens)
+    k, v = _randn(24, tot, Hkv, 64), _randn(25, tot, Hkv, 64)
+    _append(na, c, k, v, _cu(lens), _i32([0, 0]), 0.0, 700)
+    kk, vv = na.ne_kv_read(c.k, c.v, c.table, _cu(lens), _i32([0, 0]), tot, c.ks, c.vs)
+    assert na.ne_attn_get_device_status() == 0
+    for got, x in ((kk, k), (vv, v)):
+        assert torch.equal(got.to(F64), quantise4(x.to(F64))[0])
+    assert torch.equal(c.rows(0)[0], kk[:700].to(F64))
+    _check_decode(na, c, H, lens, BASE, 26)
 
 
 def test_append_many_sequences(na):
@@ -227,6 +270,14 @@ def test_decode_head_layouts(na, H, Hkv):
     _check_decode(na, c, H, lens, BASE, 46)
 
 
+@pytest.mark.parametrize("page", [128, 256])
+@pytest.mark.parametrize("H,Hkv", [(9, 1), (16, 1), (32, 2), (40, 1), (21, 7)])
+def test_decode_head_layouts_of_large_pages(na, H, Hkv, page):
+    lens = [333, 1, 1030, 0, 256]
+    c = Cache4(lens, Hkv, page, seed=44).fill_random(45)
+    _check_decode(na, c, H, lens, BASE, 46)
+
+
 @pytest.mark.parametrize("H,Hkv,B,n", [(8, 2, 1, 20000), (8, 2, 3, 9001), (32, 2, 2, 5000)])
 def test_decode_long(na, H, Hkv, B, n):
     lens = [n - 777 * i for i in range(B)]
@@ -265,8 +316,9 @@ def test_decode_sharp_scores(na):
         _check_sequence(c, s, n, q[s:s + 1], out[s], lse[s])
 
 
+@pytest.mark.parametrize("H", [4, 13])
 @pytest.mark.parametrize("halves", [(True, False), (False, True), (True, True)])
-def test_decode_values_of_very_different_scales(na, halves):
+def test_decode_values_of_very_different_scales(na, halves, H):
     """Rows whose scales differ by 2^40, in one half or in both: the small ones with the
     weight."""
     lens = [200]
@@ -274,17 +326,18 @@ def test_decode_values_of_very_different_scales(na, halves):
     page, slot = (t.cuda() for t in c.where(0, torch.arange(200)))
     for h in (h for h in (0, 1) if halves[h]):
         c.vs[page, 0, slot, h] = torch.where(torch.arange(200) < 3, 150, 110).to(torch.uint8).cuda()
-    _check_decode(na, c, 4, lens, BASE, 63)
+    _check_decode(na, c, H, lens, BASE, 63)
     # The keys with large values get almost no weight (scores near -60).
     c.k[page[:3], 0, slot[:3]] = 0xee  # -4, times 2^1
     c.ks[page[:3], 0, slot[:3]] = 128
-    q = torch.ones((1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.ones((1, H, 64), dtype=torch.bfloat16, device="cuda")
     out, lse = _decode(na, c, q, _i32(lens), 200, 0.0)
     _check_sequence(c, 0, 200, q, out[0], lse[0])
 
 
+@pytest.mark.parametrize("H", [4, 16])
 @pytest.mark.parametrize("up", [6, 9, 20, 40])
-def test_decode_values_whose_scales_rise_along_the_sequence(na, up):
+def test_decode_values_whose_scales_rise_along_the_sequence(na, up, H):
     """The weight on early keys with small values, and tiles of much larger ones behind
     them, each tile's scales alike: what the later keys add counts by its size, not by its
     weight."""
@@ -297,7 +350,7 @@ def test_decode_values_whose_scales_rise_along_the_sequence(na, up):
         # Scores of 0 for the first keys, -0.125 * 64 * 2.25 = -18 (2^-26) for the others.
         c.k[page, 0, slot] = torch.where(late, 0xcc, 0x00).to(torch.uint8)[:, None].expand(n, 32)
         c.ks[page, 0, slot] = 127
-    q = torch.full((2, 4, 64), 1.125, dtype=torch.bfloat16, device="cuda")
+    q = torch.full((2, H, 64), 1.125, dtype=torch.bfloat16, device="cuda")
     out, lse = _decode(na, c, q, _i32(lens), 1500, 0.0)
     for s, n in enumerate(lens):
         _check_sequence(c, s, n, q[s:s + 1], out[s], lse[s])
@@ -381,7 +434,6 @@ def test_decode_workspace_streams_and_graphs(na):
 def test_decode_of_what_was_stored(na):
     """Rows written in 4 bits: the attention's answer is that of the values read back in
     bf16, by the bf16 cache's kernel, within the bounds of either."""
-    from grouped import Cache
     lens, H, Hkv = [400, 77], 8, 2
     tot = sum(lens)
     c, b = Cache4(lens, Hkv, 64, seed=90), Cache(lens, Hkv, 64, False, seed=90)

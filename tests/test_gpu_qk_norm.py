@@ -79,6 +79,31 @@ def test_many_rows(na, N, H, Hkv):
     _check_backward(na, *a)
 
 
+@pytest.mark.parametrize("N,H,Hkv", [(9001, 9, 3), (3001, 33, 1), (20001, 3, 2), (20003, 1, 3),
+                                     (40001, 1, 1)])
+def test_many_rows_of_odd_heads(na, N, H, Hkv):
+    """Rows enough to fill the GPU, with heads that a quad's share divides or not."""
+    a = _inputs(2, N, H, Hkv, False)
+    _check_forward(na, *a)
+    _check_backward(na, *a)
+
+
+def test_rows_far_apart(na):
+    """Rows 2^30 elements apart (2 GiB): offsets past 32 bits, of inputs and of gradients."""
+    N, H, Hkv, far = 3, 5, 2, 2 ** 30
+    q, k, wq, wk, pos = _inputs(8, N, H, Hkv, False)
+
+    def spread(x, at):
+        room = torch.empty((N - 1) * far + 1024, dtype=torch.bfloat16, device="cuda")
+        y = room.as_strided(x.shape, (far, 64, 1), at)
+        y.copy_(x)
+        return y
+
+    a = spread(q, 0), spread(k, 64), wq, wk, pos
+    _check_forward(na, *a)
+    _check_backward(na, *a, dq=spread(torch.zeros_like(q), 8), dk=spread(torch.zeros_like(k), 512))
+
+
 def test_norm_alone(na):
     q, k, wq, wk, _ = _inputs(3, 130, 4, 2, True)
     for pos in (None, _i32([5] * 130)):
