@@ -45,13 +45,21 @@
 //   loses nothing however far the rows' scales are apart; the sum of weights
 //   runs against the scores' own reference m.  Rounding to half: 2^-11.
 //
+// e2m1: as e4m3, in tiles of 64 keys a warp, with other weights: FourBit says which.
+//
 // Measured: 16 sequences of 16k, 32 heads on 8, bf16 80.5 us (6.3 TB/s, 94% of the
-// copy rate); 64 ragged sequences of 1 to 16k, e4m3, 28.0 us (3.7 TB/s: the
+// copy rate); 64 ragged sequences of 1 to 16k, e4m3, 26.8 us (3.9 TB/s: the
 // products, weights and conversions of a key take 43% of the issue slots, and
 // the segments' ends, joins and the slowest CTA the rest); one sequence of 777,
 // 7.4 us (launch, prefix sums, a short ring, the join).  Tried: four CTAs an SM
 // with two stages, three q slots, other overheads (2, 3, 6) and part limits
 // (16-256): none faster on all of these.
+// e2m1: 64 sequences of 16k, 32 heads on 8, 109 us (5.0 TB/s, 74% of the copy rate; a
+// byte has four times the keys of bf16, and what bounds a tile is its arithmetic: the
+// integer pipe busy half of the time, issue slots 53%, three dependent warps a scheduler);
+// 64 ragged ones 30.6 us (2.8 TB/s), 777 keys 9.4 us, 64 of 2000 27.8 us.  Tried: four
+// CTAs an SM with two stages (136, 40, 11 and 37 us: 96 registers spill), tiles of 32
+// keys a warp, warps that take tiles of their own without meeting (113, 33 us).
 //
 // Keys of a tile past the sequence's end (what the page holds there, or an
 // older tile's bytes) get the score -inf, and their value rows are cleared in
@@ -72,7 +80,10 @@ constexpr int kPartRow = 68;                   // floats: lse (log2 units), 3 pa
 constexpr float kBad = INFINITY;               // lse of a part that met a page outside the pool
 constexpr int kQRow = 144;                     // bytes of a q row in shared memory (banks)
 constexpr int kQSlots = 2;
-constexpr int kBulkShift = 7;                  // e2m1: pages from 2^7 keys on come as bulk copies
+// e2m1: pages from 2^7 keys on come as bulk copies, smaller ones by copies of 16 bytes a
+// lane.  (A bulk copy costs 60 cycles and more: 64 sequences of 2000 with pages of 16, 37.4 us
+// by bulk copies, 27.9 by lanes; 64 of 16k with pages of 128, 109 and 114 us.)
+constexpr int kBulkShift = 7;
 
 template <Kv kType>
 struct Tile {

@@ -17,6 +17,13 @@
 // kept for the next step (lengths, the stack's height) may be updated in place:
 // the CTA that has read it last does that (one CTA: itself), so that no CTA reads
 // a new value for an old one.
+//
+// What bounds it is latency: launch, the lengths' loads, two exchanges of the sums, a
+// row's bisection in shared memory and its table entry.  Measured: 64 sequences, a row
+// each, 4.6 us; 4096 sequences with a million rows in all 12.4 us (the rows' 8 MB alone
+// 1.2 us): every CTA sums the 4096 lengths, and a thread's four rows take a bisection of 12
+// steps.  (Two CTAs an SM where they fit; the sums updated behind the rows' stores,
+// whose fence waits for them, 14.6 us.)
 #include "ne_paged.cuh"
 #include "ne_sm100.cuh"
 
