@@ -1,8 +1,10 @@
-"""Build ``libne_attn.so`` in-tree with nvcc for sm_103a (GB300).
+"""Build ``libne_attn.so`` in-tree with nvcc for sm_103a (GB300), and the module
+``ne_step`` that makes a generation step's calls from Python.
 
 The translation units are compiled in parallel, then linked into
 ``causal_self_attention_gb300/_build/libne_attn.so``.  No CMake, no torch
-extension machinery: the library is plain C ABI (include/ne_attn.h).
+extension machinery: the library is plain C ABI (include/ne_attn.h).  The module
+alone knows torch's tensors; it is built for the torch that is installed.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libne_attn.so")
 SOURCES = ["ne_attn_api.cu", "ne_attn_fwd.cu", "ne_attn_gqa_fwd.cu", "ne_attn_bwd.cu", "ne_attn_noalloc.cu",
            "ne_attn_decode.cu", "ne_attn_paged.cu", "ne_kv_cache.cu", "ne_kv_pages.cu", "ne_qk_norm.cu", "ne_debug.cu", "ne_proj.cu", "ne_sched.cu"]
+STEP_SOURCE = "ne_step.cpp"
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -41,12 +45,48 @@ def compile_flags(extra=()) -> list:
             "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include"), *extra]
 
 
+def step_path() -> str:
+    """The path of the module ``ne_step`` for this torch."""
+    import torch
+    return os.path.join(BUILD_DIR, f"ne_step-{torch.__version__}.so")
+
+
+def _build_step(path: str, cuda: str) -> None:
+    import torch
+    home = os.path.dirname(torch.__file__)
+    include = (os.path.join(home, "include"),
+               os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
+               os.path.join(ROOT, "include"))
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           *("-I" + d for d in include), os.path.join(CSRC, STEP_SOURCE), "-o", tmp,
+           "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {STEP_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile (if stale) and return the library path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    if not force and os.path.exists(LIB_PATH) and os.path.getmtime(LIB_PATH) >= _deps_mtime():
-        return LIB_PATH
-    nvcc = nvcc_path()
+    step, deps = step_path(), _deps_mtime()
+    fresh = [not force and os.path.exists(p) and os.path.getmtime(p) >= deps for p in (LIB_PATH, step)]
+    nvcc = None if all(fresh) else nvcc_path()
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        module = None
+        if not fresh[1]:
+            cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+            module = ex.submit(_build_step, step, cuda)
+        if not fresh[0]:
+            _build_library(nvcc, verbose, ptxas_info)
+        if module is not None:
+            module.result()
+    return LIB_PATH
+
+
+def _build_library(nvcc: str, verbose: bool, ptxas_info: bool) -> None:
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
     def compile_one(src):
@@ -67,7 +107,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":

@@ -6,10 +6,17 @@ function keeps the C name; tensors replace raw pointers and the sizes are read
 from their shapes.  A nonzero status raises :class:`NeAttnError`.  There is no
 fallback: if the library is missing, or the device is not an sm_103 GPU, the
 call fails.
+
+The calls of a generation step (norms of queries and keys, pages, rows of the paged cache,
+decode over it) are marshalled by the module ``ne_step`` (csrc/ne_step.cpp) where they are
+regular -- tensors on the current device, its current stream -- in a third of the time;
+what is not, it hands back, and the function here goes on.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -17,6 +24,7 @@ import torch
 from . import build as _build
 
 _lib = None
+_step = None  # the module ne_step, once the library is loaded
 
 NE_OK = 0
 STATUS_NAMES = {0: "NE_OK", 1: "NE_ERR_INVALID_ARG", 2: "NE_ERR_UNSUPPORTED",
@@ -56,7 +64,7 @@ def library_path() -> str:
 
 def lib():
     """Load the library (built in-tree by ``causal_self_attention_gb300.build``)."""
-    global _lib
+    global _lib, _step
     if _lib is not None:
         return _lib
     path = library_path()
@@ -129,13 +137,35 @@ def lib():
     L.ne_qk_norm_rope_bwd_workspace_bytes.restype = Z
     L.ne_status_string.argtypes = [I]
     L.ne_status_string.restype = ctypes.c_char_p
+    _step = _load_step(L)
     _lib = L
     return L
+
+
+def _load_step(L):
+    path = _build.step_path()
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with "
+                           "`python -m causal_self_attention_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader("ne_step", path)
+    step = importlib.util.module_from_spec(importlib.util.spec_from_loader("ne_step", loader))
+    loader.exec_module(step)
+    step.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+        L.ne_qk_norm_rope_fwd, L.ne_qk_norm_rope_bwd, L.ne_kv_reserve, L.ne_kv_release,
+        L.ne_kv_append, L.ne_kv_read, L.ne_attn_decode_paged)))
+    return step
 
 
 def _check(name, rc):
     if rc != NE_OK:
         raise NeAttnError(name, rc)
+
+
+def _made(name, got):
+    """What a call of ne_step returned: the tensors, or raises for its status."""
+    if got.__class__ is not tuple:
+        _check(name, got)
+    return got
 
 
 def _stream(stream):
@@ -512,9 +542,8 @@ def _raw_stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
-# (The step's calls take 10 to 20 us of host time, most of it in what marshals them: the
-# checks below look at everything in one expression, and call the functions that say
-# what is wrong only where something is.)
+# (The calls on a paged cache are short: the checks below look at everything in one
+# expression, and call the functions that say what is wrong only where something is.)
 if hasattr(torch._C, "_cuda_getDevice"):
     _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
@@ -756,6 +785,10 @@ def ne_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, max_seqlen, eps=1e-
     no sequence, left alone), in one pass.  ``rope_base=0``: the norms alone, and
     ``positions`` may be None.  Returns ``(qr, kr)``, contiguous, for the ``_rotated``
     attention calls and, with ``rope_base=0``, the paged cache's."""
+    if stream is None and _step is not None:
+        got = _step.norm_fwd(q, k, q_weight, k_weight, positions, max_seqlen, eps, rope_base, qr, kr)
+        if got is not None:
+            return _made("ne_qk_norm_rope_fwd", got)
     dev, N, H, Hkv, D, q_row, k_row = _qk_norm_shapes(q, k, q_weight, k_weight, positions,
                                                       rope_base)
     if qr is not None:
@@ -790,6 +823,11 @@ def ne_qk_norm_rope_bwd(dqr, dkr, q, k, q_weight, k_weight, positions, max_seqle
     the forward's ``q``, ``k``.  Returns ``(dq, dk, dq_weight, dk_weight)``: bf16 ``[N, H,
     64]``, ``[N, Hkv, 64]`` (contiguous unless given, as slices of a joint gradient, say)
     and fp32 ``[64]``."""
+    if stream is None and workspace is None and _step is not None:
+        got = _step.norm_bwd(dqr, dkr, q, k, q_weight, k_weight, positions, max_seqlen, eps,
+                             rope_base, dq, dk, dq_weight, dk_weight)
+        if got is not None:
+            return _made("ne_qk_norm_rope_bwd", got)
     dev, N, H, Hkv, D, q_row, k_row = _qk_norm_shapes(q, k, q_weight, k_weight, positions,
                                                       rope_base)
     if not (dqr.dtype is _BF16 and dkr.dtype is _BF16
@@ -865,6 +903,12 @@ def ne_kv_reserve(new_lens, seq_lens, block_table, free_pages, n_free, n_tot, pa
     pages (``NE_ERR_NO_PAGES``), rows (more than ``n_tot``) or positions
     (``NE_ERR_BAD_SEQLEN``) show in :func:`ne_attn_get_device_status`, and then nothing
     is handed out and there are no rows."""
+    if stream is None and _step is not None:
+        got = _step.reserve(new_lens, seq_lens, block_table, free_pages, n_free, n_tot, page_size,
+                            max_seqlen, cu_seqlens, start_pos, positions, slots, seq_lens_out,
+                            n_free_out)
+        if got is not None:
+            return _made("ne_kv_reserve", got)
     dev, nseq, max_pages, n_pages = _pages(seq_lens, block_table, free_pages, n_free, new_lens,
                                            "new_lens")
     _need_on(new_lens, _I32, dev, "new_lens")
@@ -903,6 +947,10 @@ def ne_kv_release(finished, seq_lens, block_table, free_pages, n_free, page_size
     """Take back the pages of every sequence with ``finished[s]`` (bool or uint8 CUDA
     ``[nseq]``): they go onto the stack of :func:`ne_kv_reserve`, their entries of
     ``block_table`` become -1 and ``seq_lens[s]`` 0, all in place.  Returns None."""
+    if stream is None and _step is not None:
+        rc = _step.release(finished, seq_lens, block_table, free_pages, n_free, page_size, max_seqlen)
+        if rc is not None:
+            return _check("ne_kv_release", rc)
     dev, nseq, max_pages, n_pages = _pages(seq_lens, block_table, free_pages, n_free, finished,
                                            "finished")
     _need_on(finished, torch.bool if finished.dtype is torch.bool else _U8, dev, "finished")
@@ -982,6 +1030,12 @@ def ne_kv_append(k, v, cu_seqlens, start_pos, k_pages, v_pages, block_table, max
     ``[n_pages, Hkv, page_size, 2]``; ``block_table`` int32 ``[nseq, max_pages]``.
     ``rope_base=0``: ``k`` is rotated already.  Returns ``(k_pages, v_pages)``,
     written in place (with no rows at all, ``n_tot = 0``, as they are)."""
+    if stream is None and _step is not None:
+        rc = _step.append(k, v, cu_seqlens, start_pos, k_pages, v_pages, block_table, max_seqlen,
+                          k_scale, v_scale, rope_base)
+        if rc is not None:
+            _check("ne_kv_append", rc)
+            return k_pages, v_pages
     dev = _device(k, "k")
     if not (k.dtype is _BF16 and v.dtype is _BF16 and dev == v.get_device()
             and k.is_contiguous() and v.is_contiguous()):
@@ -1015,6 +1069,11 @@ def ne_kv_read(k_pages, v_pages, block_table, cu_seqlens, start_pos, n_tot, k_sc
     ``start_pos[s] + i``.  The keys come rotated, as the cache holds them.
     ``max_seqlen``: the block table's reach unless given.  Returns ``(k, v)``;
     rows of the caller's ``k``, ``v`` that no sequence covers stay as they are."""
+    if stream is None and _step is not None:
+        got = _step.read(k_pages, v_pages, block_table, cu_seqlens, start_pos, n_tot, k_scale, v_scale,
+                         max_seqlen, k, v)
+        if got is not None:
+            return _made("ne_kv_read", got)
     dev = _device(k_pages, "k_pages")
     nseq = _row_places(cu_seqlens, start_pos, dev)
     kv_type, n_pages, Hkv, page_size, max_pages = _paged(k_pages, v_pages, k_scale, v_scale,
@@ -1057,6 +1116,11 @@ def ne_attn_decode_paged(q, k_pages, v_pages, block_table, seq_lens, max_seqlen,
     :func:`ne_kv_append` with the new tokens' rows in it, ``seq_lens`` int32
     ``[B]`` on the device (positions 0 .. seq_lens[b] - 1 are attended; 0 gives
     zeros and -inf).  Returns ``(out [B, H, 64] bf16, lse [B, H] fp32)``."""
+    if stream is None and workspace is None and _step is not None:
+        got = _step.decode(q, k_pages, v_pages, block_table, seq_lens, max_seqlen, k_scale, v_scale,
+                           rope_base, scale, out, lse)
+        if got is not None:
+            return _made("ne_attn_decode_paged", got)
     dev = _device(q, "q")
     if not (q.dtype is _BF16 and seq_lens.dtype is _I32 and dev == seq_lens.get_device()
             and q.is_contiguous() and seq_lens.is_contiguous()):

@@ -202,6 +202,20 @@ def test_binding_refuses_before_the_library(monkeypatch):
             pytest.fail(f"refusal {n} did not happen")
 
 
+def test_native_marshalling_hands_back_what_is_not_regular(lib):
+    from causal_self_attention_gb300 import ne_attn as na
+    na.lib()
+    step, bf, i = na._step, torch.zeros((4, 2, 64), dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    counts = dict(norm_fwd=10, norm_bwd=14, reserve=14, release=7, append=11, read=11, decode=12)
+    for name, n in counts.items():
+        call = getattr(step, name)
+        for args in ((), (None,) * n, (bf,) * n, (i,) * n, (1,) * n, ("x",) * n, (None,) * (n + 1)):
+            assert call(*args) is None  # CPU tensors, no tensors, too many
+    for args in ((), (1,) * 8, ("x",) * 7):
+        with pytest.raises(TypeError):
+            step.bind(*args)
+
+
 # ------------------------------------------------- the plain implementations
 
 def test_plain_four_bit_rounding():
