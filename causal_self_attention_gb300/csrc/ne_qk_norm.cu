@@ -16,7 +16,7 @@
 // once (bf16; dw is fp32).
 // Measured, forward: 92,604 rows of 40 heads 152 us (6.2 TB/s, 92% of the copy rate),
 // 18,641 of 16 heads 14.0 us (5.5 TB/s), 64 of 16 heads 1.6 us (a launch); backward:
-// 65,536 rows of 40 heads 181 us (5.6 TB/s, 82%), 8192 of 16 heads 16.1 us (3.1 TB/s: two
+// 65,536 rows of 40 heads 180 us (5.6 TB/s, 83%), 8192 of 16 heads 14.7 us (3.4 TB/s: two
 // rounds of loads that wait, the sums of dw, the CTA that adds them up).
 #include "ne_sm100.cuh"
 
@@ -24,6 +24,7 @@ namespace ne {
 
 namespace qkn {
 constexpr int kParts = 4;  // lanes per (row, head)
+constexpr int kQkNormSms = 160;  // an upper bound on the part's SMs (152), and on the backward's CTAs
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -228,25 +229,18 @@ __device__ __forceinline__ void grad_rows(const QkNormParams& p, const __nv_bflo
   }
 }
 
-// The CTA's sum of acc into row[64] (a partial of dw), in a fixed order.
-template <int kWarps>
-__device__ __forceinline__ void cta_sum(float (&acc)[16], int c, float (*sum)[kHD], float* row) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// The warp's sum of acc into row[64] (in shared memory), in a fixed order.  (By halves,
+// 14 exchanges for these 48: 0.3 us less for 8192 rows of 16 heads, and 3% more for 65,536 of
+// 40, whose loop the compiler then arranges otherwise.)
+__device__ __forceinline__ void warp_sum(float (&acc)[16], int c, float* row) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
 #pragma unroll
     for (int sh = 4; sh < 32; sh <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], sh);
-    if (lane < kParts) sum[warp][(j & 8) * 4 + 8 * c + (j & 7)] = acc[j];
+    if (lane < kParts) row[(j & 8) * 4 + 8 * c + (j & 7)] = acc[j];
     acc[j] = 0.f;
   }
-  __syncthreads();
-  if (threadIdx.x < kHD) {
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += sum[w][threadIdx.x];
-    row[threadIdx.x] = s;
-  }
-  __syncthreads();
 }
 }  // namespace qkn
 
@@ -257,7 +251,7 @@ template <int kThreads, int kHeads, int kCtas>
 __global__ void __launch_bounds__(kThreads, kCtas) ne_qk_norm_rope_bwd_kernel(const QkNormParams p) {
   using namespace qkn;
   constexpr int kWarps = kThreads / 32;
-  __shared__ float sum[kWarps][kHD];
+  __shared__ float sum[kWarps][2][kHD];
   __shared__ int last;
   pdl_wait();
   const int c = threadIdx.x % kParts, quad = threadIdx.x / kParts;
@@ -265,10 +259,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) ne_qk_norm_rope_bwd_kernel(co
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = 0.f;
   float* part = p.part + static_cast<long long>(blockIdx.x) * 2 * kHD;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grad_rows<kThreads, kHeads>(p, p.dqr, p.q, p.q_stride, p.qw, p.H, p.dq, p.dq_stride, c, quad, acc);
-  cta_sum<kWarps>(acc, c, sum, part);
+  warp_sum(acc, c, sum[warp][0]);
   grad_rows<kThreads, kHeads>(p, p.dkr, p.k, p.k_stride, p.kw, p.Hkv, p.dk, p.dk_stride, c, quad, acc);
-  cta_sum<kWarps>(acc, c, sum, part + kHD);
+  warp_sum(acc, c, sum[warp][1]);
+  __syncthreads();
+  if (threadIdx.x < 2 * kHD) {  // in the order of the warps
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += sum[w][threadIdx.x / kHD][threadIdx.x % kHD];
+    part[threadIdx.x] = s;
+  }
+  __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();  // the CTA's partials (ordered before this by the barrier), then the arrival
     last = atomicAdd(p.arrived, 1) == static_cast<int>(gridDim.x) - 1;
@@ -279,15 +282,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) ne_qk_norm_rope_bwd_kernel(co
   if (!last) return;
   // Thread t: columns 4 (t % 32) .. + 3 of every 16th partial.
   const float4* src = reinterpret_cast<const float4*>(p.part);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = gridDim.x;
+  const int n = gridDim.x;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = warp; i < n; i += kWarps) {
-    const float4 v = __ldcg(src + i * 32 + lane);
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
+  constexpr int kEach = (kQkNormSms + kWarps - 1) / kWarps;  // all of them on their way at once
+  float4 v[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    v[i] = warp + i * kWarps < n ? __ldcg(src + (warp + i * kWarps) * 32 + lane)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    s.x += v[i].x;
+    s.y += v[i].y;
+    s.z += v[i].z;
+    s.w += v[i].w;
   }
   __shared__ float4 all[kWarps][32];
   all[warp][lane] = s;
@@ -306,11 +314,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) ne_qk_norm_rope_bwd_kernel(co
   }
 }
 
-namespace {
-constexpr int kQkNormSms = 160;  // an upper bound on the part's SMs (152), for the workspace's size
-}
-
-size_t qk_norm_part_bytes() { return kQkNormSms * 2 * kHD * sizeof(float); }
+size_t qk_norm_part_bytes() { return qkn::kQkNormSms * 2 * kHD * sizeof(float); }
 
 namespace {
 template <int kHeads, int kCtas>
@@ -339,11 +343,12 @@ cudaError_t launch_qk_norm(const QkNormParams& p, int sms, cudaStream_t stream) 
 namespace {
 template <int kThreads, int kHeads, int kCtas>
 cudaError_t launch_backward(const QkNormParams& p, int sms, cudaStream_t stream) {
+  static_assert(kCtas == 1, "the workspace and the sums of dw have a place for one an SM");
   constexpr int kQuads = kThreads / qkn::kParts;
   const int H = p.H > p.Hkv ? p.H : p.Hkv;
   const long long units = static_cast<long long>(p.n_tot) * ((H + kHeads - 1) / kHeads);
   long long ctas = (units + kQuads - 1) / kQuads;
-  if (sms > kQkNormSms) sms = kQkNormSms;
+  if (sms > qkn::kQkNormSms) sms = qkn::kQkNormSms;
   if (ctas > kCtas * sms) ctas = kCtas * sms;
   return launch_pdl(ne_qk_norm_rope_bwd_kernel<kThreads, kHeads, kCtas>, dim3(static_cast<unsigned>(ctas)),
                     dim3(kThreads), 0, stream, p);
@@ -351,10 +356,11 @@ cudaError_t launch_backward(const QkNormParams& p, int sms, cudaStream_t stream)
 }  // namespace
 
 // A CTA of 512 threads an SM, two heads a quad: what is in flight is bounded by the
-// registers, 128 of each thread.  (65,536 rows of 40 heads, 18,641 and 8192 of 16: 184, 28.7
-// and 16.2 us; 384 threads and four heads, the table and weights read again for each, 181, 33.7
-// and 19.5; 384 threads with the next unit's rows on their way 199 for the first, and
-// through shared memory by asynchronous copies 203.)
+// registers, 128 of each thread.  (65,536 rows of 40 heads, 18,600 and 8192 of 16: 184, 28.5
+// and 16.7 us, before the two sums of dw shared a barrier; 384 threads and four heads, the
+// table and weights read again for each, 181, 33.7 and 19.5; 384 threads with the next unit's
+// rows on their way 199 for the first, through shared memory by asynchronous copies 203;
+// the next unit's rows fetched into L2, 194; two CTAs' work an SM, one after the other, 187.)
 cudaError_t launch_qk_norm_bwd(const QkNormParams& p, int sms, cudaStream_t stream) {
   return launch_backward<512, 2, 1>(p, sms, stream);
 }
