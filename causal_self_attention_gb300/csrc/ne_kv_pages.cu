@@ -16,14 +16,16 @@
 // of the rows and of the pages, finding a row's sequence by bisection.  What is
 // kept for the next step (lengths, the stack's height) may be updated in place:
 // the CTA that has read it last does that (one CTA: itself), so that no CTA reads
-// a new value for an old one.
+// a new value for an old one.  A page taken is entered into the block table by its first
+// row's thread.
 //
-// What bounds it is latency: launch, the lengths' loads, two exchanges of the sums, a
-// row's bisection in shared memory and its table entry.  Measured: 64 sequences, a row
-// each, 4.6 us; 4096 sequences with a million rows in all 12.4 us (the rows' 8 MB alone
-// 1.2 us): every CTA sums the 4096 lengths, and a thread's four rows take a bisection of 12
-// steps.  (Two CTAs an SM where they fit; the sums updated behind the rows' stores,
-// whose fence waits for them, 14.6 us.)
+// What bounds it is latency and, with thousands of sequences, every CTA's instructions for
+// their sums.  Measured: 64 sequences, a row each, 3.8 us (launch, the lengths, two barriers,
+// a bisection, a table entry); 4096 sequences with a million rows in all 10.6 us (the rows'
+// 8 MB alone 1.2 us); 16384 with a row each 21.8 us.  (Sequences in runs of a thread's own 4.7,
+// 12.8 and 46.6 us; two CTAs an SM 12 to 14% slower for the second; lengths updated behind the
+// rows' stores, whose fence waits for them, or all threads waiting for the arrival, 1 to 2 us
+// more.)
 #include "ne_paged.cuh"
 #include "ne_sm100.cuh"
 
@@ -34,20 +36,28 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowsPerThread = 4;
 
+constexpr int kMaxRounds = (kMaxPagedSequences + kThreads - 1) / kThreads;
+constexpr uint32_t kMany = 0x7fffffffu;  // sums stop here: more than any bound allows
+
 struct Shared {
-  uint32_t warp_rows[kWarps], warp_pages[kWarps];
-  int last;
+  uint2 sums[kMaxRounds][kWarps];  // a warp's rows and pages
+  int last, n_free;
 };
 
+__device__ __forceinline__ uint2 add(uint2 a, uint2 b) {
+  return make_uint2(min(a.x + b.x, kMany), min(a.y + b.y, kMany));
+}
 // Inclusive sums over the lanes.
-template <typename T>
-__device__ __forceinline__ T scan_warp(T v, int lane) {
+__device__ __forceinline__ uint2 scan_warp(uint2 v, int lane) {
 #pragma unroll
   for (int sh = 1; sh < 32; sh <<= 1) {
-    const T u = __shfl_up_sync(0xffffffffu, v, sh);
-    if (lane >= sh) v += u;
+    const uint2 u = make_uint2(__shfl_up_sync(0xffffffffu, v.x, sh), __shfl_up_sync(0xffffffffu, v.y, sh));
+    if (lane >= sh) v = add(v, u);
   }
   return v;
+}
+__device__ __forceinline__ uint2 from_lane(uint2 v, int lane) {
+  return make_uint2(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane));
 }
 
 // The last s with first[s] <= x (first[0] = 0, nondecreasing, first[n] > x).
@@ -61,67 +71,75 @@ __device__ __forceinline__ int find(const int* first, int n, int x) {
 }
 
 // Exclusive prefix sums of rows(s) and pages(s) over the sequences into shared
-// memory, [nseq + 1] each, and their totals (64 bits: the entries hold where the
-// totals fit).  one(s, rows, pages): what sequence s adds, at most 65535 * 128 rows, so that
-// a warp's 512 sequences fit 32 bits.  Every thread calls it, with neighbouring sequences of
-// its own: one exchange between the warps, however many there are.
-template <typename One>
+// memory, [nseq + 1] each, and their totals (at most kMany).  load(s): what is known of sequence
+// s, one(s, what, rows, pages): what it adds (at most 65535 * 128 rows).  Every thread calls
+// it.  A round is a sequence a thread, neighbours side by side (loads and shared memory
+// without conflicts: 16384 sequences in runs of 16 a thread took 46 us); the warps' sums of
+// all rounds are exchanged once.
+template <typename Load, typename One>
 __device__ __forceinline__ void prefix_sums(int nseq, int* row_at, int* page_at, Shared& sh,
-                                            long long& rows, long long& pages, One one) {
-  static_assert(kMaxPagedSequences <= 16 * kThreads, "32 bits for a warp's sums");
+                                            int& rows, int& pages, Load load, One one) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (nseq + kThreads - 1) / kThreads;
-  const int s0 = min(static_cast<int>(threadIdx.x) * per, nseq), s1 = min(s0 + per, nseq);
-  uint32_t m_sum = 0, t_sum = 0;
-#pragma unroll 4
-  for (int s = s0; s < s1; ++s) {
-    int m = 0, t = 0;
-    one(s, m, t);
-    row_at[s] = m;
-    page_at[s] = t;
-    m_sum += m;
-    t_sum += t;
-  }
-  const uint32_t a = scan_warp(m_sum, lane), b = scan_warp(t_sum, lane);
-  if (lane == 31) {
-    sh.warp_rows[warp] = a;
-    sh.warp_pages[warp] = b;
+  const int rounds = (nseq + kThreads - 1) / kThreads;
+  constexpr int kAhead = 4;  // rounds whose loads are on their way together
+  for (int r0 = 0; r0 < rounds; r0 += kAhead) {
+    int2 what[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = (r0 + i) * kThreads + threadIdx.x;
+      what[i] = s < nseq ? load(s) : make_int2(0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (r0 + i >= rounds) break;
+      const int s = (r0 + i) * kThreads + threadIdx.x;
+      int m = 0, t = 0;
+      if (s < nseq) one(s, what[i], m, t);
+      const uint2 sum = scan_warp(make_uint2(m, t), lane);
+      if (s < nseq) {
+        row_at[s] = static_cast<int>(sum.x) - m;
+        page_at[s] = static_cast<int>(sum.y) - t;
+      }
+      if (lane == 31) sh.sums[r0 + i][warp] = sum;
+    }
   }
   __syncthreads();
-  const long long wr = scan_warp(static_cast<long long>(sh.warp_rows[lane]), lane);
-  const long long wp = scan_warp(static_cast<long long>(sh.warp_pages[lane]), lane);
-  rows = __shfl_sync(0xffffffffu, wr, 31);
-  pages = __shfl_sync(0xffffffffu, wp, 31);
-  long long r = __shfl_sync(0xffffffffu, wr, max(warp - 1, 0)), p = __shfl_sync(0xffffffffu, wp, max(warp - 1, 0));
-  r = (warp ? r : 0) + a - m_sum;
-  p = (warp ? p : 0) + b - t_sum;
-  for (int s = s0; s < s1; ++s) {
-    const int m = row_at[s], t = page_at[s];
-    row_at[s] = static_cast<int>(r);
-    page_at[s] = static_cast<int>(p);
-    r += m;
-    p += t;
+  uint2 before = make_uint2(0u, 0u);  // the rounds before
+  for (int r = 0; r < rounds; ++r) {
+    const uint2 sum = scan_warp(sh.sums[r][lane], lane);
+    const uint2 left = from_lane(sum, max(warp - 1, 0));
+    const uint2 mine = add(before, warp ? left : make_uint2(0u, 0u));
+    const int s = r * kThreads + threadIdx.x;
+    if (s < nseq) {
+      row_at[s] = static_cast<int>(min(mine.x + row_at[s], kMany));
+      page_at[s] = static_cast<int>(min(mine.y + page_at[s], kMany));
+    }
+    before = add(before, from_lane(sum, 31));
   }
+  rows = static_cast<int>(before.x);
+  pages = static_cast<int>(before.y);
   if (threadIdx.x == 0) {
-    row_at[nseq] = static_cast<int>(rows);
-    page_at[nseq] = static_cast<int>(pages);
+    row_at[nseq] = rows;
+    page_at[nseq] = pages;
   }
   __syncthreads();
 }
 
-// Whether this CTA is the last of the launch to come here, with its reads of what is
-// updated in place behind it (and no store, which the fence would wait for).  Every
-// thread calls it.
-__device__ __forceinline__ bool last_to_read(int* arrived, Shared& sh) {
-  if (gridDim.x == 1) return true;
-  if (threadIdx.x == 0) {
+// A CTA's reads of what is updated in place are behind it (and it has stored nothing yet,
+// which the fence would wait for): thread 0 says so, and the others need not wait for it.
+__device__ __forceinline__ void has_read(int* arrived, Shared& sh) {
+  if (threadIdx.x != 0) return;
+  sh.last = 1;
+  if (gridDim.x == 1) return;
+  __threadfence();
+  sh.last = atomicAdd(arrived, 1) == static_cast<int>(gridDim.x) - 1;
+  if (sh.last) {
+    *arrived = 0;  // as the next launch wants it
     __threadfence();
-    sh.last = atomicAdd(arrived, 1) == static_cast<int>(gridDim.x) - 1;
-    if (sh.last) {
-      *arrived = 0;  // as the next launch wants it
-      __threadfence();
-    }
   }
+}
+// Whether this CTA was the launch's last to say so.  Every thread calls it.
+__device__ __forceinline__ bool last_to_read(const Shared& sh) {
   __syncthreads();
   return sh.last != 0;
 }
@@ -136,12 +154,13 @@ __global__ void __launch_bounds__(pages::kThreads) ne_kv_reserve_kernel(const Pa
   int* lens = page_at + p.nseq + 1;   // [nseq] positions that it holds
   pdl_wait();
   const int P1 = (1 << p.page_shift) - 1;
-  const int n_free = __ldcg(p.n_free);
+  if (threadIdx.x == 0) sh.n_free = __ldcg(p.n_free);  // (read for good before the sums' barrier)
   bool bad = false;
-  long long rows, taken;
-  prefix_sums(p.nseq, row_at, page_at, sh, rows, taken, [&](int s, int& m, int& t) {
-    const int n = __ldcg(p.seq_lens + s);
-    m = __ldg(p.new_lens + s);
+  int rows, taken;
+  auto load = [&](int s) { return make_int2(__ldcg(p.seq_lens + s), __ldg(p.new_lens + s)); };
+  prefix_sums(p.nseq, row_at, page_at, sh, rows, taken, load, [&](int s, int2 what, int& m, int& t) {
+    const int n = what.x;
+    m = what.y;
     lens[s] = n;
     if (n < 0 || m < 0 || n > p.max_seqlen || m > p.max_seqlen - n) {
       bad = true;
@@ -150,49 +169,53 @@ __global__ void __launch_bounds__(pages::kThreads) ne_kv_reserve_kernel(const Pa
     }
     t = ((n + m + P1) >> p.page_shift) - ((n + P1) >> p.page_shift);
   });
-  const bool updates = last_to_read(p.arrived, sh);
   bad = __syncthreads_or(bad) || rows > p.max_rows;
+  has_read(p.arrived, sh);
+  const int n_free = sh.n_free;
   const bool short_of = taken > n_free || n_free > p.n_pages || n_free < 0;
   const bool ok = !bad && !short_of;
   if (!ok && blockIdx.x == 0 && threadIdx.x == 0)
     atomicCAS(p.status, 0, bad ? NE_DEV_BAD_SEQLEN : NE_DEV_NO_PAGES);
 
   const int id = blockIdx.x * kThreads + threadIdx.x, all = gridDim.x * kThreads;
-  // The pages taken, into the block table.
-  if (ok)
-    for (int t = id; t < static_cast<int>(taken); t += all) {
+  // The pages taken, into the block table, where no row's thread does it.
+  if (ok && p.n_tot == 0)
+    for (int t = id; t < taken; t += all) {
       const int s = find(page_at, p.nseq, t);
       const int at = ((lens[s] + P1) >> p.page_shift) + t - page_at[s];
       p.block_table[static_cast<long long>(s) * p.max_pages + at] = __ldg(p.free_pages + n_free - 1 - t);
     }
-  // Positions and slots, neighbouring rows in a thread's hands (a page looked up once).
-  const int n_rows = ok ? static_cast<int>(rows) : 0;
+  // Positions and slots, neighbouring rows in a thread's hands; the first row of a new page
+  // enters it into the block table.
+  const int n_rows = ok ? rows : 0;
   const bool aligned = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15) == 0;
   for (int r0 = id * kRowsPerThread; r0 < p.n_tot; r0 += all * kRowsPerThread) {
     int s = r0 < n_rows ? find(row_at, p.nseq, r0) : 0;
-    int pos[kRowsPerThread], slot[kRowsPerThread], seen = -1, page = -1;
+    int pos[kRowsPerThread], slot[kRowsPerThread], page[kRowsPerThread];
+    int* enter[kRowsPerThread];
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {  // (all entries on their way before one is used)
+      const int r = r0 + i;
+      pos[i] = page[i] = -1;
+      enter[i] = nullptr;
+      if (r >= n_rows) continue;
+      while (row_at[s + 1] <= r) ++s;
+      const int n = lens[s], had = (n + P1) >> p.page_shift;
+      pos[i] = n + r - row_at[s];
+      const int at = pos[i] >> p.page_shift;
+      int* entry = p.block_table + static_cast<long long>(s) * p.max_pages + at;
+      page[i] = __ldcg(at < had ? entry : p.free_pages + n_free - 1 - (page_at[s] + at - had));
+      if (at >= had && (pos[i] & P1) == 0) enter[i] = entry;
+    }
+    bool outside = false;
 #pragma unroll
     for (int i = 0; i < kRowsPerThread; ++i) {
-      const int r = r0 + i;
-      pos[i] = slot[i] = -1;
-      if (r >= n_rows) continue;
-      while (row_at[s + 1] <= r) {
-        ++s;
-        seen = -1;
-      }
-      pos[i] = lens[s] + r - row_at[s];
-      const int at = pos[i] >> p.page_shift;
-      if (at != seen) {
-        const int had = (lens[s] + P1) >> p.page_shift;
-        page = at < had ? __ldcg(p.block_table + static_cast<long long>(s) * p.max_pages + at)
-                        : __ldg(p.free_pages + n_free - 1 - (page_at[s] + at - had));
-        seen = at;
-      }
-      if (page >= 0 && page < p.n_pages)
-        slot[i] = (page << p.page_shift) + (pos[i] & P1);
-      else
-        atomicCAS(p.status, 0, NE_DEV_BAD_PAGE);
+      if (enter[i]) *enter[i] = page[i];
+      const bool there = page[i] >= 0 && page[i] < p.n_pages;
+      slot[i] = there ? (page[i] << p.page_shift) + (pos[i] & P1) : -1;
+      outside |= !there && pos[i] >= 0;
     }
+    if (outside) atomicCAS(p.status, 0, NE_DEV_BAD_PAGE);
     if (aligned && r0 + kRowsPerThread <= p.n_tot) {
       if (p.positions) *reinterpret_cast<int4*>(p.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
       if (p.slots) *reinterpret_cast<int4*>(p.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
@@ -208,10 +231,10 @@ __global__ void __launch_bounds__(pages::kThreads) ne_kv_reserve_kernel(const Pa
     if (p.cu_seqlens) p.cu_seqlens[s] = ok ? row_at[s] : 0;
     if (p.start_pos && s < p.nseq) p.start_pos[s] = lens[s];
   }
-  if (!updates) return;
+  if (!last_to_read(sh)) return;
   for (int s = threadIdx.x; s < p.nseq; s += kThreads)
     p.seq_lens_out[s] = ok ? lens[s] + row_at[s + 1] - row_at[s] : lens[s];
-  if (threadIdx.x == 0) *p.n_free_out = ok ? n_free - static_cast<int>(taken) : n_free;
+  if (threadIdx.x == 0) *p.n_free_out = ok ? n_free - taken : n_free;
 }
 
 __global__ void __launch_bounds__(pages::kThreads) ne_kv_release_kernel(const PagesParams p) {
@@ -222,37 +245,39 @@ __global__ void __launch_bounds__(pages::kThreads) ne_kv_release_kernel(const Pa
   int* page_at = row_at + p.nseq + 1;  // [nseq + 1] first page given back by it
   pdl_wait();
   const int P1 = (1 << p.page_shift) - 1;
-  const int n_free = __ldcg(p.n_free);
+  if (threadIdx.x == 0) sh.n_free = __ldcg(p.n_free);  // (read for good before the sums' barrier)
   bool bad = false;
-  long long done, given;
-  prefix_sums(p.nseq, row_at, page_at, sh, done, given, [&](int s, int& m, int& t) {
-    m = __ldg(p.finished + s) != 0;
+  int done, given;
+  auto load = [&](int s) { return make_int2(__ldcg(p.seq_lens + s), __ldg(p.finished + s)); };
+  prefix_sums(p.nseq, row_at, page_at, sh, done, given, load, [&](int s, int2 what, int& m, int& t) {
+    const int n = what.x;
+    m = what.y != 0;
     if (!m) return;
-    const int n = __ldcg(p.seq_lens + s);
     if (n < 0 || n > p.max_seqlen) {
       bad = true;
       return;
     }
     t = (n + P1) >> p.page_shift;
   });
-  const bool updates = last_to_read(p.arrived, sh);
   bad = __syncthreads_or(bad);
+  has_read(p.arrived, sh);
+  const int n_free = sh.n_free;
   const bool over = n_free < 0 || n_free > p.n_pages || given > p.n_pages - n_free;
   const bool ok = !bad && !over;
   if (!ok && blockIdx.x == 0 && threadIdx.x == 0)
     atomicCAS(p.status, 0, bad ? NE_DEV_BAD_SEQLEN : NE_DEV_NO_PAGES);
   const int id = blockIdx.x * kThreads + threadIdx.x, all = gridDim.x * kThreads;
   if (ok)
-    for (int t = id; t < static_cast<int>(given); t += all) {
+    for (int t = id; t < given; t += all) {
       const int s = find(page_at, p.nseq, t);
       int* entry = p.block_table + static_cast<long long>(s) * p.max_pages + t - page_at[s];
       p.free_pages_out[n_free + t] = *entry;
       *entry = -1;
     }
-  if (!updates || !ok) return;
+  if (!last_to_read(sh) || !ok) return;
   for (int s = threadIdx.x; s < p.nseq; s += kThreads)
     if (row_at[s + 1] != row_at[s]) p.seq_lens_out[s] = 0;
-  if (threadIdx.x == 0) *p.n_free_out = n_free + static_cast<int>(given);
+  if (threadIdx.x == 0) *p.n_free_out = n_free + given;
 }
 
 namespace {
@@ -266,8 +291,7 @@ cudaError_t launch(void (*kernel)(const PagesParams), int arrays, long long work
   }
   long long ctas = (work + pages::kThreads * pages::kRowsPerThread - 1) /
                    (pages::kThreads * pages::kRowsPerThread);
-  const long long most = bytes <= 96 * 1024 ? 2LL * sms : sms;  // (resident at once)
-  ctas = ctas < 1 ? 1 : ctas > most ? most : ctas;
+  ctas = ctas < 1 ? 1 : ctas > sms ? sms : ctas;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(pages::kThreads), bytes, stream,
                     p);
 }

@@ -1,5 +1,6 @@
 """The calls of a generation step as they are marshalled in native code (the regular ones)
 and in Python (the others): the same results, the same refusals."""
+import gc
 import threading
 
 import numpy as np
@@ -273,6 +274,7 @@ def test_nothing_is_kept(na):
     a = _norm_args()
     na.ne_qk_norm_rope_fwd(*a)
     torch.cuda.synchronize()
+    gc.collect()  # (what other tests left)
     before = torch.cuda.memory_allocated()
     for _ in range(200):
         na.ne_qk_norm_rope_fwd(*a)
