@@ -23,10 +23,10 @@
 // A row's way is a chain of loads -- its sequence (two rounds of probes for 64
 // sequences), the position, the page, the row -- so that small calls are its
 // latency and large ones hide it under the other CTAs' rows.  Measured: a token
-// each for 64 sequences, 4 heads, 2.6 us; 32 prompts, 19,540 rows of 4 heads, to
-// e4m3 7.7 us (3.9 TB/s; the rows of the output stay in L2); 77,305 rows of 8
-// heads read from e4m3 38.3 us (6.2 TB/s, 92% of the copy rate); 69,524 rows of 12 heads
-// to e2m1 60.6 us, back 44.3 us.
+// each for 64 sequences, 4 heads, 2.4 us; 32 prompts, 19,540 rows of 4 heads, to
+// e4m3 6.9 us (4.3 TB/s; the rows of the output stay in L2); 77,305 rows of 8
+// heads read from e4m3 38.1 us (6.3 TB/s, 92% of the copy rate); 69,524 rows of 12 heads
+// to e2m1 55.3 us (4.9 TB/s), back 44.0 us (6.1 TB/s).
 #include "ne_attn_debug.h"
 #include "ne_paged.cuh"
 #include "ne_sm100.cuh"
@@ -34,7 +34,9 @@
 namespace ne {
 
 namespace kv {
-constexpr int kThreads = 256;
+// Small CTAs, whose loads and stores overlap others': 69,524 rows of 12 heads to e2m1 55.2 us of
+// 64 threads, 55.3 of 128, 60.6 of 256, back 43.8, 44.0, 44.3; 32 prompts to e4m3 6.8, 6.9, 7.6.
+constexpr int kThreads = 128;
 constexpr int kParts = 4;  // lanes per (row, head)
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
@@ -322,7 +324,8 @@ cudaError_t read(__nv_bfloat16* k, __nv_bfloat16* v, const int* cu, const int* s
 // Two heads a quad for rows with scales, once they fill the GPU: what finds a row's place is
 // half of the instructions of a (row, head) otherwise.  (69,524 rows of 12 heads, a head and
 // two: e2m1 written 70.2 and 60.6 us, read 51.8 and 44.3; e4m3 63.7 and 59.2, 53.6 and 51.4;
-// bf16, which only moves bytes, 67.3 and 65.5, 65.5 and 66.5.  Four: as two, or slower.)
+// bf16, which only moves bytes, 67.3 and 65.5, 65.5 and 66.5.  Four: as two, or slower.  CTAs
+// of 256 threads.)
 bool two_heads(int n_tot, int Hkv) {
   return Hkv % 2 == 0 && static_cast<long long>(n_tot) * Hkv >= 1 << 16;
 }

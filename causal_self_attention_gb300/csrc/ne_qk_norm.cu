@@ -14,8 +14,8 @@
 // 4, so that each rotation pair (i, i + 32) sits in one lane and the sums over
 // the head are two shuffles.  All arithmetic is fp32; each output is rounded
 // once (bf16; dw is fp32).
-// Measured, forward: 92,604 rows of 40 heads 152 us (6.2 TB/s, 92% of the copy rate),
-// 18,641 of 16 heads 14.0 us (5.5 TB/s), 64 of 16 heads 1.6 us (a launch); backward:
+// Measured, forward: 92,604 rows of 40 heads 145 us (6.5 TB/s, 96% of the copy rate),
+// 18,641 of 16 heads 13.3 us (5.7 TB/s), 64 of 16 heads 1.5 us (a launch); backward:
 // 65,536 rows of 40 heads 180 us (5.6 TB/s, 83%), 8192 of 16 heads 14.7 us (3.4 TB/s: two
 // rounds of loads that wait, the sums of dw, the CTA that adds them up).
 #include "ne_sm100.cuh"
@@ -79,7 +79,7 @@ __device__ __forceinline__ int position(const QkNormParams& p, int row) {
 }  // namespace qkn
 
 namespace qkn {
-constexpr int kFwdThreads = 256;
+constexpr int kFwdThreads = 64;
 constexpr int kFwdQuads = kFwdThreads / kParts;
 
 // The lane's chunks of w, 8 dims each, times r.
@@ -328,16 +328,18 @@ cudaError_t launch_forward(const QkNormParams& p, cudaStream_t stream) {
 }  // namespace
 
 // What a quad takes decides how many bytes are on their way: 80,000 rows of 40 heads take
-// 135 us by eight heads (6.1 TB/s), 163 by four, 169 by two, 187 by one (each with
-// the registers and CTAs that suit it best).  Few rows are spread wide instead, and eight
+// 135 us by eight heads, 161 by four, 188 by two, 187 by one (each with the registers and
+// CTAs that suit it best, 256 threads).  Few rows are spread wide instead, and eight
 // where they leave four slots or more empty are four: 8192 rows of 16 heads 7.5 us by
-// eight, 7.9 by four, 9.1 by one.
+// eight, 7.8 by four, 8.8 by one.  Small CTAs end and begin one by one, so that loads and
+// stores of different rows overlap: of 64 threads 129 us (6.4 TB/s), of 128 130, of 256
+// 135; 18,600 rows of 16 heads 17.0, 17.4, 18.2.
 cudaError_t launch_qk_norm(const QkNormParams& p, int sms, cudaStream_t stream) {
   const int heads = p.H + p.Hkv;
   const long long pairs = static_cast<long long>(p.n_tot) * heads;
-  if (pairs < 8LL * sms * qkn::kFwdQuads || heads < 4) return launch_forward<1, 4>(p, stream);
-  return (heads + 7) / 8 * 8 - heads < 4 ? launch_forward<8, 2>(p, stream)
-                                         : launch_forward<4, 2>(p, stream);
+  if (pairs < 512LL * sms || heads < 4) return launch_forward<1, 16>(p, stream);
+  return (heads + 7) / 8 * 8 - heads < 4 ? launch_forward<8, 8>(p, stream)
+                                         : launch_forward<4, 8>(p, stream);
 }
 
 namespace {
