@@ -57,7 +57,7 @@
 // e2m1: 64 sequences of 16k, 32 heads on 8, 109 us (5.0 TB/s, 74% of the copy rate; a
 // byte has four times the keys of bf16, and what bounds a tile is its arithmetic: the
 // integer pipe busy half of the time, issue slots 53%, three dependent warps a scheduler);
-// 64 ragged ones 30.6 us (2.8 TB/s), 777 keys 9.4 us, 64 of 2000 27.8 us.  Tried: four
+// 64 ragged ones 30.6 us (2.8 TB/s), 777 keys 8.9 us, 64 of 2000 27.8 us.  Tried: four
 // CTAs an SM with two stages (136, 40, 11 and 37 us: 96 registers spill), tiles of 32
 // keys a warp, warps that take tiles of their own without meeting (113, 33 us).
 //
@@ -127,6 +127,7 @@ struct Params {
   __nv_bfloat16* out;
   float* lse;
   int* status;
+  int least;     // tiles of a range, its units' overheads among them
   int drop_cta;  // kDrop: whose first tile is never loaded
 };
 
@@ -745,12 +746,12 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
       for (int i = tid; i < p.H * (kHD / 2); i += kThreads) o[i] = 0u;
       for (int i = tid; i < p.H; i += kThreads) p.lse[static_cast<long long>(b) * p.H + i] = -INFINITY;
     }
-  // Equal ranges, of two tiles of work at the least, and at most about kMaxParts
+  // Equal ranges, of p.least tiles of work at the least, and at most about kMaxParts
   // to a unit.
   const int total = prefix[B] * J;
   int W = static_cast<int>(gridDim.x);
   if (total / kMaxParts < W) W = min(W, max(1, prefix[kMaxBatch + 1] * J) * kMaxParts);
-  const int range = max((total + W - 1) / W, 2);
+  const int range = max((total + W - 1) / W, p.least);
   const int w = blockIdx.x;
   const int x0 = w * range, x1 = min(x0 + range, total);
   if (x0 >= total) return;
@@ -1424,14 +1425,27 @@ int paged_rows(int H, int Hkv) { return H / Hkv <= 8 ? 8 : 16; }
 // Launched CTAs: no more than the batch can have tiles.
 int paged_ctas(long long B, int H, int Hkv, int max_seqlen, Kv type, int sms) {
   const int rows = paged_rows(H, Hkv);
-  const int tile = type == Kv::kE2m1   ? Tile<Kv::kE2m1>::kTile
-                   : type == Kv::kE4m3 ? Tile<Kv::kE4m3>::kTile
-                                       : Tile<Kv::kBf16>::kTile;
   const long long units = B * Hkv * ((H / Hkv + rows - 1) / rows);
-  const long long tiles = units * ((max_seqlen + tile - 1) / tile);
+  auto of_tile = [&](int tile) { return (max_seqlen + tile - 1) / tile; };
+  // (e2m1: a range may be one tile of the flat order, overheads among them; never more than
+  // bf16's, which the workspace is sized for.)
+  const int each = type == Kv::kE2m1 ? std::min(of_tile(Tile<Kv::kE2m1>::kTile) + Tile<Kv::kE2m1>::kOverhead,
+                                                of_tile(Tile<Kv::kBf16>::kTile))
+                                     : of_tile(type == Kv::kE4m3 ? Tile<Kv::kE4m3>::kTile : Tile<Kv::kBf16>::kTile);
+  const long long tiles = units * each;
   const long long full =
       static_cast<long long>(rows == 8 ? Cfg<Kv::kBf16, 8>::kCtas : Cfg<Kv::kBf16, 16>::kCtas) * sms;
   return static_cast<int>(tiles < full ? tiles : full);
+}
+
+// The tiles of a range at the least.  e2m1, whose tiles take 1 us: units of three tiles or
+// fewer whole (a join costs 2 us: 4 sequences of 500, 7.4 us whole, 9.1 by single tiles),
+// others of up to 18 by single tiles (one sequence of 1000 8.8 us, by two 9.7; 4000 9.4 and
+// 10.2), longer ones not (8000 10.5 by two, 10.9 by single tiles; 12000 10.9 and 13.0).
+int paged_least(int max_seqlen, Kv type) {
+  if (type != Kv::kE2m1) return 2;
+  const int each = (max_seqlen + Tile<Kv::kE2m1>::kTile - 1) / Tile<Kv::kE2m1>::kTile;
+  return each <= 3 ? each + Tile<Kv::kE2m1>::kOverhead : each <= 18 ? 1 : 2;
 }
 
 template <Kv kType, int kRows, bool kDrop = false>
@@ -1492,6 +1506,7 @@ cudaError_t launch_decode_paged(const CUtensorMap& tmK, const CUtensorMap& tmV,
   p.part = part;
   p.arrived = arrived;
   p.status = status;
+  p.least = paged_least(pc.max_seqlen, type);
   p.drop_cta = drop_cta;
   if (drop_cta >= 0 && (type != Kv::kBf16 || rows != 8)) return cudaErrorInvalidValue;
   const int batch = paged_batch(H, pc.Hkv, pc.max_seqlen);
