@@ -91,7 +91,8 @@ class Call {
   const Tensor* dense(PyObject* o, at::ScalarType type) {
     if (!THPVariable_CheckExact(o)) return nullptr;
     const Tensor& t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || t.layout() != at::kStrided || t.scalar_type() != type) return nullptr;
+    if (!t.is_cuda() || t.layout() != at::kStrided || t.scalar_type() != type || !t.has_storage())
+      return nullptr;  // (a tensor that stands for others has no storage)
     if (dev_ < 0) dev_ = t.get_device();
     return t.get_device() == dev_ ? &t : nullptr;
   }
@@ -130,14 +131,15 @@ PyObject* result(ne_status rc, std::initializer_list<Tensor> out) {
   return all;
 }
 
-// Calls the library without the interpreter's lock, as ctypes does.
+// Calls the library without the interpreter's lock, as ctypes does (and has it again
+// whichever way the call ends).
 template <typename F>
 ne_status unlocked(F f) {
-  ne_status rc;
-  Py_BEGIN_ALLOW_THREADS
-  rc = f();
-  Py_END_ALLOW_THREADS
-  return rc;
+  struct Lock {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Lock() { PyEval_RestoreThread(state); }
+  } lock;
+  return f();
 }
 
 // What the norms' two directions share.

@@ -168,6 +168,31 @@ def test_a_page_outside_the_pool(na):
     assert na.ne_attn_get_device_status() == 9 and slots.tolist() == [-1] * 5
 
 
+@pytest.mark.parametrize("left", ["cu_seqlens", "start_pos", "positions", "slots", "both", "all"])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_outputs_that_are_not_wanted(na, left, shift):
+    """The C entry with NULL for some of the outputs, and outputs that are 4-byte aligned."""
+    lens, new = [0, 30, 5], [40, 3, 0]
+    plain = step.Pages(3, 6, 18, 16, range(18))
+    gpu = Gpu(plain)
+    gpu.reserve(na, lens, 35)
+    plain.reserve(lens, 35)
+    want = plain.reserve(new, 50)
+    room = [torch.full((n + shift,), -9, dtype=torch.int32, device="cuda")[shift:] for n in (4, 3, 50, 50)]
+    names = ("cu_seqlens", "start_pos", "positions", "slots")
+    none = {"both": names[2:], "all": names}.get(left, (left,))
+    out = [None if n in none else t.data_ptr() for n, t in zip(names, room)]
+    more = _i32(new)
+    rc = na.lib().ne_kv_reserve(
+        more.data_ptr(), gpu.lens.data_ptr(), 3, gpu.table.data_ptr(), 6, gpu.free.data_ptr(),
+        gpu.n_free.data_ptr(), 18, 16, 96, 50, *out, gpu.lens.data_ptr(), gpu.n_free.data_ptr(),
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and na.ne_attn_get_device_status() == 0
+    for n, t, w in zip(names, room, want):
+        assert t.tolist() == ([-9] * t.numel() if n in none else w), n
+    gpu.check()
+
+
 def test_slots_up_to_31_bits(na):
     """The largest pool: its last pages' slots, and rows of a long sequence of them."""
     n_pages = (2 ** 31 - 1) // 256

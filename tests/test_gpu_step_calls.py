@@ -250,6 +250,16 @@ def test_the_other_way_takes_what_it_took(na, spy):
     assert spy.seen[-1][1] is not None and not got[0].requires_grad and _same(got, want)
 
 
+def test_tensors_that_stand_for_others(na, spy):
+    """In a transform a tensor has no memory of its own: an error, as it was."""
+    a = _norm_args()
+    many = torch.stack([a[0], a[0]])
+    with pytest.raises(RuntimeError):
+        torch.vmap(lambda q: na.ne_qk_norm_rope_fwd(q, *a[1:]))(many)
+    assert spy.seen == [("norm_fwd", None)]
+    assert na.ne_qk_norm_rope_fwd(*a)[0].shape == a[0].shape
+
+
 def test_current_stream_and_threads(na):
     """The stream that is current where the call is made, in any thread."""
     a = _norm_args()
