@@ -458,12 +458,16 @@ struct FourBit {
         t = column_max(t) - kHeadroom;
         const float old = m2[nt][e][h];
         float now = fmaxf(t, old);
+        bool empty = false;
         if (first) {
           size = column_max(size);
-          now = fmaxf(t, size > 0.f ? old + __log2f(size) : kNone);
+          empty = size == 0.f;
+          now = fmaxf(t, empty ? kNone : old + __log2f(size));
         }
         m2[nt][e][h] = now;
-        const float part = ex2_approx(0.5f * (old - now));  // (2^(old - now) may leave fp32's range)
+        // (2^(old - now) may leave fp32's range; zero is zero under any reference, also under
+        // one so far below that the factor is infinite.)
+        const float part = empty ? 1.f : ex2_approx(0.5f * (old - now));
 #pragma unroll
         for (int i = 2 * h; i < 2 * h + 2; ++i) {
           o[nt][i][e] = o[nt][i][e] * part * part;
