@@ -225,12 +225,12 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -265,9 +265,11 @@ __device__ __forceinline__ int e2m1_key(int mt, int x) {
 
 // The state of a warp's softmax over 4-bit rows, and a tile of 64 keys, two a lane.
 //
-// Scores: the products with the two halves of a key's row, each with its scale: x =
-// s0 a0 + s1 a1, f x in log2 units.  Weights p = 2^(f x - m), in halves, with a reference
-// m that was kHeadroom below the largest score when it was set; for a value row's half h
+// Scores: the products with the two halves of a key's row, each with its scale: x = f (s0
+// a0 + s1 a1), in log2 units.  The scales are taken 2^-10 down and f 2^10 up: |a| <= 2^9, so
+// that no sum overflows before f, however large the keys and small the query.  (f from 2^117
+// on: the query's halves are 2^10 up instead.)  Weights p = 2^(x - m), in halves, with a
+// reference m that was kHeadroom below the largest score when it was set; for a value row's half h
 // they take its scale, p 2^(e_h - E_h), E_h an exponent that the warp keeps, so that a
 // weight is formed once and scaled by a product of two halves.  E_h - e_h is 0 .. 7 for
 // every row that the warp has seen.  What halves cost is their smallest step, two
@@ -283,7 +285,9 @@ __device__ __forceinline__ int e2m1_key(int mt, int x) {
 // so that choices are made by masks and pairs of bytes are looked at together.
 template <int kNT>
 struct FourBit {
-  static constexpr float kNone = -1e30f;  // no score yet: a finite one exceeds it by any measure
+  static constexpr float kNone = -3.402823466e38f;  // no score yet: the lowest number
+  static constexpr float kScoreUp = 1024.f;         // what f has more, and the scales less
+  static constexpr float kLargeF = 1.6615349947311448e35f;  // 2^117
   static constexpr int kMT = 4;           // row tiles of 16 keys
   static constexpr int kRange = 7;
   static constexpr float kHeadroom = 8.f;  // weights of 2^15 at most: within a half
@@ -324,14 +328,14 @@ struct FourBit {
   }
   // The references as the segment's end wants them.
   __device__ __forceinline__ float ref(int nt, int e) const {
-    return m[nt][e] > 0.5f * kNone ? m[nt][e] : -INFINITY;
+    return m[nt][e] > kNone ? m[nt][e] : -INFINITY;
   }
   __device__ __forceinline__ float of_o(int nt, int e, int h) const {
     return slow ? m2[nt][e][h] : m[nt][e] + static_cast<float>(eb(h) - 127);
   }
   __device__ __forceinline__ float ref2(int nt, int e, int h) const {
     const float x = of_o(nt, e, h);
-    return x > 0.5f * kNone ? x : -INFINITY;
+    return x > kNone ? x : -INFINITY;
   }
 
   // Where the keys of a lane, j and j + 32, stand: rows r of tiles t = 2 mt + hf and t + 4
@@ -369,8 +373,7 @@ struct FourBit {
 
   // Moves the references to what this tile holds (vb: the scale bytes of this lane's value
   // rows, -1 for none).  Returns whether the mode changed.
-  __device__ __forceinline__ bool move(const float (&x)[kMT][kNT][4], const float (&f)[kNT][2],
-                                       const int (&vb)[2][2]) {
+  __device__ __forceinline__ bool move(const float (&x)[kMT][kNT][4], const int (&vb)[2][2]) {
     bool turned = false;
     if (!slow) {
       int hi[2];
@@ -419,7 +422,9 @@ struct FourBit {
         float a = -INFINITY;
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt) a = fmaxf(a, fmaxf(x[mt][nt][e], x[mt][nt][2 + e]));
-        a = column_max(a) * f[nt][e] - kHeadroom;
+        const float top = column_max(a);
+        a = top - kHeadroom;
+        if (top - a > 15.f) a = top;  // (steps of 16 there: weights stay within a half)
         if (a > m[nt][e]) {
           const float up = ex2_approx(m[nt][e] - a);
           m[nt][e] = a;
@@ -440,7 +445,6 @@ struct FourBit {
   // first: the mode's first tile, where a reference may be far above o's size (exponents of
   // rows without weight made it): there it comes down to that size.
   __device__ __forceinline__ void far_references(const float (&x)[kMT][kNT][4],
-                                                 const float (&f)[kNT][2],
                                                  const float (&ev)[kMT][2], int h, bool first) {
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt)
@@ -451,7 +455,7 @@ struct FourBit {
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
-            t = fmaxf(t, __fmaf_rn(x[mt][nt][2 * hf + e], f[nt][e], ev[mt][hf]));
+            t = fmaxf(t, x[mt][nt][2 * hf + e] + ev[mt][hf]);
 #pragma unroll
         for (int i = 2 * h; i < 2 * h + 2; ++i)
           size = fmaxf(size, fmaxf(fabsf(o[nt][i][e]), fabsf(o[nt][i][2 + e])));
@@ -519,7 +523,8 @@ struct FourBit {
       const uint32_t kb = ks[lane + 32 * i];
       bytes[i] = vs[lane + 32 * i];
       reinterpret_cast<float2*>(scratch)[at.k + 4 * i] =
-          make_float2(kv::scale_value(kb & 255u), kv::scale_value(kb >> 8));
+          make_float2(kv::scale_value(kb & 255u) * (1.f / kScoreUp),
+                      kv::scale_value(kb >> 8) * (1.f / kScoreUp));
       const uint32_t u = __byte_perm(bytes[i], 0u, 0x4140) - base;
       static_assert(kRange == 7, "three bits, and 2^-7 as a half: 8 << 10");
       longer |= (u & 0xfff8fff8u) != 0u;
@@ -551,8 +556,14 @@ struct FourBit {
           mma16816<true>(a[1], hi, qb[nt][2 + k][0], qb[nt][2 + k][1]);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[mt][nt][e] = __fmaf_rn(a[1][e], e < 2 ? s.y : s.w, a[0][e] * (e < 2 ? s.x : s.z));
+        for (int hf = 0; hf < 2; ++hf) {
+          const float s0 = hf ? s.z : s.x, s1 = hf ? s.w : s.y;
+          const float2 sum = make_float2(__fmaf_rn(a[1][2 * hf], s1, a[0][2 * hf] * s0),
+                                         __fmaf_rn(a[1][2 * hf + 1], s1, a[0][2 * hf + 1] * s0));
+          const float2 score = mul2(sum, make_float2(f[nt][0], f[nt][1]));
+          x[mt][nt][2 * hf] = score.x;
+          x[mt][nt][2 * hf + 1] = score.y;
+        }
       }
     }
     uint32_t w[kMT][kNT][2];
@@ -567,8 +578,8 @@ struct FourBit {
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const float2 y = fma2(make_float2(x[mt][nt][2 * hf], x[mt][nt][2 * hf + 1]),
-                                  make_float2(f[nt][0], f[nt][1]), make_float2(-m[nt][0], -m[nt][1]));
+            const float2 y = add2(make_float2(x[mt][nt][2 * hf], x[mt][nt][2 * hf + 1]),
+                                  make_float2(-m[nt][0], -m[nt][1]));
             const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
             sum[nt] = add2(sum[nt], p);
             w[mt][nt][hf] = pack_f16x2(p.x, p.y);
@@ -594,10 +605,10 @@ struct FourBit {
         vb[i][0] = mine ? static_cast<int>(bytes[i] & 255u) : -1;
         vb[i][1] = mine ? static_cast<int>(bytes[i] >> 8) : -1;
       }
-      const bool first = move(x, f, vb);
+      const bool first = move(x, vb);
       weigh();
       if (slow) {
-        far_values(x, f, sv, vs, live, first, r, c);
+        far_values(x, sv, vs, live, first, r, c);
         add_sums(sum);
         return;
       }
@@ -634,9 +645,8 @@ struct FourBit {
     }
   }
 
-  __device__ __forceinline__ void far_values(const float (&x)[kMT][kNT][4], const float (&f)[kNT][2],
-                                             const uint8_t* sv, const uint16_t* vs, int live,
-                                             bool first, int r, int c) {
+  __device__ __forceinline__ void far_values(const float (&x)[kMT][kNT][4], const uint8_t* sv,
+                                             const uint16_t* vs, int live, bool first, int r, int c) {
     float ev[2][kMT][2];
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt)
@@ -649,7 +659,7 @@ struct FourBit {
           ev[h][mt][hf] = key >= live ? 0.f : byte == 255 ? NAN : static_cast<float>(byte - 127);
         }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) far_references(x, f, ev[h], h, first);
+    for (int h = 0; h < 2; ++h) far_references(x, ev[h], h, first);
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
       uint32_t b[2][kNT][2];
@@ -660,8 +670,8 @@ struct FourBit {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
             b[h][nt][hf] = transpose8x8(pack_f16x2(
-                ex2_approx(__fmaf_rn(x[mt][nt][2 * hf], f[nt][0], ev[h][mt][hf]) - m2[nt][0][h]),
-                ex2_approx(__fmaf_rn(x[mt][nt][2 * hf + 1], f[nt][1], ev[h][mt][hf]) - m2[nt][1][h])));
+                ex2_approx(x[mt][nt][2 * hf] + ev[h][mt][hf] - m2[nt][0][h]),
+                ex2_approx(x[mt][nt][2 * hf + 1] + ev[h][mt][hf] - m2[nt][1][h])));
       add_values(sv, mt, r, c, b);
     }
   }
@@ -973,16 +983,17 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 2^-e with 2^e <= top < 2^(e+1): |q' 2^-e| < 2.  (0 and what is not
         // finite or normal keep 1.)
-        const uint32_t eb = (__float_as_uint(top) >> 23) & 255u;
+        uint32_t eb = (__float_as_uint(top) >> 23) & 255u;
+        if (kE2m1 && eb != 255u) eb = min(max(eb, 1u), 253u);  // (all finite ones: |q' 2^-e| < 4)
         const bool plain = eb >= 1u && eb <= 253u;
-        const float down = plain ? __uint_as_float((254u - eb) << 23) : 1.f;
-        const float up = p.scale_log2 * (plain ? __uint_as_float(eb << 23) : 1.f);  // of head r
+        float down = plain ? __uint_as_float((254u - eb) << 23) : 1.f;
+        float up = p.scale_log2 * (plain ? __uint_as_float(eb << 23) : 1.f);  // of head r
+        if (kE2m1) {  // as FourBit wants it
+          if (up >= FourBit<kNT>::kLargeF) down *= FourBit<kNT>::kScoreUp;
+          else up *= FourBit<kNT>::kScoreUp;
+        }
         f[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
         f[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
-        if (kE2m1) {  // (positive: FourBit multiplies scores of -inf by it)
-          f[nt][0] = fmaxf(f[nt][0], 1.17549435e-38f);
-          f[nt][1] = fmaxf(f[nt][1], 1.17549435e-38f);
-        }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll

@@ -1,10 +1,12 @@
 """Decode attention over the 4-bit cache at the ends of the range: sums that are zero when
-the references move, against the plain 64-bit implementation of grouped.py."""
+the references move, large keys beside small queries, scores of any size, against the
+plain 64-bit implementation of grouped.py."""
 import pytest
 import torch
 
+from grouped import F64, U16, U32, within
 from step import Cache4
-from test_gpu_paged import _decode, _i32
+from test_gpu_paged import _decode, _i32, _randn
 from test_gpu_paged4 import _check_sequence
 
 pytestmark = pytest.mark.gpu
@@ -70,3 +72,44 @@ def test_zero_rows_before_scales_far_apart(na, H, halves, n, zeros):
     for h in halves:
         assert bool((out[:, 32 * h:32 * h + 32] == 0).all())
     r.check(na, q)
+
+
+@pytest.mark.parametrize("H", [4, 13])
+@pytest.mark.parametrize("q_exp,lo,hi", [
+    (-118, 245, 252), (-126, 250, 252),  # large keys: the sums before the query's factor pass 2^128
+    (-133, 250, 252),                    # a query below the smallest normal number
+    (100, 27, 33), (118, 1, 8), (125, 0, 4), (126, 0, 2)])  # and the other way round
+def test_keys_and_queries_of_far_apart_sizes(na, H, q_exp, lo, hi):
+    n = 700
+    r, i = Rows(n, Hkv=1), torch.arange(n)
+    for h in (0, 1):
+        r.what("k", i, None, lo + (i + h) % (hi - lo + 1), h)
+    q = (_randn(3, 1, H, 64).double().clamp(-1.9, 1.9) * 2.0 ** q_exp).bfloat16()
+    assert bool((q != 0).any()) and bool(torch.isfinite(q).all())
+    r.check(na, q)
+
+
+def _winner(na, n, H, k, sign, v_byte, at, spread=0):
+    """Scores of 15 * 2^k: sign times that for the key `at`, which has all the weight, and
+    -2 (sign > 0: -1) times that for the others.  What comes out is its value row."""
+    r = Rows(n)
+    half = k // 2
+    q = _ones(H, 1.25 * 2.0 ** half)           # 64 * 1.25 * 1.5 / 8 = 15
+    r.what("k", range(n), 0xbb, 127 + k - half + (sign < 0))
+    r.what("k", [at], 0x33 if sign > 0 else 0xbb, 127 + k - half)
+    i = torch.arange(n)
+    r.what("v", i, None, v_byte + spread * (i % 2))
+    out, lse = r.decode(na, q)
+    v = r.c.rows(0)[1][at].expand(H, 64)
+    # The weight in a half, its sum in fp32 (and the powers of two, 2^-22 each); bf16.
+    within(out, v, v.abs() * (U16 + 2.0 ** -11 + 16 * U32), "out")
+    score = torch.full((H,), sign * 15 * 2.0 ** k, dtype=F64, device="cuda")
+    within(lse, score, score.abs() * 72 * U32 + 16 * U32, "lse")
+
+
+@pytest.mark.parametrize("n,at", [(1, 0), (100, 77), (700, 3), (700, 699)])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("H", [4, 13])
+def test_scores_of_any_size(na, n, at, sign, H):
+    for k in (*range(4, 40), 60, 90, 97, 100, 110, 118):
+        _winner(na, n, H, k, sign, 127, at)
