@@ -101,7 +101,7 @@ struct Cfg {
   static constexpr int kCtas = kRows == 8 ? 3 : 2;      // per SM
   static constexpr int kStages = kRows == 8 ? 3 : 4;
   static constexpr int OFF_RED = kStages * Tile<kType>::kStageBytes;
-  // m, l, m2, bad, o[64]; e2m1: the other half's m2
+  // m, l, m2, bad, o[64]; e2m1: m2 above m, behind o the other half's
   static constexpr int kRedRow = kHD + (kType == Kv::kE2m1 ? 8 : 4);
   static constexpr int kScratch = kType == Kv::kE2m1 ? 768 : 0;  // of a warp: FourBit's
   static constexpr int OFF_SCRATCH = OFF_RED + kWarps * kRows * kRedRow * 4;
@@ -279,7 +279,8 @@ __device__ __forceinline__ int e2m1_key(int mt, int x) {
 // sequence ends in the tile -- one vote tells --, the tile takes a longer way, on which the
 // references move.  Rows whose scales differ by more (never mind zeros) put the warp into
 // another mode for the rest of the segment: a reference of its own for every (query head,
-// half), 2^(f x + e_h - m2), which loses nothing however far the scales are apart.
+// half), 2^(x - m + e_h - m2), which loses nothing however far the scales are apart.  (Taken
+// from m on: beside a score of 2^24 an exponent would be lost.)
 //
 // What bounds a tile is the integer pipe: 128 of its conversions take two cycles each,
 // so that choices are made by masks and pairs of bytes are looked at together.
@@ -300,7 +301,7 @@ struct FourBit {
   uint32_t base;                          // E_h + 127 - kRange, as one word's halves
   uint32_t lowest;                        // smallest scale bytes of this lane's rows, 16 bits each
   bool slow;
-  float m2[kNT][2][2];                    // slow: o's references
+  float m2[kNT][2][2];                    // slow: o's references, above m
 
   __device__ __forceinline__ void begin() {
     slow = false;
@@ -310,8 +311,8 @@ struct FourBit {
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[nt][e] = m2[nt][e][0] = m2[nt][e][1] = kNone;
-        l[nt][e] = 0.f;
+        m[nt][e] = kNone;
+        m2[nt][e][0] = m2[nt][e][1] = l[nt][e] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -330,12 +331,8 @@ struct FourBit {
   __device__ __forceinline__ float ref(int nt, int e) const {
     return m[nt][e] > kNone ? m[nt][e] : -INFINITY;
   }
-  __device__ __forceinline__ float of_o(int nt, int e, int h) const {
-    return slow ? m2[nt][e][h] : m[nt][e] + static_cast<float>(eb(h) - 127);
-  }
-  __device__ __forceinline__ float ref2(int nt, int e, int h) const {
-    const float x = of_o(nt, e, h);
-    return x > kNone ? x : -INFINITY;
+  __device__ __forceinline__ float above(int nt, int e, int h) const {  // o's, above m
+    return slow ? m2[nt][e][h] : static_cast<float>(eb(h) - 127);
   }
 
   // Where the keys of a lane, j and j + 32, stand: rows r of tiles t = 2 mt + hf and t + 4
@@ -393,13 +390,13 @@ struct FourBit {
         low[h] = static_cast<uint32_t>(least);
       }
       lowest = low[0] | low[1] << 16;
-      if (turned) {  // o stays as it is, under the references that it has
+      if (turned) {  // o stays as it is, under the reference that it has
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) m2[nt][e][h] = of_o(nt, e, h);
+            for (int h = 0; h < 2; ++h) m2[nt][e][h] = above(nt, e, h);
         slow = true;
       } else {
 #pragma unroll
@@ -426,10 +423,13 @@ struct FourBit {
         a = top - kHeadroom;
         if (top - a > 15.f) a = top;  // (steps of 16 there: weights stay within a half)
         if (a > m[nt][e]) {
-          const float up = ex2_approx(m[nt][e] - a);
+          const float by = m[nt][e] - a, up = ex2_approx(by);
           m[nt][e] = a;
           l[nt][e] *= up;
-          if (!slow) {
+          if (slow) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) m2[nt][e][h] = fmaxf(m2[nt][e][h] + by, kNone);
+          } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               o[nt][i][e] *= up;
@@ -455,7 +455,7 @@ struct FourBit {
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
-            t = fmaxf(t, x[mt][nt][2 * hf + e] + ev[mt][hf]);
+            t = fmaxf(t, x[mt][nt][2 * hf + e] - m[nt][e] + ev[mt][hf]);
 #pragma unroll
         for (int i = 2 * h; i < 2 * h + 2; ++i)
           size = fmaxf(size, fmaxf(fabsf(o[nt][i][e]), fabsf(o[nt][i][2 + e])));
@@ -670,8 +670,8 @@ struct FourBit {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
             b[h][nt][hf] = transpose8x8(pack_f16x2(
-                ex2_approx(x[mt][nt][2 * hf] + ev[h][mt][hf] - m2[nt][0][h]),
-                ex2_approx(x[mt][nt][2 * hf + 1] + ev[h][mt][hf] - m2[nt][1][h])));
+                ex2_approx(x[mt][nt][2 * hf] - m[nt][0] + ev[h][mt][hf] - m2[nt][0][h]),
+                ex2_approx(x[mt][nt][2 * hf + 1] - m[nt][1] + ev[h][mt][hf] - m2[nt][1][h])));
       add_values(sv, mt, r, c, b);
     }
   }
@@ -1262,9 +1262,9 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
         if (r == 0) {
           dst[0] = kE2m1 ? four.ref(nt, e) : m[nt][e];
           dst[1] = sum;
-          dst[2] = kE2m1 ? four.ref2(nt, e, 0) : kE4m3 ? m2[nt][e] : m[nt][e];
+          dst[2] = kE2m1 ? four.above(nt, e, 0) : kE4m3 ? m2[nt][e] : m[nt][e];
           dst[3] = bad ? 1.f : 0.f;
-          if (kE2m1) dst[4 + kHD] = four.ref2(nt, e, 1);
+          if (kE2m1) dst[4 + kHD] = four.above(nt, e, 1);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -1298,9 +1298,10 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
 #pragma unroll
       for (int v = 0; v < kWarps; ++v) {
         const float* src = red + (v * kRows + row) * L::kRedRow;
-        if (src[2] == -INFINITY && src[0] == -INFINITY && src[1] == 0.f) continue;  // no keys
+        if ((kE2m1 || src[2] == -INFINITY) && src[0] == -INFINITY && src[1] == 0.f) continue;  // no keys
         sum += src[1] * ex2_approx(src[0] - ref);
-        const float wt = ex2_approx(src[kE2m1 && d0 >= kHD / 2 ? 4 + kHD : 2] - ref);
+        const float wt = kE2m1 ? ex2_approx(src[0] - ref + src[d0 < kHD / 2 ? 2 : 4 + kHD])
+                               : ex2_approx(src[2] - ref);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] += src[4 + d0 + e] * wt;
       }

@@ -113,3 +113,13 @@ def _winner(na, n, H, k, sign, v_byte, at, spread=0):
 def test_scores_of_any_size(na, n, at, sign, H):
     for k in (*range(4, 40), 60, 90, 97, 100, 110, 118):
         _winner(na, n, H, k, sign, 127, at)
+
+
+@pytest.mark.parametrize("n,at", [(1, 0), (100, 76), (100, 77), (700, 3), (700, 698)])
+@pytest.mark.parametrize("v_byte,spread", [(122, 0), (130, 0), (110, 40), (116, 9)])
+@pytest.mark.parametrize("H", [4, 13])
+def test_exponents_of_values_beside_scores_of_any_size(na, n, at, v_byte, spread, H):
+    """The value rows' scales, alike or far apart (both modes)."""
+    for k in (4, 10, *range(18, 34), 60, 110):
+        for sign in (1, -1):
+            _winner(na, n, H, k, sign, v_byte, at, spread)
