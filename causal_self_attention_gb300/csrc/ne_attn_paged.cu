@@ -76,6 +76,7 @@ constexpr int kWarps = 4;                      // consumers
 constexpr int kThreads = (kWarps + 1) * 32;    // and the loading warp
 constexpr int kMaxBatch = 512;                 // sequences per launch (prefix sums in shared memory)
 constexpr int kMaxParts = 96;                  // parts of one (sequence, head), about
+constexpr int kMaxJoin = 512;                  // more than CTAs can have a part of one
 constexpr int kPartRow = 68;                   // floats: lse (log2 units), 3 pad, o[64]
 constexpr float kBad = INFINITY;               // lse of a part that met a page outside the pool
 constexpr int kQRow = 144;                     // bytes of a q row in shared memory (banks)
@@ -1295,18 +1296,34 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
       }
       const float ref = M == -INFINITY ? 0.f : M;
       float sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      auto no_keys = [](const float* src) {
+        return (kE2m1 || src[2] == -INFINITY) && src[0] == -INFINITY && src[1] == 0.f;
+      };
 #pragma unroll
       for (int v = 0; v < kWarps; ++v) {
         const float* src = red + (v * kRows + row) * L::kRedRow;
-        if ((kE2m1 || src[2] == -INFINITY) && src[0] == -INFINITY && src[1] == 0.f) continue;  // no keys
-        sum += src[1] * ex2_approx(src[0] - ref);
-        const float wt = kE2m1 ? ex2_approx(src[0] - ref + src[d0 < kHD / 2 ? 2 : 4 + kHD])
+        if (!no_keys(src)) sum += src[1] * ex2_approx(src[0] - ref);
+      }
+      const float lse2 = any_bad ? kBad : ref + __log2f(sum);
+      // e2m1: the weights' size, 2^8 and more of a half's headroom, leaves before the values'
+      // scales come in, which may be 2^125: the sum's power of two, exact.
+      float down = 0.f, inv = 1.f / sum;
+      if constexpr (kE2m1) {
+        const uint32_t bits = __float_as_uint(sum), eb = bits >> 23;  // (sum >= 0, or NaN)
+        if (eb - 1u < 254u) {
+          down = static_cast<float>(static_cast<int>(eb) - 126);
+          inv = 1.f / __uint_as_float((bits & 0x7fffffu) | 126u << 23);
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        const float* src = red + (v * kRows + row) * L::kRedRow;
+        if (no_keys(src)) continue;
+        const float wt = kE2m1 ? ex2_approx(src[0] - ref + (src[d0 < kHD / 2 ? 2 : 4 + kHD] - down))
                                : ex2_approx(src[2] - ref);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] += src[4 + d0 + e] * wt;
       }
-      float inv = 1.f / sum;
-      const float lse2 = any_bad ? kBad : ref + __log2f(sum);
       if (whole) {
         const long long oh = static_cast<long long>(s.b) * p.H + h0 + row;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -1355,6 +1372,8 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
       return p.part + (static_cast<long long>(w_first + i) * 2 + (i == 0 ? 1 : 0)) * kRows * kPartRow +
              min(row, rows - 1) * kPartRow;
     };
+    // e2m1: a sum of up to kMaxJoin rows of values that may fill fp32's range, scaled for it.
+    constexpr float kJoin = kE2m1 ? 1.f / kMaxJoin : 1.f;
     float ref = -INFINITY, sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     bool any_bad = false;
     for (int i0 = 8 * group; i0 < n_parts; i0 += 8 * groups) {
@@ -1384,8 +1403,9 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
         const float wt = __shfl_sync(lanes, mine, (lane & 24) + u);
         if (i0 + u >= n_parts) continue;
         sum += wt;
-        acc[0] += va[u].x * wt; acc[1] += va[u].y * wt; acc[2] += va[u].z * wt; acc[3] += va[u].w * wt;
-        acc[4] += vb[u].x * wt; acc[5] += vb[u].y * wt; acc[6] += vb[u].z * wt; acc[7] += vb[u].w * wt;
+        const float wv = wt * kJoin;
+        acc[0] += va[u].x * wv; acc[1] += va[u].y * wv; acc[2] += va[u].z * wv; acc[3] += va[u].w * wv;
+        acc[4] += vb[u].x * wv; acc[5] += vb[u].y * wv; acc[6] += vb[u].z * wv; acc[7] += vb[u].w * wv;
       }
     }
 #pragma unroll
@@ -1415,7 +1435,7 @@ __global__ void __launch_bounds__(paged::kThreads, paged::Cfg<kType, kRows>::kCt
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] += src[4 + d0 + e] * wt;
       }
-      const float inv = 1.f / sum;
+      const float inv = 1.f / kJoin / sum;
       const long long oh = static_cast<long long>(s.b) * p.H + h0 + row;
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (!any_bad)
@@ -1499,6 +1519,7 @@ unsigned paged_box_rows(int page_size) {
   return page_size < Tile<Kv::kBf16>::kTile ? page_size : Tile<Kv::kBf16>::kTile;
 }
 
+static_assert(kPagedSms * Cfg<Kv::kBf16, 8>::kCtas <= kMaxJoin, "parts of a unit");
 size_t paged_counter_bytes() { return kPagedSms * Cfg<Kv::kBf16, 8>::kCtas * sizeof(int); }
 
 // tmK, tmV: the bf16 pools as [rows, 64] in boxes of paged_box_rows rows

@@ -1,6 +1,6 @@
 """Decode attention over the 4-bit cache at the ends of the range: sums that are zero when
-the references move, large keys beside small queries, scores of any size, against the
-plain 64-bit implementation of grouped.py."""
+the references move, large keys beside small queries, scores of any size, values up to bf16's largest, against
+the plain 64-bit implementation of grouped.py."""
 import pytest
 import torch
 
@@ -123,3 +123,31 @@ def test_exponents_of_values_beside_scores_of_any_size(na, n, at, v_byte, spread
     for k in (4, 10, *range(18, 34), 60, 110):
         for sign in (1, -1):
             _winner(na, n, H, k, sign, v_byte, at, spread)
+
+
+@pytest.mark.parametrize("H", [4, 13])
+@pytest.mark.parametrize("n", [1, 5, 300, 1500, 20000])
+@pytest.mark.parametrize("lo,hi", [(245, 252), (252, 252), (200, 252), (27, 252), (27, 28)])
+def test_values_of_any_size(na, H, n, lo, hi):
+    """Scale bytes up to the largest that the cache writes (2^125): one key, several, parts
+    that are joined; alike and far apart."""
+    r, i = Rows(n), torch.arange(n)
+    for h in (0, 1):
+        r.what("v", i, None, lo + (i * 7 + h) % (hi - lo + 1), h)
+    r.check(na, _randn(5, 1, H, 64))
+    # All of the largest size and one sign: nothing is larger on the way.
+    r.what("v", i, 0x77, hi)
+    out, _ = r.decode(na, _randn(5, 1, H, 64))
+    want = 6 * 2.0 ** (hi - 127)
+    # Weights in halves (2^-11) and their sum of n terms, bf16.
+    err = want * (U16 + 2.0 ** -11 + (n + 32) * U32)
+    within(out, torch.full_like(out, want), torch.full_like(out, err, dtype=F64), "out")
+
+
+def test_values_whose_scales_are_beyond_bf16(na):
+    """Scale bytes that the cache itself never writes, of values that bf16 holds."""
+    for byte, code in ((253, 0x22), (254, 0x11), (0, 0x77), (20, 0x22)):
+        r = Rows(300).what("v", range(300), code, byte)
+        out, _ = r.decode(na, _randn(6, 1, 4, 64))
+        want = r.c.rows(0)[1][0, 0, 0]
+        within(out, want.expand(4, 64), (want * (U16 + 2.0 ** -11 + 332 * U32)).expand(4, 64), "out")
