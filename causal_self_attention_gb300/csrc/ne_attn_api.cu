@@ -1383,7 +1383,7 @@ ne_status ne_kv_reserve(const int* new_lens, const int* seq_lens, int nseq, int*
   p.new_lens = new_lens;
   p.block_table = block_table;
   p.n_tot = positions || slots ? n_tot : 0;
-  p.max_rows = positions || slots ? n_tot : 0x7ffffffe;  // (int32 prefix sums)
+  p.max_rows = n_tot > 0 || positions || slots ? n_tot : 0x7ffffffe;  // (int32 prefix sums)
   p.cu_seqlens = cu_seqlens;
   p.start_pos = start_pos;
   p.positions = positions;

@@ -113,7 +113,7 @@ struct PagesParams {
   const int* n_free;
   int* n_free_out;          // (may be n_free)
   int nseq, n_tot, max_pages, n_pages, page_shift, max_seqlen;
-  int max_rows;     // reserve: n_tot, or no bound where neither positions nor slots are wanted
+  int max_rows;     // reserve: the caller's n_tot (n_tot here: 0 where no row is written out), or no bound
   int* cu_seqlens;  // reserve: [nseq + 1], [nseq], [n_tot], [n_tot], each or nullptr
   int* start_pos;
   int* positions;

@@ -430,8 +430,9 @@ ne_status ne_kv_read(int kv_type, const void* k_pages, const void* v_pages,
  *   seq_lens_out  [nseq], seq_lens + new_lens (may be seq_lens itself);
  *   n_free_out    [1], n_free less the pages taken (may be n_free itself).
  * cu_seqlens, start_pos, positions, slots: NULL where not wanted.  Rows from the sum
- * of new_lens on have position and slot -1.  n_tot: 0 .. 2^30; 0 where neither
- * positions nor slots are wanted leaves the number of rows unbounded (below 2^31 - 1).  All or nothing:
+ * of new_lens on have position and slot -1.  n_tot: 0 .. 2^30, a bound on the rows also
+ * where neither positions nor slots are wanted; 0 there leaves their number unbounded (below
+ * 2^31 - 1).  All or nothing:
  * a length out of place (seq_lens[s] or new_lens[s] negative, their sum beyond
  * max_seqlen, more rows than n_tot) is reported as NE_ERR_BAD_SEQLEN, more pages than
  * are free as NE_ERR_NO_PAGES; then no page is handed out, cu_seqlens is zero,
