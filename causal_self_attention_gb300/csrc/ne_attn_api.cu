@@ -64,7 +64,7 @@ cudaError_t launch_kv_read(__nv_bfloat16* k, __nv_bfloat16* v, const int* cu,
                            const int* start_pos, int nseq, int n_tot, const PagedCache& pc,
                            Kv type, int* status, cudaStream_t stream);
 cudaError_t launch_kv_reserve(const PagesParams& p, int sms, cudaStream_t stream);
-cudaError_t launch_kv_release(const PagesParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_kv_release(const PagesParams& p, cudaStream_t stream);
 size_t qk_norm_part_bytes();
 cudaError_t launch_qk_norm(const QkNormParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_qk_norm_bwd(const QkNormParams& p, int sms, cudaStream_t stream);
@@ -1415,10 +1415,8 @@ ne_status ne_kv_release(const uint8_t* finished, int* seq_lens, int nseq, int* b
   std::lock_guard<std::mutex> lock(g_mutex);
   DeviceState* st = nullptr;
   if ((rc = device_state(&st)) != NE_OK) return rc;
-  cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if ((rc = arrival_counter(*st, cs, &p.arrived)) != NE_OK) return rc;
   p.status = st->status;
-  return cuda_status(ne::launch_kv_release(p, st->sm_count, cs));
+  return cuda_status(ne::launch_kv_release(p, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

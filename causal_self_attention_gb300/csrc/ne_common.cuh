@@ -118,7 +118,7 @@ struct PagesParams {
   int* start_pos;
   int* positions;
   int* slots;
-  int* arrived;  // zero before and after the launch
+  int* arrived;  // reserve: zero before and after the launch
   int* status;
 };
 

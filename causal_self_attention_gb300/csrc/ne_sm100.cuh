@@ -190,21 +190,51 @@ inline cudaError_t allow_smem(void (*kernel)(KArgs...), int bytes, bool (&done)[
 }
 
 // Launch `kernel` on `stream` with programmatic stream serialization allowed,
-// so that its CTAs may start while the previous kernel on the stream drains.
+// so that its CTAs may start while the previous kernel on the stream drains;
+// in clusters of `cluster` CTAs, which run at the same time.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                              cudaStream_t stream, Args&&... args) {
+inline cudaError_t launch_pdl_clusters(unsigned cluster, void (*kernel)(KArgs...), dim3 grid,
+                                       dim3 block, size_t smem, cudaStream_t stream,
+                                       Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+}
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t stream, Args&&... args) {
+  return launch_pdl_clusters(1, kernel, grid, block, smem, stream, static_cast<Args&&>(args)...);
+}
+
+// The cluster's barrier (every thread arrives and waits): what they did before they arrived
+// is seen behind the wait.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// A word of the shared memory of CTA `rank` of the cluster, `mine` here.
+__device__ __forceinline__ int cluster_load(const int* mine, unsigned rank) {
+  int v;
+  asm volatile(
+      "{\n\t.reg .u32 at;\n\tmapa.shared::cluster.u32 at, %1, %2;\n\t"
+      "ld.shared::cluster.s32 %0, [at];\n\t}"
+      : "=r"(v)
+      : "r"(smem_u32(mine)), "r"(rank)
+      : "memory");
+  return v;
 }
 
 // Named barrier among `nthreads` threads (a warpgroup) with id `id` (1..15).

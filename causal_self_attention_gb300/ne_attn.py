@@ -946,7 +946,9 @@ def ne_kv_release(finished, seq_lens, block_table, free_pages, n_free, page_size
                   stream=None):
     """Take back the pages of every sequence with ``finished[s]`` (bool or uint8 CUDA
     ``[nseq]``): they go onto the stack of :func:`ne_kv_reserve`, their entries of
-    ``block_table`` become -1 and ``seq_lens[s]`` 0, all in place.  Returns None."""
+    ``block_table`` become -1 and ``seq_lens[s]`` 0, all in place.  An entry that is no page
+    of the pool shows in :func:`ne_attn_get_device_status` (``NE_ERR_BAD_PAGE``), and then
+    nothing is taken back.  Returns None."""
     if stream is None and _step is not None:
         rc = _step.release(finished, seq_lens, block_table, free_pages, n_free, page_size, max_seqlen)
         if rc is not None:

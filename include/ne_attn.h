@@ -40,8 +40,7 @@
  *    needed; inside a capture each call allocates and frees its own), the
  *    backward's work-schedule tables (one per fixed-length shape, a few KB,
  *    made on first use outside graph capture), the arrival counters of the paged
- *    decode, the norms' backward and the calls that hand pages out and take them
- *    back (in blocks; 2 KB for each stream and each captured call) -- all released by
+ *    decode, the norms' backward and the call that hands pages out (in blocks; 2 KB for each stream and each captured call) -- all released by
  *    ne_attn_release -- and, when a backward is given no workspace, a
  *    stream-ordered temporary it frees itself.
  *  - `stream` is a cudaStream_t (NULL = legacy default stream).  Work is
@@ -443,7 +442,8 @@ ne_status ne_kv_read(int kv_type, const void* k_pages, const void* v_pages,
  * [nseq]), ceil(seq_lens[s] / page_size) of them, go onto the stack, the first page
  * of the first such sequence first; their entries of the block table become -1 and
  * seq_lens[s] 0.  All or nothing, too: NE_ERR_BAD_SEQLEN for a length outside [0,
- * max_seqlen], NE_ERR_NO_PAGES where the stack would hold more than n_pages.
+ * max_seqlen], NE_ERR_NO_PAGES where the stack would hold more than n_pages,
+ * NE_ERR_BAD_PAGE for an entry to be given back outside [0, n_pages).
  *
  * The arrays written must not overlap the others or each other but as stated. */
 ne_status ne_kv_reserve(const int* new_lens, const int* seq_lens, int nseq, int* block_table,

@@ -55,3 +55,57 @@ def test_no_bound_without_rows_wanted(na, outs):  # noqa: F811
     want = dict(zip(("cu_seqlens", "start_pos"), plain.reserve([40, 3, 0], 43)))
     assert code == 0 and all(room[n].tolist() == want[n] for n in outs)
     gpu.check()
+
+
+@pytest.mark.parametrize("nseq", [2, 1024, 3000, 16384])
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 2 ** 31 - 1, "n_pages"])
+def test_release_of_what_is_no_page(na, nseq, bad):  # noqa: F811
+    """All or nothing: an entry outside the pool is told, and none of the others is given
+    back; entries of sequences that go on, and behind a sequence's pages, do not matter."""
+    width, page = 4, 16
+    plain = step.Pages(nseq, width, nseq * width, page, range(nseq * width))
+    gpu = Gpu(plain)
+    new = [(7 * s) % (width * page) + 1 for s in range(nseq)]
+    gpu.reserve(na, new, sum(new))
+    plain.reserve(new, sum(new))
+    bad = plain.n_pages if bad == "n_pages" else bad
+    on = nseq // 2  # the sequence that goes on
+    finished = [s != on for s in range(nseq)]
+    for s in {0, nseq // 3, nseq - 1} - {on}:
+        for col in {0, (new[s] - 1) // page}:
+            good = int(gpu.table[s, col])
+            gpu.table[s, col] = bad
+            before = gpu.state()
+            gpu.release(na, finished)
+            assert na.ne_attn_get_device_status() == 9
+            assert gpu.state() == before
+            gpu.table[s, col] = good
+    gpu.table[on] = bad
+    gpu.table[0, 3] = bad  # (its one row is on page 0)
+    gpu.release(na, finished)
+    plain.release(finished)
+    assert na.ne_attn_get_device_status() == 0
+    gpu.table[on] = _i32(plain.table[on])
+    gpu.table[0, 3] = -1
+    gpu.check()
+
+
+def test_release_of_many_pages(na):  # noqa: F811
+    """Several CTAs' shares of one sequence's pages beside many short ones."""
+    nseq, width = 5000, 3000
+    plain = step.Pages(nseq, width, 8000, 16, range(8000))
+    gpu = Gpu(plain)
+    new = [1] * nseq
+    new[1234] = width * 16
+    gpu.reserve(na, new, sum(new))
+    plain.reserve(new, sum(new))
+    good = gpu.table[1234, 2999].clone()
+    gpu.table[1234, 2999] = 8000
+    before = gpu.state()
+    gpu.release(na, [True] * nseq)
+    assert na.ne_attn_get_device_status() == 9 and gpu.state() == before
+    gpu.table[1234, 2999] = good
+    gpu.release(na, [True] * nseq)
+    plain.release([True] * nseq)
+    assert na.ne_attn_get_device_status() == 0
+    gpu.check()
