@@ -132,14 +132,17 @@ PyObject* result(ne_status rc, std::initializer_list<Tensor> out) {
 }
 
 // Calls the library without the interpreter's lock, as ctypes does (and has it again
-// whichever way the call ends).
-template <typename F>
-ne_status unlocked(F f) {
+// whichever way the call ends).  The arguments come by value: addresses, sizes and the stream
+// are read under the lock, where the checks were made, and another thread that gives a tensor
+// other memory meanwhile changes nothing of this call.
+template <typename... Wanted, typename... Given>
+ne_status unlocked(ne_status (*call)(Wanted...), Given... given) {
+  static_assert(sizeof...(Wanted) == sizeof...(Given), "");
   struct Lock {
     PyThreadState* state = PyEval_SaveThread();
     ~Lock() { PyEval_RestoreThread(state); }
   } lock;
-  return f();
+  return call(given...);
 }
 
 // What the norms' two directions share.
@@ -173,14 +176,11 @@ PyObject* norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !m.c.maybe(a[9], kBf16, {m.n, m.Hkv, kDim}, gk) || !m.c.current())
     Py_RETURN_NONE;
   const Tensor qr = output(gq, m.q->sizes(), kBf16, *m.q), kr = output(gk, m.k->sizes(), kBf16, *m.k);
-  const ne_status rc = unlocked([&] {
-    return lib.norm_fwd(static_cast<const ne_bf16*>(at_(m.q)), static_cast<const ne_bf16*>(at_(m.k)),
-                        m.q_row, m.k_row, static_cast<const ne_bf16*>(at_(m.qw)),
-                        static_cast<const ne_bf16*>(at_(m.kw)), static_cast<const int*>(at_(m.pos)),
-                        m.n, m.H, m.Hkv, kDim, m.max_seqlen, m.eps, m.base,
-                        static_cast<ne_bf16*>(at_(&qr)), static_cast<ne_bf16*>(at_(&kr)),
-                        m.c.stream());
-  });
+  const ne_status rc = unlocked(lib.norm_fwd, static_cast<const ne_bf16*>(at_(m.q)),
+      static_cast<const ne_bf16*>(at_(m.k)), m.q_row, m.k_row,
+      static_cast<const ne_bf16*>(at_(m.qw)), static_cast<const ne_bf16*>(at_(m.kw)),
+      static_cast<const int*>(at_(m.pos)), m.n, m.H, m.Hkv, kDim, m.max_seqlen, m.eps, m.base,
+      static_cast<ne_bf16*>(at_(&qr)), static_cast<ne_bf16*>(at_(&kr)), m.c.stream());
   return result(rc, {qr, kr});
   END_HANDLE_TH_ERRORS
 }
@@ -201,15 +201,13 @@ PyObject* norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (a[11] != Py_None && (!(gk = m.c.rows(a[11], dk_row)) || gk->sizes() != m.k->sizes())) Py_RETURN_NONE;
   const Tensor dq = output(gq, m.q->sizes(), kBf16, *m.q), dk = output(gk, m.k->sizes(), kBf16, *m.k);
   const Tensor dqw = output(gqw, {kDim}, kF32, *m.q), dkw = output(gkw, {kDim}, kF32, *m.q);
-  const ne_status rc = unlocked([&] {
-    return lib.norm_bwd(
-        static_cast<const ne_bf16*>(at_(dqr)), static_cast<const ne_bf16*>(at_(dkr)),
-        static_cast<const ne_bf16*>(at_(m.q)), static_cast<const ne_bf16*>(at_(m.k)), m.q_row, m.k_row,
-        static_cast<const ne_bf16*>(at_(m.qw)), static_cast<const ne_bf16*>(at_(m.kw)),
-        static_cast<const int*>(at_(m.pos)), m.n, m.H, m.Hkv, kDim, m.max_seqlen, m.eps, m.base,
-        static_cast<ne_bf16*>(at_(&dq)), static_cast<ne_bf16*>(at_(&dk)), dq_row, dk_row,
-        static_cast<float*>(at_(&dqw)), static_cast<float*>(at_(&dkw)), nullptr, 0, m.c.stream());
-  });
+  const ne_status rc = unlocked(lib.norm_bwd, static_cast<const ne_bf16*>(at_(dqr)),
+      static_cast<const ne_bf16*>(at_(dkr)), static_cast<const ne_bf16*>(at_(m.q)),
+      static_cast<const ne_bf16*>(at_(m.k)), m.q_row, m.k_row,
+      static_cast<const ne_bf16*>(at_(m.qw)), static_cast<const ne_bf16*>(at_(m.kw)),
+      static_cast<const int*>(at_(m.pos)), m.n, m.H, m.Hkv, kDim, m.max_seqlen, m.eps, m.base,
+      static_cast<ne_bf16*>(at_(&dq)), static_cast<ne_bf16*>(at_(&dk)), dq_row, dk_row,
+      static_cast<float*>(at_(&dqw)), static_cast<float*>(at_(&dkw)), nullptr, 0, m.c.stream());
   return result(rc, {dq, dk, dqw, dkw});
   END_HANDLE_TH_ERRORS
 }
@@ -246,16 +244,14 @@ PyObject* reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   const Tensor cu = output(g[0], {p.nseq + 1LL}, kI32, *more), start = output(g[1], {p.nseq}, kI32, *more);
   const Tensor pos = output(g[2], {n_tot}, kI32, *more), slots = output(g[3], {n_tot}, kI32, *more);
-  const ne_status rc = unlocked([&] {
-    return lib.reserve(static_cast<const int*>(at_(more)), static_cast<const int*>(at_(p.lens)), p.nseq,
-                       static_cast<int*>(at_(p.table)), len(p.table, 1),
-                       static_cast<const int*>(at_(p.free)), static_cast<const int*>(at_(p.n_free)),
-                       len(p.free, 0), page_size, max_seqlen, n_tot, static_cast<int*>(at_(&cu)),
-                       static_cast<int*>(at_(&start)), n_tot ? static_cast<int*>(at_(&pos)) : nullptr,
-                       n_tot ? static_cast<int*>(at_(&slots)) : nullptr,
-                       static_cast<int*>(at_(lens_out ? lens_out : p.lens)),
-                       static_cast<int*>(at_(n_free_out ? n_free_out : p.n_free)), p.c.stream());
-  });
+  const ne_status rc = unlocked(lib.reserve, static_cast<const int*>(at_(more)),
+      static_cast<const int*>(at_(p.lens)), p.nseq, static_cast<int*>(at_(p.table)),
+      len(p.table, 1), static_cast<const int*>(at_(p.free)), static_cast<const int*>(at_(p.n_free)),
+      len(p.free, 0), page_size, max_seqlen, n_tot, static_cast<int*>(at_(&cu)),
+      static_cast<int*>(at_(&start)), n_tot ? static_cast<int*>(at_(&pos)) : nullptr,
+      n_tot ? static_cast<int*>(at_(&slots)) : nullptr,
+      static_cast<int*>(at_(lens_out ? lens_out : p.lens)),
+      static_cast<int*>(at_(n_free_out ? n_free_out : p.n_free)), p.c.stream());
   return result(rc, {cu, start, pos, slots});
   END_HANDLE_TH_ERRORS
 }
@@ -269,12 +265,10 @@ PyObject* release(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor* done = p.c.get(a[0], at::kBool, {p.nseq});
   if (!done) done = p.c.get(a[0], kU8, {p.nseq});
   if (!done || !as_int(a[5], page_size) || !as_int(a[6], max_seqlen) || !p.c.current()) Py_RETURN_NONE;
-  return PyLong_FromLong(unlocked([&] {
-    return lib.release(static_cast<const uint8_t*>(at_(done)), static_cast<int*>(at_(p.lens)), p.nseq,
-                       static_cast<int*>(at_(p.table)), len(p.table, 1), static_cast<int*>(at_(p.free)),
-                       static_cast<int*>(at_(p.n_free)), len(p.free, 0), page_size, max_seqlen,
-                       p.c.stream());
-  }));
+  return PyLong_FromLong(unlocked(lib.release, static_cast<const uint8_t*>(at_(done)),
+      static_cast<int*>(at_(p.lens)), p.nseq, static_cast<int*>(at_(p.table)), len(p.table, 1),
+      static_cast<int*>(at_(p.free)), static_cast<int*>(at_(p.n_free)), len(p.free, 0), page_size,
+      max_seqlen, p.c.stream()));
   END_HANDLE_TH_ERRORS
 }
 
@@ -324,14 +318,12 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!v || !cu || !s.parse(c, a + 4, a[8], a[9], len(start, 0)) || s.Hkv != k->size(1) ||
       !as_int(a[7], max_seqlen) || !as_float(a[10], base) || !c.current())
     Py_RETURN_NONE;
-  return PyLong_FromLong(unlocked([&] {
-    return lib.append(static_cast<const ne_bf16*>(at_(k)), static_cast<const ne_bf16*>(at_(v)),
-                      static_cast<const int*>(at_(cu)), static_cast<const int*>(at_(start)),
-                      len(start, 0), len(k, 0), s.Hkv, kDim, base, s.type, at_(s.k), at_(s.v),
-                      static_cast<uint8_t*>(at_(s.ks)), static_cast<uint8_t*>(at_(s.vs)),
-                      static_cast<const int*>(at_(s.table)), len(s.table, 1), len(s.k, 0), len(s.k, 2),
-                      max_seqlen, c.stream());
-  }));
+  return PyLong_FromLong(unlocked(lib.append, static_cast<const ne_bf16*>(at_(k)),
+      static_cast<const ne_bf16*>(at_(v)), static_cast<const int*>(at_(cu)),
+      static_cast<const int*>(at_(start)), len(start, 0), len(k, 0), s.Hkv, kDim, base, s.type,
+      at_(s.k), at_(s.v), static_cast<uint8_t*>(at_(s.ks)), static_cast<uint8_t*>(at_(s.vs)),
+      static_cast<const int*>(at_(s.table)), len(s.table, 1), len(s.k, 0), len(s.k, 2), max_seqlen,
+      c.stream()));
   END_HANDLE_TH_ERRORS
 }
 
@@ -357,13 +349,10 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   const Tensor k = output(gk, {n_tot, s.Hkv, kDim}, kBf16, *start),
                v = output(gv, {n_tot, s.Hkv, kDim}, kBf16, *start);
-  const ne_status rc = unlocked([&] {
-    return lib.read(s.type, at_(s.k), at_(s.v), s.scale(s.ks), s.scale(s.vs),
-                    static_cast<const int*>(at_(s.table)), len(s.table, 1), len(s.k, 0), len(s.k, 2),
-                    max_seqlen, static_cast<const int*>(at_(cu)), static_cast<const int*>(at_(start)),
-                    len(start, 0), n_tot, s.Hkv, kDim, static_cast<ne_bf16*>(at_(&k)),
-                    static_cast<ne_bf16*>(at_(&v)), c.stream());
-  });
+  const ne_status rc = unlocked(lib.read, s.type, at_(s.k), at_(s.v), s.scale(s.ks), s.scale(s.vs),
+      static_cast<const int*>(at_(s.table)), len(s.table, 1), len(s.k, 0), len(s.k, 2), max_seqlen,
+      static_cast<const int*>(at_(cu)), static_cast<const int*>(at_(start)), len(start, 0), n_tot,
+      s.Hkv, kDim, static_cast<ne_bf16*>(at_(&k)), static_cast<ne_bf16*>(at_(&v)), c.stream());
   return result(rc, {k, v});
   END_HANDLE_TH_ERRORS
 }
@@ -388,13 +377,11 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !c.maybe(a[11], kF32, {B, H}, gl) || !c.current())
     Py_RETURN_NONE;
   const Tensor out = output(go, q->sizes(), kBf16, *q), lse = output(gl, {B, H}, kF32, *q);
-  const ne_status rc = unlocked([&] {
-    return lib.decode(static_cast<const ne_bf16*>(at_(q)), s.type, at_(s.k), at_(s.v), s.scale(s.ks),
-                      s.scale(s.vs), static_cast<const int*>(at_(s.table)), len(s.table, 1),
-                      len(s.k, 0), len(s.k, 2), max_seqlen, static_cast<const int*>(at_(lens)), B, H,
-                      s.Hkv, kDim, base, scale, static_cast<ne_bf16*>(at_(&out)),
-                      static_cast<float*>(at_(&lse)), nullptr, 0, c.stream());
-  });
+  const ne_status rc = unlocked(lib.decode, static_cast<const ne_bf16*>(at_(q)), s.type, at_(s.k),
+      at_(s.v), s.scale(s.ks), s.scale(s.vs), static_cast<const int*>(at_(s.table)),
+      len(s.table, 1), len(s.k, 0), len(s.k, 2), max_seqlen, static_cast<const int*>(at_(lens)), B,
+      H, s.Hkv, kDim, base, scale, static_cast<ne_bf16*>(at_(&out)), static_cast<float*>(at_(&lse)),
+      nullptr, 0, c.stream());
   return result(rc, {out, lse});
   END_HANDLE_TH_ERRORS
 }
