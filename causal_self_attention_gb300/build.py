@@ -46,9 +46,10 @@ def compile_flags(extra=()) -> list:
 
 
 def step_path() -> str:
-    """The path of the module ``ne_step`` for this torch."""
+    """The path of the module ``ne_step`` for this torch and this interpreter's ABI."""
     import torch
-    return os.path.join(BUILD_DIR, f"ne_step-{torch.__version__}.so")
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    return os.path.join(BUILD_DIR, f"ne_step-{torch.__version__}{suffix}")
 
 
 def _build_step(path: str, cuda: str) -> None:

@@ -39,3 +39,15 @@ def test_the_same_results_without_the_module(monkeypatch):
     for (name, call), w in zip(calls, want):
         assert _same(call(), w), name
     assert na.ne_attn_get_device_status() == 0
+
+
+def test_the_module_belongs_to_this_python_and_torch():
+    """Its name says for which interpreter and torch it was built: another one's is not
+    loaded."""
+    import importlib.machinery
+    import sysconfig
+
+    from causal_self_attention_gb300 import build
+    name = build.step_path()
+    assert torch.__version__ in name and name.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert sysconfig.get_config_var("EXT_SUFFIX") in importlib.machinery.EXTENSION_SUFFIXES
