@@ -13,6 +13,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -52,13 +53,23 @@ def step_path() -> str:
     return os.path.join(BUILD_DIR, f"ne_step-{torch.__version__}{suffix}")
 
 
-def _build_step(path: str, cuda: str) -> None:
+def _cuda_include() -> str:
+    """The folder of CUDA's headers (of the runtime, which torch's name)."""
+    nvcc = os.environ.get("NVCC") or shutil.which("nvcc")
+    homes = [os.environ.get("CUDA_HOME"), os.environ.get("CUDA_PATH"),
+             nvcc and os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "/usr/local/cuda"]
+    for home in filter(None, homes):
+        if os.path.exists(os.path.join(home, "include", "cuda_runtime_api.h")):
+            return os.path.join(home, "include")
+    raise RuntimeError("cuda_runtime_api.h not found (CUDA_HOME names where CUDA is)")
+
+
+def _build_step(path: str) -> None:
     import torch
     home = os.path.dirname(torch.__file__)
     include = (os.path.join(home, "include"),
                os.path.join(home, "include", "torch", "csrc", "api", "include"),
-               sysconfig.get_paths()["include"], os.path.join(cuda, "include"),
-               os.path.join(ROOT, "include"))
+               sysconfig.get_paths()["include"], _cuda_include(), os.path.join(ROOT, "include"))
     tmp = path + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
            *("-I" + d for d in include), os.path.join(CSRC, STEP_SOURCE), "-o", tmp,
@@ -70,24 +81,28 @@ def _build_step(path: str, cuda: str) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile (if stale) and return the library path."""
+    """Compile (if stale) and return the library path.  Where the module cannot be built, a
+    warning says so: the binding makes its calls itself then."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     step, deps = step_path(), _deps_mtime()
     fresh = [not force and os.path.exists(p) and os.path.getmtime(p) >= deps for p in (LIB_PATH, step)]
-    nvcc = None if all(fresh) else nvcc_path()
     with ThreadPoolExecutor(max_workers=1) as ex:
-        module = None
-        if not fresh[1]:
-            cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
-            module = ex.submit(_build_step, step, cuda)
+        module = None if fresh[1] else ex.submit(_build_step, step)
         if not fresh[0]:
-            _build_library(nvcc, verbose, ptxas_info)
+            _build_library(verbose, ptxas_info)
         if module is not None:
-            module.result()
+            try:
+                module.result()
+            except (RuntimeError, OSError) as e:
+                if os.path.exists(step):  # (one of older sources)
+                    os.remove(step)
+                warnings.warn(f"the module ne_step is not built, calls are marshalled in Python: {e}",
+                              RuntimeWarning, stacklevel=2)
     return LIB_PATH
 
 
-def _build_library(nvcc: str, verbose: bool, ptxas_info: bool) -> None:
+def _build_library(verbose: bool, ptxas_info: bool) -> None:
+    nvcc = nvcc_path()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
     def compile_one(src):
