@@ -54,10 +54,11 @@
 // 7.4 us (launch, prefix sums, a short ring, the join).  Tried: four CTAs an SM
 // with two stages, three q slots, other overheads (2, 3, 6) and part limits
 // (16-256): none faster on all of these.
-// e2m1: 64 sequences of 16k, 32 heads on 8, 109 us (5.0 TB/s, 74% of the copy rate; a
+// e2m1: 64 sequences of 16k, 32 heads on 8, 110 us (5.0 TB/s, 73% of the copy rate; a
 // byte has four times the keys of bf16, and what bounds a tile is its arithmetic: the
-// integer pipe busy half of the time, issue slots 53%, three dependent warps a scheduler);
-// 64 ragged ones 30.6 us (2.8 TB/s), 777 keys 8.9 us, 64 of 2000 27.8 us.  Tried: four
+// integer pipe busy half of the time, issue slots 54%, three dependent warps a scheduler);
+// 64 ragged ones 30.8 us (2.8 TB/s), 777 keys 8.4 us, 64 of 2000 28.8 us, 96 of 512 19.2,
+// 16 of 16k with 16 heads a group 26.8 (a tile of 64 keys by 16 heads spills).  Tried: four
 // CTAs an SM with two stages (136, 40, 11 and 37 us: 96 registers spill), tiles of 32
 // keys a warp, warps that take tiles of their own without meeting (113, 33 us).
 //
@@ -1477,7 +1478,9 @@ int paged_ctas(long long B, int H, int Hkv, int max_seqlen, Kv type, int sms) {
 // The tiles of a range at the least.  e2m1, whose tiles take 1 us: units of three tiles or
 // fewer whole (a join costs 2 us: 4 sequences of 500, 7.4 us whole, 9.1 by single tiles),
 // others of up to 18 by single tiles (one sequence of 1000 8.8 us, by two 9.7; 4000 9.4 and
-// 10.2), longer ones not (8000 10.5 by two, 10.9 by single tiles; 12000 10.9 and 13.0).
+// 10.2), longer ones not (8000 10.5 by two, 10.9 by single tiles; 12000 10.9 and 13.0).  The
+// rule goes by the caller's bound on the lengths, which the host knows, not by the lengths:
+// with a bound of 16384 one sequence of 777 takes 9.4 us (8.4 to 8.8), of 4000 10.1 (9.0).
 int paged_least(int max_seqlen, Kv type) {
   if (type != Kv::kE2m1) return 2;
   const int each = (max_seqlen + Tile<Kv::kE2m1>::kTile - 1) / Tile<Kv::kE2m1>::kTile;

@@ -22,8 +22,9 @@
 //
 // What bounds it is latency and, with thousands of sequences, every CTA's instructions for
 // their sums.  Measured: 64 sequences, a row each, 3.8 us (launch, the lengths, two barriers,
-// a bisection, a table entry); 4096 sequences with a million rows in all 10.6 us (the rows'
-// 8 MB alone 1.2 us); 16384 with a row each 21.8 us.  (Sequences in runs of a thread's own 4.7,
+// a bisection, a table entry); 4096 sequences with a million rows in all 10.1 us (the rows'
+// 8 MB alone 1.2 us), with a row each 9.4: the sums, every warp's of all warps' in each round;
+// 16384 with a row each 21.8 us.  (Sequences in runs of a thread's own 4.7,
 // 12.8 and 46.6 us; two CTAs an SM 12 to 14% slower for the second; lengths updated behind the
 // rows' stores, whose fence waits for them, or all threads waiting for the arrival, 1 to 2 us
 // more.)

@@ -15,8 +15,9 @@
 // the head are two shuffles.  All arithmetic is fp32; each output is rounded
 // once (bf16; dw is fp32).
 // Measured, forward: 92,604 rows of 40 heads 145 us (6.5 TB/s, 96% of the copy rate),
-// 18,641 of 16 heads 13.3 us (5.7 TB/s), 64 of 16 heads 1.5 us (a launch); backward:
-// 65,536 rows of 40 heads 180 us (5.6 TB/s, 83%), 8192 of 16 heads 14.7 us (3.4 TB/s: two
+// 18,641 of 16 heads 13.4 us where passes write the same memory (5.7 TB/s: part of it stays in
+// L2), 15.3 where each writes its own (5.0 TB/s), 64 of 16 heads 1.5 us (a launch); backward:
+// 65,536 rows of 40 heads 180 us (5.6 TB/s, 83%), 8192 of 16 heads 15.4 us (3.3 TB/s: two
 // rounds of loads that wait, the sums of dw, the CTA that adds them up).
 #include "ne_sm100.cuh"
 
@@ -333,7 +334,7 @@ cudaError_t launch_forward(const QkNormParams& p, cudaStream_t stream) {
 // where they leave four slots or more empty are four: 8192 rows of 16 heads 7.5 us by
 // eight, 7.8 by four, 8.8 by one.  Small CTAs end and begin one by one, so that loads and
 // stores of different rows overlap: of 64 threads 129 us (6.4 TB/s), of 128 130, of 256
-// 135; 18,600 rows of 16 heads 17.0, 17.4, 18.2.
+// 135; 18,600 rows of 16 heads, outputs of its own each pass, 15.3, 15.5, 16.2.
 cudaError_t launch_qk_norm(const QkNormParams& p, int sms, cudaStream_t stream) {
   const int heads = p.H + p.Hkv;
   const long long pairs = static_cast<long long>(p.n_tot) * heads;

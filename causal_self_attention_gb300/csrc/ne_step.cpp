@@ -3,8 +3,8 @@
 // ne_attn.py goes through).
 //
 // What it is for: these calls' kernels take 2 to 20 us, and marshalling them in Python took
-// as long or longer (64 rows of norms: 1.6 us of kernel, 15 us of call; 4.7 us this way,
-// two outputs' allocation among them).
+// as long or longer (64 rows of norms: 1.5 us of kernel, 15 us of call; 6 to 9 us this way, by
+// the host's state, two outputs' allocation among them).
 //
 // The regular call is made here: plain tensors on the current device, its current stream,
 // the library's own workspace.  Anything else -- an argument of another type or shape,

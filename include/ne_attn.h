@@ -507,8 +507,9 @@ ne_status ne_qk_norm_rope_bwd(const ne_bf16* dqr, const ne_bf16* dkr, const ne_b
  * as above and its outputs are zero and -inf.  What the cache holds beyond a
  * sequence's length never reaches its outputs.  Where a wait ran out (NE_ERR_TIMEOUT)
  * the outputs of the heads concerned are zero and -inf, too.  How the work is split depends
- * on the whole batch's lengths, and with it the last bits of a result; the
- * same call gives the same bits.  workspace:
+ * on the whole batch's lengths and on max_seqlen, and with it the last bits of a result; the
+ * same call gives the same bits.  NE_KV_E2M1: value rows of scale 2^-100 or less count as
+ * zeros beside rows of scales more than 2^7 above.  workspace:
  * ne_attn_decode_paged_workspace_bytes(B, H, Hkv, max_seqlen) bytes, 16-byte
  * aligned, or NULL for a stream-ordered temporary. */
 size_t ne_attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int max_seqlen);
