@@ -57,7 +57,7 @@
 // e2m1: 64 sequences of 16k, 32 heads on 8, 110 us (5.0 TB/s, 73% of the copy rate; a
 // byte has four times the keys of bf16, and what bounds a tile is its arithmetic: the
 // integer pipe busy half of the time, issue slots 54%, three dependent warps a scheduler);
-// 64 ragged ones 30.8 us (2.8 TB/s), 777 keys 8.4 us, 64 of 2000 28.8 us, 96 of 512 19.2,
+// 64 ragged ones 31.0 us (2.8 TB/s), 777 keys 8.5 us, 64 of 2000 28.8 us, 96 of 512 19.2,
 // 16 of 16k with 16 heads a group 26.8 (a tile of 64 keys by 16 heads spills).  Tried: four
 // CTAs an SM with two stages (136, 40, 11 and 37 us: 96 registers spill), tiles of 32
 // keys a warp, warps that take tiles of their own without meeting (113, 33 us).
@@ -274,13 +274,14 @@ __device__ __forceinline__ int e2m1_key(int mt, int x) {
 // reference m that was kHeadroom below the largest score when it was set; for a value row's half h
 // they take its scale, p 2^(e_h - E_h), E_h an exponent that the warp keeps, so that a
 // weight is formed once and scaled by a product of two halves.  E_h - e_h is 0 .. 7 for
-// every row that the warp has seen.  What halves cost is their smallest step, two
+// every row that the warp has seen, zeros aside.  What halves cost is their smallest step, two
 // roundings of at most 2^-25 + 2^-26 of 2^(m + E_h) for a key; the key of the largest score
 // alone has a term of 2^(m + 8 + E_h - 7), so that it is less than 2^-25 of the largest term.
 // Where a score exceeds the reference's by more than 2^7, or an exponent its range, or the
 // sequence ends in the tile -- one vote tells --, the tile takes a longer way, on which the
-// references move.  Rows whose scales differ by more (never mind zeros) put the warp into
-// another mode for the rest of the segment: a reference of its own for every (query head,
+// references move.  Rows whose scales differ by more, and a row of zeros with the largest score
+// (which has no term), put the warp into another mode for the rest of the segment: a reference
+// of its own for every (query head,
 // half), 2^(x - m + e_h - m2), which loses nothing however far the scales are apart.  (Taken
 // from m on: beside a score of 2^24 an exponent would be lost.)
 //
@@ -294,8 +295,8 @@ struct FourBit {
   static constexpr int kMT = 4;           // row tiles of 16 keys
   static constexpr int kRange = 7;
   static constexpr float kHeadroom = 8.f;  // weights of 2^15 at most: within a half
-  // The scale byte of zeros, 2^-100; rows of it or less count as zeros beside rows 2^7 above.
-  static constexpr int kZero = 27;
+  // The scale byte of zeros, 2^-100; rows of it or less count as zeros beside rows 2^kFar above.
+  static constexpr int kZero = 27, kFar = 32;
   static constexpr int kUnset = -1000;
   static constexpr int kScratch = 16 * kMT * 12;  // a warp's: key scales (float2), value factors
   float m[kNT][2], l[kNT][2];             // l: of this lane's keys
@@ -370,10 +371,44 @@ struct FourBit {
     }
   }
 
+  __device__ __forceinline__ void turn() {  // o stays as it is, under the reference that it has
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) m2[nt][e][h] = above(nt, e, h);
+    slow = true;
+  }
+
+  // Whether a row of zeros (of a scale far below) has one of the weights w, which are 2^8 for a
+  // column's largest score yet; from 2^7 on, or, where scores have coarse steps, from 2^-1.
+  __device__ __forceinline__ bool zeros_on_top(const uint32_t (&w)[kMT][kNT][2], const uint16_t* vs,
+                                               int live, int r) const {
+    uint32_t found = 0u;
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      const bool coarse = fmaxf(fabsf(m[nt][0]), fabsf(m[nt][1])) >= 16777216.f;
+      const uint32_t up = coarse ? 0x48004800u : 0x28002800u;  // 2^-1 or 2^7 becomes the sign
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int key = e2m1_key(mt, r + 8 * hf);
+          const int b0 = vs[key] & 255, b1 = vs[key] >> 8;
+          if (key < live && (b0 < eb(0) - kRange || b1 < eb(1) - kRange))
+            found |= w[mt][nt][hf] + up;
+        }
+    }
+    return __any_sync(0xffffffffu, (found & 0x80008000u) != 0u);
+  }
+
   // Moves the references to what this tile holds (vb: the scale bytes of this lane's value
-  // rows, -1 for none).  Returns whether the mode changed.
-  __device__ __forceinline__ bool move(const float (&x)[kMT][kNT][4], const int (&vb)[2][2]) {
+  // rows, -1 for none).  Returns whether the mode changed; zeros: this lane has a row of them.
+  __device__ __forceinline__ bool move(const float (&x)[kMT][kNT][4], const int (&vb)[2][2],
+                                       bool& zeros) {
     bool turned = false;
+    zeros = false;
     if (!slow) {
       int hi[2];
       uint32_t low[2];
@@ -381,25 +416,21 @@ struct FourBit {
       for (int h = 0; h < 2; ++h) {
         int most = eb(h), least = static_cast<int>(h ? lowest >> 16 : lowest & 0xffffu);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (vb[i][h] >= 0 && vb[i][h] != 255) {
-            most = max(most, vb[i][h]);
-            if (vb[i][h] > kZero) least = min(least, vb[i][h]);
-          }
-        }
+        for (int i = 0; i < 2; ++i)
+          if (vb[i][h] != 255) most = max(most, vb[i][h]);
         hi[h] = __reduce_max_sync(0xffffffffu, most);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (vb[i][h] < 0 || vb[i][h] == 255) continue;
+          if (vb[i][h] > kZero || hi[h] < kZero + kFar) least = min(least, vb[i][h]);
+          zeros |= vb[i][h] < hi[h] - kRange;
+        }
         turned |= __reduce_min_sync(0xffffffffu, least) < hi[h] - kRange;
         low[h] = static_cast<uint32_t>(least);
       }
       lowest = low[0] | low[1] << 16;
-      if (turned) {  // o stays as it is, under the reference that it has
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) m2[nt][e][h] = above(nt, e, h);
-        slow = true;
+      if (turned) {
+        turn();
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -607,8 +638,12 @@ struct FourBit {
         vb[i][0] = mine ? static_cast<int>(bytes[i] & 255u) : -1;
         vb[i][1] = mine ? static_cast<int>(bytes[i] >> 8) : -1;
       }
-      const bool first = move(x, vb);
+      bool zeros, first = move(x, vb, zeros);
       weigh();
+      if (!slow && __any_sync(0xffffffffu, zeros) && zeros_on_top(w, vs, live, r)) {
+        turn();
+        first = true;
+      }
       if (slow) {
         far_values(x, sv, vs, live, first, r, c);
         add_sums(sum);
@@ -1480,7 +1515,7 @@ int paged_ctas(long long B, int H, int Hkv, int max_seqlen, Kv type, int sms) {
 // others of up to 18 by single tiles (one sequence of 1000 8.8 us, by two 9.7; 4000 9.4 and
 // 10.2), longer ones not (8000 10.5 by two, 10.9 by single tiles; 12000 10.9 and 13.0).  The
 // rule goes by the caller's bound on the lengths, which the host knows, not by the lengths:
-// with a bound of 16384 one sequence of 777 takes 9.4 us (8.4 to 8.8), of 4000 10.1 (9.0).
+// with a bound of 16384 one sequence of 777 takes 9.4 us (8.5 to 8.8), of 4000 10.1 (9.0).
 int paged_least(int max_seqlen, Kv type) {
   if (type != Kv::kE2m1) return 2;
   const int each = (max_seqlen + Tile<Kv::kE2m1>::kTile - 1) / Tile<Kv::kE2m1>::kTile;

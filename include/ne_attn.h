@@ -509,7 +509,7 @@ ne_status ne_qk_norm_rope_bwd(const ne_bf16* dqr, const ne_bf16* dkr, const ne_b
  * the outputs of the heads concerned are zero and -inf, too.  How the work is split depends
  * on the whole batch's lengths and on max_seqlen, and with it the last bits of a result; the
  * same call gives the same bits.  NE_KV_E2M1: value rows of scale 2^-100 or less count as
- * zeros beside rows of scales more than 2^7 above.  workspace:
+ * zeros beside rows of scales 2^32 above and more.  workspace:
  * ne_attn_decode_paged_workspace_bytes(B, H, Hkv, max_seqlen) bytes, 16-byte
  * aligned, or NULL for a stream-ordered temporary. */
 size_t ne_attn_decode_paged_workspace_bytes(int B, int H, int Hkv, int max_seqlen);

@@ -151,3 +151,33 @@ def test_values_whose_scales_are_beyond_bf16(na):
         out, _ = r.decode(na, _randn(6, 1, 4, 64))
         want = r.c.rows(0)[1][0, 0, 0]
         within(out, want.expand(4, 64), (want * (U16 + 2.0 ** -11 + 332 * U32)).expand(4, 64), "out")
+
+
+@pytest.mark.parametrize("H", [4, 13])
+@pytest.mark.parametrize("halves", [(0,), (1,), (0, 1)])
+@pytest.mark.parametrize("n,at", [(1, 0), (64, 5), (500, 3), (500, 301), (5000, 4000)])
+@pytest.mark.parametrize("gap", [10, 24, 30, 60])
+def test_zeros_with_the_largest_score(na, n, at, halves, H, gap):
+    """A row of zeros, as the cache holds them (scale byte 27), has nearly all the weight: what
+    comes out is the others', 2^-gap of it, as exact as their weights among themselves."""
+    r = Rows(n).what("k", range(n), 0x00, 127)  # scores of 0
+    r.what("k", [at], 0x22, 127)                # (1) a score of 8 |q|: 8 q / ln 2 in powers of two
+    for h in halves:
+        r.what("v", [at], 0x00, 27, h)
+    r.check(na, _ones(H, gap * 0.6931 / 8))
+
+
+@pytest.mark.parametrize("H", [4, 13])
+@pytest.mark.parametrize("above", [1, 7, 8, 9, 20, 31, 32, 33, 50])
+def test_rows_of_the_smallest_scale_beside_others(na, H, above):
+    """Rows of scale 2^-100 that hold values, beside a few a little larger."""
+    for n in (64, 700):
+        r, i = Rows(n), torch.arange(n)
+        r.what("v", i, 0x77, 27)
+        r.what("v", i[::50], 0x11, 27 + above)
+        # (What is left out is 12 2^-32 of the largest rows' values a key, n keys.)
+        out, _ = r.decode(na, _ones(H, 0.0))
+        v = r.c.rows(0)[1].mean(0)[0].expand(H, 64)
+        left = 12 * 2.0 ** -32 * 2.0 ** (above - 101) if above >= 32 else 0.0
+        within(out * 2.0 ** 90, v * 2.0 ** 90,
+               (v.abs() * (U16 + 2.0 ** -10 + (n + 32) * U32) + left) * 2.0 ** 90, "out")
