@@ -472,7 +472,8 @@ ne_status ne_kv_release(const uint8_t* finished, int* seq_lens, int nseq, int* b
  *              attention calls, and with rope_base = 0 ne_kv_append and
  *              ne_attn_decode_paged, take.
  * H and Hkv are independent; n_tot * (H + Hkv) < 2^31.  (The squares are summed in
- * fp32: magnitudes from 2^60 on may overflow there.)
+ * fp32: magnitudes from 2^60 on may overflow there, and with eps = 0 rows below 2^-60
+ * vanish there.)
  * The backward takes the gradients dqr, dkr of qr, kr and the forward's q and k, and
  * returns dq, dk (bf16, rows dq_stride, dk_stride apart) and dq_weight, dk_weight
  * (fp32 [64], 16-byte aligned, written: sums over all rows and heads in an order that
