@@ -281,9 +281,8 @@ __device__ __forceinline__ int e2m1_key(int mt, int x) {
 // sequence ends in the tile -- one vote tells --, the tile takes a longer way, on which the
 // references move.  Rows whose scales differ by more, and a row of zeros with the largest score
 // (which has no term), put the warp into another mode for the rest of the segment: a reference
-// of its own for every (query head,
-// half), 2^(x - m + e_h - m2), which loses nothing however far the scales are apart.  (Taken
-// from m on: beside a score of 2^24 an exponent would be lost.)
+// of its own for every (query head, half), 2^(x - m + e_h - m2), which loses nothing however far
+// the scales are apart.  (Taken from m on: beside a score of 2^24 an exponent would be lost.)
 //
 // What bounds a tile is the integer pipe: 128 of its conversions take two cycles each,
 // so that choices are made by masks and pairs of bytes are looked at together.
